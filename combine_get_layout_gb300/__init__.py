@@ -53,6 +53,15 @@ ABI_SYMBOLS = (
     "ep_combine_ranks",
     "ep_dispatch_from_host",
     "ep_combine_to_host",
+    "ep_route",
+    "ep_route_workspace_bytes",
+    "ep_route_balance",
+    "ep_route_backward",
+    "ep_w4_codes_bytes",
+    "ep_w4_scales_bytes",
+    "ep_w4_zeros_bytes",
+    "ep_w4_pack",
+    "ep_expert_w4",
     "ep_check_error",
     "ep_selftest_wait_timeout",
     "ep_selftest_layout_timeout",
@@ -93,6 +102,31 @@ class EpLayout(ctypes.Structure):
         ("rank_src", ctypes.c_void_p),
         ("num_tokens", ctypes.c_int32),
         ("reserved", ctypes.c_int32),
+    ]
+
+
+class EpRouterConfig(ctypes.Structure):
+    _fields_ = [
+        ("num_experts", ctypes.c_int32),
+        ("num_topk", ctypes.c_int32),
+        ("score", ctypes.c_int32),
+        ("num_groups", ctypes.c_int32),
+        ("topk_groups", ctypes.c_int32),
+        ("renormalize", ctypes.c_int32),
+        ("logits_bf16", ctypes.c_int32),
+        ("route_scale", ctypes.c_float),
+    ]
+
+
+class EpW4Config(ctypes.Structure):
+    _fields_ = [
+        ("num_experts", ctypes.c_int32),
+        ("in_features", ctypes.c_int32),
+        ("out_features", ctypes.c_int32),
+        ("group_size", ctypes.c_int32),
+        ("x_fp8", ctypes.c_int32),
+        ("gated", ctypes.c_int32),
+        ("has_zeros", ctypes.c_int32),
     ]
 
 
@@ -142,6 +176,23 @@ def _load():
                                         i32, vp]
     L.ep_combine_to_host.restype = i32
     L.ep_combine_to_host.argtypes = [P(EpConfig), P(EpLayout), vp, vp, vp, vp, i32, vp]
+    L.ep_route.restype = i32
+    L.ep_route.argtypes = [P(EpRouterConfig), i32, vp, i64, vp, vp, vp, vp, vp]
+    L.ep_route_workspace_bytes.restype = i64
+    L.ep_route_workspace_bytes.argtypes = [P(EpRouterConfig), i32]
+    L.ep_route_balance.restype = i32
+    L.ep_route_balance.argtypes = [P(EpRouterConfig), i32, vp, i64, vp, vp, i32, vp, vp, vp,
+                                   vp, vp, vp, vp, vp, vp]
+    L.ep_route_backward.restype = i32
+    L.ep_route_backward.argtypes = [P(EpRouterConfig), i32, vp, i64, vp, vp, vp, i32, vp, vp,
+                                    vp, vp, vp, i64, vp]
+    for f in (L.ep_w4_codes_bytes, L.ep_w4_scales_bytes, L.ep_w4_zeros_bytes):
+        f.restype = i64
+        f.argtypes = [P(EpW4Config)]
+    L.ep_w4_pack.restype = i32
+    L.ep_w4_pack.argtypes = [P(EpW4Config), vp, vp, vp, vp, vp, vp, vp]
+    L.ep_expert_w4.restype = i32
+    L.ep_expert_w4.argtypes = [P(EpW4Config), i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp]
     L.ep_check_error.restype = i32
     L.ep_check_error.argtypes = [P(EpLayout), vp]
     L.ep_selftest_fp8_quotient.restype = i32
@@ -272,6 +323,57 @@ def ep_combine_to_host(cfg, layout, d_expert_out, d_topk_weights, d_y, h_y, num_
                        stream) -> int:
     return int(_lib.ep_combine_to_host(ctypes.byref(cfg), ctypes.byref(layout), d_expert_out,
                                        d_topk_weights, d_y, h_y, int(num_chunks), stream))
+
+
+def ep_route(cfg, num_tokens, d_logits, ld_logits, d_bias, d_token_mask, d_topk_idx,
+             d_topk_weights, stream) -> int:
+    return _lib.ep_route(cfg, num_tokens, d_logits, ld_logits, d_bias, d_token_mask,
+                         d_topk_idx, d_topk_weights, stream)
+
+
+def ep_route_workspace_bytes(cfg: EpRouterConfig, num_seqs: int) -> int:
+    return _lib.ep_route_workspace_bytes(cfg, num_seqs)
+
+
+def ep_route_balance(cfg, num_tokens, d_logits, ld_logits, d_bias, d_token_mask, num_seqs,
+                     d_seq_start, d_topk_idx, d_topk_weights, d_expert_count, d_expert_prob,
+                     d_seq_tokens, d_loss, d_workspace, stream) -> int:
+    return _lib.ep_route_balance(cfg, num_tokens, d_logits, ld_logits, d_bias, d_token_mask,
+                                 num_seqs, d_seq_start, d_topk_idx, d_topk_weights,
+                                 d_expert_count, d_expert_prob, d_seq_tokens, d_loss,
+                                 d_workspace, stream)
+
+
+def ep_route_backward(cfg, num_tokens, d_logits, ld_logits, d_token_mask, d_topk_idx, d_grad_w,
+                      num_seqs, d_seq_start, d_expert_count, d_seq_tokens, d_grad_loss,
+                      d_grad_logits, ld_grad, stream) -> int:
+    return _lib.ep_route_backward(cfg, num_tokens, d_logits, ld_logits, d_token_mask,
+                                  d_topk_idx, d_grad_w, num_seqs, d_seq_start, d_expert_count,
+                                  d_seq_tokens, d_grad_loss, d_grad_logits, ld_grad, stream)
+
+
+def ep_w4_codes_bytes(cfg: EpW4Config) -> int:
+    return _lib.ep_w4_codes_bytes(cfg)
+
+
+def ep_w4_scales_bytes(cfg: EpW4Config) -> int:
+    return _lib.ep_w4_scales_bytes(cfg)
+
+
+def ep_w4_zeros_bytes(cfg: EpW4Config) -> int:
+    return _lib.ep_w4_zeros_bytes(cfg)
+
+
+def ep_w4_pack(cfg, d_codes, d_scales, d_zeros, d_packed_codes, d_packed_scales,
+               d_packed_zeros, stream) -> int:
+    return _lib.ep_w4_pack(cfg, d_codes, d_scales, d_zeros, d_packed_codes, d_packed_scales,
+                           d_packed_zeros, stream)
+
+
+def ep_expert_w4(cfg, cap, num_rows, d_x, d_x_scale, d_codes, d_scales, d_zeros,
+                 d_expert_start, d_expert_end, d_out, stream) -> int:
+    return _lib.ep_expert_w4(cfg, cap, num_rows, d_x, d_x_scale, d_codes, d_scales, d_zeros,
+                             d_expert_start, d_expert_end, d_out, stream)
 
 
 def ep_check_error(layout, stream) -> int:
@@ -675,3 +777,232 @@ def combine_ranks(cfg: Config, layout: Layout, rank_y, y=None, stream=None):
     st = ep_combine_ranks(cfg.c(), layout.c, _ptr(rank_y), _ptr(y), _stream(stream))
     _check(st, "ep_combine_ranks")
     return y
+
+
+# ---- router gate -----------------------------------------------------------------
+
+def _need(ok: bool, what: str):
+    if not ok:
+        raise EpError(EP_ERR_INVALID_ARG, what)
+
+
+def _need_flat(what: str, dtype, shape, *tensors):
+    """Optional tensors of one type and shape, contiguous, on the GPU."""
+    for t in tensors:
+        if t is not None:
+            _need(t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.is_cuda,
+                  f"{what}: a tensor is not a contiguous CUDA {dtype} {tuple(shape)}")
+
+
+@dataclasses.dataclass(frozen=True)
+class RouterConfig:
+    """Mirror of ep_router_config (see include/ep.h); the logits' type is
+    taken from the tensors."""
+
+    num_experts: int
+    num_topk: int
+    score: str = "softmax"          # or "sigmoid"
+    num_groups: int = 1
+    topk_groups: int = 1
+    renormalize: bool = True
+    route_scale: float = 1.0
+
+    def __post_init__(self):
+        _need(self.score in ("softmax", "sigmoid"), f"RouterConfig: score {self.score!r}")
+        both = tuple(EpRouterConfig(self.num_experts, self.num_topk,
+                                    int(self.score == "sigmoid"), self.num_groups,
+                                    self.topk_groups, int(self.renormalize), bf16,
+                                    self.route_scale) for bf16 in (0, 1))
+        object.__setattr__(self, "_c", both)
+
+    def c(self, bf16: bool = False) -> EpRouterConfig:
+        return self._c[bf16]
+
+
+def _logits_args(cfg: RouterConfig, what: str, logits):
+    """(ABI config, T, row stride) of a [T, E] tensor with unit column stride."""
+    import torch
+
+    bf16 = logits.dtype is torch.bfloat16
+    _need(bf16 or logits.dtype is torch.float32, f"{what}: logits are {logits.dtype}")
+    T, E = logits.shape
+    row, col = logits.stride()
+    _need(E == cfg.num_experts and (col == 1 or E == 1) and logits.is_cuda,
+          f"{what}: logits are not CUDA [T, {cfg.num_experts}] with unit column stride")
+    return cfg._c[bf16], T, row if T > 1 else E
+
+
+def route(cfg: RouterConfig, logits, bias=None, token_mask=None, topk_idx=None,
+          topk_weights=None, stream=None):
+    """ep_route.  logits: fp32 or bf16 CUDA tensor [T, E], rows may be strided;
+    bias: fp32 [E]; token_mask: uint8 or bool [T].  Returns (topk_idx int64
+    [T, K], topk_weights fp32 [T, K])."""
+    import torch
+
+    c, T, ld = _logits_args(cfg, "route", logits)
+    dev, shape = logits.device, (T, cfg.num_topk)
+    if topk_idx is None:
+        topk_idx = torch.empty(shape, dtype=torch.int64, device=dev)
+    if topk_weights is None:
+        topk_weights = torch.empty(shape, dtype=torch.float32, device=dev)
+    _need_flat("route", torch.int64, shape, topk_idx)
+    _need_flat("route", torch.float32, shape, topk_weights)
+    _need_router_inputs("route", cfg, T, bias, token_mask)
+    st = ep_route(c, T, logits.data_ptr(), ld, _ptr(bias), _ptr(token_mask),
+                  topk_idx.data_ptr(), topk_weights.data_ptr(), _stream(stream))
+    _check(st, "ep_route")
+    return topk_idx, topk_weights
+
+
+def _need_router_inputs(what: str, cfg: RouterConfig, T: int, bias, token_mask):
+    import torch
+
+    _need_flat(what, torch.float32, (cfg.num_experts,), bias)
+    if token_mask is not None:
+        _need_flat(what, torch.bool if token_mask.dtype is torch.bool else torch.uint8, (T,),
+                   token_mask)
+
+
+def route_balance(cfg: RouterConfig, logits, bias=None, token_mask=None, seq_start=None,
+                  out=None, workspace=None, stream=None):
+    """ep_route_balance.  seq_start: int32 [B + 1] CUDA tensor, or None for one
+    sequence.  Returns (topk_idx, topk_weights, expert_count int32 [B, E],
+    expert_prob fp32 [B, E], seq_tokens int32 [B + 2], loss fp32 [2]), which
+    `out` may give; workspace: ep_route_workspace_bytes bytes (allocated when
+    None)."""
+    import torch
+
+    c, T, ld = _logits_args(cfg, "route_balance", logits)
+    B = 1 if seq_start is None else seq_start.shape[0] - 1
+    E, K, dev = cfg.num_experts, cfg.num_topk, logits.device
+    i32, f32 = torch.int32, torch.float32
+    wanted = (((T, K), torch.int64), ((T, K), f32), ((B, E), i32), ((B, E), f32), ((B + 2,), i32),
+              ((2,), f32))
+    if out is None:
+        out = tuple(torch.empty(s, dtype=d, device=dev) for s, d in wanted)
+    for t, (s, d) in zip(out, wanted, strict=True):
+        _need_flat("route_balance", d, s, t)
+    _need_router_inputs("route_balance", cfg, T, bias, token_mask)
+    _need_flat("route_balance", i32, (B + 1,), seq_start)
+    size = ep_route_workspace_bytes(c, B)
+    _need(size >= 0, "route_balance: config")
+    if workspace is None:
+        workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+    _need(workspace.is_cuda and workspace.nbytes >= size, "route_balance: workspace")
+    st = ep_route_balance(c, T, logits.data_ptr(), ld, _ptr(bias), _ptr(token_mask), B,
+                          _ptr(seq_start), *(t.data_ptr() for t in out), workspace.data_ptr(),
+                          _stream(stream))
+    _check(st, "ep_route_balance")
+    return tuple(out)
+
+
+def route_backward(cfg: RouterConfig, logits, topk_idx=None, grad_w=None, token_mask=None,
+                   seq_start=None, expert_count=None, seq_tokens=None, grad_loss=None,
+                   grad_logits=None, stream=None):
+    """ep_route_backward.  grad_w: the gate weights' gradient (combine_backward
+    returns it); expert_count, seq_tokens: route_balance's; grad_loss: fp32 [2]
+    CUDA tensor.  Returns grad_logits [T, E] of the logits' type."""
+    import torch
+
+    c, T, ld = _logits_args(cfg, "route_backward", logits)
+    B = 1 if seq_start is None else seq_start.shape[0] - 1
+    E, K = cfg.num_experts, cfg.num_topk
+    if grad_logits is None:
+        grad_logits = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+    _need(grad_logits.dtype is logits.dtype, "route_backward: grad_logits' type")
+    _, Tg, ld_grad = _logits_args(cfg, "route_backward", grad_logits)
+    _need(Tg == T, "route_backward: grad_logits' rows")
+    _need_router_inputs("route_backward", cfg, T, None, token_mask)
+    _need_flat("route_backward", torch.int64, (T, K), topk_idx)
+    _need_flat("route_backward", torch.float32, (T, K), grad_w)
+    _need_flat("route_backward", torch.int32, (B + 1,), seq_start)
+    _need_flat("route_backward", torch.int32, (B, E), expert_count)
+    _need_flat("route_backward", torch.int32, (B + 2,), seq_tokens)
+    _need_flat("route_backward", torch.float32, (2,), grad_loss)
+    st = ep_route_backward(c, T, logits.data_ptr(), ld, _ptr(token_mask), _ptr(topk_idx),
+                           _ptr(grad_w), B, _ptr(seq_start), _ptr(expert_count),
+                           _ptr(seq_tokens), _ptr(grad_loss), grad_logits.data_ptr(), ld_grad,
+                           _stream(stream))
+    _check(st, "ep_route_backward")
+    return grad_logits
+
+
+# ---- experts' products with 4-bit weights ----------------------------------------
+
+@dataclasses.dataclass(frozen=True)
+class W4Config:
+    """Mirror of ep_w4_config (see include/ep.h)."""
+
+    num_experts: int
+    in_features: int
+    out_features: int
+    group_size: int = 128
+    x_fp8: bool = False
+    gated: bool = False
+    has_zeros: bool = False
+
+    def __post_init__(self):
+        object.__setattr__(self, "_c", EpW4Config(
+            self.num_experts, self.in_features, self.out_features, self.group_size,
+            int(self.x_fp8), int(self.gated), int(self.has_zeros)))
+        sizes = (ep_w4_codes_bytes(self._c), ep_w4_scales_bytes(self._c),
+                 ep_w4_zeros_bytes(self._c))
+        _need(min(sizes) >= 0, "W4Config")
+        object.__setattr__(self, "_sizes", sizes)
+
+    def c(self) -> EpW4Config:
+        return self._c
+
+    @property
+    def out_width(self) -> int:
+        return self.out_features // 2 if self.gated else self.out_features
+
+
+def w4_pack(cfg: W4Config, codes, scales, zeros=None, stream=None):
+    """ep_w4_pack.  codes: uint8 CUDA tensor [E, N, H / 2]; scales: bf16
+    [E, N, H / group]; zeros: uint8, as the scales.  Returns the packed (codes
+    int32 [E, tiles, blocks, 8, 32, 4], scales bf16 [E, tiles, groups, 64],
+    zeros uint8 or None)."""
+    import torch
+
+    E, N, H, g = cfg.num_experts, cfg.out_features, cfg.in_features, cfg.group_size
+    _need_flat("w4_pack", torch.uint8, (E, N, H // 2), codes)
+    _need_flat("w4_pack", torch.bfloat16, (E, N, H // g), scales)
+    _need_flat("w4_pack", torch.uint8, (E, N, H // g), zeros)
+    tiles, blocks, dev = -(-cfg.out_width // (32 if cfg.gated else 64)), -(-H // 128), codes.device
+    pc = torch.empty((E, tiles, blocks, 8, 32, 4), dtype=torch.int32, device=dev)
+    ps = torch.empty((E, tiles, blocks * 128 // g, 64), dtype=torch.bfloat16, device=dev)
+    pz = torch.empty(ps.shape, dtype=torch.uint8, device=dev) if cfg.has_zeros else None
+    st = ep_w4_pack(cfg._c, codes.data_ptr(), scales.data_ptr(), _ptr(zeros), pc.data_ptr(),
+                    ps.data_ptr(), _ptr(pz), _stream(stream))
+    _check(st, "ep_w4_pack")
+    return pc, ps, pz
+
+
+def expert_w4(cfg: W4Config, x, codes, scales, expert_start, expert_end, num_rows, zeros=None,
+              x_scale=None, out=None, stream=None):
+    """ep_expert_w4.  x: bf16 [cap, H], or uint8 (E4M3 bits) with x_scale fp32
+    [cap, H / 128]; codes, scales, zeros: w4_pack's; expert_start, expert_end:
+    a Layout's; num_rows: rows of all experts together at most (T * K).
+    Returns out, bf16 [cap, N] ([cap, N / 2] when gated)."""
+    import torch
+
+    cap, H, E = x.shape[0], cfg.in_features, cfg.num_experts
+    _need_flat("expert_w4", torch.uint8 if cfg.x_fp8 else torch.bfloat16, (cap, H), x)
+    if cfg.x_fp8:
+        _need_flat("expert_w4", torch.float32, (cap, H // 128), x_scale)
+    if out is None:
+        out = torch.empty((cap, cfg.out_width), dtype=torch.bfloat16, device=x.device)
+    _need_flat("expert_w4", torch.bfloat16, (cap, cfg.out_width), out)
+    sizes = cfg._sizes
+    _need(codes.nbytes == sizes[0] and scales.nbytes == sizes[1] and codes.is_contiguous()
+          and scales.is_contiguous() and scales.dtype is torch.bfloat16
+          and (zeros is None or zeros.nbytes == sizes[2] and zeros.is_contiguous()),
+          "expert_w4: packed weights")
+    _need(expert_start.dtype is torch.int32 and expert_end.dtype is torch.int32
+          and expert_start.shape[0] >= E and expert_end.shape[0] >= E, "expert_w4: segments")
+    st = ep_expert_w4(cfg._c, cap, num_rows, x.data_ptr(), _ptr(x_scale), codes.data_ptr(),
+                      scales.data_ptr(), _ptr(zeros), expert_start.data_ptr(),
+                      expert_end.data_ptr(), out.data_ptr(), _stream(stream))
+    _check(st, "ep_expert_w4")
+    return out

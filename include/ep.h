@@ -508,6 +508,163 @@ EP_API int32_t ep_selftest_layout_timeout(const ep_config *cfg, int32_t num_toke
                                           int32_t stall_tile, int64_t timeout_ns,
                                           void *stream);
 
+/* ---- Router gate ----------------------------------------------------------
+ * What produces topk_idx and topk_weights: scores, choice, gate weights, the
+ * balance and z losses over them, and the gradient by the logits.
+ *
+ * Score s_te of token t for expert e: softmax over e of the logits l_te, or
+ * sigmoid(l_te).  Choice score: l_te itself (softmax; the same order), or
+ * s_te + bias_e (sigmoid; the bias orders, it never enters a weight).  A
+ * logit of -inf takes its expert out of service for that token (score 0,
+ * never chosen); a NaN logit is never chosen either and its row's softmax
+ * scores are NaN.  With num_groups > 1, groups of E / num_groups consecutive
+ * experts are ranked by their highest choice score (softmax) or the sum of
+ * their two highest (sigmoid), and only experts of the topk_groups best
+ * groups can be chosen.  The K highest choice scores are chosen in
+ * descending order; equal scores, of experts or of groups, go to the lower
+ * index.  w_tk = route_scale * s of choice k, divided by the sum of the
+ * chosen s when renormalize is set (0 where that sum is 0).  Where fewer than
+ * K experts can be chosen, and for masked tokens, idx = -1 and w = 0 (an
+ * unused selection of ep_get_layout). */
+enum { EP_SCORE_SOFTMAX = 0, EP_SCORE_SIGMOID = 1 };
+
+typedef struct {
+  int32_t num_experts;   /* E in [1, 2048]                                  */
+  int32_t num_topk;      /* K in [1, 32], K <= topk_groups * E / num_groups */
+  int32_t score;         /* EP_SCORE_SOFTMAX or EP_SCORE_SIGMOID            */
+  int32_t num_groups;    /* in [1, 32], divides E; 1: no groups             */
+  int32_t topk_groups;   /* in [1, num_groups]                              */
+  int32_t renormalize;   /* 1: the chosen scores are divided by their sum   */
+  int32_t logits_bf16;   /* logits and their gradient: 0 fp32, 1 bf16       */
+  float route_scale;     /* factor of every gate weight                     */
+} ep_router_config;
+
+/* Choice and gate weights of num_tokens tokens.
+ * d_logits: device [T, ld_logits] fp32 or bf16, ld_logits >= E (entries past
+ *   E are not read).
+ * d_bias: device fp32 [E] or NULL; sigmoid scores only.
+ * d_token_mask: device uint8 [T] or NULL; 0 marks a padding token.
+ * d_topk_idx: device int64 [T, K]; d_topk_weights: device fp32 [T, K].
+ * Returns EP_OK or an error. */
+EP_API int32_t ep_route(const ep_router_config *cfg, int32_t num_tokens,
+                        const void *d_logits, int64_t ld_logits, const float *d_bias,
+                        const uint8_t *d_token_mask, int64_t *d_topk_idx,
+                        float *d_topk_weights, void *stream);
+
+/* Bytes of device scratch memory ep_route_balance needs on the current
+ * device, for any number of tokens.  -1 if the arguments are invalid. */
+EP_API int64_t ep_route_workspace_bytes(const ep_router_config *cfg, int32_t num_seqs);
+
+/* ep_route together with the balance statistics and losses of its tokens.
+ *
+ * The tokens form num_seqs sequences: d_seq_start (device int32 [B + 1],
+ * NULL when B = 1) ascends from 0 to T, sequence b owns tokens
+ * [seq_start[b], seq_start[b+1]) and may be empty.  Masked tokens count
+ * nowhere.  With n_b the tokens of sequence b, c_be their selections of
+ * expert e, and p_te = s_te / (sum of s_t over the experts):
+ *   d_expert_count: int32 [B, E]  c_be
+ *   d_expert_prob:  fp32 [B, E]   P_be = mean of p_te over the n_b tokens
+ *   d_seq_tokens:   int32 [B+2]   n_b; then sum n_b; then how many n_b > 0
+ *   d_loss[0] = mean over sequences with n_b > 0 of
+ *               sum_e (c_be E / (K n_b)) P_be       (1 when balanced)
+ *   d_loss[1] = mean over tokens of logsumexp(l_t)^2 (softmax; else 0)
+ * A row with no expert in service adds nothing to P or the z loss.  Both
+ * losses are 0 without tokens.  Sums are fp32 in a fixed order: the same
+ * inputs give the same bits.  d_workspace: ep_route_workspace_bytes bytes,
+ * used until the call's work is done.  num_tokens may be 0.
+ * Returns EP_OK or an error. */
+EP_API int32_t ep_route_balance(const ep_router_config *cfg, int32_t num_tokens,
+                                const void *d_logits, int64_t ld_logits,
+                                const float *d_bias, const uint8_t *d_token_mask,
+                                int32_t num_seqs, const int32_t *d_seq_start,
+                                int64_t *d_topk_idx, float *d_topk_weights,
+                                int32_t *d_expert_count, float *d_expert_prob,
+                                int32_t *d_seq_tokens, float *d_loss, void *d_workspace,
+                                void *stream);
+
+/* Gradient by the logits of  sum_tk grad_w_tk w_tk + grad_loss . loss, the
+ * choice and the counts c_be held constant.
+ * d_grad_w: device fp32 [T, K] or NULL (no gate term; ep_combine_backward
+ *   writes it); d_topk_idx: the forward's choice, needed with d_grad_w.
+ * d_expert_count, d_seq_tokens (ep_route_balance's) and d_grad_loss (device
+ *   fp32 [2]): all three, or all NULL (no loss terms).  grad_loss[1] is not
+ *   used with sigmoid scores.
+ * d_grad_logits: device [T, ld_grad], the type of the logits; columns past E
+ *   are not written.  Masked tokens and experts out of service get 0.
+ * Everything else is recomputed from the logits.  Returns EP_OK or an
+ * error. */
+EP_API int32_t ep_route_backward(const ep_router_config *cfg, int32_t num_tokens,
+                                 const void *d_logits, int64_t ld_logits,
+                                 const uint8_t *d_token_mask, const int64_t *d_topk_idx,
+                                 const float *d_grad_w, int32_t num_seqs,
+                                 const int32_t *d_seq_start,
+                                 const int32_t *d_expert_count,
+                                 const int32_t *d_seq_tokens, const float *d_grad_loss,
+                                 void *d_grad_logits, int64_t ld_grad, void *stream);
+
+/* ---- Experts' products with 4-bit weights ----------------------------------
+ * y_r = W_e x_r for the rows r of every expert e, between ep_dispatch and
+ * ep_combine, with W_e [N, H] held as 4-bit codes: W = (code - zero) * scale,
+ * one bf16 scale (and optionally one zero point; 8 otherwise) per row and
+ * group of group_size inputs.  With `gated`, W_e stacks a gate and an up
+ * matrix ([N/2, H] each) and y = silu(gate x) * (up x), N/2 wide.
+ *
+ * Made for few rows an expert (decode: one to some dozens), where reading
+ * the weights once is the cost; any number of rows is computed correctly.
+ *
+ * Packed weights: tiles of 64 packed rows by blocks of 128 inputs.  Packed
+ * row n of a tile is row 64 * tile + n of W; when gated, a tile covers 32
+ * outputs and packed row 8 g + p is gate row 32 * tile + 4 g + p for p < 4,
+ * up row 32 * tile + 4 g + p - 4 for p >= 4.
+ *   codes:  uint32 [E, tiles, blocks, 8, 32, 4]; word (p, l, i) holds inputs
+ *           32 i + 8 (l % 4) + 2 j and + 2 j + 1 of the block, for packed row
+ *           8 (l / 4) + p, in its 4-bit fields j and j + 4 (j = 0..3)
+ *   scales: bf16 [E, tiles, blocks * 128 / group_size, 64] (group, packed row)
+ *   zeros:  uint8, as the scales
+ * Rows past N and inputs past H are padding: code 8, scale 0, zero 8. */
+typedef struct {
+  int32_t num_experts;   /* E in [1, 2048]                                   */
+  int32_t in_features;   /* H: a multiple of group_size, <= 2^20; of 128 when
+                            x_fp8                                            */
+  int32_t out_features;  /* N in [1, 2^20]; even when gated                  */
+  int32_t group_size;    /* 32, 64 or 128 inputs a scale                     */
+  int32_t x_fp8;         /* 0: bf16 rows; 1: E4M3 rows with 1x128 fp32 scales */
+  int32_t gated;         /* 1: silu(gate) * up                               */
+  int32_t has_zeros;     /* 1: zero points, in [0, 15]                       */
+} ep_w4_config;
+
+/* Bytes of the packed codes, scales and zeros (0 without zero points);
+ * -1 if the config is invalid. */
+EP_API int64_t ep_w4_codes_bytes(const ep_w4_config *cfg);
+EP_API int64_t ep_w4_scales_bytes(const ep_w4_config *cfg);
+EP_API int64_t ep_w4_zeros_bytes(const ep_w4_config *cfg);
+
+/* Packs weights once, before serving.  d_codes: device uint8 [E, N, H / 2],
+ * input 2 i in the low four bits of byte i; d_scales: device bf16
+ * [E, N, H / group_size]; d_zeros: device uint8, as the scales (has_zeros).
+ * Returns EP_OK or an error. */
+EP_API int32_t ep_w4_pack(const ep_w4_config *cfg, const uint8_t *d_codes,
+                          const void *d_scales, const uint8_t *d_zeros,
+                          void *d_packed_codes, void *d_packed_scales,
+                          uint8_t *d_packed_zeros, void *stream);
+
+/* The product.  cap: rows that d_x and d_out hold.  num_rows: how many rows
+ * the experts have together, at most (T * K of the layout's call; it sizes
+ * the launch, and more rows are still computed).
+ * d_x: device [cap, H] bf16, or E4M3 bytes with d_x_scale (device fp32
+ *   [cap, H / 128]), as ep_dispatch writes them.
+ * d_expert_start, d_expert_end: device int32 [E] at least, a layout's: expert
+ *   e owns rows [start[e], end[e]), clipped to [0, cap); none when empty.
+ * d_out: device bf16 [cap, N] ([cap, N/2] when gated); rows of no expert
+ *   are not written.
+ * Products and sums are fp32 (codes and inputs enter them exactly), rounded
+ * once at the end.  Returns EP_OK or an error. */
+EP_API int32_t ep_expert_w4(const ep_w4_config *cfg, int32_t cap, int32_t num_rows,
+                            const void *d_x, const float *d_x_scale, const void *d_codes,
+                            const void *d_scales, const uint8_t *d_zeros,
+                            const int32_t *d_expert_start, const int32_t *d_expert_end,
+                            void *d_out, void *stream);
+
 /* The cudaError_t of the last CUDA runtime call of this library that failed
  * in the calling thread (0 if none since the previous query); reading it
  * clears it.  Explains an EP_ERR_CUDA status. */
