@@ -20,11 +20,8 @@
 namespace ep {
 namespace {
 
-constexpr int kW4Threads = 256;
-constexpr int kW4Warps = kW4Threads / 32;
 constexpr int kTileRows = 64;      // packed weight rows a tile
 constexpr int kBlockIn = 128;      // inputs a block
-constexpr int kChunk = 8;          // rows of x a warp multiplies at once
 constexpr int kWordsPerBlock = kTileRows * kBlockIn / 8;
 
 struct W4Params {
@@ -90,12 +87,72 @@ __device__ __forceinline__ uint32_t e4m3_pair(uint32_t two) {
 
 // ---- the product ----------------------------------------------------------------
 
-// Chunks of kChunk rows before each expert, in shared memory: pre[e] of e's
+// A warp's stage in shared memory: one block (128 inputs) of its tile and
+// chunk.  x rows are swizzled in units of the fragments' reads, so that the
+// eight lanes (FP8: sixteen) of one shared-memory pass meet different banks.
+template <bool FP8, int GROUP, bool ZEROS, int NT>
+struct Stage {
+  static constexpr int kGroups = kBlockIn / GROUP;
+  static constexpr int kRowBytes = FP8 ? 128 : 256;
+  static constexpr int kX = kTileRows * kBlockIn / 2;              // after the codes
+  static constexpr int kScales = kX + 8 * NT * kRowBytes;
+  static constexpr int kZeros = kScales + kGroups * kTileRows * 2;
+  static constexpr int kXScale = kZeros + (ZEROS ? kGroups * kTileRows : 0);
+  static constexpr int kBytes = kXScale + (FP8 ? 8 * NT * 4 : 0);
+  static_assert(kBytes % 16 == 0);
+
+  // Byte offset of 16-byte piece c of row t of x.
+  static __device__ __forceinline__ int x_piece(int t, int c) {
+    if constexpr (FP8) return kX + t * 128 + ((((c >> 1) ^ (t & 3)) << 1) | (c & 1)) * 16;
+    return kX + t * 256 + (c ^ ((t & 1) << 2)) * 16;
+  }
+};
+
+// 16 bytes global -> shared, or zeros when !have.
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool have) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(have ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async4_or_zero(uint32_t dst, const void* src, bool have) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
+               "r"(have ? 4 : 0)
+               : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint4 lds16(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(at));
+  return v;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t at) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds4(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at));
+  return v;
+}
+
+__device__ __forceinline__ uint32_t word_of(const uint4& v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+
+// Chunks of kRows rows before each expert, in shared memory: pre[e] of e's
 // predecessors, pre[E] of all.
+template <int kRows>
 __device__ void count_chunks(const W4Params& p, int* pre) {
-  for (int e = threadIdx.x; e < p.E; e += kW4Threads) {
+  for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
     const int lo = max(0, p.start[e]), hi = min(p.cap, p.end[e]);
-    pre[e] = hi > lo ? (hi - lo + kChunk - 1) / kChunk : 0;
+    pre[e] = hi > lo ? (hi - lo + kRows - 1) / kRows : 0;
   }
   __syncthreads();
   if (threadIdx.x < 32) {
@@ -130,123 +187,264 @@ __device__ __forceinline__ int expert_of(const int* pre, int E, int c) {
   return lo;
 }
 
-// One warp: a tile of 64 packed weight rows by a chunk of up to 8 rows of x.
-// Lane (g = lane / 4, q = lane % 4) holds packed rows 8 g .. 8 g + 7 (piece
-// 2 r + h is row g + 8 h of the r-th 16-row operand) and columns 2 q, 2 q + 1.
-template <bool FP8, int GROUP, bool ZEROS>
-__global__ void __launch_bounds__(kW4Threads) expert_w4_kernel(W4Params p) {
-  extern __shared__ int pre[];
-  pdl_wait();
-  count_chunks(p, pre);
-  const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-  constexpr int kGroups = kBlockIn / GROUP;       // scale groups a block
-  constexpr int kWords = GROUP / 32;              // words of a lane a group
-  const int64_t items = int64_t(pre[p.E]) * p.tiles;
-  const int64_t step = int64_t(gridDim.x) * kW4Warps;
-  for (int64_t it = int64_t(blockIdx.x) * kW4Warps + (threadIdx.x >> 5); it < items; it += step) {
-    const int chunk = int(it / p.tiles), tile = int(it % p.tiles);
+// A tile of 64 packed weight rows by a chunk of up to 8 NT rows of x.
+struct Item {
+  int tile, row0, rows;
+  int64_t unit0;       // first (tile, block) unit of the codes
+  template <int kRows>
+  __device__ __forceinline__ void find(const W4Params& p, const int* pre, int64_t it) {
+    const int chunk = int(it / p.tiles);
+    tile = int(it % p.tiles);
     const int e = expert_of(pre, p.E, chunk);
-    const int row0 = max(0, p.start[e]) + (chunk - pre[e]) * kChunk;
-    const int rows = min(kChunk, min(p.cap, p.end[e]) - row0);
-    const int64_t unit0 = (int64_t(e) * p.tiles + tile) * p.blocks;
-    const uint4* codes = reinterpret_cast<const uint4*>(p.codes) + unit0 * (kWordsPerBlock / 4) + lane;
-    const __nv_bfloat16* scales = p.scales + unit0 * kGroups * kTileRows + 8 * g;
-    const uint8_t* zeros = ZEROS ? p.zeros + unit0 * kGroups * kTileRows + 8 * g : nullptr;
-    float acc[4][4] = {};
-    for (int kb = 0; kb < p.blocks; ++kb) {
-      uint4 w[8];
+    row0 = max(0, p.start[e]) + (chunk - pre[e]) * kRows;
+    rows = min(kRows, min(p.cap, p.end[e]) - row0);
+    unit0 = (int64_t(e) * p.tiles + tile) * p.blocks;
+  }
+};
+
+// Copies one unit (block kb of an item) into a stage; every lane of the warp
+// takes its share.
+template <bool FP8, int GROUP, bool ZEROS, int NT>
+__device__ __forceinline__ void load_unit(const W4Params& p, const Item& it, int kb, uint32_t stage,
+                                          int lane) {
+  using St = Stage<FP8, GROUP, ZEROS, NT>;
+  const int64_t unit = it.unit0 + kb;
+  const uint4* codes = reinterpret_cast<const uint4*>(p.codes) + unit * (kWordsPerBlock / 4) + lane;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = ld_stream_u4(codes + kb * (kWordsPerBlock / 4) + i * 32);
-      // columns: row g of the chunk, inputs 32 i + 8 q .. + 7
-      uint32_t b[16] = {};
-      float sx[2] = {1.0f, 1.0f};
-      if constexpr (FP8) {
-        if (g < rows) {
-          const uint8_t* x = static_cast<const uint8_t*>(p.x) + int64_t(row0 + g) * p.H + kb * kBlockIn + 8 * q;
+  for (int i = 0; i < 8; ++i) cp_async16_or_zero(stage + i * 512 + lane * 16, codes + i * 32, true);
+  const char* x = static_cast<const char*>(p.x);
+  if constexpr (FP8) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint2 v = *reinterpret_cast<const uint2*>(x + 32 * i);
-            b[4 * i] = e4m3_pair(v.x);
-            b[4 * i + 1] = e4m3_pair(v.x >> 16);
-            b[4 * i + 2] = e4m3_pair(v.y);
-            b[4 * i + 3] = e4m3_pair(v.y >> 16);
-          }
-        }
+    for (int i = 0; i < 2 * NT; ++i) {
+      const int t = i * 4 + (lane >> 3), c = lane & 7;
+      const bool have = t < it.rows;
+      cp_async16_or_zero(stage + St::x_piece(t, c),
+                         x + int64_t(it.row0 + (have ? t : 0)) * p.H + kb * 128 + c * 16, have);
+    }
+    if (lane < 8 * NT) {
+      const bool have = lane < it.rows;
+      cp_async4_or_zero(stage + St::kXScale + lane * 4,
+                        p.x_scale + int64_t(it.row0 + (have ? lane : 0)) * p.blocks + kb, have);
+    }
+  } else {
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-          sx[c] = 2 * q + c < rows ? p.x_scale[int64_t(row0 + 2 * q + c) * p.blocks + kb] : 0.0f;
-      } else {
-        if (g < rows) {
-          const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.x) + int64_t(row0 + g) * p.H;
+    for (int i = 0; i < 4 * NT; ++i) {
+      const int t = i * 2 + (lane >> 4), c = lane & 15;
+      const int k = kb * 128 + c * 8;
+      const bool have = t < it.rows && k < p.H;
+      cp_async16_or_zero(stage + St::x_piece(t, c),
+                         x + (int64_t(it.row0 + (have ? t : 0)) * p.H + (have ? k : 0)) * 2, have);
+    }
+  }
+  const char* scales = reinterpret_cast<const char*>(p.scales) + unit * (St::kGroups * kTileRows * 2);
+  if (lane < St::kGroups * 8)
+    cp_async16_or_zero(stage + St::kScales + lane * 16, scales + lane * 16, true);
+  if constexpr (ZEROS) {
+    const uint8_t* zeros = p.zeros + unit * (St::kGroups * kTileRows);
+    if (lane < St::kGroups * 4)
+      cp_async16_or_zero(stage + St::kZeros + lane * 16, zeros + lane * 16, true);
+  }
+}
+
+// acc += the unit in a stage.  Lane (g = lane / 4, q = lane % 4) holds packed
+// rows 8 g .. 8 g + 7 (piece 2 r + h is row g + 8 h of the r-th 16-row
+// operand) and columns 8 t + 2 q, + 1: acc[t][r][2 h + c].
+template <bool FP8, int GROUP, bool ZEROS, int NT>
+__device__ __forceinline__ void multiply_unit(uint32_t stage, int lane, int tiles_used,
+                                              float (&acc)[NT][4][4]) {
+  using St = Stage<FP8, GROUP, ZEROS, NT>;
+  constexpr int kWords = GROUP / 32;              // words of a lane a group
+  const int g = lane >> 2, q = lane & 3;
+  uint4 w[8];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int k = kb * kBlockIn + 32 * i + 8 * q;
-            if (k < p.H) {
-              const uint4 v = *reinterpret_cast<const uint4*>(x + k);
-              b[4 * i] = v.x;
-              b[4 * i + 1] = v.y;
-              b[4 * i + 2] = v.z;
-              b[4 * i + 3] = v.w;
-            }
-          }
+  for (int i = 0; i < 8; ++i) w[i] = lds16(stage + i * 512 + lane * 16);
+  float sx[NT][2];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    sx[t][0] = sx[t][1] = 1.0f;
+    if constexpr (FP8) {
+      const uint2 v = lds8(stage + St::kXScale + (8 * t + 2 * q) * 4);
+      sx[t][0] = __uint_as_float(v.x);
+      sx[t][1] = __uint_as_float(v.y);
+    }
+  }
+#pragma unroll
+  for (int s = 0; s < St::kGroups; ++s) {
+    const uint4 sv = lds16(stage + St::kScales + s * 128 + g * 16);
+    uint2 zv = make_uint2(0x08080808u, 0x08080808u);
+    if constexpr (ZEROS) zv = lds8(stage + St::kZeros + s * 64 + g * 8);
+    float d[NT][4][4];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[t][r][i] = 0.0f;
+#pragma unroll
+    for (int i = s * kWords; i < (s + 1) * kWords; ++i) {
+      uint32_t b[NT][4];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        if (NT > 1 && t >= tiles_used) continue;
+        if constexpr (FP8) {
+          const uint2 v = lds8(stage + St::x_piece(8 * t + g, 2 * i + (q >> 1)) + (q & 1) * 8);
+          b[t][0] = e4m3_pair(v.x);
+          b[t][1] = e4m3_pair(v.x >> 16);
+          b[t][2] = e4m3_pair(v.y);
+          b[t][3] = e4m3_pair(v.y >> 16);
+        } else {
+          const uint4 v = lds16(stage + St::x_piece(8 * t + g, 4 * i + q));
+          b[t][0] = v.x;
+          b[t][1] = v.y;
+          b[t][2] = v.z;
+          b[t][3] = v.w;
         }
       }
 #pragma unroll
-      for (int s = 0; s < kGroups; ++s) {
-        const int64_t at = (int64_t(kb) * kGroups + s) * kTileRows;
-        const uint4 sv = *reinterpret_cast<const uint4*>(scales + at);
-        const uint32_t sw[4] = {sv.x, sv.y, sv.z, sv.w};
-        uint2 zv = make_uint2(0x08080808u, 0x08080808u);
-        if constexpr (ZEROS) zv = *reinterpret_cast<const uint2*>(zeros + at);
+      for (int r = 0; r < 4; ++r) {
+        const uint32_t z = (r < 2 ? zv.x : zv.y) >> (16 * (r & 1));
+        const uint32_t o0 = offset_pair<FP8>(z & 0xFFu), o1 = offset_pair<FP8>((z >> 8) & 0xFFu);
+        const uint32_t lo = word_of(w[2 * r], i), hi = word_of(w[2 * r + 1], i);
+        uint32_t a[8];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const uint32_t z = (r < 2 ? zv.x : zv.y) >> (16 * (r & 1));
-          const uint32_t o0 = offset_pair<FP8>(z & 0xFFu), o1 = offset_pair<FP8>((z >> 8) & 0xFFu);
-          float d[4] = {};
+        for (int j = 0; j < 4; ++j) {
+          a[2 * j] = decode<FP8>(lo, j, o0);
+          a[2 * j + 1] = decode<FP8>(hi, j, o1);
+        }
 #pragma unroll
-          for (int i = s * kWords; i < (s + 1) * kWords; ++i) {
-            const uint4 lo4 = w[2 * r], hi4 = w[2 * r + 1];
-            const uint32_t lo = i == 0 ? lo4.x : i == 1 ? lo4.y : i == 2 ? lo4.z : lo4.w;
-            const uint32_t hi = i == 0 ? hi4.x : i == 1 ? hi4.y : i == 2 ? hi4.z : hi4.w;
-            mma<FP8>(d, decode<FP8>(lo, 0, o0), decode<FP8>(hi, 0, o1), decode<FP8>(lo, 1, o0),
-                     decode<FP8>(hi, 1, o1), b[4 * i], b[4 * i + 1]);
-            mma<FP8>(d, decode<FP8>(lo, 2, o0), decode<FP8>(hi, 2, o1), decode<FP8>(lo, 3, o0),
-                     decode<FP8>(hi, 3, o1), b[4 * i + 2], b[4 * i + 3]);
-          }
-          const float s0 = bf16_lo(sw[r]), s1 = bf16_hi(sw[r]);
-          acc[r][0] = fmaf(d[0], s0 * sx[0], acc[r][0]);
-          acc[r][1] = fmaf(d[1], s0 * sx[1], acc[r][1]);
-          acc[r][2] = fmaf(d[2], s1 * sx[0], acc[r][2]);
-          acc[r][3] = fmaf(d[3], s1 * sx[1], acc[r][3]);
+        for (int t = 0; t < NT; ++t) {
+          if (NT > 1 && t >= tiles_used) continue;
+          mma<FP8>(d[t][r], a[0], a[1], a[2], a[3], b[t][0], b[t][1]);
+          mma<FP8>(d[t][r], a[4], a[5], a[6], a[7], b[t][2], b[t][3]);
         }
       }
     }
-    // lane: packed rows 8 g + 2 r + h of columns 2 q + c in acc[r][2 h + c]
+    const uint32_t sw[4] = {sv.x, sv.y, sv.z, sv.w};
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      if (2 * q + c >= rows) continue;
-      float y[8];
+    for (int r = 0; r < 4; ++r) {
+      const float s0 = bf16_lo(sw[r]), s1 = bf16_hi(sw[r]);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        y[2 * r] = acc[r][c];
-        y[2 * r + 1] = acc[r][2 + c];
-      }
-      __nv_bfloat16* o = p.out + int64_t(row0 + 2 * q + c) * p.N;
-      if (p.gated) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int n = tile * 32 + 4 * g + i;
-          if (n < p.N) o[n] = __float2bfloat16_rn(y[i] / (1.0f + expf(-y[i])) * y[i + 4]);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int n = tile * 64 + 8 * g + i;
-          if (n < p.N) o[n] = __float2bfloat16_rn(y[i]);
-        }
+      for (int t = 0; t < NT; ++t) {
+        if (NT > 1 && t >= tiles_used) continue;
+        acc[t][r][0] = fmaf(d[t][r][0], FP8 ? s0 * sx[t][0] : s0, acc[t][r][0]);
+        acc[t][r][1] = fmaf(d[t][r][1], FP8 ? s0 * sx[t][1] : s0, acc[t][r][1]);
+        acc[t][r][2] = fmaf(d[t][r][2], FP8 ? s1 * sx[t][0] : s1, acc[t][r][2]);
+        acc[t][r][3] = fmaf(d[t][r][3], FP8 ? s1 * sx[t][1] : s1, acc[t][r][3]);
       }
     }
   }
+}
+
+// Writes packed rows p and p + 4 (0 <= p < 4) of the lane's eight, column
+// `col` of the item.
+__device__ __forceinline__ void store_pair(const W4Params& p, const Item& it, int g, int i, int col,
+                                           float lo, float hi) {
+  if (col >= it.rows) return;
+  __nv_bfloat16* o = p.out + int64_t(it.row0 + col) * p.N;
+  if (p.gated) {
+    const int n = it.tile * 32 + 4 * g + i;
+    if (n < p.N) o[n] = __float2bfloat16_rn(lo / (1.0f + expf(-lo)) * hi);
+  } else {
+    const int n = it.tile * 64 + 8 * g + i;
+    if (n < p.N) o[n] = __float2bfloat16_rn(lo);
+    if (n + 4 < p.N) o[n + 4] = __float2bfloat16_rn(hi);
+  }
+}
+
+// WARPS warps a CTA in groups of `split`: a group shares an item, warp j of
+// it taking the blocks j, j + split, ...; the warps of a group add up their
+// sums in shared memory.  Each warp keeps STAGES units on their way in
+// shared memory of its own (cp.async, so no barrier and no flag).
+template <bool FP8, int GROUP, bool ZEROS, int NT, int WARPS, int STAGES>
+__global__ void __launch_bounds__(WARPS * 32) expert_w4_kernel(W4Params p, int split) {
+  using St = Stage<FP8, GROUP, ZEROS, NT>;
+  extern __shared__ __align__(16) char smem[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  char* const ring = smem + warp * (STAGES * St::kBytes);
+  float* const sums = reinterpret_cast<float*>(smem + WARPS * STAGES * St::kBytes);
+  int* const pre = reinterpret_cast<int*>(sums + (split > 1 ? WARPS * NT * 512 : 0));
+  pdl_wait();
+  count_chunks<8 * NT>(p, pre);
+  const int groups = WARPS / split, group = warp / split, slice = warp % split;
+  const int64_t items = int64_t(pre[p.E]) * p.tiles;
+  const int64_t step = int64_t(gridDim.x) * groups;
+  const uint32_t base = smem_addr(ring);
+
+  // the unit to load next
+  int64_t ahead = int64_t(blockIdx.x) * groups + group;
+  int ahead_kb = slice;
+  Item from;
+  if (ahead < items) from.find<8 * NT>(p, pre, ahead);
+  int slot = 0;
+  const auto load_next = [&](int to) {
+    if (ahead < items && ahead_kb < p.blocks) {
+      load_unit<FP8, GROUP, ZEROS, NT>(p, from, ahead_kb, base + to * St::kBytes, lane);
+      ahead_kb += split;
+      if (ahead_kb >= p.blocks) {
+        ahead_kb = slice;
+        ahead += step;
+        if (ahead < items) from.find<8 * NT>(p, pre, ahead);
+      }
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < STAGES - 1; ++i) load_next(i);
+
+  for (int64_t now = int64_t(blockIdx.x) * groups + group; now < items; now += step) {
+    Item it;
+    it.find<8 * NT>(p, pre, now);
+    const int used = (it.rows + 7) >> 3;
+    float acc[NT][4][4];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[t][r][i] = 0.0f;
+    for (int kb = slice; kb < p.blocks; kb += split) {
+      cp_async_wait<STAGES - 2>();
+      __syncwarp();      // the unit is there, and the slot before it is free
+      load_next(slot == 0 ? STAGES - 1 : slot - 1);
+      multiply_unit<FP8, GROUP, ZEROS, NT>(base + slot * St::kBytes, lane, used, acc);
+      slot = slot + 1 == STAGES ? 0 : slot + 1;
+    }
+    const int g = lane >> 2, q = lane & 3;
+    if (split == 1) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            store_pair(p, it, g, i, 8 * t + 2 * q + c, acc[t][i >> 1][2 * (i & 1) + c],
+                       acc[t][2 + (i >> 1)][2 * (i & 1) + c]);
+      continue;
+    }
+    // pair (t, i, c) of a warp at [2 (8 t + 2 i + c) + half][lane]
+    float* const mine = sums + warp * NT * 512 + lane;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          mine[(2 * (8 * t + 2 * i + c)) * 32] = acc[t][i >> 1][2 * (i & 1) + c];
+          mine[(2 * (8 * t + 2 * i + c) + 1) * 32] = acc[t][2 + (i >> 1)][2 * (i & 1) + c];
+        }
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(32 * split) : "memory");
+    for (int pair = slice; pair < 8 * used; pair += split) {
+      const float* at = sums + group * split * NT * 512 + 2 * pair * 32 + lane;
+      float lo = 0.0f, hi = 0.0f;
+      for (int v = 0; v < split; ++v) {
+        lo += at[v * NT * 512];
+        hi += at[v * NT * 512 + 32];
+      }
+      store_pair(p, it, g, (pair & 7) >> 1, 8 * (pair >> 3) + 2 * q + (pair & 1), lo, hi);
+    }
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(32 * split) : "memory");
+  }
+  cp_async_wait<0>();
 }
 
 // ---- packing ----------------------------------------------------------------------
@@ -337,26 +535,55 @@ int64_t w4_scales(const ep_w4_config* c) {
 
 int32_t status(cudaError_t e) { return note_cuda(e) == cudaSuccess ? EP_OK : EP_ERR_CUDA; }
 
+#ifndef W4_WARPS
+#define W4_WARPS 8
+#endif
+#ifndef W4_SPLIT
+#define W4_SPLIT 0
+#endif
+// Shared memory a CTA may use, less the table of chunks of 2048 experts.
+constexpr int kSmemBudget = 227 * 1024 - 8 * 1024 - 256;
+
 template <bool FP8, int GROUP, bool ZEROS>
-cudaError_t launch_w4(const W4Params& p, int64_t items, cudaStream_t stream) {
-  const int64_t want = (items + kW4Warps - 1) / kW4Warps;
-  const int64_t most = int64_t(device_info().sm_count) * 2;
-  const int grid = int(want < most ? want : most);
-  return launch_pdl(expert_w4_kernel<FP8, GROUP, ZEROS>, dim3(grid), dim3(kW4Threads),
-                    sizeof(int) * (p.E + 1), stream, p);
+cudaError_t launch_w4(const W4Params& p, int num_rows, cudaStream_t stream) {
+  constexpr int NT = 1;
+  constexpr int WARPS = W4_WARPS;
+  constexpr int kSums = WARPS * NT * 512 * 4;
+  constexpr int STAGES = (kSmemBudget - kSums) / (WARPS * Stage<FP8, GROUP, ZEROS, NT>::kBytes);
+  static_assert(STAGES >= 2);
+  // an upper bound of the items: an expert's last chunk may be short
+  const int64_t chunks = int64_t(num_rows) / (8 * NT) + (num_rows < p.E ? num_rows : p.E);
+  const int64_t items = chunks * p.tiles;
+  const int sms = device_info().sm_count;
+  int split = W4_SPLIT;
+  if (split == 0) {
+    split = 1;
+    while (WARPS % (split * 2) == 0 && split * 2 <= p.blocks &&
+           items * split < int64_t(sms) * WARPS * 2)
+      split *= 2;
+  }
+  const int64_t want = (items + WARPS / split - 1) / (WARPS / split);
+  const int grid = int(want < sms ? want : sms);
+  const size_t smem = WARPS * STAGES * Stage<FP8, GROUP, ZEROS, NT>::kBytes +
+                      (split > 1 ? kSums : 0) + sizeof(int) * (p.E + 1);
+  auto* kernel = expert_w4_kernel<FP8, GROUP, ZEROS, NT, WARPS, STAGES>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kernel, dim3(grid), dim3(WARPS * 32), smem, stream, p, split);
 }
 
 template <bool FP8, int GROUP>
-cudaError_t launch_w4(const W4Params& p, int64_t items, cudaStream_t s) {
-  return p.zeros != nullptr ? launch_w4<FP8, GROUP, true>(p, items, s)
-                            : launch_w4<FP8, GROUP, false>(p, items, s);
+cudaError_t launch_w4(const W4Params& p, int num_rows, cudaStream_t s) {
+  return p.zeros != nullptr ? launch_w4<FP8, GROUP, true>(p, num_rows, s)
+                            : launch_w4<FP8, GROUP, false>(p, num_rows, s);
 }
 
 template <bool FP8>
-cudaError_t launch_w4(const W4Params& p, int group, int64_t items, cudaStream_t s) {
-  if (group == 32) return launch_w4<FP8, 32>(p, items, s);
-  if (group == 64) return launch_w4<FP8, 64>(p, items, s);
-  return launch_w4<FP8, 128>(p, items, s);
+cudaError_t launch_w4(const W4Params& p, int group, int num_rows, cudaStream_t s) {
+  if (group == 32) return launch_w4<FP8, 32>(p, num_rows, s);
+  if (group == 64) return launch_w4<FP8, 64>(p, num_rows, s);
+  return launch_w4<FP8, 128>(p, num_rows, s);
 }
 
 }  // namespace
@@ -437,13 +664,9 @@ int32_t ep_expert_w4(const ep_w4_config* cfg, int32_t cap, int32_t num_rows, con
   p.start = d_expert_start;
   p.end = d_expert_end;
   p.out = static_cast<__nv_bfloat16*>(d_out);
-  // an upper bound of the warps' items: an expert's last chunk may be short
-  const int64_t chunks = int64_t(num_rows) / kChunk +
-                         (num_rows < cfg->num_experts ? num_rows : cfg->num_experts);
-  const int64_t items = chunks * p.tiles;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return status(cfg->x_fp8 ? launch_w4<true>(p, cfg->group_size, items, s)
-                           : launch_w4<false>(p, cfg->group_size, items, s));
+  return status(cfg->x_fp8 ? launch_w4<true>(p, cfg->group_size, num_rows, s)
+                           : launch_w4<false>(p, cfg->group_size, num_rows, s));
 }
 
 }  // extern "C"
