@@ -55,27 +55,61 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// The exponent that makes a 16-bit float with integer mantissa bits: 128 + q
-// in bf16 (7 mantissa bits), 1024 + q in f16 (10), both exact.
+// d = the same products with no sum before them.
 template <bool FP8>
-constexpr uint32_t kOffsetBits = FP8 ? 0x64006400u : 0x43004300u;
-
-// 16-bit float pair (offset + zero, offset + zero).
-template <bool FP8>
-__device__ __forceinline__ uint32_t offset_pair(uint32_t zero) {
-  return kOffsetBits<FP8> + zero * 0x00010001u;
+__device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                          uint32_t a3, uint32_t b0, uint32_t b1) {
+  if constexpr (FP8)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
-// Fields j and j + 4 of a word minus the zero point, as a 16-bit float pair.
-template <bool FP8>
-__device__ __forceinline__ uint32_t decode(uint32_t word, int j, uint32_t offset) {
-  const uint32_t u = ((word >> (4 * j)) & 0x000F000Fu) | kOffsetBits<FP8>;
+// (v & mask) | bits in one instruction.
+__device__ __forceinline__ uint32_t mask_or(uint32_t v, uint32_t mask, uint32_t bits) {
   uint32_t r;
-  if constexpr (FP8)
-    asm("sub.f16x2 %0, %1, %2;" : "=r"(r) : "r"(u), "r"(offset));
-  else
-    asm("sub.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(u), "r"(offset));
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(v), "r"(mask), "r"(bits));
   return r;
+}
+
+// A code becomes a 16-bit float without a conversion: its bits are the last
+// integer bits of a mantissa whose exponent gives them weight 1.  bf16 (7
+// mantissa bits) has one such place, bits 0-3 under 128; f16 (10) has bits
+// 0-3 under 1024 and bits 4-7 under 64, which saves half the shifts.  The
+// zero point and that offset then come off in one exact subtraction.
+template <bool FP8>
+__device__ __forceinline__ void decode(uint32_t word, uint32_t even, uint32_t odd,
+                                       uint32_t (&pairs)[4]) {
+  if constexpr (FP8) {
+    const uint32_t high = word >> 8;
+    pairs[0] = mask_or(word, 0x000F000Fu, 0x64006400u);
+    pairs[1] = mask_or(word, 0x00F000F0u, 0x54005400u);
+    pairs[2] = mask_or(high, 0x000F000Fu, 0x64006400u);
+    pairs[3] = mask_or(high, 0x00F000F0u, 0x54005400u);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      asm("sub.f16x2 %0, %0, %1;" : "+r"(pairs[j]) : "r"(j & 1 ? odd : even));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      pairs[j] = mask_or(word >> (4 * j), 0x000F000Fu, 0x43004300u);
+      asm("sub.bf16x2 %0, %0, %1;" : "+r"(pairs[j]) : "r"(even));
+    }
+  }
+}
+
+// What decode takes off the even and odd pairs of a row with zero point z:
+// pairs of 1024 + z and 64 + z in f16, of 128 + z in bf16.
+template <bool FP8>
+__device__ __forceinline__ void offsets(uint32_t z, uint32_t* even, uint32_t* odd) {
+  *even = (FP8 ? 0x64006400u : 0x43004300u) + z * 0x00010001u;
+  *odd = 0x54005400u + z * 0x00100010u;
 }
 
 // Two E4M3 values as an f16 pair (exact).
@@ -108,16 +142,13 @@ struct Stage {
   }
 };
 
-// 16 bytes global -> shared, or zeros when !have.
-__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool have) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(have ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async4_or_zero(uint32_t dst, const void* src, bool have) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
-               "r"(have ? 4 : 0)
-               : "memory");
+// Global -> shared, asynchronously.
+template <int BYTES>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
@@ -189,68 +220,79 @@ __device__ __forceinline__ int expert_of(const int* pre, int E, int c) {
 
 // A tile of 64 packed weight rows by a chunk of up to 8 NT rows of x.
 struct Item {
-  int tile, row0, rows;
-  int64_t unit0;       // first (tile, block) unit of the codes
+  int expert, tile, row0, rows;
   template <int kRows>
   __device__ __forceinline__ void find(const W4Params& p, const int* pre, int64_t it) {
     const int chunk = int(it / p.tiles);
     tile = int(it % p.tiles);
-    const int e = expert_of(pre, p.E, chunk);
-    row0 = max(0, p.start[e]) + (chunk - pre[e]) * kRows;
-    rows = min(kRows, min(p.cap, p.end[e]) - row0);
-    unit0 = (int64_t(e) * p.tiles + tile) * p.blocks;
+    expert = expert_of(pre, p.E, chunk);
+    row0 = max(0, p.start[expert]) + (chunk - pre[expert]) * kRows;
+    rows = min(kRows, min(p.cap, p.end[expert]) - row0);
   }
 };
 
-// Copies one unit (block kb of an item) into a stage; every lane of the warp
-// takes its share.
+// A lane's share of the copies of an item's units, one unit after another.
+// Columns past the item's rows and inputs past H are not copied: what a
+// stage holds there meets only columns that are not stored, and is skipped.
 template <bool FP8, int GROUP, bool ZEROS, int NT>
-__device__ __forceinline__ void load_unit(const W4Params& p, const Item& it, int kb, uint32_t stage,
-                                          int lane) {
+struct Loader {
   using St = Stage<FP8, GROUP, ZEROS, NT>;
-  const int64_t unit = it.unit0 + kb;
-  const uint4* codes = reinterpret_cast<const uint4*>(p.codes) + unit * (kWordsPerBlock / 4) + lane;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) cp_async16_or_zero(stage + i * 512 + lane * 16, codes + i * 32, true);
-  const char* x = static_cast<const char*>(p.x);
-  if constexpr (FP8) {
-#pragma unroll
-    for (int i = 0; i < 2 * NT; ++i) {
-      const int t = i * 4 + (lane >> 3), c = lane & 7;
-      const bool have = t < it.rows;
-      cp_async16_or_zero(stage + St::x_piece(t, c),
-                         x + int64_t(it.row0 + (have ? t : 0)) * p.H + kb * 128 + c * 16, have);
-    }
-    if (lane < 8 * NT) {
-      const bool have = lane < it.rows;
-      cp_async4_or_zero(stage + St::kXScale + lane * 4,
-                        p.x_scale + int64_t(it.row0 + (have ? lane : 0)) * p.blocks + kb, have);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4 * NT; ++i) {
-      const int t = i * 2 + (lane >> 4), c = lane & 15;
-      const int k = kb * 128 + c * 8;
-      const bool have = t < it.rows && k < p.H;
-      cp_async16_or_zero(stage + St::x_piece(t, c),
-                         x + (int64_t(it.row0 + (have ? t : 0)) * p.H + (have ? k : 0)) * 2, have);
-    }
+  const char *codes, *scales, *x, *x_scale, *zeros;
+  int rows;      // left of the lane's first row
+  int k;         // first input of the lane's pieces of x
+  int kb;
+
+  __device__ __forceinline__ void start(const W4Params& p, const Item& it, int slice, int lane) {
+    const int64_t unit = (int64_t(it.expert) * p.tiles + it.tile) * p.blocks + slice;
+    codes = reinterpret_cast<const char*>(p.codes) + unit * 4096 + lane * 16;
+    scales = reinterpret_cast<const char*>(p.scales) + unit * (St::kGroups * kTileRows * 2) + lane * 16;
+    if constexpr (ZEROS)
+      zeros = reinterpret_cast<const char*>(p.zeros) + unit * (St::kGroups * kTileRows) + lane * 16;
+    const int t = FP8 ? lane >> 3 : lane >> 4, c = FP8 ? lane & 7 : lane & 15;
+    rows = it.rows - t;
+    k = slice * kBlockIn + c * (FP8 ? 16 : 8);
+    x = static_cast<const char*>(p.x) + (int64_t(it.row0 + t) * p.H + k) * (FP8 ? 1 : 2);
+    if constexpr (FP8)
+      x_scale = reinterpret_cast<const char*>(p.x_scale + int64_t(it.row0 + lane) * p.blocks + slice);
+    kb = slice;
   }
-  const char* scales = reinterpret_cast<const char*>(p.scales) + unit * (St::kGroups * kTileRows * 2);
-  if (lane < St::kGroups * 8)
-    cp_async16_or_zero(stage + St::kScales + lane * 16, scales + lane * 16, true);
-  if constexpr (ZEROS) {
-    const uint8_t* zeros = p.zeros + unit * (St::kGroups * kTileRows);
-    if (lane < St::kGroups * 4)
-      cp_async16_or_zero(stage + St::kZeros + lane * 16, zeros + lane * 16, true);
+
+  __device__ __forceinline__ void copy(const W4Params& p, uint32_t stage, int lane, int split) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) cp_async<16>(stage + i * 512 + lane * 16, codes + i * 512);
+    codes += split * 4096;
+    if constexpr (FP8) {
+      const int t = lane >> 3, c = lane & 7;
+#pragma unroll
+      for (int i = 0; i < 2 * NT; ++i)
+        if (4 * i < rows) cp_async<16>(stage + St::x_piece(4 * i + t, c), x + int64_t(4 * i) * p.H);
+      if (lane < 8 * NT && lane < rows + t) cp_async<4>(stage + St::kXScale + lane * 4, x_scale);
+      x += split * kBlockIn;
+      x_scale += split * 4;
+    } else {
+      const int t = lane >> 4, c = lane & 15;
+#pragma unroll
+      for (int i = 0; i < 4 * NT; ++i)
+        if (2 * i < rows && k < p.H)
+          cp_async<16>(stage + St::x_piece(2 * i + t, c), x + int64_t(4 * i) * p.H);
+      x += split * kBlockIn * 2;
+      k += split * kBlockIn;
+    }
+    if (lane < St::kGroups * 8) cp_async<16>(stage + St::kScales + lane * 16, scales);
+    scales += split * (St::kGroups * kTileRows * 2);
+    if constexpr (ZEROS) {
+      if (lane < St::kGroups * 4) cp_async<16>(stage + St::kZeros + lane * 16, zeros);
+      zeros += split * (St::kGroups * kTileRows);
+    }
+    kb += split;
   }
-}
+};
 
 // acc += the unit in a stage.  Lane (g = lane / 4, q = lane % 4) holds packed
 // rows 8 g .. 8 g + 7 (piece 2 r + h is row g + 8 h of the r-th 16-row
 // operand) and columns 8 t + 2 q, + 1: acc[t][r][2 h + c].
 template <bool FP8, int GROUP, bool ZEROS, int NT>
-__device__ __forceinline__ void multiply_unit(uint32_t stage, int lane, int tiles_used,
+__device__ __forceinline__ void multiply_unit(uint32_t stage, int lane, int tiles_used, int inputs,
                                               float (&acc)[NT][4][4]) {
   using St = Stage<FP8, GROUP, ZEROS, NT>;
   constexpr int kWords = GROUP / 32;              // words of a lane a group
@@ -273,13 +315,12 @@ __device__ __forceinline__ void multiply_unit(uint32_t stage, int lane, int tile
     const uint4 sv = lds16(stage + St::kScales + s * 128 + g * 16);
     uint2 zv = make_uint2(0x08080808u, 0x08080808u);
     if constexpr (ZEROS) zv = lds8(stage + St::kZeros + s * 64 + g * 8);
+    if (!FP8 && 32 * kWords * s >= inputs) break;      // groups past H
+    uint32_t even[8], odd[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      offsets<FP8>((i < 4 ? zv.x : zv.y) >> (8 * (i & 3)) & 0xFFu, &even[i], &odd[i]);
     float d[NT][4][4];
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) d[t][r][i] = 0.0f;
 #pragma unroll
     for (int i = s * kWords; i < (s + 1) * kWords; ++i) {
       uint32_t b[NT][4];
@@ -302,20 +343,17 @@ __device__ __forceinline__ void multiply_unit(uint32_t stage, int lane, int tile
       }
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const uint32_t z = (r < 2 ? zv.x : zv.y) >> (16 * (r & 1));
-        const uint32_t o0 = offset_pair<FP8>(z & 0xFFu), o1 = offset_pair<FP8>((z >> 8) & 0xFFu);
-        const uint32_t lo = word_of(w[2 * r], i), hi = word_of(w[2 * r + 1], i);
-        uint32_t a[8];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          a[2 * j] = decode<FP8>(lo, j, o0);
-          a[2 * j + 1] = decode<FP8>(hi, j, o1);
-        }
+        uint32_t lo[4], hi[4];
+        decode<FP8>(word_of(w[2 * r], i), even[2 * r], odd[2 * r], lo);
+        decode<FP8>(word_of(w[2 * r + 1], i), even[2 * r + 1], odd[2 * r + 1], hi);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           if (NT > 1 && t >= tiles_used) continue;
-          mma<FP8>(d[t][r], a[0], a[1], a[2], a[3], b[t][0], b[t][1]);
-          mma<FP8>(d[t][r], a[4], a[5], a[6], a[7], b[t][2], b[t][3]);
+          if (i == s * kWords)
+            mma_first<FP8>(d[t][r], lo[0], hi[0], lo[1], hi[1], b[t][0], b[t][1]);
+          else
+            mma<FP8>(d[t][r], lo[0], hi[0], lo[1], hi[1], b[t][0], b[t][1]);
+          mma<FP8>(d[t][r], lo[2], hi[2], lo[3], hi[3], b[t][2], b[t][3]);
         }
       }
     }
@@ -358,39 +396,44 @@ __device__ __forceinline__ void store_pair(const W4Params& p, const Item& it, in
 template <bool FP8, int GROUP, bool ZEROS, int NT, int WARPS, int STAGES>
 __global__ void __launch_bounds__(WARPS * 32) expert_w4_kernel(W4Params p, int split) {
   using St = Stage<FP8, GROUP, ZEROS, NT>;
+  static_assert(St::kBytes >= NT * 2048, "a stage holds a warp's sums");
   extern __shared__ __align__(16) char smem[];
+  int* const pre = reinterpret_cast<int*>(smem + WARPS * STAGES * St::kBytes);
+  __shared__ uint32_t sums_at[WARPS];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  char* const ring = smem + warp * (STAGES * St::kBytes);
-  float* const sums = reinterpret_cast<float*>(smem + WARPS * STAGES * St::kBytes);
-  int* const pre = reinterpret_cast<int*>(sums + (split > 1 ? WARPS * NT * 512 : 0));
+  const uint32_t base = smem_addr(smem) + warp * (STAGES * St::kBytes);
   pdl_wait();
   count_chunks<8 * NT>(p, pre);
   const int groups = WARPS / split, group = warp / split, slice = warp % split;
   const int64_t items = int64_t(pre[p.E]) * p.tiles;
   const int64_t step = int64_t(gridDim.x) * groups;
-  const uint32_t base = smem_addr(ring);
 
   // the unit to load next
   int64_t ahead = int64_t(blockIdx.x) * groups + group;
-  int ahead_kb = slice;
-  Item from;
-  if (ahead < items) from.find<8 * NT>(p, pre, ahead);
-  int slot = 0;
-  const auto load_next = [&](int to) {
-    if (ahead < items && ahead_kb < p.blocks) {
-      load_unit<FP8, GROUP, ZEROS, NT>(p, from, ahead_kb, base + to * St::kBytes, lane);
-      ahead_kb += split;
-      if (ahead_kb >= p.blocks) {
-        ahead_kb = slice;
+  Item next;
+  Loader<FP8, GROUP, ZEROS, NT> loader;
+  loader.kb = p.blocks;
+  if (ahead < items) {
+    next.find<8 * NT>(p, pre, ahead);
+    loader.start(p, next, slice, lane);
+  }
+  const auto load_next = [&](uint32_t stage) {
+    if (loader.kb < p.blocks) {
+      loader.copy(p, stage, lane, split);
+      if (loader.kb >= p.blocks) {
         ahead += step;
-        if (ahead < items) from.find<8 * NT>(p, pre, ahead);
+        if (ahead < items) {
+          next.find<8 * NT>(p, pre, ahead);
+          loader.start(p, next, slice, lane);
+        }
       }
     }
     cp_async_commit();
   };
 #pragma unroll
-  for (int i = 0; i < STAGES - 1; ++i) load_next(i);
+  for (int i = 0; i < STAGES - 1; ++i) load_next(base + i * St::kBytes);
 
+  uint32_t stage = base, idle = base + (STAGES - 1) * St::kBytes;
   for (int64_t now = int64_t(blockIdx.x) * groups + group; now < items; now += step) {
     Item it;
     it.find<8 * NT>(p, pre, now);
@@ -404,10 +447,11 @@ __global__ void __launch_bounds__(WARPS * 32) expert_w4_kernel(W4Params p, int s
         for (int i = 0; i < 4; ++i) acc[t][r][i] = 0.0f;
     for (int kb = slice; kb < p.blocks; kb += split) {
       cp_async_wait<STAGES - 2>();
-      __syncwarp();      // the unit is there, and the slot before it is free
-      load_next(slot == 0 ? STAGES - 1 : slot - 1);
-      multiply_unit<FP8, GROUP, ZEROS, NT>(base + slot * St::kBytes, lane, used, acc);
-      slot = slot + 1 == STAGES ? 0 : slot + 1;
+      __syncwarp();      // the unit is there, and the idle stage was read by all
+      load_next(idle);
+      multiply_unit<FP8, GROUP, ZEROS, NT>(stage, lane, used, p.H - kb * kBlockIn, acc);
+      idle = stage;
+      stage = stage == base + (STAGES - 1) * St::kBytes ? base : stage + St::kBytes;
     }
     const int g = lane >> 2, q = lane & 3;
     if (split == 1) {
@@ -421,24 +465,28 @@ __global__ void __launch_bounds__(WARPS * 32) expert_w4_kernel(W4Params p, int s
                        acc[t][2 + (i >> 1)][2 * (i & 1) + c]);
       continue;
     }
-    // pair (t, i, c) of a warp at [2 (8 t + 2 i + c) + half][lane]
-    float* const mine = sums + warp * NT * 512 + lane;
+    // pair (t, i, c) of a warp at [2 (8 t + 2 i + c) + half][lane] of its idle stage
+    __syncwarp();
+    char* const mine = smem + (idle - smem_addr(smem)) + lane * 4;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          mine[(2 * (8 * t + 2 * i + c)) * 32] = acc[t][i >> 1][2 * (i & 1) + c];
-          mine[(2 * (8 * t + 2 * i + c) + 1) * 32] = acc[t][2 + (i >> 1)][2 * (i & 1) + c];
+          float* const at = reinterpret_cast<float*>(mine + (8 * t + 2 * i + c) * 256);
+          at[0] = acc[t][i >> 1][2 * (i & 1) + c];
+          at[32] = acc[t][2 + (i >> 1)][2 * (i & 1) + c];
         }
+    if (lane == 0) sums_at[warp] = idle - smem_addr(smem);
     asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(32 * split) : "memory");
     for (int pair = slice; pair < 8 * used; pair += split) {
-      const float* at = sums + group * split * NT * 512 + 2 * pair * 32 + lane;
       float lo = 0.0f, hi = 0.0f;
       for (int v = 0; v < split; ++v) {
-        lo += at[v * NT * 512];
-        hi += at[v * NT * 512 + 32];
+        const float* const at =
+            reinterpret_cast<const float*>(smem + sums_at[group * split + v] + pair * 256) + lane;
+        lo += at[0];
+        hi += at[32];
       }
       store_pair(p, it, g, (pair & 7) >> 1, 8 * (pair >> 3) + 2 * q + (pair & 1), lo, hi);
     }
@@ -536,7 +584,7 @@ int64_t w4_scales(const ep_w4_config* c) {
 int32_t status(cudaError_t e) { return note_cuda(e) == cudaSuccess ? EP_OK : EP_ERR_CUDA; }
 
 #ifndef W4_WARPS
-#define W4_WARPS 8
+#define W4_WARPS 16
 #endif
 #ifndef W4_SPLIT
 #define W4_SPLIT 0
@@ -548,8 +596,7 @@ template <bool FP8, int GROUP, bool ZEROS>
 cudaError_t launch_w4(const W4Params& p, int num_rows, cudaStream_t stream) {
   constexpr int NT = 1;
   constexpr int WARPS = W4_WARPS;
-  constexpr int kSums = WARPS * NT * 512 * 4;
-  constexpr int STAGES = (kSmemBudget - kSums) / (WARPS * Stage<FP8, GROUP, ZEROS, NT>::kBytes);
+  constexpr int STAGES = kSmemBudget / (WARPS * Stage<FP8, GROUP, ZEROS, NT>::kBytes);
   static_assert(STAGES >= 2);
   // an upper bound of the items: an expert's last chunk may be short
   const int64_t chunks = int64_t(num_rows) / (8 * NT) + (num_rows < p.E ? num_rows : p.E);
@@ -564,8 +611,7 @@ cudaError_t launch_w4(const W4Params& p, int num_rows, cudaStream_t stream) {
   }
   const int64_t want = (items + WARPS / split - 1) / (WARPS / split);
   const int grid = int(want < sms ? want : sms);
-  const size_t smem = WARPS * STAGES * Stage<FP8, GROUP, ZEROS, NT>::kBytes +
-                      (split > 1 ? kSums : 0) + sizeof(int) * (p.E + 1);
+  const size_t smem = WARPS * STAGES * Stage<FP8, GROUP, ZEROS, NT>::kBytes + sizeof(int) * (p.E + 1);
   auto* kernel = expert_w4_kernel<FP8, GROUP, ZEROS, NT, WARPS, STAGES>;
   const cudaError_t e =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
