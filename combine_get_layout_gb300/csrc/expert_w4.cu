@@ -13,6 +13,8 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <cmath>
+
 #include "../../include/ep.h"
 #include "ep_device.cuh"
 #include "ep_internal.h"
@@ -178,29 +180,36 @@ __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) {
 }
 
 // Chunks of kRows rows before each expert, in shared memory: pre[e] of e's
-// predecessors, pre[E] of all.
+// predecessors, pre[E] of all.  Every thread takes a run of experts, so that
+// up to blockDim.x experts need one pass and two barriers.
 template <int kRows>
 __device__ void count_chunks(const W4Params& p, int* pre) {
-  for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
+  __shared__ int warp_sum[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int each = (p.E + blockDim.x - 1) / blockDim.x;
+  const int e0 = min(p.E, int(threadIdx.x) * each), e1 = min(p.E, e0 + each);
+  int mine = 0;
+  for (int e = e0; e < e1; ++e) {
     const int lo = max(0, p.start[e]), hi = min(p.cap, p.end[e]);
-    pre[e] = hi > lo ? (hi - lo + kRows - 1) / kRows : 0;
+    const int n = hi > lo ? (hi - lo + kRows - 1) / kRows : 0;
+    pre[e] = n;
+    mine += n;
   }
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    int carry = 0;
-    for (int e0 = 0; e0 < p.E; e0 += 32) {
-      const int e = e0 + threadIdx.x;
-      const int mine = e < p.E ? pre[e] : 0;
-      int sum = mine;
+  int sum = mine;
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int up = __shfl_up_sync(0xffffffffu, sum, d);
-        if (int(threadIdx.x) >= d) sum += up;
-      }
-      if (e < p.E) pre[e] = carry + sum - mine;
-      carry += __shfl_sync(0xffffffffu, sum, 31);
-    }
-    if (threadIdx.x == 0) pre[p.E] = carry;
+  for (int d = 1; d < 32; d <<= 1) {
+    const int up = __shfl_up_sync(0xffffffffu, sum, d);
+    if (lane >= d) sum += up;
+  }
+  if (lane == 31) warp_sum[warp] = sum;
+  __syncthreads();
+  int before = sum - mine;
+  for (int v = 0; v < warp; ++v) before += warp_sum[v];
+  if (threadIdx.x == blockDim.x - 1) pre[p.E] = before + mine;
+  for (int e = e0; e < e1; ++e) {
+    const int n = pre[e];
+    pre[e] = before;
+    before += n;
   }
   __syncthreads();
 }
@@ -218,15 +227,31 @@ __device__ __forceinline__ int expert_of(const int* pre, int E, int c) {
   return lo;
 }
 
-// A tile of 64 packed weight rows by a chunk of up to 8 NT rows of x.
+// Steps through (chunk, tile) items, tiles first, `stride` items at a time.
+struct Walk {
+  int chunk, tile, chunks, skip_chunks, skip_tiles;
+  __device__ __forceinline__ Walk(const W4Params& p, int first, int stride, int total)
+      : chunk(first / p.tiles), tile(first % p.tiles), chunks(total),
+        skip_chunks(stride / p.tiles), skip_tiles(stride % p.tiles) {}
+  __device__ __forceinline__ bool done() const { return chunk >= chunks; }
+  __device__ __forceinline__ void advance(const W4Params& p) {
+    chunk += skip_chunks;
+    tile += skip_tiles;
+    if (tile >= p.tiles) {
+      tile -= p.tiles;
+      ++chunk;
+    }
+  }
+};
+
+// A tile of 64 packed weight rows by a chunk of up to kRows rows of x.
 struct Item {
   int expert, tile, row0, rows;
   template <int kRows>
-  __device__ __forceinline__ void find(const W4Params& p, const int* pre, int64_t it) {
-    const int chunk = int(it / p.tiles);
-    tile = int(it % p.tiles);
-    expert = expert_of(pre, p.E, chunk);
-    row0 = max(0, p.start[expert]) + (chunk - pre[expert]) * kRows;
+  __device__ __forceinline__ void find(const W4Params& p, const int* pre, const Walk& at) {
+    tile = at.tile;
+    expert = expert_of(pre, p.E, at.chunk);
+    row0 = max(0, p.start[expert]) + (at.chunk - pre[expert]) * kRows;
     rows = min(kRows, min(p.cap, p.end[expert]) - row0);
   }
 };
@@ -404,28 +429,25 @@ __global__ void __launch_bounds__(WARPS * 32) expert_w4_kernel(W4Params p, int s
   const uint32_t base = smem_addr(smem) + warp * (STAGES * St::kBytes);
   pdl_wait();
   count_chunks<8 * NT>(p, pre);
-  const int groups = WARPS / split, group = warp / split, slice = warp % split;
-  const int64_t items = int64_t(pre[p.E]) * p.tiles;
-  const int64_t step = int64_t(gridDim.x) * groups;
-
-  // the unit to load next
-  int64_t ahead = int64_t(blockIdx.x) * groups + group;
-  Item next;
+  // groups are numbered across the CTAs first: a last partial round of items
+  // then spreads over all SMs
+  const int group = warp / split, slice = warp % split;
+  Walk now(p, group * gridDim.x + blockIdx.x, gridDim.x * (WARPS / split), pre[p.E]);
+  Walk ahead = now;      // the item of the unit to load next
   Loader<FP8, GROUP, ZEROS, NT> loader;
   loader.kb = p.blocks;
-  if (ahead < items) {
+  const auto enter = [&] {
+    Item next;
     next.find<8 * NT>(p, pre, ahead);
     loader.start(p, next, slice, lane);
-  }
+  };
+  if (!ahead.done()) enter();
   const auto load_next = [&](uint32_t stage) {
     if (loader.kb < p.blocks) {
       loader.copy(p, stage, lane, split);
       if (loader.kb >= p.blocks) {
-        ahead += step;
-        if (ahead < items) {
-          next.find<8 * NT>(p, pre, ahead);
-          loader.start(p, next, slice, lane);
-        }
+        ahead.advance(p);
+        if (!ahead.done()) enter();
       }
     }
     cp_async_commit();
@@ -434,7 +456,7 @@ __global__ void __launch_bounds__(WARPS * 32) expert_w4_kernel(W4Params p, int s
   for (int i = 0; i < STAGES - 1; ++i) load_next(base + i * St::kBytes);
 
   uint32_t stage = base, idle = base + (STAGES - 1) * St::kBytes;
-  for (int64_t now = int64_t(blockIdx.x) * groups + group; now < items; now += step) {
+  for (; !now.done(); now.advance(p)) {
     Item it;
     it.find<8 * NT>(p, pre, now);
     const int used = (it.rows + 7) >> 3;
@@ -482,9 +504,10 @@ __global__ void __launch_bounds__(WARPS * 32) expert_w4_kernel(W4Params p, int s
     asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(32 * split) : "memory");
     for (int pair = slice; pair < 8 * used; pair += split) {
       float lo = 0.0f, hi = 0.0f;
+      const char* const from = smem + pair * 256 + lane * 4;
+#pragma unroll 4
       for (int v = 0; v < split; ++v) {
-        const float* const at =
-            reinterpret_cast<const float*>(smem + sums_at[group * split + v] + pair * 256) + lane;
+        const float* const at = reinterpret_cast<const float*>(from + sums_at[group * split + v]);
         lo += at[0];
         hi += at[32];
       }
@@ -583,33 +606,38 @@ int64_t w4_scales(const ep_w4_config* c) {
 
 int32_t status(cudaError_t e) { return note_cuda(e) == cudaSuccess ? EP_OK : EP_ERR_CUDA; }
 
-#ifndef W4_WARPS
-#define W4_WARPS 16
-#endif
-#ifndef W4_SPLIT
-#define W4_SPLIT 0
-#endif
 // Shared memory a CTA may use, less the table of chunks of 2048 experts.
-constexpr int kSmemBudget = 227 * 1024 - 8 * 1024 - 256;
+constexpr int kSmemBudget = 227 * 1024 - 8 * 1024 - 512;
+
+// Chunks of `size` rows that `rows` rows of E experts make, on average.
+double expected_chunks(int rows, int E, int size) {
+  const double active = E * (1.0 - pow(1.0 - 1.0 / E, rows));
+  const double full = double(rows) / size + 0.5 * active;
+  return active > full ? active : full;
+}
 
 template <bool FP8, int GROUP, bool ZEROS>
 cudaError_t launch_w4(const W4Params& p, int num_rows, cudaStream_t stream) {
-  constexpr int NT = 1;
-  constexpr int WARPS = W4_WARPS;
+  constexpr int NT = 1, WARPS = 16;
   constexpr int STAGES = kSmemBudget / (WARPS * Stage<FP8, GROUP, ZEROS, NT>::kBytes);
   static_assert(STAGES >= 2);
+  const double items = expected_chunks(num_rows, p.E, 8 * NT) * p.tiles;
+  const int sms = device_info().sm_count;
+  // Units one warp works through: rounds of items times its blocks of each,
+  // and about one unit's time to add up a group's sums.
+  int split = 1;
+  double least = 0.0;
+  for (int s = 1; s <= WARPS; s *= 2) {
+    const double cost = ceil(items * s / (double(sms) * WARPS)) *
+                        ((p.blocks + s - 1) / s + (s > 1 ? 1.0 : 0.0));
+    if (s == 1 || cost < least) {
+      split = s;
+      least = cost;
+    }
+  }
   // an upper bound of the items: an expert's last chunk may be short
   const int64_t chunks = int64_t(num_rows) / (8 * NT) + (num_rows < p.E ? num_rows : p.E);
-  const int64_t items = chunks * p.tiles;
-  const int sms = device_info().sm_count;
-  int split = W4_SPLIT;
-  if (split == 0) {
-    split = 1;
-    while (WARPS % (split * 2) == 0 && split * 2 <= p.blocks &&
-           items * split < int64_t(sms) * WARPS * 2)
-      split *= 2;
-  }
-  const int64_t want = (items + WARPS / split - 1) / (WARPS / split);
+  const int64_t want = (chunks * p.tiles + WARPS / split - 1) / (WARPS / split);
   const int grid = int(want < sms ? want : sms);
   const size_t smem = WARPS * STAGES * Stage<FP8, GROUP, ZEROS, NT>::kBytes + sizeof(int) * (p.E + 1);
   auto* kernel = expert_w4_kernel<FP8, GROUP, ZEROS, NT, WARPS, STAGES>;
