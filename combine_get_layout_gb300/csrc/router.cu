@@ -42,6 +42,7 @@ struct RouteParams {
   int32_t* part_count;       // [ctas + B, E]
   int32_t* part_tokens;      // [ctas + B]
   float* part_z;             // [ctas + B]
+  unsigned* done;            // cleared for the second kernel
 };
 
 // Index of register r of this lane: one logit a load (V = 1), or V
@@ -98,86 +99,150 @@ __device__ __forceinline__ float load_one(const void* base, int64_t at) {
     return static_cast<const float*>(base)[at];
 }
 
-// Order-preserving 32-bit key of a float; -0 and +0 share one key.
-__device__ __forceinline__ uint32_t order_key(float f) {
-  const uint32_t u = __float_as_uint(f + 0.0f);
-  return u ^ (uint32_t(int32_t(u) >> 31) | 0x80000000u);
-}
-
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(kFull, v, d);
   return v;
 }
 
+// Largest of the lanes' values; a NaN counts only where all are NaN.
 __device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int d = 16; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, d));
-  return v;
+  float m;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+  return m;
 }
 
-__device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
+constexpr float kLog2e = 1.4426950408889634f;
 
-// Scores of a token: s = exp(x - max) / sum (softmax) or sigmoid(x).  Leaves
-// the scores in `s`; returns their total over the experts (softmax: the sum
-// of exponentials) and the row's maximum.  A row with no finite maximum
-// below has all-zero scores.
+// 2^x and 1 / x to 2^-22 of the value: what a score is rounded to anyway
+// once 32-bit sums and products have passed over it.
+__device__ __forceinline__ float fast_exp2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float fast_reciprocal(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ float sigmoid(float x) {
+  return fast_reciprocal(1.0f + fast_exp2(-kLog2e * x));
+}
+
+// exp(l - top); the difference first, so that no size of logit overflows.
+__device__ __forceinline__ float soft_score(float l, float top) {
+  return fast_exp2((l - top) * kLog2e);
+}
+
+// Scores of a token: s = exp(x - max) (softmax, before its division by the
+// total) or sigmoid(x).  Returns their total over the experts and the row's
+// maximum in *top.  -inf scores 0; a row of nothing else scores 0 throughout.
 template <int VPL, bool SIG>
 __device__ __forceinline__ float scores(const float (&x)[VPL], float (&s)[VPL], float* top) {
   float total = 0.0f;
   if constexpr (SIG) {
 #pragma unroll
     for (int r = 0; r < VPL; ++r) {
-      s[r] = x[r] == -CUDART_INF_F ? 0.0f : sigmoid(x[r]);
+      s[r] = sigmoid(x[r]);      // exp2(+inf) = inf, its reciprocal 0
       total += s[r];
     }
     *top = 0.0f;
-    return warp_sum(total);
   } else {
     float m = x[0];
 #pragma unroll
     for (int r = 1; r < VPL; ++r) m = fmaxf(m, x[r]);
     m = warp_max(m);
     *top = m;
+    const float base = m == -CUDART_INF_F ? 0.0f : m;
 #pragma unroll
     for (int r = 0; r < VPL; ++r) {
-      // an expert out of service, and a row with none in service, score 0
-      s[r] = x[r] == -CUDART_INF_F ? 0.0f : expf(x[r] - m);
+      s[r] = soft_score(x[r], base);
       total += s[r];
     }
-    return warp_sum(total);
   }
+  return warp_sum(total);
 }
 
-// Clears the choice scores of every group but the `kept` best.  `row` is
+// The `kept` best of G groups (G <= 32) by the scores that lanes g < G hold,
+// as a bit mask; equal scores go to the lower group, -inf is never kept.
+__device__ __forceinline__ uint32_t best_groups(float score, int G, int kept, int lane) {
+  uint32_t keep = 0;
+  float left = lane < G ? score : -CUDART_INF_F;
+  for (int i = 0; i < kept; ++i) {
+    const float top = warp_max(left);
+    const uint32_t at = __ballot_sync(kFull, left == top);
+    // no NaN reaches this, so that a lane always answers
+    const int g = __ffs(at) - 1;
+    keep |= top > -CUDART_INF_F ? 1u << g : 0u;
+    if (lane == g) left = -CUDART_INF_F;
+  }
+  return keep;
+}
+
+// Adds (best, second) of another set to a running pair.
+__device__ __forceinline__ void top_two(float& best, float& second, float b, float s) {
+  second = fmaxf(fminf(best, b), fmaxf(second, s));
+  best = fmaxf(best, b);
+}
+
+// Sigmoid: a group's two best scores' sum, an expert out of service adding
+// none.  Softmax: its best.
+template <bool SIG>
+__device__ __forceinline__ float group_score(float best, float second) {
+  return SIG && second > -CUDART_INF_F ? best + second : best;
+}
+
+// Clears the choice scores of every group but the `kept` best.  Groups of
+// four times a power of two experts, up to 128, are whole aligned runs of
+// lanes of one vector (V = 4), and reduce by shuffles; other sizes go through
 // this warp's shared scratch of E floats.
 template <int VPL, int V, bool SIG>
 __device__ void keep_groups(float (&c)[VPL], float* row, int E, int G, int kept, int lane) {
+  const int per = E / G;
+#pragma unroll
+  for (int r = 0; r < VPL; ++r) c[r] = fmaxf(c[r], -CUDART_INF_F);      // a NaN is not chosen
+  if constexpr (V == 4) {
+    if ((per & (per - 1)) == 0 && per >= 4 && per <= 128) {
+      const int lanes = per / 4, per_vec = 128 / per;      // groups in a vector of all lanes
+      const int at = lane % per_vec * lanes;               // the first lane of this lane's group
+      float mine = -CUDART_INF_F;
+#pragma unroll
+      for (int v = 0; v < VPL / 4; ++v) {
+        float best = -CUDART_INF_F, second = -CUDART_INF_F;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top_two(best, second, c[4 * v + i], -CUDART_INF_F);
+        for (int d = 1; d < lanes; d <<= 1) {
+          const float b = __shfl_xor_sync(kFull, best, d);
+          const float s = __shfl_xor_sync(kFull, second, d);
+          top_two(best, second, b, s);
+        }
+        const float score = __shfl_sync(kFull, group_score<SIG>(best, second), at);
+        if (lane / per_vec == v) mine = score;
+      }
+      const uint32_t keep = best_groups(mine, G, kept, lane);
+#pragma unroll
+      for (int v = 0; v < VPL / 4; ++v) {
+        const int g = v * per_vec + lane / lanes;
+        if (!((keep >> (g & 31)) & 1u)) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) c[4 * v + i] = -CUDART_INF_F;
+        }
+      }
+      return;
+    }
+  }
 #pragma unroll
   for (int r = 0; r < VPL; ++r) {
     const int e = element_of<V>(r, lane);
     if (e < E) row[e] = c[r];
   }
   __syncwarp();
-  const int per = E / G;
   float best = -CUDART_INF_F, second = -CUDART_INF_F;
-  if (lane < G) {
-    for (int i = 0; i < per; ++i) {
-      const float v = row[lane * per + i];
-      second = fmaxf(second, fminf(best, v));
-      best = fmaxf(best, v);
-    }
-  }
-  // sigmoid: the two best scores' sum, an expert out of service adding none
-  float mine = best;
-  if (SIG && second > -CUDART_INF_F) mine += second;
-  const uint32_t key = lane < G ? order_key(mine) : 0u;
-  int beaten_by = 0;
-  for (int g = 0; g < G; ++g) {
-    const uint32_t other = __shfl_sync(kFull, key, g);
-    beaten_by += (other > key || (other == key && g < lane)) ? 1 : 0;
-  }
-  const uint32_t keep = __ballot_sync(kFull, lane < G ? beaten_by < kept : false);
+  if (lane < G)
+    for (int i = 0; i < per; ++i) top_two(best, second, row[lane * per + i], -CUDART_INF_F);
+  const uint32_t keep = best_groups(group_score<SIG>(best, second), G, kept, lane);
 #pragma unroll
   for (int r = 0; r < VPL; ++r) {
     const int e = element_of<V>(r, lane);
@@ -186,69 +251,136 @@ __device__ void keep_groups(float (&c)[VPL], float* row, int E, int G, int kept,
   __syncwarp();
 }
 
-// The K largest of a warp's choice scores, in descending order, equal ones
-// by ascending index: lane k returns the k-th index, or -1 when fewer than
-// k + 1 experts can be chosen.
+// A lane's share of a token's choice: expert e takes rank `rank`, its choice
+// score is c; e = -1 where a rank stays empty or the lane has nothing.
+struct Chosen {
+  int e, rank;
+  float c;
+};
+
+// The K largest of a warp's choice scores, one after another: any number of
+// equal ones.
 template <int VPL, int V>
-__device__ __forceinline__ int choose(float (&c)[VPL], int K, int lane) {
-  int mine = -1;
+__device__ __noinline__ Chosen choose_in_turn(float (&c)[VPL], int K, int lane) {
+  Chosen mine = {-1, lane, 0.0f};
   for (int k = 0; k < K; ++k) {
-    float best = c[0];
-    int at = element_of<V>(0, lane);
+    float best = -CUDART_INF_F;
+    int at = 0x7fffffff;
 #pragma unroll
-    for (int r = 1; r < VPL; ++r) {
+    for (int r = 0; r < VPL; ++r) {
       if (c[r] > best) {
         best = c[r];
         at = element_of<V>(r, lane);
       }
     }
-    const uint32_t key = order_key(best);
-    const uint32_t top = __reduce_max_sync(kFull, key);
-    if (top == order_key(-CUDART_INF_F)) break;
-    const int win = int(__reduce_min_sync(kFull, key == top ? uint32_t(at) : 0xffffffffu));
+    const float top = warp_max(best);
+    if (top == -CUDART_INF_F) break;
+    const int win = __reduce_min_sync(kFull, best == top ? at : 0x7fffffff);
 #pragma unroll
     for (int r = 0; r < VPL; ++r)
       if (element_of<V>(r, lane) == win) c[r] = -CUDART_INF_F;
-    if (lane == k) mine = win;
+    if (lane == k) mine = {win, k, top};
   }
   return mine;
 }
 
-// One token: choice and gate weights, and the normalised scores in `s`.
-// Returns the expert of lane k < K.
+constexpr int kCandidates = 32;
+
+// The K largest of a warp's choice scores, equal ones by ascending index.
+// The K-th largest of the lanes' maxima (each distinct value counted once)
+// is a bound that at least K scores reach, and with scores spread over the
+// lanes few more do: those go to shared memory, one a lane, where each counts
+// the ones before it.  `best` is the lane's maximum; -inf and NaN are not
+// chosen.
+template <int VPL, int V>
+__device__ __forceinline__ Chosen choose(float (&c)[VPL], float best, int K, int lane,
+                                         float2* list) {
+  float bound = -CUDART_INF_F;
+  for (int k = 0; k < K; ++k) {
+    bound = warp_max(best);
+    best = best == bound ? -CUDART_INF_F : best;
+  }
+  bound = fmaxf(bound, -3.402823466e38f);
+  const uint32_t before = lanemask_lt();
+  int n = 0;
+#pragma unroll
+  for (int r = 0; r < VPL; ++r) {
+    const bool in = c[r] >= bound;
+    const uint32_t who = __ballot_sync(kFull, in);
+    if (in) {
+      const int at = n + __popc(who & before);
+      if (at < kCandidates)
+        list[at] = make_float2(c[r], __int_as_float(element_of<V>(r, lane)));
+    }
+    n += __popc(who);
+  }
+  __syncwarp();
+  if (n > kCandidates) {
+    float left[VPL];      // a copy: c itself then stays in registers
+#pragma unroll
+    for (int r = 0; r < VPL; ++r) left[r] = c[r];
+    return choose_in_turn<VPL, V>(left, K, lane);
+  }
+  Chosen mine = {-1, lane, 0.0f};
+  if (lane < n) {
+    const float2 m = list[lane];
+    mine.c = m.x;
+    mine.e = __float_as_int(m.y);
+    mine.rank = 0;
+  }
+  for (int i = 0; i < n; ++i) {
+    const float2 o = list[i];
+    const bool ahead = o.x > mine.c || (o.x == mine.c && __float_as_int(o.y) < mine.e);
+    if (lane < n && ahead) ++mine.rank;
+  }
+  __syncwarp();
+  if (lane < n && mine.rank >= K) mine.e = -1;
+  return mine;
+}
+
+// One token, given its logits: choice and gate weights; leaves the scores in
+// `s`.  Returns the lane's chosen expert or -1.
 template <int VPL, int V, bool BF16, bool SIG>
 __device__ __forceinline__ int route_token(const RouteParams& p, int t, int lane, float* row,
-                                           float (&s)[VPL], float* total, float* top) {
-  float x[VPL];
-  load_row<VPL, V, BF16>(p.logits, int64_t(t) * p.ld, p.E, lane, x);
+                                           float2* list, const float (&x)[VPL], float (&s)[VPL],
+                                           float* total, float* top) {
   *total = scores<VPL, SIG>(x, s, top);
   float c[VPL];
 #pragma unroll
   for (int r = 0; r < VPL; ++r) {
     c[r] = x[r];
-    if (SIG) {
+    if constexpr (SIG) {
       const int e = element_of<V>(r, lane);
       const float b = p.bias != nullptr && e < p.E ? p.bias[e] : 0.0f;
       c[r] = x[r] == -CUDART_INF_F ? -CUDART_INF_F : s[r] + b;
     }
-    if (c[r] != c[r]) c[r] = -CUDART_INF_F;   // a NaN is not chosen
   }
   if (p.G > 1) keep_groups<VPL, V, SIG>(c, row, p.E, p.G, p.kept, lane);
-  const int mine = choose<VPL, V>(c, p.K, lane);
+  float best = c[0];
+#pragma unroll
+  for (int r = 1; r < VPL; ++r) best = fmaxf(best, c[r]);
+  const Chosen mine = choose<VPL, V>(c, best, p.K, lane, list);
   float w = 0.0f;
-  if (mine >= 0) {
-    const float l = load_one<BF16>(p.logits, int64_t(t) * p.ld + mine);
-    w = SIG ? sigmoid(l) : expf(l - *top) / *total;
+  if (mine.e >= 0) {
+    // softmax: the choice score is the logit; sigmoid: it has the bias in it
+    w = SIG ? sigmoid(load_one<BF16>(p.logits, int64_t(t) * p.ld + mine.e))
+            : soft_score(mine.c, *top);
   }
+  float scale = p.scale;
   if (p.renorm) {
     const float sum = warp_sum(w);
-    w = sum == 0.0f ? 0.0f : w / sum;
+    scale = sum == 0.0f ? 0.0f : scale / sum;
+    // softmax scores of a row with a NaN are all NaN
+    if (!SIG && *total != *total) scale = *total;
+  } else if (!SIG) {
+    scale /= *total;
   }
-  if (lane < p.K) {
-    p.idx[int64_t(t) * p.K + lane] = mine;
-    p.w[int64_t(t) * p.K + lane] = w * p.scale;
+  if (mine.rank < p.K) {
+    const int64_t at = int64_t(t) * p.K + mine.rank;
+    p.idx[at] = mine.e;
+    p.w[at] = mine.e >= 0 ? w * scale : 0.0f;
   }
-  return mine;
+  return mine.e;
 }
 
 __device__ __forceinline__ void route_masked(const RouteParams& p, int t, int lane) {
@@ -258,19 +390,38 @@ __device__ __forceinline__ void route_masked(const RouteParams& p, int t, int la
   }
 }
 
+// Logits that a warp loads ahead of the token it works on: the next token's,
+// where two rows fit its registers.
+template <int VPL>
+constexpr bool kAhead = VPL <= 16;
+
 template <int VPL, int V, bool BF16, bool SIG>
 __global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteParams p) {
   extern __shared__ float smem[];
+  __shared__ float2 lists[kRouteWarps][kCandidates];
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float* row = smem + warp * p.E;
-  float s[VPL], total, top;
-  for (int t = blockIdx.x * kRouteWarps + warp; t < p.T; t += gridDim.x * kRouteWarps) {
-    if (p.mask != nullptr && p.mask[t] == 0) {
-      route_masked(p, t, lane);
-      continue;
+  const int stride = gridDim.x * kRouteWarps;
+  float x[VPL], s[VPL], total, top;
+  int t = blockIdx.x * kRouteWarps + warp;
+  if (kAhead<VPL> && t < p.T) load_row<VPL, V, BF16>(p.logits, int64_t(t) * p.ld, p.E, lane, x);
+  for (; t < p.T; t += stride) {
+    float next[VPL];
+    if constexpr (kAhead<VPL>) {
+      const int u = t + stride;
+      if (u < p.T) load_row<VPL, V, BF16>(p.logits, int64_t(u) * p.ld, p.E, lane, next);
+    } else {
+      load_row<VPL, V, BF16>(p.logits, int64_t(t) * p.ld, p.E, lane, x);
     }
-    route_token<VPL, V, BF16, SIG>(p, t, lane, row, s, &total, &top);
+    if (p.mask != nullptr && p.mask[t] == 0)
+      route_masked(p, t, lane);
+    else
+      route_token<VPL, V, BF16, SIG>(p, t, lane, row, lists[warp], x, s, &total, &top);
+    if constexpr (kAhead<VPL>) {
+#pragma unroll
+      for (int r = 0; r < VPL; ++r) x[r] = next[r];
+    }
   }
 }
 
@@ -296,11 +447,13 @@ __global__ void __launch_bounds__(kRouteThreads) balance_kernel(RouteParams p) {
   extern __shared__ float smem[];
   float* probs = smem;                                         // [kRouteWarps][E]
   int* counts = reinterpret_cast<int*>(smem + kRouteWarps * p.E);   // [E]
+  __shared__ float2 lists[kRouteWarps][kCandidates];
   __shared__ float warp_z[kRouteWarps];
   __shared__ int warp_n[kRouteWarps];
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float* row = probs + warp * p.E;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.done = 0;
   for (int e = threadIdx.x; e < p.E; e += kRouteThreads) counts[e] = 0;
   __syncthreads();
   const int first = blockIdx.x * p.tokens_per_cta;
@@ -313,22 +466,36 @@ __global__ void __launch_bounds__(kRouteThreads) balance_kernel(RouteParams p) {
     int n = 0;
 #pragma unroll
     for (int r = 0; r < VPL; ++r) sum[r] = 0.0f;
-    for (int u = t + warp; u < end; u += kRouteWarps) {
+    float x[VPL], s[VPL], total, top;
+    int u = t + warp;
+    if (kAhead<VPL> && u < end) load_row<VPL, V, BF16>(p.logits, int64_t(u) * p.ld, p.E, lane, x);
+    for (; u < end; u += kRouteWarps) {
+      float next[VPL];
+      if constexpr (kAhead<VPL>) {
+        if (u + kRouteWarps < end)
+          load_row<VPL, V, BF16>(p.logits, int64_t(u + kRouteWarps) * p.ld, p.E, lane, next);
+      } else {
+        load_row<VPL, V, BF16>(p.logits, int64_t(u) * p.ld, p.E, lane, x);
+      }
       if (p.mask != nullptr && p.mask[u] == 0) {
         route_masked(p, u, lane);
-        continue;
-      }
-      float s[VPL], total, top;
-      const int mine = route_token<VPL, V, BF16, SIG>(p, u, lane, row, s, &total, &top);
-      if (mine >= 0) atomicAdd(&counts[mine], 1);
-      // total is 0 only where no expert is in service: the token adds nothing
-      const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+      } else {
+        const int mine =
+            route_token<VPL, V, BF16, SIG>(p, u, lane, row, lists[warp], x, s, &total, &top);
+        if (mine >= 0) atomicAdd(&counts[mine], 1);
+        // total is 0 only where no expert is in service: the token adds nothing
+        const float inv = total == 0.0f ? 0.0f : 1.0f / total;
 #pragma unroll
-      for (int r = 0; r < VPL; ++r) sum[r] += s[r] * inv;
-      ++n;
-      if (!SIG && total != 0.0f) {
-        const float lse = top + logf(total);
-        z += lse * lse;
+        for (int r = 0; r < VPL; ++r) sum[r] = fmaf(s[r], inv, sum[r]);
+        ++n;
+        if (!SIG && total != 0.0f) {
+          const float lse = top + logf(total);
+          z += lse * lse;
+        }
+      }
+      if constexpr (kAhead<VPL>) {
+#pragma unroll
+        for (int r = 0; r < VPL; ++r) x[r] = next[r];
       }
     }
     __syncwarp();
@@ -366,9 +533,12 @@ __global__ void __launch_bounds__(kRouteThreads) balance_kernel(RouteParams p) {
   }
 }
 
+constexpr int kSumRows = 16;
+constexpr int kSumThreads = 32 * kSumRows;
+
 struct BalanceParams {
   const int32_t* seq_start;
-  int T, E, K, B, tokens_per_cta, ctas;
+  int T, E, K, B, tokens_per_cta;
   const float* part_prob;
   const int32_t* part_count;
   const int32_t* part_tokens;
@@ -376,27 +546,38 @@ struct BalanceParams {
   int32_t* expert_count;   // [B, E]
   float* expert_prob;      // [B, E]
   int32_t* seq_tokens;     // [B + 2]
-  float* seq_loss;         // [B] workspace: sum over e of count * prob
-  float* seq_z;            // [B] workspace
+  float* dots;             // [B, gridDim.y]: sum over 32 experts of count * prob
+  float* seq_z;            // [B]
+  unsigned* done;          // CTAs that have finished
   float* loss;             // [2]
 };
 
-// Sum over a block of kRouteThreads, in a fixed order, in every thread.
-__device__ float block_sum(float v, float* scratch) {
-  v = warp_sum(v);
+// Sum over a block, in a fixed order, in every thread.  The block is whole
+// warps, at most 32 of them.
+template <typename T>
+__device__ T block_sum(T v, T* scratch) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(kFull, v, d);
   __syncthreads();
   if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
   __syncthreads();
-  float s = 0.0f;
-  for (int i = 0; i < kRouteWarps; ++i) s += scratch[i];
+  T s = T(0);
+  for (int i = 0; i < int(blockDim.x >> 5); ++i) s += scratch[i];
   return s;
 }
 
-// Second kernel: one CTA a sequence adds up its partial rows in order.
-__global__ void __launch_bounds__(kRouteThreads) balance_sum_kernel(BalanceParams p) {
-  __shared__ float scratch[kRouteWarps];
+// Second kernel: CTA (b, i) adds up the partial rows of sequence b for the
+// experts [32 i, 32 i + 32), 16 rows at a time, in a fixed order; the CTA
+// that finishes last forms the losses from what all have written.
+__global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(BalanceParams p) {
+  __shared__ float probs[kSumRows][33];
+  __shared__ int counts[kSumRows][33];
+  __shared__ float fscratch[32];
+  __shared__ int iscratch[32];
+  __shared__ bool is_last;
   pdl_wait();
-  const int b = blockIdx.x;
+  const int b = blockIdx.x, lane = threadIdx.x & 31, part = threadIdx.x >> 5;
+  const int e = blockIdx.y * 32 + lane;
   const int lo = b == 0 ? 0 : min(max(p.seq_start[b], 0), p.T);
   const int hi = b == p.B - 1 ? p.T : min(max(p.seq_start[b + 1], 0), p.T);
   int c0 = 0, c1 = 0;
@@ -404,59 +585,74 @@ __global__ void __launch_bounds__(kRouteThreads) balance_sum_kernel(BalanceParam
     c0 = lo / p.tokens_per_cta;
     c1 = (hi - 1) / p.tokens_per_cta + 1;
   }
-  int n = 0;
-  float z = 0.0f;
-  for (int c = c0; c < c1; ++c) {
+  float prob = 0.0f, z = 0.0f;
+  int count = 0, n = 0;
+  if (e < p.E) {
+    const float* fp = p.part_prob + int64_t(c0 + b) * p.E + e;
+    const int32_t* ip = p.part_count + int64_t(c0 + b) * p.E + e;
+#pragma unroll 8
+    for (int c = part; c < c1 - c0; c += kSumRows) {
+      prob += fp[int64_t(c) * p.E];
+      count += ip[int64_t(c) * p.E];
+    }
+  }
+  for (int c = c0 + threadIdx.x; c < c1; c += kSumThreads) {
     n += p.part_tokens[c + b];
     z += p.part_z[c + b];
   }
-  const float inv_n = n > 0 ? 1.0f / float(n) : 0.0f;
-  float dot = 0.0f;
-  for (int e = threadIdx.x; e < p.E; e += kRouteThreads) {
-    float prob = 0.0f;
-    int count = 0;
-    for (int c = c0; c < c1; ++c) {
-      prob += p.part_prob[int64_t(c + b) * p.E + e];
-      count += p.part_count[int64_t(c + b) * p.E + e];
+  probs[part][lane] = prob;
+  counts[part][lane] = count;
+  n = block_sum(n, iscratch);
+  z = block_sum(z, fscratch);
+  if (part == 0) {
+    prob = 0.0f;
+    count = 0;
+#pragma unroll
+    for (int r = 0; r < kSumRows; ++r) {
+      prob += probs[r][lane];
+      count += counts[r][lane];
     }
+    const float inv_n = n > 0 ? 1.0f / float(n) : 0.0f;
     prob *= inv_n;
-    p.expert_prob[int64_t(b) * p.E + e] = prob;
-    p.expert_count[int64_t(b) * p.E + e] = count;
-    dot += float(count) * inv_n * prob;
+    if (e < p.E) {
+      p.expert_prob[int64_t(b) * p.E + e] = prob;
+      p.expert_count[int64_t(b) * p.E + e] = count;
+    }
+    const float dot = warp_sum(float(count) * inv_n * prob);
+    if (lane == 0) {
+      p.dots[int64_t(b) * gridDim.y + blockIdx.y] = dot;
+      if (blockIdx.y == 0) {
+        p.seq_tokens[b] = n;
+        p.seq_z[b] = z;
+      }
+      __threadfence();
+      is_last = atomicAdd(p.done, 1u) == gridDim.x * gridDim.y - 1;
+    }
   }
-  dot = block_sum(dot, scratch);
-  if (threadIdx.x == 0) {
-    p.seq_tokens[b] = n;
-    p.seq_loss[b] = dot * (float(p.E) / float(p.K));
-    p.seq_z[b] = z;
-  }
-}
-
-// Third kernel: the losses over all sequences.
-__global__ void __launch_bounds__(kRouteThreads) balance_loss_kernel(BalanceParams p) {
-  __shared__ float scratch[kRouteWarps];
-  pdl_wait();
-  float loss = 0.0f, z = 0.0f;
-  int n = 0, full = 0;
-  for (int b = threadIdx.x; b < p.B; b += kRouteThreads) {
-    loss += p.seq_loss[b];
-    z += p.seq_z[b];
-    n += p.seq_tokens[b];
-    full += p.seq_tokens[b] > 0 ? 1 : 0;
-  }
-  loss = block_sum(loss, scratch);
-  z = block_sum(z, scratch);
-  __shared__ int totals[2];
-  if (threadIdx.x < 2) totals[threadIdx.x] = 0;
   __syncthreads();
-  atomicAdd(&totals[0], n);
-  atomicAdd(&totals[1], full);
-  __syncthreads();
+  if (!is_last) return;
+  __threadfence();
+  float loss = 0.0f;
+  int full = 0;
+  n = 0;
+  z = 0.0f;
+  for (int64_t i = threadIdx.x; i < int64_t(p.B) * gridDim.y; i += kSumThreads)
+    loss += __ldcg(p.dots + i);
+  for (int i = threadIdx.x; i < p.B; i += kSumThreads) {
+    const int m = __ldcg(p.seq_tokens + i);
+    n += m;
+    full += m > 0 ? 1 : 0;
+    z += __ldcg(p.seq_z + i);
+  }
+  loss = block_sum(loss, fscratch);
+  z = block_sum(z, fscratch);
+  n = block_sum(n, iscratch);
+  full = block_sum(full, iscratch);
   if (threadIdx.x == 0) {
-    p.seq_tokens[p.B] = totals[0];
-    p.seq_tokens[p.B + 1] = totals[1];
-    p.loss[0] = totals[1] > 0 ? loss / float(totals[1]) : 0.0f;
-    p.loss[1] = totals[0] > 0 ? z / float(totals[0]) : 0.0f;
+    p.seq_tokens[p.B] = n;
+    p.seq_tokens[p.B + 1] = full;
+    p.loss[0] = full > 0 ? loss * (float(p.E) / float(p.K)) / float(full) : 0.0f;
+    p.loss[1] = n > 0 ? z / float(n) : 0.0f;
   }
 }
 
@@ -567,7 +763,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_backward_kernel(RouteBack
       }
       if (mine >= 0) {
         const float l = load_one<BF16>(p.logits, int64_t(t) * p.ld + mine);
-        sk = SIG ? sigmoid(l) : expf(l - top) * inv;
+        sk = SIG ? sigmoid(l) : soft_score(l, top) * inv;
         ds = p.grad_w[int64_t(t) * p.K + lane] * p.scale;
       }
       if (p.renorm) {
@@ -631,11 +827,12 @@ bool router_ok(const ep_router_config* c) {
 
 constexpr int kMaxSequences = 1 << 20;
 
-// CTAs of the per-token kernels over `tokens` tokens: at most eight an SM
-// (2048 threads), each warp with a token at least.
+// CTAs of the per-token kernels over `tokens` tokens: at most four an SM
+// (32 warps), each warp with a token at least.
+constexpr int kRouteCtasPerSm = 4;
 int route_ctas(int tokens) {
   const int want = (tokens + kRouteWarps - 1) / kRouteWarps;
-  const int most = device_info().sm_count * 8;
+  const int most = device_info().sm_count * kRouteCtasPerSm;
   return want < most ? want : most;
 }
 
@@ -644,7 +841,7 @@ int route_ctas(int tokens) {
 // those; narrow rows keep more lanes busy with single loads.
 template <typename F>
 cudaError_t with_shape(int E, int64_t ld, bool bf16, bool sig, F&& f) {
-  const bool vec = E >= 128 && E % 4 == 0 && ld % 4 == 0;
+  const bool vec = E >= 128 && E <= 512 && E % 4 == 0 && ld % 4 == 0;
   int vpl = vec ? 4 : 1;
   while (vpl * 32 < E) vpl *= 2;
 #define EP_SHAPE(N, W)                                                    \
@@ -656,7 +853,7 @@ cudaError_t with_shape(int E, int64_t ld, bool bf16, bool sig, F&& f) {
   }
   EP_SHAPE(1, 1) EP_SHAPE(2, 1) EP_SHAPE(4, 1) EP_SHAPE(8, 1) EP_SHAPE(16, 1)
   EP_SHAPE(32, 1) EP_SHAPE(64, 1)
-  EP_SHAPE(4, 4) EP_SHAPE(8, 4) EP_SHAPE(16, 4) EP_SHAPE(32, 4) EP_SHAPE(64, 4)
+  EP_SHAPE(4, 4) EP_SHAPE(8, 4) EP_SHAPE(16, 4)
 #undef EP_SHAPE
   return cudaErrorInvalidValue;
 }
@@ -715,19 +912,23 @@ int run_length(int T) {
   return ctas > 0 ? (T + ctas - 1) / ctas : 1;
 }
 
+// CTAs of the second kernel along the experts.
+int sum_ctas(int E) { return (E + 31) / 32; }
+
 struct BalanceWorkspace {
   float* prob;
   int32_t* count;
   int32_t* tokens;
   float* z;
-  float* seq_loss;
+  float* dots;
   float* seq_z;
+  unsigned* done;
   int64_t bytes;
 };
 
-// ctas <= sm_count * 8, so that the size does not depend on T.
+// ctas <= sm_count * kRouteCtasPerSm, so that the size does not depend on T.
 BalanceWorkspace carve(void* base, int E, int B) {
-  const int64_t rows = int64_t(device_info().sm_count) * 8 + B;
+  const int64_t rows = int64_t(device_info().sm_count) * kRouteCtasPerSm + B;
   char* at = static_cast<char*>(base);
   auto take = [&](int64_t n) {
     char* p = at;
@@ -739,7 +940,8 @@ BalanceWorkspace carve(void* base, int E, int B) {
   w.count = reinterpret_cast<int32_t*>(take(rows * E));
   w.tokens = reinterpret_cast<int32_t*>(take(rows));
   w.z = reinterpret_cast<float*>(take(rows));
-  w.seq_loss = reinterpret_cast<float*>(take(B));
+  w.dots = reinterpret_cast<float*>(take(int64_t(B) * sum_ctas(E)));
+  w.done = reinterpret_cast<unsigned*>(take(1));
   w.seq_z = reinterpret_cast<float*>(take(B));
   w.bytes = at - static_cast<char*>(base);
   return w;
@@ -825,11 +1027,11 @@ int32_t ep_route_balance(const ep_router_config* cfg, int32_t num_tokens, const 
   l.p.part_count = w.count;
   l.p.part_tokens = w.tokens;
   l.p.part_z = w.z;
-  if (num_tokens > 0) {
-    const cudaError_t e = with_shape(l.p.E, ld_logits, cfg->logits_bf16 != 0,
-                                     cfg->score == EP_SCORE_SIGMOID, l);
-    if (note_cuda(e) != cudaSuccess) return EP_ERR_CUDA;
-  }
+  l.p.done = w.done;
+  if (l.p.ctas == 0) l.p.ctas = 1;      // no tokens: `done` is still cleared
+  cudaError_t e = with_shape(l.p.E, ld_logits, cfg->logits_bf16 != 0,
+                             cfg->score == EP_SCORE_SIGMOID, l);
+  if (note_cuda(e) != cudaSuccess) return EP_ERR_CUDA;
   BalanceParams q;
   q.seq_start = d_seq_start;
   q.T = num_tokens;
@@ -837,7 +1039,6 @@ int32_t ep_route_balance(const ep_router_config* cfg, int32_t num_tokens, const 
   q.K = l.p.K;
   q.B = num_seqs;
   q.tokens_per_cta = l.p.tokens_per_cta;
-  q.ctas = l.p.ctas;
   q.part_prob = w.prob;
   q.part_count = w.count;
   q.part_tokens = w.tokens;
@@ -845,14 +1046,12 @@ int32_t ep_route_balance(const ep_router_config* cfg, int32_t num_tokens, const 
   q.expert_count = d_expert_count;
   q.expert_prob = d_expert_prob;
   q.seq_tokens = d_seq_tokens;
-  q.seq_loss = w.seq_loss;
+  q.dots = w.dots;
   q.seq_z = w.seq_z;
+  q.done = w.done;
   q.loss = d_loss;
-  cudaError_t e = launch_pdl(balance_sum_kernel, dim3(num_seqs), dim3(kRouteThreads), 0,
-                             l.stream, q);
-  if (e == cudaSuccess)
-    e = launch_pdl(balance_loss_kernel, dim3(1), dim3(kRouteThreads), 0, l.stream, q);
-  return status(e);
+  return status(launch_pdl(balance_sum_kernel, dim3(num_seqs, sum_ctas(q.E)), dim3(kSumThreads), 0,
+                           l.stream, q));
 }
 
 int32_t ep_route_backward(const ep_router_config* cfg, int32_t num_tokens, const void* d_logits,

@@ -557,7 +557,7 @@ EP_API int64_t ep_route_workspace_bytes(const ep_router_config *cfg, int32_t num
 
 /* ep_route together with the balance statistics and losses of its tokens.
  *
- * The tokens form num_seqs sequences: d_seq_start (device int32 [B + 1],
+ * The tokens form num_seqs (B in [1, 2^20]) sequences: d_seq_start (device int32 [B + 1],
  * NULL when B = 1) ascends from 0 to T, sequence b owns tokens
  * [seq_start[b], seq_start[b+1]) and may be empty.  Masked tokens count
  * nowhere.  With n_b the tokens of sequence b, c_be their selections of
