@@ -12,6 +12,8 @@
 #include <cuda_runtime.h>
 #include <math_constants.h>
 
+#include <type_traits>
+
 #include "../../include/ep.h"
 #include "ep_device.cuh"
 #include "ep_internal.h"
@@ -136,33 +138,41 @@ __device__ __forceinline__ float soft_score(float l, float top) {
   return fast_exp2((l - top) * kLog2e);
 }
 
-// Scores of a token: s = exp(x - max) (softmax, before its division by the
-// total) or sigmoid(x).  Returns their total over the experts and the row's
-// maximum in *top.  -inf scores 0; a row of nothing else scores 0 throughout.
+// Softmax scores of a token before their division: s = exp(x - top), top the
+// row's maximum; returns their total.  -inf scores 0, and so does all of a
+// row of nothing else.
+template <int VPL>
+__device__ __forceinline__ float soft_scores(const float (&x)[VPL], float (&s)[VPL], float top) {
+  const float base = top == -CUDART_INF_F ? 0.0f : top;
+  float total = 0.0f;
+#pragma unroll
+  for (int r = 0; r < VPL; ++r) {
+    s[r] = soft_score(x[r], base);
+    total += s[r];
+  }
+  return warp_sum(total);
+}
+
+// Scores of a token as soft_scores or sigmoid has them, their total, and
+// (softmax) the row's maximum.
 template <int VPL, bool SIG>
 __device__ __forceinline__ float scores(const float (&x)[VPL], float (&s)[VPL], float* top) {
-  float total = 0.0f;
   if constexpr (SIG) {
+    float total = 0.0f;
 #pragma unroll
     for (int r = 0; r < VPL; ++r) {
       s[r] = sigmoid(x[r]);      // exp2(+inf) = inf, its reciprocal 0
       total += s[r];
     }
     *top = 0.0f;
+    return warp_sum(total);
   } else {
     float m = x[0];
 #pragma unroll
     for (int r = 1; r < VPL; ++r) m = fmaxf(m, x[r]);
-    m = warp_max(m);
-    *top = m;
-    const float base = m == -CUDART_INF_F ? 0.0f : m;
-#pragma unroll
-    for (int r = 0; r < VPL; ++r) {
-      s[r] = soft_score(x[r], base);
-      total += s[r];
-    }
+    *top = warp_max(m);
+    return soft_scores<VPL>(x, s, *top);
   }
-  return warp_sum(total);
 }
 
 // The `kept` best of G groups (G <= 32) by the scores that lanes g < G hold,
@@ -251,18 +261,11 @@ __device__ void keep_groups(float (&c)[VPL], float* row, int E, int G, int kept,
   __syncwarp();
 }
 
-// A lane's share of a token's choice: expert e takes rank `rank`, its choice
-// score is c; e = -1 where a rank stays empty or the lane has nothing.
-struct Chosen {
-  int e, rank;
-  float c;
-};
-
-// The K largest of a warp's choice scores, one after another: any number of
-// equal ones.
+// The K largest of a warp's choice scores one after another, equal ones by
+// ascending index: lane k returns the k-th expert or -1.
 template <int VPL, int V>
-__device__ __noinline__ Chosen choose_in_turn(float (&c)[VPL], int K, int lane) {
-  Chosen mine = {-1, lane, 0.0f};
+__device__ __noinline__ int choose_in_turn(float (&c)[VPL], int K, int lane) {
+  int mine = -1;
   for (int k = 0; k < K; ++k) {
     float best = -CUDART_INF_F;
     int at = 0x7fffffff;
@@ -279,108 +282,179 @@ __device__ __noinline__ Chosen choose_in_turn(float (&c)[VPL], int K, int lane) 
 #pragma unroll
     for (int r = 0; r < VPL; ++r)
       if (element_of<V>(r, lane) == win) c[r] = -CUDART_INF_F;
-    if (lane == k) mine = {win, k, top};
+    if (lane == k) mine = win;
   }
   return mine;
 }
 
-constexpr int kCandidates = 32;
+// A set of the registers 0 .. VPL - 1.
+template <int VPL>
+struct RegisterSet {
+  using Bits = std::conditional_t<(VPL > 32), unsigned long long, uint32_t>;
+  Bits bits = 0;
+  __device__ __forceinline__ void add(int r, bool in) { bits |= in ? Bits(1) << r : Bits(0); }
+  __device__ __forceinline__ int first() const {
+    if constexpr (VPL > 32) return __ffsll(bits) - 1;
+    return __ffs(bits) - 1;
+  }
+  __device__ __forceinline__ void drop_first() { bits &= bits - 1; }
+};
 
-// The K largest of a warp's choice scores, equal ones by ascending index.
-// The K-th largest of the lanes' maxima (each distinct value counted once)
-// is a bound that at least K scores reach, and with scores spread over the
-// lanes few more do: those go to shared memory, one a lane, where each counts
-// the ones before it.  `best` is the lane's maximum; -inf and NaN are not
-// chosen.
-template <int VPL, int V>
-__device__ __forceinline__ Chosen choose(float (&c)[VPL], float best, int K, int lane,
-                                         float2* list) {
+// What a warp's lanes share while they choose: candidates, one a lane.
+struct Candidates {
+  int expert[32];
+  unsigned long long key[32];
+};
+
+// Order of choice as one number: the higher score first, then the lower
+// index.  -0 and +0 are equal scores.
+__device__ __forceinline__ unsigned long long choice_key(float c, int e) {
+  const uint32_t u = __float_as_uint(c + 0.0f);
+  const uint32_t hi = u ^ (uint32_t(int32_t(u) >> 31) | 0x80000000u);
+  return static_cast<unsigned long long>(hi) << 32 | uint32_t(~e);
+}
+
+// A lane's share of a token's choice: expert e, with logit l, takes `rank`;
+// e = -1 where the rank stays empty, rank >= K where the lane has none.
+struct Chosen {
+  int e, rank;
+  float l;
+};
+
+// Chooses the K largest of a warp's choice scores c, `best` the lane's
+// largest; -inf and NaN are never chosen.  The K-th largest of the lanes'
+// largest (equal ones taken together) is a bound that at least K scores
+// reach, where K can be chosen at all; with scores spread over the lanes few
+// more do.  Those become candidates, one a lane, that each count the
+// candidates before them.  More than 32 candidates (many equal scores, K
+// near 32) are chosen in turn.
+template <int VPL, int V, bool BF16, bool SIG>
+__device__ __forceinline__ Chosen choose(const RouteParams& p, const float (&c)[VPL], float best,
+                                         const void* logits, int64_t offset, int lane,
+                                         Candidates& cand) {
   float bound = -CUDART_INF_F;
-  for (int k = 0; k < K; ++k) {
+#pragma unroll 4
+  for (int k = 0; k < p.K; ++k) {
     bound = warp_max(best);
     best = best == bound ? -CUDART_INF_F : best;
   }
   bound = fmaxf(bound, -3.402823466e38f);
+  RegisterSet<VPL> mine;
+#pragma unroll
+  for (int r = 0; r < VPL; ++r) mine.add(r, c[r] >= bound);
   const uint32_t before = lanemask_lt();
   int n = 0;
-#pragma unroll
-  for (int r = 0; r < VPL; ++r) {
-    const bool in = c[r] >= bound;
-    const uint32_t who = __ballot_sync(kFull, in);
-    if (in) {
-      const int at = n + __popc(who & before);
-      if (at < kCandidates)
-        list[at] = make_float2(c[r], __int_as_float(element_of<V>(r, lane)));
-    }
+  for (;;) {
+    const uint32_t who = __ballot_sync(kFull, mine.bits != 0);
+    if (who == 0) break;
+    const int at = n + __popc(who & before);
+    if (mine.bits != 0 && at < 32) cand.expert[at] = element_of<V>(mine.first(), lane);
+    mine.drop_first();
     n += __popc(who);
   }
   __syncwarp();
-  if (n > kCandidates) {
+  Chosen out = {-1, lane, 0.0f};
+  if (n > 32) {
     float left[VPL];      // a copy: c itself then stays in registers
 #pragma unroll
     for (int r = 0; r < VPL; ++r) left[r] = c[r];
-    return choose_in_turn<VPL, V>(left, K, lane);
+    out.e = choose_in_turn<VPL, V>(left, p.K, lane);
+    if (out.e >= 0) out.l = load_one<BF16>(logits, offset + out.e);
+    return out;
   }
-  Chosen mine = {-1, lane, 0.0f};
+  unsigned long long key = 0;
   if (lane < n) {
-    const float2 m = list[lane];
-    mine.c = m.x;
-    mine.e = __float_as_int(m.y);
-    mine.rank = 0;
+    out.e = cand.expert[lane];
+    out.l = load_one<BF16>(logits, offset + out.e);
+    float score = out.l;
+    if constexpr (SIG) score = sigmoid(out.l) + (p.bias != nullptr ? p.bias[out.e] : 0.0f);
+    key = choice_key(score, out.e);
   }
-  for (int i = 0; i < n; ++i) {
-    const float2 o = list[i];
-    const bool ahead = o.x > mine.c || (o.x == mine.c && __float_as_int(o.y) < mine.e);
-    if (lane < n && ahead) ++mine.rank;
+  cand.key[lane] = key;      // the rest come after any candidate
+  __syncwarp();
+  int rank = 0;
+  for (int i = 0; i < n; i += 4) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) rank += cand.key[i + j] > key ? 1 : 0;
   }
   __syncwarp();
-  if (lane < n && mine.rank >= K) mine.e = -1;
-  return mine;
+  if (lane < n) out.rank = rank;
+  return out;
 }
 
-// One token, given its logits: choice and gate weights; leaves the scores in
-// `s`.  Returns the lane's chosen expert or -1.
-template <int VPL, int V, bool BF16, bool SIG>
-__device__ __forceinline__ int route_token(const RouteParams& p, int t, int lane, float* row,
-                                           float2* list, const float (&x)[VPL], float (&s)[VPL],
-                                           float* total, float* top) {
-  *total = scores<VPL, SIG>(x, s, top);
-  float c[VPL];
+// The choice bias in registers, where a warp keeps it over its tokens.
+template <int VPL, int V>
+__device__ __forceinline__ void load_bias(const RouteParams& p, int lane, float (&bias)[VPL]) {
 #pragma unroll
   for (int r = 0; r < VPL; ++r) {
-    c[r] = x[r];
-    if constexpr (SIG) {
-      const int e = element_of<V>(r, lane);
-      const float b = p.bias != nullptr && e < p.E ? p.bias[e] : 0.0f;
-      c[r] = x[r] == -CUDART_INF_F ? -CUDART_INF_F : s[r] + b;
+    const int e = element_of<V>(r, lane);
+    bias[r] = p.bias != nullptr && e < p.E ? p.bias[e] : 0.0f;
+  }
+}
+
+// One token, given its logits: choice and gate weights.  Leaves the scores in
+// `s` with their total and the row's maximum; softmax needs those only for
+// statistics (STATS) or for weights that are not renormalised.  Returns the
+// lane's chosen expert or -1.
+template <int VPL, int V, bool BF16, bool SIG, bool STATS>
+__device__ __forceinline__ int route_token(const RouteParams& p, int t, int lane, float* row,
+                                           Candidates& cand, const float (&bias)[VPL],
+                                           const float (&x)[VPL], float (&s)[VPL], float* total,
+                                           float* top) {
+  float best, scale = p.scale;
+  const int64_t offset = int64_t(t) * p.ld;
+  Chosen mine;
+  if constexpr (SIG) {
+    *total = scores<VPL, SIG>(x, s, top);
+    float c[VPL];
+#pragma unroll
+    for (int r = 0; r < VPL; ++r) c[r] = x[r] == -CUDART_INF_F ? -CUDART_INF_F : s[r] + bias[r];
+    if (p.G > 1) keep_groups<VPL, V, SIG>(c, row, p.E, p.G, p.kept, lane);
+    best = c[0];
+#pragma unroll
+    for (int r = 1; r < VPL; ++r) best = fmaxf(best, c[r]);
+    mine = choose<VPL, V, BF16, SIG>(p, c, best, p.logits, offset, lane, cand);
+  } else {
+    best = x[0];
+#pragma unroll
+    for (int r = 1; r < VPL; ++r) best = fmaxf(best, x[r]);
+    *top = warp_max(best);
+    if (STATS || !p.renorm) {
+      *total = soft_scores<VPL>(x, s, *top);
+      if (!p.renorm) scale = scale / *total;
+      if (*total != *total) scale = *total;
+    } else {
+      bool nan = false;
+#pragma unroll
+      for (int r = 0; r < VPL; ++r) nan |= x[r] != x[r];
+      if (__any_sync(kFull, nan)) scale = CUDART_NAN_F;
+    }
+    if (p.G > 1) {
+      float c[VPL];
+#pragma unroll
+      for (int r = 0; r < VPL; ++r) c[r] = x[r];
+      keep_groups<VPL, V, SIG>(c, row, p.E, p.G, p.kept, lane);
+      best = c[0];
+#pragma unroll
+      for (int r = 1; r < VPL; ++r) best = fmaxf(best, c[r]);
+      mine = choose<VPL, V, BF16, SIG>(p, c, best, p.logits, offset, lane, cand);
+    } else {
+      mine = choose<VPL, V, BF16, SIG>(p, x, best, p.logits, offset, lane, cand);
     }
   }
-  if (p.G > 1) keep_groups<VPL, V, SIG>(c, row, p.E, p.G, p.kept, lane);
-  float best = c[0];
-#pragma unroll
-  for (int r = 1; r < VPL; ++r) best = fmaxf(best, c[r]);
-  const Chosen mine = choose<VPL, V>(c, best, p.K, lane, list);
+  const bool taken = mine.e >= 0 && mine.rank < p.K;
   float w = 0.0f;
-  if (mine.e >= 0) {
-    // softmax: the choice score is the logit; sigmoid: it has the bias in it
-    w = SIG ? sigmoid(load_one<BF16>(p.logits, int64_t(t) * p.ld + mine.e))
-            : soft_score(mine.c, *top);
-  }
-  float scale = p.scale;
+  if (taken) w = SIG ? sigmoid(mine.l) : soft_score(mine.l, *top);
   if (p.renorm) {
     const float sum = warp_sum(w);
     scale = sum == 0.0f ? 0.0f : scale / sum;
-    // softmax scores of a row with a NaN are all NaN
-    if (!SIG && *total != *total) scale = *total;
-  } else if (!SIG) {
-    scale /= *total;
   }
   if (mine.rank < p.K) {
     const int64_t at = int64_t(t) * p.K + mine.rank;
     p.idx[at] = mine.e;
-    p.w[at] = mine.e >= 0 ? w * scale : 0.0f;
+    p.w[at] = taken ? w * scale : 0.0f;
   }
-  return mine.e;
+  return taken ? mine.e : -1;
 }
 
 __device__ __forceinline__ void route_masked(const RouteParams& p, int t, int lane) {
@@ -398,12 +472,13 @@ constexpr bool kAhead = VPL <= 16;
 template <int VPL, int V, bool BF16, bool SIG>
 __global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteParams p) {
   extern __shared__ float smem[];
-  __shared__ float2 lists[kRouteWarps][kCandidates];
+  __shared__ Candidates cands[kRouteWarps];
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float* row = smem + warp * p.E;
   const int stride = gridDim.x * kRouteWarps;
-  float x[VPL], s[VPL], total, top;
+  float x[VPL], s[VPL], bias[VPL], total, top;
+  load_bias<VPL, V>(p, lane, bias);
   int t = blockIdx.x * kRouteWarps + warp;
   if (kAhead<VPL> && t < p.T) load_row<VPL, V, BF16>(p.logits, int64_t(t) * p.ld, p.E, lane, x);
   for (; t < p.T; t += stride) {
@@ -417,7 +492,8 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteParams p) {
     if (p.mask != nullptr && p.mask[t] == 0)
       route_masked(p, t, lane);
     else
-      route_token<VPL, V, BF16, SIG>(p, t, lane, row, lists[warp], x, s, &total, &top);
+      route_token<VPL, V, BF16, SIG, false>(p, t, lane, row, cands[warp], bias, x, s, &total,
+                                            &top);
     if constexpr (kAhead<VPL>) {
 #pragma unroll
       for (int r = 0; r < VPL; ++r) x[r] = next[r];
@@ -447,7 +523,7 @@ __global__ void __launch_bounds__(kRouteThreads) balance_kernel(RouteParams p) {
   extern __shared__ float smem[];
   float* probs = smem;                                         // [kRouteWarps][E]
   int* counts = reinterpret_cast<int*>(smem + kRouteWarps * p.E);   // [E]
-  __shared__ float2 lists[kRouteWarps][kCandidates];
+  __shared__ Candidates cands[kRouteWarps];
   __shared__ float warp_z[kRouteWarps];
   __shared__ int warp_n[kRouteWarps];
   pdl_wait();
@@ -458,6 +534,8 @@ __global__ void __launch_bounds__(kRouteThreads) balance_kernel(RouteParams p) {
   __syncthreads();
   const int first = blockIdx.x * p.tokens_per_cta;
   const int last = min(p.T, first + p.tokens_per_cta);
+  float bias[VPL];
+  load_bias<VPL, V>(p, lane, bias);
   int b = p.B > 1 ? sequence_of(p.seq_start, p.B, first) : 0;
   for (int t = first; t < last;) {
     while (b < p.B - 1 && p.seq_start[b + 1] <= t) ++b;
@@ -480,16 +558,16 @@ __global__ void __launch_bounds__(kRouteThreads) balance_kernel(RouteParams p) {
       if (p.mask != nullptr && p.mask[u] == 0) {
         route_masked(p, u, lane);
       } else {
-        const int mine =
-            route_token<VPL, V, BF16, SIG>(p, u, lane, row, lists[warp], x, s, &total, &top);
+        const int mine = route_token<VPL, V, BF16, SIG, true>(p, u, lane, row, cands[warp], bias,
+                                                              x, s, &total, &top);
         if (mine >= 0) atomicAdd(&counts[mine], 1);
         // total is 0 only where no expert is in service: the token adds nothing
-        const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+        const float inv = total == 0.0f ? 0.0f : fast_reciprocal(total);
 #pragma unroll
         for (int r = 0; r < VPL; ++r) sum[r] = fmaf(s[r], inv, sum[r]);
         ++n;
         if (!SIG && total != 0.0f) {
-          const float lse = top + logf(total);
+          const float lse = top + __logf(total);
           z += lse * lse;
         }
       }
@@ -533,8 +611,9 @@ __global__ void __launch_bounds__(kRouteThreads) balance_kernel(RouteParams p) {
   }
 }
 
-constexpr int kSumRows = 16;
-constexpr int kSumThreads = 32 * kSumRows;
+constexpr int kSumExperts = 8;       // of a CTA of the second kernel: a 32-byte sector of a row
+constexpr int kSumRows = 32;         // partial rows it adds at a time
+constexpr int kSumThreads = kSumExperts * kSumRows;
 
 struct BalanceParams {
   const int32_t* seq_start;
@@ -546,7 +625,7 @@ struct BalanceParams {
   int32_t* expert_count;   // [B, E]
   float* expert_prob;      // [B, E]
   int32_t* seq_tokens;     // [B + 2]
-  float* dots;             // [B, gridDim.y]: sum over 32 experts of count * prob
+  float* dots;             // [B, gridDim.y]: a CTA's sum of count * prob / n
   float* seq_z;            // [B]
   unsigned* done;          // CTAs that have finished
   float* loss;             // [2]
@@ -567,17 +646,17 @@ __device__ T block_sum(T v, T* scratch) {
 }
 
 // Second kernel: CTA (b, i) adds up the partial rows of sequence b for the
-// experts [32 i, 32 i + 32), 16 rows at a time, in a fixed order; the CTA
-// that finishes last forms the losses from what all have written.
+// experts from kSumExperts i on, kSumRows rows at a time, in a fixed order;
+// the CTA that finishes last forms the losses from what all have written.
 __global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(BalanceParams p) {
-  __shared__ float probs[kSumRows][33];
-  __shared__ int counts[kSumRows][33];
+  __shared__ float probs[kSumRows][kSumExperts];
+  __shared__ int counts[kSumRows][kSumExperts];
   __shared__ float fscratch[32];
   __shared__ int iscratch[32];
   __shared__ bool is_last;
   pdl_wait();
-  const int b = blockIdx.x, lane = threadIdx.x & 31, part = threadIdx.x >> 5;
-  const int e = blockIdx.y * 32 + lane;
+  const int b = blockIdx.x, lane = threadIdx.x % kSumExperts, part = threadIdx.x / kSumExperts;
+  int e = blockIdx.y * kSumExperts + lane;
   const int lo = b == 0 ? 0 : min(max(p.seq_start[b], 0), p.T);
   const int hi = b == p.B - 1 ? p.T : min(max(p.seq_start[b + 1], 0), p.T);
   int c0 = 0, c1 = 0;
@@ -604,22 +683,25 @@ __global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(BalanceParams 
   counts[part][lane] = count;
   n = block_sum(n, iscratch);
   z = block_sum(z, fscratch);
-  if (part == 0) {
+  if (threadIdx.x < 32) {      // lanes from kSumExperts on add nothing
     prob = 0.0f;
     count = 0;
-#pragma unroll
-    for (int r = 0; r < kSumRows; ++r) {
-      prob += probs[r][lane];
-      count += counts[r][lane];
-    }
+    e = blockIdx.y * kSumExperts + threadIdx.x;
     const float inv_n = n > 0 ? 1.0f / float(n) : 0.0f;
-    prob *= inv_n;
-    if (e < p.E) {
-      p.expert_prob[int64_t(b) * p.E + e] = prob;
-      p.expert_count[int64_t(b) * p.E + e] = count;
+    if (threadIdx.x < kSumExperts) {
+#pragma unroll
+      for (int r = 0; r < kSumRows; ++r) {
+        prob += probs[r][threadIdx.x];
+        count += counts[r][threadIdx.x];
+      }
+      prob *= inv_n;
+      if (e < p.E) {
+        p.expert_prob[int64_t(b) * p.E + e] = prob;
+        p.expert_count[int64_t(b) * p.E + e] = count;
+      }
     }
     const float dot = warp_sum(float(count) * inv_n * prob);
-    if (lane == 0) {
+    if (threadIdx.x == 0) {
       p.dots[int64_t(b) * gridDim.y + blockIdx.y] = dot;
       if (blockIdx.y == 0) {
         p.seq_tokens[b] = n;
@@ -722,86 +804,121 @@ __global__ void __launch_bounds__(kRouteThreads) route_backward_kernel(RouteBack
     dlse = n > 0 ? p.grad_loss[1] * 2.0f / float(n) : 0.0f;
   }
   int b = -1;
-  for (int t = first + warp; t < last; t += kRouteWarps) {
+  // a token's logits, choice and gate gradient are loaded a token ahead
+  float x[VPL], s[VPL], top, dw = 0.0f;
+  int64_t choice = -1;
+  const bool selects = p.grad_w != nullptr && lane < p.K;
+  const auto load_choice = [&](int t, int64_t& e, float& g) {
+    e = p.idx[int64_t(t) * p.K + lane];
+    g = p.grad_w[int64_t(t) * p.K + lane];
+  };
+  int t = first + warp;
+  if (t < last) {
+    if constexpr (kAhead<VPL>) load_row<VPL, V, BF16>(p.logits, int64_t(t) * p.ld, p.E, lane, x);
+    if (selects) load_choice(t, choice, dw);
+  }
+  for (; t < last; t += kRouteWarps) {
+    float next[VPL], next_dw = 0.0f;
+    int64_t next_choice = -1;
+    if (t + kRouteWarps < last) {
+      if constexpr (kAhead<VPL>)
+        load_row<VPL, V, BF16>(p.logits, int64_t(t + kRouteWarps) * p.ld, p.E, lane, next);
+      if (selects) load_choice(t + kRouteWarps, next_choice, next_dw);
+    }
+    if constexpr (!kAhead<VPL>)
+      load_row<VPL, V, BF16>(p.logits, int64_t(t) * p.ld, p.E, lane, x);
     float g[VPL];
-    const int64_t out = int64_t(t) * p.ld_grad;
     if (p.mask != nullptr && p.mask[t] == 0) {
 #pragma unroll
       for (int r = 0; r < VPL; ++r) g[r] = 0.0f;
-      store_row<VPL, V, BF16>(p.grad, out, p.E, lane, g);
-      continue;
-    }
-    if (losses) {
-      const int was = b;
-      if (b < 0)
-        b = p.B > 1 ? sequence_of(p.seq_start, p.B, t) : 0;
-      else
-        while (b < p.B - 1 && p.seq_start[b + 1] <= t) ++b;
-      if (b != was) {
-        const int n = p.seq_tokens[b], full = p.seq_tokens[p.B + 1];
-        const float each = n > 0 && full > 0 ? p.grad_loss[0] * (float(p.E) / float(p.K)) /
-                                                   (float(n) * float(n) * float(full))
-                                             : 0.0f;
+    } else {
+      if (losses) {
+        const int was = b;
+        if (b < 0)
+          b = p.B > 1 ? sequence_of(p.seq_start, p.B, t) : 0;
+        else
+          while (b < p.B - 1 && p.seq_start[b + 1] <= t) ++b;
+        if (b != was) {
+          const int n = p.seq_tokens[b], full = p.seq_tokens[p.B + 1];
+          const float each = n > 0 && full > 0 ? p.grad_loss[0] * (float(p.E) / float(p.K)) /
+                                                     (float(n) * float(n) * float(full))
+                                               : 0.0f;
 #pragma unroll
-        for (int r = 0; r < VPL; ++r) {
-          const int e = element_of<V>(r, lane);
-          dq[r] = e < p.E ? each * float(p.expert_count[int64_t(b) * p.E + e]) : 0.0f;
+          for (int r = 0; r < VPL; ++r) {
+            const int e = element_of<V>(r, lane);
+            dq[r] = e < p.E ? each * float(p.expert_count[int64_t(b) * p.E + e]) : 0.0f;
+          }
         }
       }
-    }
-    float x[VPL], s[VPL], top;
-    load_row<VPL, V, BF16>(p.logits, int64_t(t) * p.ld, p.E, lane, x);
-    const float total = scores<VPL, SIG>(x, s, &top);
-    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-    // gate weights: lane k holds selection k
-    int mine = -1;
-    float ds = 0.0f, sk = 0.0f;
-    if (p.grad_w != nullptr) {
-      if (lane < p.K) {
-        const int64_t e = p.idx[int64_t(t) * p.K + lane];
-        mine = e >= 0 && e < p.E ? int(e) : -1;
-      }
-      if (mine >= 0) {
-        const float l = load_one<BF16>(p.logits, int64_t(t) * p.ld + mine);
-        sk = SIG ? sigmoid(l) : soft_score(l, top) * inv;
-        ds = p.grad_w[int64_t(t) * p.K + lane] * p.scale;
-      }
-      if (p.renorm) {
-        const float sum = warp_sum(sk);
-        const float is = sum == 0.0f ? 0.0f : 1.0f / sum;
-        const float mean = warp_sum(ds * sk) * is;
-        if (mine >= 0) ds = (ds - mean) * is;
-      }
-      if (mine >= 0) row[mine] = ds;
-      __syncwarp();
-    }
-    float dot = 0.0f;
+      // gate weights: lane k holds selection k
+      const int mine = choice >= 0 && choice < p.E ? int(choice) : -1;
+      const float l = mine >= 0 ? load_one<BF16>(p.logits, int64_t(t) * p.ld + mine) : 0.0f;
+      const float total = scores<VPL, SIG>(x, s, &top);
+      const float inv = total == 0.0f ? 0.0f : fast_reciprocal(total);
+      if (p.grad_w != nullptr) {
+        float ds = 0.0f, sk = 0.0f;
+        if (mine >= 0) {
+          sk = SIG ? sigmoid(l) : soft_score(l, top) * inv;
+          ds = dw * p.scale;
+        }
+        if (p.renorm) {
+          const float sum = warp_sum(sk);
+          const float is = sum == 0.0f ? 0.0f : fast_reciprocal(sum);
+          const float mean = warp_sum(ds * sk) * is;
+          ds = (ds - mean) * is;
+        }
+        if (mine >= 0) row[mine] = ds;
+        __syncwarp();
 #pragma unroll
-    for (int r = 0; r < VPL; ++r) {
-      const int e = element_of<V>(r, lane);
-      g[r] = e < p.E ? row[e] : 0.0f;
-      if constexpr (!SIG) {
-        s[r] *= inv;
-        g[r] += dq[r];
-        dot += s[r] * g[r];
+        for (int r = 0; r < VPL; r += V) {
+          const int e = element_of<V>(r, lane);
+          if constexpr (V == 4) {
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (e < p.E) v = *reinterpret_cast<const float4*>(row + e);
+            g[r] = v.x;
+            g[r + 1] = v.y;
+            g[r + 2] = v.z;
+            g[r + 3] = v.w;
+          } else {
+            g[r] = e < p.E ? row[e] : 0.0f;
+          }
+        }
+        __syncwarp();
+        if (mine >= 0) row[mine] = 0.0f;
       } else {
-        dot += s[r] * inv * dq[r];
+#pragma unroll
+        for (int r = 0; r < VPL; ++r) g[r] = 0.0f;
+      }
+      float dot = 0.0f;
+#pragma unroll
+      for (int r = 0; r < VPL; ++r) {
+        if constexpr (SIG) {
+          dot = fmaf(s[r], dq[r], dot);
+        } else {
+          s[r] *= inv;
+          g[r] += dq[r];
+          dot = fmaf(s[r], g[r], dot);
+        }
+      }
+      dot = warp_sum(dot);
+      if constexpr (SIG) {
+        dot *= inv;
+#pragma unroll
+        for (int r = 0; r < VPL; ++r)
+          g[r] = fmaf(dq[r] - dot, inv, g[r]) * (s[r] * (1.0f - s[r]));
+      } else {
+        const float z = total != 0.0f ? dlse * (top + __logf(total)) : 0.0f;
+#pragma unroll
+        for (int r = 0; r < VPL; ++r) g[r] = s[r] * (g[r] - (dot - z));
       }
     }
-    dot = warp_sum(dot);
-    const float z = !SIG && total != 0.0f ? dlse * (top + logf(total)) : 0.0f;
+    store_row<VPL, V, BF16>(p.grad, int64_t(t) * p.ld_grad, p.E, lane, g);
+    __syncwarp();
+    choice = next_choice;
+    dw = next_dw;
+    if constexpr (kAhead<VPL>) {
 #pragma unroll
-    for (int r = 0; r < VPL; ++r) {
-      if constexpr (SIG)
-        g[r] = (g[r] + (dq[r] - dot) * inv) * s[r] * (1.0f - s[r]);
-      else
-        g[r] = s[r] * (g[r] - dot + z);
-    }
-    store_row<VPL, V, BF16>(p.grad, out, p.E, lane, g);
-    if (p.grad_w != nullptr) {
-      __syncwarp();
-      if (mine >= 0) row[mine] = 0.0f;
-      __syncwarp();
+      for (int r = 0; r < VPL; ++r) x[r] = next[r];
     }
   }
 }
@@ -913,7 +1030,7 @@ int run_length(int T) {
 }
 
 // CTAs of the second kernel along the experts.
-int sum_ctas(int E) { return (E + 31) / 32; }
+int sum_ctas(int E) { return (E + kSumExperts - 1) / kSumExperts; }
 
 struct BalanceWorkspace {
   float* prob;
