@@ -780,18 +780,42 @@ def combine_ranks(cfg: Config, layout: Layout, rank_y, y=None, stream=None):
 
 
 # ---- router gate -----------------------------------------------------------------
+# The wrappers below sit in decode loops where a call is a few microseconds:
+# they build their ABI configs once, test each tensor with one expression and
+# read the current stream's handle directly.
 
-def _need(ok: bool, what: str):
-    if not ok:
-        raise EpError(EP_ERR_INVALID_ARG, what)
+def _refuse(what: str):
+    raise EpError(EP_ERR_INVALID_ARG, what)
 
 
-def _need_flat(what: str, dtype, shape, *tensors):
-    """Optional tensors of one type and shape, contiguous, on the GPU."""
-    for t in tensors:
-        if t is not None:
-            _need(t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.is_cuda,
-                  f"{what}: a tensor is not a contiguous CUDA {dtype} {tuple(shape)}")
+def _flat(t, dtype, shape) -> bool:
+    """t is None, or a contiguous CUDA tensor of this type and shape."""
+    return t is None or (t.dtype is dtype and t.shape == shape and t.is_contiguous()
+                         and t.is_cuda)
+
+
+def _mask_ok(t, T: int) -> bool:
+    return t is None or _flat(t, _torch.bool, (T,)) or _flat(t, _torch.uint8, (T,))
+
+
+def _stream_of(t, stream):
+    """The stream's handle; the current stream of t's device when None."""
+    if stream is not None:
+        return stream.cuda_stream
+    return _torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
+class _LazyTorch:
+    """torch, imported by the first call that needs it."""
+
+    def __getattr__(self, name):
+        global _torch
+        import torch as _torch
+
+        return getattr(_torch, name)
+
+
+_torch = _LazyTorch()
 
 
 @dataclasses.dataclass(frozen=True)
@@ -808,7 +832,8 @@ class RouterConfig:
     route_scale: float = 1.0
 
     def __post_init__(self):
-        _need(self.score in ("softmax", "sigmoid"), f"RouterConfig: score {self.score!r}")
+        if self.score not in ("softmax", "sigmoid"):
+            _refuse(f"RouterConfig: score {self.score!r}")
         both = tuple(EpRouterConfig(self.num_experts, self.num_topk,
                                     int(self.score == "sigmoid"), self.num_groups,
                                     self.topk_groups, int(self.renormalize), bf16,
@@ -821,15 +846,14 @@ class RouterConfig:
 
 def _logits_args(cfg: RouterConfig, what: str, logits):
     """(ABI config, T, row stride) of a [T, E] tensor with unit column stride."""
-    import torch
-
-    bf16 = logits.dtype is torch.bfloat16
-    _need(bf16 or logits.dtype is torch.float32, f"{what}: logits are {logits.dtype}")
+    dtype = logits.dtype
+    if dtype is not _torch.float32 and dtype is not _torch.bfloat16:
+        _refuse(f"{what}: logits are {dtype}")
     T, E = logits.shape
     row, col = logits.stride()
-    _need(E == cfg.num_experts and (col == 1 or E == 1) and logits.is_cuda,
-          f"{what}: logits are not CUDA [T, {cfg.num_experts}] with unit column stride")
-    return cfg._c[bf16], T, row if T > 1 else E
+    if E != cfg.num_experts or (col != 1 and E != 1) or not logits.is_cuda:
+        _refuse(f"{what}: logits are not CUDA [T, {cfg.num_experts}] with unit column stride")
+    return cfg._c[dtype is _torch.bfloat16], T, row if T > 1 else E
 
 
 def route(cfg: RouterConfig, logits, bias=None, token_mask=None, topk_idx=None,
@@ -837,30 +861,20 @@ def route(cfg: RouterConfig, logits, bias=None, token_mask=None, topk_idx=None,
     """ep_route.  logits: fp32 or bf16 CUDA tensor [T, E], rows may be strided;
     bias: fp32 [E]; token_mask: uint8 or bool [T].  Returns (topk_idx int64
     [T, K], topk_weights fp32 [T, K])."""
-    import torch
-
     c, T, ld = _logits_args(cfg, "route", logits)
-    dev, shape = logits.device, (T, cfg.num_topk)
+    shape = (T, cfg.num_topk)
     if topk_idx is None:
-        topk_idx = torch.empty(shape, dtype=torch.int64, device=dev)
+        topk_idx = _torch.empty(shape, dtype=_torch.int64, device=logits.device)
     if topk_weights is None:
-        topk_weights = torch.empty(shape, dtype=torch.float32, device=dev)
-    _need_flat("route", torch.int64, shape, topk_idx)
-    _need_flat("route", torch.float32, shape, topk_weights)
-    _need_router_inputs("route", cfg, T, bias, token_mask)
-    st = ep_route(c, T, logits.data_ptr(), ld, _ptr(bias), _ptr(token_mask),
-                  topk_idx.data_ptr(), topk_weights.data_ptr(), _stream(stream))
-    _check(st, "ep_route")
+        topk_weights = _torch.empty(shape, dtype=_torch.float32, device=logits.device)
+    if not (_flat(topk_idx, _torch.int64, shape) and _flat(topk_weights, _torch.float32, shape)
+            and _flat(bias, _torch.float32, (cfg.num_experts,)) and _mask_ok(token_mask, T)):
+        _refuse("route: type, shape or place of a tensor")
+    st = _lib.ep_route(c, T, logits.data_ptr(), ld, _ptr(bias), _ptr(token_mask),
+                       topk_idx.data_ptr(), topk_weights.data_ptr(), _stream_of(logits, stream))
+    if st:
+        _check(st, "ep_route")
     return topk_idx, topk_weights
-
-
-def _need_router_inputs(what: str, cfg: RouterConfig, T: int, bias, token_mask):
-    import torch
-
-    _need_flat(what, torch.float32, (cfg.num_experts,), bias)
-    if token_mask is not None:
-        _need_flat(what, torch.bool if token_mask.dtype is torch.bool else torch.uint8, (T,),
-                   token_mask)
 
 
 def route_balance(cfg: RouterConfig, logits, bias=None, token_mask=None, seq_start=None,
@@ -870,30 +884,37 @@ def route_balance(cfg: RouterConfig, logits, bias=None, token_mask=None, seq_sta
     expert_prob fp32 [B, E], seq_tokens int32 [B + 2], loss fp32 [2]), which
     `out` may give; workspace: ep_route_workspace_bytes bytes (allocated when
     None)."""
-    import torch
-
     c, T, ld = _logits_args(cfg, "route_balance", logits)
     B = 1 if seq_start is None else seq_start.shape[0] - 1
     E, K, dev = cfg.num_experts, cfg.num_topk, logits.device
-    i32, f32 = torch.int32, torch.float32
-    wanted = (((T, K), torch.int64), ((T, K), f32), ((B, E), i32), ((B, E), f32), ((B + 2,), i32),
-              ((2,), f32))
+    i32, f32 = _torch.int32, _torch.float32
     if out is None:
-        out = tuple(torch.empty(s, dtype=d, device=dev) for s, d in wanted)
-    for t, (s, d) in zip(out, wanted, strict=True):
-        _need_flat("route_balance", d, s, t)
-    _need_router_inputs("route_balance", cfg, T, bias, token_mask)
-    _need_flat("route_balance", i32, (B + 1,), seq_start)
-    size = ep_route_workspace_bytes(c, B)
-    _need(size >= 0, "route_balance: config")
+        out = (_torch.empty((T, K), dtype=_torch.int64, device=dev),
+               _torch.empty((T, K), dtype=f32, device=dev),
+               _torch.empty((B, E), dtype=i32, device=dev),
+               _torch.empty((B, E), dtype=f32, device=dev),
+               _torch.empty((B + 2,), dtype=i32, device=dev),
+               _torch.empty((2,), dtype=f32, device=dev))
+    idx, w, count, prob, tokens, loss = out
+    size = _lib.ep_route_workspace_bytes(c, B)
+    if size < 0:
+        _refuse("route_balance: config or number of sequences")
     if workspace is None:
-        workspace = torch.empty(size, dtype=torch.uint8, device=dev)
-    _need(workspace.is_cuda and workspace.nbytes >= size, "route_balance: workspace")
-    st = ep_route_balance(c, T, logits.data_ptr(), ld, _ptr(bias), _ptr(token_mask), B,
-                          _ptr(seq_start), *(t.data_ptr() for t in out), workspace.data_ptr(),
-                          _stream(stream))
-    _check(st, "ep_route_balance")
-    return tuple(out)
+        workspace = _torch.empty(size, dtype=_torch.uint8, device=dev)
+    if not (_flat(idx, _torch.int64, (T, K)) and _flat(w, f32, (T, K))
+            and _flat(count, i32, (B, E)) and _flat(prob, f32, (B, E))
+            and _flat(tokens, i32, (B + 2,)) and _flat(loss, f32, (2,))
+            and _flat(bias, f32, (E,)) and _mask_ok(token_mask, T)
+            and _flat(seq_start, i32, (B + 1,))
+            and workspace.is_cuda and workspace.nbytes >= size):
+        _refuse("route_balance: type, shape or place of a tensor")
+    st = _lib.ep_route_balance(c, T, logits.data_ptr(), ld, _ptr(bias), _ptr(token_mask), B,
+                               _ptr(seq_start), idx.data_ptr(), w.data_ptr(), count.data_ptr(),
+                               prob.data_ptr(), tokens.data_ptr(), loss.data_ptr(),
+                               workspace.data_ptr(), _stream_of(logits, stream))
+    if st:
+        _check(st, "ep_route_balance")
+    return idx, w, count, prob, tokens, loss
 
 
 def route_backward(cfg: RouterConfig, logits, topk_idx=None, grad_w=None, token_mask=None,
@@ -902,28 +923,24 @@ def route_backward(cfg: RouterConfig, logits, topk_idx=None, grad_w=None, token_
     """ep_route_backward.  grad_w: the gate weights' gradient (combine_backward
     returns it); expert_count, seq_tokens: route_balance's; grad_loss: fp32 [2]
     CUDA tensor.  Returns grad_logits [T, E] of the logits' type."""
-    import torch
-
     c, T, ld = _logits_args(cfg, "route_backward", logits)
     B = 1 if seq_start is None else seq_start.shape[0] - 1
     E, K = cfg.num_experts, cfg.num_topk
+    i32, f32 = _torch.int32, _torch.float32
     if grad_logits is None:
-        grad_logits = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
-    _need(grad_logits.dtype is logits.dtype, "route_backward: grad_logits' type")
-    _, Tg, ld_grad = _logits_args(cfg, "route_backward", grad_logits)
-    _need(Tg == T, "route_backward: grad_logits' rows")
-    _need_router_inputs("route_backward", cfg, T, None, token_mask)
-    _need_flat("route_backward", torch.int64, (T, K), topk_idx)
-    _need_flat("route_backward", torch.float32, (T, K), grad_w)
-    _need_flat("route_backward", torch.int32, (B + 1,), seq_start)
-    _need_flat("route_backward", torch.int32, (B, E), expert_count)
-    _need_flat("route_backward", torch.int32, (B + 2,), seq_tokens)
-    _need_flat("route_backward", torch.float32, (2,), grad_loss)
-    st = ep_route_backward(c, T, logits.data_ptr(), ld, _ptr(token_mask), _ptr(topk_idx),
-                           _ptr(grad_w), B, _ptr(seq_start), _ptr(expert_count),
-                           _ptr(seq_tokens), _ptr(grad_loss), grad_logits.data_ptr(), ld_grad,
-                           _stream(stream))
-    _check(st, "ep_route_backward")
+        grad_logits = _torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+    c_grad, Tg, ld_grad = _logits_args(cfg, "route_backward", grad_logits)
+    if not (c_grad is c and Tg == T and _mask_ok(token_mask, T)
+            and _flat(topk_idx, _torch.int64, (T, K)) and _flat(grad_w, f32, (T, K))
+            and _flat(seq_start, i32, (B + 1,)) and _flat(expert_count, i32, (B, E))
+            and _flat(seq_tokens, i32, (B + 2,)) and _flat(grad_loss, f32, (2,))):
+        _refuse("route_backward: type, shape or place of a tensor")
+    st = _lib.ep_route_backward(c, T, logits.data_ptr(), ld, _ptr(token_mask), _ptr(topk_idx),
+                                _ptr(grad_w), B, _ptr(seq_start), _ptr(expert_count),
+                                _ptr(seq_tokens), _ptr(grad_loss), grad_logits.data_ptr(),
+                                ld_grad, _stream_of(logits, stream))
+    if st:
+        _check(st, "ep_route_backward")
     return grad_logits
 
 
@@ -942,20 +959,22 @@ class W4Config:
     has_zeros: bool = False
 
     def __post_init__(self):
-        object.__setattr__(self, "_c", EpW4Config(
-            self.num_experts, self.in_features, self.out_features, self.group_size,
-            int(self.x_fp8), int(self.gated), int(self.has_zeros)))
-        sizes = (ep_w4_codes_bytes(self._c), ep_w4_scales_bytes(self._c),
-                 ep_w4_zeros_bytes(self._c))
-        _need(min(sizes) >= 0, "W4Config")
+        c = EpW4Config(self.num_experts, self.in_features, self.out_features, self.group_size,
+                       int(self.x_fp8), int(self.gated), int(self.has_zeros))
+        sizes = ep_w4_codes_bytes(c), ep_w4_scales_bytes(c), ep_w4_zeros_bytes(c)
+        if min(sizes) < 0:
+            _refuse("W4Config")
+        object.__setattr__(self, "_c", c)
         object.__setattr__(self, "_sizes", sizes)
+        object.__setattr__(self, "_width",
+                           self.out_features // 2 if self.gated else self.out_features)
 
     def c(self) -> EpW4Config:
         return self._c
 
     @property
     def out_width(self) -> int:
-        return self.out_features // 2 if self.gated else self.out_features
+        return self._width
 
 
 def w4_pack(cfg: W4Config, codes, scales, zeros=None, stream=None):
@@ -963,20 +982,27 @@ def w4_pack(cfg: W4Config, codes, scales, zeros=None, stream=None):
     [E, N, H / group]; zeros: uint8, as the scales.  Returns the packed (codes
     int32 [E, tiles, blocks, 8, 32, 4], scales bf16 [E, tiles, groups, 64],
     zeros uint8 or None)."""
-    import torch
-
     E, N, H, g = cfg.num_experts, cfg.out_features, cfg.in_features, cfg.group_size
-    _need_flat("w4_pack", torch.uint8, (E, N, H // 2), codes)
-    _need_flat("w4_pack", torch.bfloat16, (E, N, H // g), scales)
-    _need_flat("w4_pack", torch.uint8, (E, N, H // g), zeros)
-    tiles, blocks, dev = -(-cfg.out_width // (32 if cfg.gated else 64)), -(-H // 128), codes.device
-    pc = torch.empty((E, tiles, blocks, 8, 32, 4), dtype=torch.int32, device=dev)
-    ps = torch.empty((E, tiles, blocks * 128 // g, 64), dtype=torch.bfloat16, device=dev)
-    pz = torch.empty(ps.shape, dtype=torch.uint8, device=dev) if cfg.has_zeros else None
+    if not (_flat(codes, _torch.uint8, (E, N, H // 2))
+            and _flat(scales, _torch.bfloat16, (E, N, H // g))
+            and _flat(zeros, _torch.uint8, (E, N, H // g))):
+        _refuse("w4_pack: type, shape or place of a tensor")
+    tiles, blocks, dev = -(-cfg._width // (32 if cfg.gated else 64)), -(-H // 128), codes.device
+    pc = _torch.empty((E, tiles, blocks, 8, 32, 4), dtype=_torch.int32, device=dev)
+    ps = _torch.empty((E, tiles, blocks * 128 // g, 64), dtype=_torch.bfloat16, device=dev)
+    pz = _torch.empty(ps.shape, dtype=_torch.uint8, device=dev) if cfg.has_zeros else None
     st = ep_w4_pack(cfg._c, codes.data_ptr(), scales.data_ptr(), _ptr(zeros), pc.data_ptr(),
-                    ps.data_ptr(), _ptr(pz), _stream(stream))
+                    ps.data_ptr(), _ptr(pz), _stream_of(codes, stream))
     _check(st, "ep_w4_pack")
     return pc, ps, pz
+
+
+def _packed(t, size: int) -> bool:
+    return t.nbytes == size and t.is_contiguous() and t.is_cuda
+
+
+def _segments(t, E: int) -> bool:
+    return t.dtype is _torch.int32 and t.shape[0] >= E and t.is_contiguous() and t.is_cuda
 
 
 def expert_w4(cfg: W4Config, x, codes, scales, expert_start, expert_end, num_rows, zeros=None,
@@ -985,24 +1011,20 @@ def expert_w4(cfg: W4Config, x, codes, scales, expert_start, expert_end, num_row
     [cap, H / 128]; codes, scales, zeros: w4_pack's; expert_start, expert_end:
     a Layout's; num_rows: rows of all experts together at most (T * K).
     Returns out, bf16 [cap, N] ([cap, N / 2] when gated)."""
-    import torch
-
-    cap, H, E = x.shape[0], cfg.in_features, cfg.num_experts
-    _need_flat("expert_w4", torch.uint8 if cfg.x_fp8 else torch.bfloat16, (cap, H), x)
-    if cfg.x_fp8:
-        _need_flat("expert_w4", torch.float32, (cap, H // 128), x_scale)
+    H, E, sizes = cfg.in_features, cfg.num_experts, cfg._sizes
+    cap, shape = x.shape[0], (x.shape[0], cfg._width)
     if out is None:
-        out = torch.empty((cap, cfg.out_width), dtype=torch.bfloat16, device=x.device)
-    _need_flat("expert_w4", torch.bfloat16, (cap, cfg.out_width), out)
-    sizes = cfg._sizes
-    _need(codes.nbytes == sizes[0] and scales.nbytes == sizes[1] and codes.is_contiguous()
-          and scales.is_contiguous() and scales.dtype is torch.bfloat16
-          and (zeros is None or zeros.nbytes == sizes[2] and zeros.is_contiguous()),
-          "expert_w4: packed weights")
-    _need(expert_start.dtype is torch.int32 and expert_end.dtype is torch.int32
-          and expert_start.shape[0] >= E and expert_end.shape[0] >= E, "expert_w4: segments")
-    st = ep_expert_w4(cfg._c, cap, num_rows, x.data_ptr(), _ptr(x_scale), codes.data_ptr(),
-                      scales.data_ptr(), _ptr(zeros), expert_start.data_ptr(),
-                      expert_end.data_ptr(), out.data_ptr(), _stream(stream))
-    _check(st, "ep_expert_w4")
+        out = _torch.empty(shape, dtype=_torch.bfloat16, device=x.device)
+    if not (_flat(x, _torch.uint8 if cfg.x_fp8 else _torch.bfloat16, (cap, H))
+            and (x_scale is None or _flat(x_scale, _torch.float32, (cap, H // 128)))
+            and _flat(out, _torch.bfloat16, shape)
+            and _packed(codes, sizes[0]) and _packed(scales, sizes[1])
+            and (zeros is None or _packed(zeros, sizes[2]))
+            and _segments(expert_start, E) and _segments(expert_end, E)):
+        _refuse("expert_w4: type, shape or place of a tensor")
+    st = _lib.ep_expert_w4(cfg._c, cap, num_rows, x.data_ptr(), _ptr(x_scale), codes.data_ptr(),
+                           scales.data_ptr(), _ptr(zeros), expert_start.data_ptr(),
+                           expert_end.data_ptr(), out.data_ptr(), _stream_of(x, stream))
+    if st:
+        _check(st, "ep_expert_w4")
     return out

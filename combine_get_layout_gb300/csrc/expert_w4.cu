@@ -13,6 +13,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 
 #include "../../include/ep.h"
@@ -606,8 +607,10 @@ int64_t w4_scales(const ep_w4_config* c) {
 
 int32_t status(cudaError_t e) { return note_cuda(e) == cudaSuccess ? EP_OK : EP_ERR_CUDA; }
 
-// Shared memory a CTA may use, less the table of chunks of 2048 experts.
-constexpr int kSmemBudget = 227 * 1024 - 8 * 1024 - 512;
+// Dynamic shared memory of a CTA at most (227 KiB less its static arrays), and
+// what the table of chunks of 2048 experts leaves of it for the stages.
+constexpr int kSmemLimit = 227 * 1024 - 256;
+constexpr int kSmemBudget = kSmemLimit - 2049 * 4;
 
 // Chunks of `size` rows that `rows` rows of E experts make, on average.
 double expected_chunks(int rows, int E, int size) {
@@ -641,9 +644,16 @@ cudaError_t launch_w4(const W4Params& p, int num_rows, cudaStream_t stream) {
   const int grid = int(want < sms ? want : sms);
   const size_t smem = WARPS * STAGES * Stage<FP8, GROUP, ZEROS, NT>::kBytes + sizeof(int) * (p.E + 1);
   auto* kernel = expert_w4_kernel<FP8, GROUP, ZEROS, NT, WARPS, STAGES>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  // once per kernel and device: the limit for any number of experts
+  static std::atomic<uint64_t> raised{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (dev >= 64 || !(raised.load(std::memory_order_acquire) >> dev & 1)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) raised.fetch_or(uint64_t(1) << dev, std::memory_order_release);
+  }
   return launch_pdl(kernel, dim3(grid), dim3(WARPS * 32), smem, stream, p, split);
 }
 
