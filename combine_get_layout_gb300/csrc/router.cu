@@ -39,11 +39,11 @@ struct RouteParams {
   // balance
   const int32_t* seq_start;  // [B + 1] or null (B = 1)
   int B;
-  int tokens_per_cta, ctas;
-  float* part_prob;          // [ctas + B, E]
-  int32_t* part_count;       // [ctas + B, E]
-  int32_t* part_tokens;      // [ctas + B]
-  float* part_z;             // [ctas + B]
+  int tokens_per_cta;
+  float* part_prob;          // [CTAs + B, E]
+  int32_t* part_count;       // [CTAs + B, E]
+  int32_t* part_tokens;      // [CTAs + B]
+  float* part_z;             // [CTAs + B]
   unsigned* done;            // cleared for the second kernel
 };
 
@@ -382,13 +382,25 @@ __device__ __forceinline__ Chosen choose(const RouteParams& p, const float (&c)[
   return out;
 }
 
-// The choice bias in registers, where a warp keeps it over its tokens.
+// Floats of a row of E in shared memory: whole vectors of four.
+__host__ __device__ __forceinline__ int padded_row(int E) { return (E + 3) & ~3; }
+
+// A lane's values of a row of E floats in shared memory (16-byte aligned).
 template <int VPL, int V>
-__device__ __forceinline__ void load_bias(const RouteParams& p, int lane, float (&bias)[VPL]) {
+__device__ __forceinline__ void read_row(const float* row, int E, int lane, float (&v)[VPL]) {
 #pragma unroll
-  for (int r = 0; r < VPL; ++r) {
+  for (int r = 0; r < VPL; r += V) {
     const int e = element_of<V>(r, lane);
-    bias[r] = p.bias != nullptr && e < p.E ? p.bias[e] : 0.0f;
+    if constexpr (V == 4) {
+      float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (e < E) f = *reinterpret_cast<const float4*>(row + e);
+      v[r] = f.x;
+      v[r + 1] = f.y;
+      v[r + 2] = f.z;
+      v[r + 3] = f.w;
+    } else {
+      v[r] = e < E ? row[e] : 0.0f;
+    }
   }
 }
 
@@ -398,7 +410,7 @@ __device__ __forceinline__ void load_bias(const RouteParams& p, int lane, float 
 // lane's chosen expert or -1.
 template <int VPL, int V, bool BF16, bool SIG, bool STATS>
 __device__ __forceinline__ int route_token(const RouteParams& p, int t, int lane, float* row,
-                                           Candidates& cand, const float (&bias)[VPL],
+                                           Candidates& cand, const float* bias,
                                            const float (&x)[VPL], float (&s)[VPL], float* total,
                                            float* top) {
   float best, scale = p.scale;
@@ -407,8 +419,14 @@ __device__ __forceinline__ int route_token(const RouteParams& p, int t, int lane
   if constexpr (SIG) {
     *total = scores<VPL, SIG>(x, s, top);
     float c[VPL];
+    if (p.bias != nullptr) {
+      read_row<VPL, V>(bias, p.E, lane, c);
+    } else {
 #pragma unroll
-    for (int r = 0; r < VPL; ++r) c[r] = x[r] == -CUDART_INF_F ? -CUDART_INF_F : s[r] + bias[r];
+      for (int r = 0; r < VPL; ++r) c[r] = 0.0f;
+    }
+#pragma unroll
+    for (int r = 0; r < VPL; ++r) c[r] = x[r] == -CUDART_INF_F ? -CUDART_INF_F : s[r] + c[r];
     if (p.G > 1) keep_groups<VPL, V, SIG>(c, row, p.E, p.G, p.kept, lane);
     best = c[0];
 #pragma unroll
@@ -471,14 +489,18 @@ constexpr bool kAhead = VPL <= 16;
 
 template <int VPL, int V, bool BF16, bool SIG>
 __global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteParams p) {
-  extern __shared__ float smem[];
+  extern __shared__ __align__(16) float smem[];
   __shared__ Candidates cands[kRouteWarps];
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float* row = smem + warp * p.E;
+  const float* bias = smem;      // [E] padded to whole vectors, then the warps' rows
+  float* row = smem + (warp + 1) * padded_row(p.E);
+  if (SIG && p.bias != nullptr) {
+    for (int e = threadIdx.x; e < p.E; e += kRouteThreads) smem[e] = p.bias[e];
+    __syncthreads();
+  }
   const int stride = gridDim.x * kRouteWarps;
-  float x[VPL], s[VPL], bias[VPL], total, top;
-  load_bias<VPL, V>(p, lane, bias);
+  float x[VPL], s[VPL], total, top;
   int t = blockIdx.x * kRouteWarps + warp;
   if (kAhead<VPL> && t < p.T) load_row<VPL, V, BF16>(p.logits, int64_t(t) * p.ld, p.E, lane, x);
   for (; t < p.T; t += stride) {
@@ -518,24 +540,33 @@ __device__ __forceinline__ int sequence_of(const int32_t* seq_start, int B, int 
 // and walks the sequences they belong to; the sums of (CTA c, sequence b) go
 // to partial row c + b, which no other pair uses (both only grow along the
 // tokens).
+template <int VPL>
+constexpr int kBalanceThreads = VPL <= 16 ? 512 : 256;
+template <int VPL>
+constexpr int kBalanceCtasPerSm = VPL <= 8 ? 2 : 1;
+
 template <int VPL, int V, bool BF16, bool SIG>
-__global__ void __launch_bounds__(kRouteThreads) balance_kernel(RouteParams p) {
-  extern __shared__ float smem[];
-  float* probs = smem;                                         // [kRouteWarps][E]
-  int* counts = reinterpret_cast<int*>(smem + kRouteWarps * p.E);   // [E]
-  __shared__ Candidates cands[kRouteWarps];
-  __shared__ float warp_z[kRouteWarps];
-  __shared__ int warp_n[kRouteWarps];
+__global__ void __launch_bounds__(kBalanceThreads<VPL>, kBalanceCtasPerSm<VPL>)
+balance_kernel(RouteParams p) {
+  constexpr int kThreads = kBalanceThreads<VPL>, kWarps = kThreads / 32;
+  extern __shared__ __align__(16) float smem[];
+  const int width = padded_row(p.E);
+  float* probs = smem;                                          // [kWarps][width]
+  float* bias = smem + kWarps * width;                          // [width]
+  int* counts = reinterpret_cast<int*>(bias + width);           // [width]
+  __shared__ Candidates cands[kWarps];
+  __shared__ float warp_z[kWarps];
+  __shared__ int warp_n[kWarps];
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float* row = probs + warp * p.E;
+  float* row = probs + warp * width;
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.done = 0;
-  for (int e = threadIdx.x; e < p.E; e += kRouteThreads) counts[e] = 0;
+  for (int e = threadIdx.x; e < p.E; e += kThreads) counts[e] = 0;
+  if (SIG && p.bias != nullptr)
+    for (int e = threadIdx.x; e < p.E; e += kThreads) bias[e] = p.bias[e];
   __syncthreads();
   const int first = blockIdx.x * p.tokens_per_cta;
   const int last = min(p.T, first + p.tokens_per_cta);
-  float bias[VPL];
-  load_bias<VPL, V>(p, lane, bias);
   int b = p.B > 1 ? sequence_of(p.seq_start, p.B, first) : 0;
   for (int t = first; t < last;) {
     while (b < p.B - 1 && p.seq_start[b + 1] <= t) ++b;
@@ -547,11 +578,11 @@ __global__ void __launch_bounds__(kRouteThreads) balance_kernel(RouteParams p) {
     float x[VPL], s[VPL], total, top;
     int u = t + warp;
     if (kAhead<VPL> && u < end) load_row<VPL, V, BF16>(p.logits, int64_t(u) * p.ld, p.E, lane, x);
-    for (; u < end; u += kRouteWarps) {
+    for (; u < end; u += kWarps) {
       float next[VPL];
       if constexpr (kAhead<VPL>) {
-        if (u + kRouteWarps < end)
-          load_row<VPL, V, BF16>(p.logits, int64_t(u + kRouteWarps) * p.ld, p.E, lane, next);
+        if (u + kWarps < end)
+          load_row<VPL, V, BF16>(p.logits, int64_t(u + kWarps) * p.ld, p.E, lane, next);
       } else {
         load_row<VPL, V, BF16>(p.logits, int64_t(u) * p.ld, p.E, lane, x);
       }
@@ -588,10 +619,10 @@ __global__ void __launch_bounds__(kRouteThreads) balance_kernel(RouteParams p) {
     }
     __syncthreads();
     const int64_t part = int64_t(blockIdx.x) + b;
-    for (int e = threadIdx.x; e < p.E; e += kRouteThreads) {
+    for (int e = threadIdx.x; e < p.E; e += kThreads) {
       float acc = 0.0f;
 #pragma unroll
-      for (int v = 0; v < kRouteWarps; ++v) acc += probs[v * p.E + e];
+      for (int v = 0; v < kWarps; ++v) acc += probs[v * width + e];
       p.part_prob[part * p.E + e] = acc;
       p.part_count[part * p.E + e] = counts[e];
       counts[e] = 0;
@@ -599,7 +630,7 @@ __global__ void __launch_bounds__(kRouteThreads) balance_kernel(RouteParams p) {
     if (threadIdx.x == 0) {
       float zs = 0.0f;
       int ns = 0;
-      for (int v = 0; v < kRouteWarps; ++v) {
+      for (int v = 0; v < kWarps; ++v) {
         zs += warp_z[v];
         ns += warp_n[v];
       }
@@ -786,10 +817,10 @@ __device__ __forceinline__ void store_row(void* base, int64_t offset, int E, int
 //   sigmoid:  u = (dq - sum q dq) / sum s + ds,  dl = u s (1 - s)
 template <int VPL, int V, bool BF16, bool SIG>
 __global__ void __launch_bounds__(kRouteThreads) route_backward_kernel(RouteBackwardParams p) {
-  extern __shared__ float smem[];
+  extern __shared__ __align__(16) float smem[];
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float* row = smem + warp * p.E;
+  float* row = smem + warp * padded_row(p.E);
   for (int e = lane; e < p.E; e += 32) row[e] = 0.0f;
   __syncwarp();
   const int first = blockIdx.x * p.tokens_per_cta;
@@ -869,20 +900,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_backward_kernel(RouteBack
         }
         if (mine >= 0) row[mine] = ds;
         __syncwarp();
-#pragma unroll
-        for (int r = 0; r < VPL; r += V) {
-          const int e = element_of<V>(r, lane);
-          if constexpr (V == 4) {
-            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (e < p.E) v = *reinterpret_cast<const float4*>(row + e);
-            g[r] = v.x;
-            g[r + 1] = v.y;
-            g[r + 2] = v.z;
-            g[r + 3] = v.w;
-          } else {
-            g[r] = e < p.E ? row[e] : 0.0f;
-          }
-        }
+        read_row<VPL, V>(row, p.E, lane, g);
         __syncwarp();
         if (mine >= 0) row[mine] = 0.0f;
       } else {
@@ -975,10 +993,11 @@ cudaError_t with_shape(int E, int64_t ld, bool bf16, bool sig, F&& f) {
   return cudaErrorInvalidValue;
 }
 
-// Raises a kernel's dynamic shared-memory limit where `bytes` needs it.
+// Raises a kernel's dynamic shared-memory limit where `bytes` needs it (48 KiB
+// with the static arrays, which are under 8, need no leave).
 template <typename... P>
 cudaError_t allow_smem(void (*kernel)(P...), size_t bytes) {
-  if (bytes <= 48 * 1024) return cudaSuccess;
+  if (bytes <= 40 * 1024) return cudaSuccess;
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
 }
 
@@ -988,7 +1007,8 @@ struct LaunchRoute {
   cudaStream_t stream;
   template <int VPL, int V, bool BF16, bool SIG>
   cudaError_t operator()() const {
-    const size_t smem = p.G > 1 ? sizeof(float) * kRouteWarps * p.E : 0;
+    const size_t rows = p.G > 1 ? kRouteWarps + 1 : SIG ? 1 : 0;
+    const size_t smem = sizeof(float) * rows * padded_row(p.E);
     auto* kernel = route_kernel<VPL, V, BF16, SIG>;
     const cudaError_t e = allow_smem(kernel, smem);
     if (e != cudaSuccess) return e;
@@ -996,16 +1016,30 @@ struct LaunchRoute {
   }
 };
 
+// CTAs of the second kernel along the experts.
+int sum_ctas(int E) { return (E + kSumExperts - 1) / kSumExperts; }
+
 struct LaunchBalance {
   RouteParams p;
+  BalanceParams q;      // of the second kernel
   cudaStream_t stream;
   template <int VPL, int V, bool BF16, bool SIG>
-  cudaError_t operator()() const {
-    const size_t smem = sizeof(float) * (kRouteWarps + 1) * p.E;
+  cudaError_t operator()() {
+    constexpr int kThreads = kBalanceThreads<VPL>, kWarps = kThreads / 32;
+    // each warp with a token at least; no tokens: one CTA still clears `done`
+    const int want = (p.T + kWarps - 1) / kWarps;
+    const int most = device_info().sm_count * kBalanceCtasPerSm<VPL>;
+    const int ctas = want < most ? (want > 1 ? want : 1) : most;
+    p.tokens_per_cta = q.tokens_per_cta = p.T > 0 ? (p.T + ctas - 1) / ctas : 1;
+    const int used = p.T > 0 ? (p.T + p.tokens_per_cta - 1) / p.tokens_per_cta : 1;
+    const size_t smem = sizeof(float) * (kWarps + 2) * padded_row(p.E);
     auto* kernel = balance_kernel<VPL, V, BF16, SIG>;
-    const cudaError_t e = allow_smem(kernel, smem);
+    cudaError_t e = allow_smem(kernel, smem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kernel, dim3(p.ctas), dim3(kRouteThreads), smem, stream, p);
+    e = launch_pdl(kernel, dim3(used), dim3(kThreads), smem, stream, p);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(balance_sum_kernel, dim3(p.B, sum_ctas(p.E)), dim3(kSumThreads), 0, stream,
+                      q);
   }
 };
 
@@ -1015,7 +1049,7 @@ struct LaunchBackward {
   cudaStream_t stream;
   template <int VPL, int V, bool BF16, bool SIG>
   cudaError_t operator()() const {
-    const size_t smem = sizeof(float) * kRouteWarps * p.E;
+    const size_t smem = sizeof(float) * kRouteWarps * padded_row(p.E);
     auto* kernel = route_backward_kernel<VPL, V, BF16, SIG>;
     const cudaError_t e = allow_smem(kernel, smem);
     if (e != cudaSuccess) return e;
@@ -1029,9 +1063,6 @@ int run_length(int T) {
   return ctas > 0 ? (T + ctas - 1) / ctas : 1;
 }
 
-// CTAs of the second kernel along the experts.
-int sum_ctas(int E) { return (E + kSumExperts - 1) / kSumExperts; }
-
 struct BalanceWorkspace {
   float* prob;
   int32_t* count;
@@ -1043,9 +1074,9 @@ struct BalanceWorkspace {
   int64_t bytes;
 };
 
-// ctas <= sm_count * kRouteCtasPerSm, so that the size does not depend on T.
+// The first kernel has at most two CTAs an SM, whatever T.
 BalanceWorkspace carve(void* base, int E, int B) {
-  const int64_t rows = int64_t(device_info().sm_count) * kRouteCtasPerSm + B;
+  const int64_t rows = int64_t(device_info().sm_count) * 2 + B;
   char* at = static_cast<char*>(base);
   auto take = [&](int64_t n) {
     char* p = at;
@@ -1138,37 +1169,29 @@ int32_t ep_route_balance(const ep_router_config* cfg, int32_t num_tokens, const 
   l.stream = static_cast<cudaStream_t>(stream);
   l.p.seq_start = d_seq_start;
   l.p.B = num_seqs;
-  l.p.tokens_per_cta = run_length(num_tokens);
-  l.p.ctas = (num_tokens + l.p.tokens_per_cta - 1) / l.p.tokens_per_cta;
   l.p.part_prob = w.prob;
   l.p.part_count = w.count;
   l.p.part_tokens = w.tokens;
   l.p.part_z = w.z;
   l.p.done = w.done;
-  if (l.p.ctas == 0) l.p.ctas = 1;      // no tokens: `done` is still cleared
-  cudaError_t e = with_shape(l.p.E, ld_logits, cfg->logits_bf16 != 0,
-                             cfg->score == EP_SCORE_SIGMOID, l);
-  if (note_cuda(e) != cudaSuccess) return EP_ERR_CUDA;
-  BalanceParams q;
-  q.seq_start = d_seq_start;
-  q.T = num_tokens;
-  q.E = l.p.E;
-  q.K = l.p.K;
-  q.B = num_seqs;
-  q.tokens_per_cta = l.p.tokens_per_cta;
-  q.part_prob = w.prob;
-  q.part_count = w.count;
-  q.part_tokens = w.tokens;
-  q.part_z = w.z;
-  q.expert_count = d_expert_count;
-  q.expert_prob = d_expert_prob;
-  q.seq_tokens = d_seq_tokens;
-  q.dots = w.dots;
-  q.seq_z = w.seq_z;
-  q.done = w.done;
-  q.loss = d_loss;
-  return status(launch_pdl(balance_sum_kernel, dim3(num_seqs, sum_ctas(q.E)), dim3(kSumThreads), 0,
-                           l.stream, q));
+  l.q.seq_start = d_seq_start;
+  l.q.T = num_tokens;
+  l.q.E = l.p.E;
+  l.q.K = l.p.K;
+  l.q.B = num_seqs;
+  l.q.part_prob = w.prob;
+  l.q.part_count = w.count;
+  l.q.part_tokens = w.tokens;
+  l.q.part_z = w.z;
+  l.q.expert_count = d_expert_count;
+  l.q.expert_prob = d_expert_prob;
+  l.q.seq_tokens = d_seq_tokens;
+  l.q.dots = w.dots;
+  l.q.seq_z = w.seq_z;
+  l.q.done = w.done;
+  l.q.loss = d_loss;
+  return status(with_shape(l.p.E, ld_logits, cfg->logits_bf16 != 0,
+                           cfg->score == EP_SCORE_SIGMOID, l));
 }
 
 int32_t ep_route_backward(const ep_router_config* cfg, int32_t num_tokens, const void* d_logits,
