@@ -32,6 +32,9 @@ struct RouteParams {
   const float* bias;         // [E] or null (sigmoid)
   const uint8_t* mask;       // [T] or null
   int T, E, K, G, kept;
+  int per;                   // experts a group
+  int per_log2;              // its logarithm where it is 4, 8, ... 128, else -1
+  uint32_t per_inverse;      // expert e is in group e * per_inverse >> 21 (e < 2048)
   bool renorm;
   float scale;
   int64_t* idx;              // [T, K]
@@ -204,37 +207,45 @@ __device__ __forceinline__ float group_score(float best, float second) {
   return SIG && second > -CUDART_INF_F ? best + second : best;
 }
 
-// Clears the choice scores of every group but the `kept` best.  Groups of
-// four times a power of two experts, up to 128, are whole aligned runs of
-// lanes of one vector (V = 4), and reduce by shuffles; other sizes go through
-// this warp's shared scratch of E floats.
+// Clears the choice scores of every group but the best.  Groups of 4, 8, ...
+// 128 experts are whole aligned runs of lanes of one vector (V = 4), and
+// reduce by shuffles; other sizes go through this warp's shared scratch of E
+// floats.
 template <int VPL, int V, bool SIG>
-__device__ void keep_groups(float (&c)[VPL], float* row, int E, int G, int kept, int lane) {
-  const int per = E / G;
+__device__ __forceinline__ void keep_groups(const RouteParams& p, float (&c)[VPL], float* row,
+                                            int lane) {
 #pragma unroll
   for (int r = 0; r < VPL; ++r) c[r] = fmaxf(c[r], -CUDART_INF_F);      // a NaN is not chosen
   if constexpr (V == 4) {
-    if ((per & (per - 1)) == 0 && per >= 4 && per <= 128) {
-      const int lanes = per / 4, per_vec = 128 / per;      // groups in a vector of all lanes
-      const int at = lane % per_vec * lanes;               // the first lane of this lane's group
+    if (p.per_log2 > 0) {
+      // a group is 2^span lanes of a vector, a vector 2^(5 - span) groups
+      const int span = p.per_log2 - 2, local = lane >> span, of_vector = 5 - span;
+      const int at = (lane & ((1 << of_vector) - 1)) << span;      // where group `lane` begins
       float mine = -CUDART_INF_F;
 #pragma unroll
       for (int v = 0; v < VPL / 4; ++v) {
-        float best = -CUDART_INF_F, second = -CUDART_INF_F;
+        const float hi0 = fmaxf(c[4 * v], c[4 * v + 1]), lo0 = fminf(c[4 * v], c[4 * v + 1]);
+        const float hi1 = fmaxf(c[4 * v + 2], c[4 * v + 3]), lo1 = fminf(c[4 * v + 2], c[4 * v + 3]);
+        float best = hi0, second = lo0;
+        top_two(best, second, hi1, lo1);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) top_two(best, second, c[4 * v + i], -CUDART_INF_F);
-        for (int d = 1; d < lanes; d <<= 1) {
-          const float b = __shfl_xor_sync(kFull, best, d);
-          const float s = __shfl_xor_sync(kFull, second, d);
-          top_two(best, second, b, s);
+        for (int i = 0; i < 5; ++i) {
+          if (i >= span) break;
+          const float b = __shfl_xor_sync(kFull, best, 1 << i);
+          if constexpr (SIG) {
+            const float s = __shfl_xor_sync(kFull, second, 1 << i);
+            top_two(best, second, b, s);
+          } else {
+            best = fmaxf(best, b);
+          }
         }
         const float score = __shfl_sync(kFull, group_score<SIG>(best, second), at);
-        if (lane / per_vec == v) mine = score;
+        if (lane >> of_vector == v) mine = score;
       }
-      const uint32_t keep = best_groups(mine, G, kept, lane);
+      const uint32_t keep = best_groups(mine, p.G, p.kept, lane);
 #pragma unroll
       for (int v = 0; v < VPL / 4; ++v) {
-        const int g = v * per_vec + lane / lanes;
+        const int g = (v << of_vector) + local;
         if (!((keep >> (g & 31)) & 1u)) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) c[4 * v + i] = -CUDART_INF_F;
@@ -246,17 +257,17 @@ __device__ void keep_groups(float (&c)[VPL], float* row, int E, int G, int kept,
 #pragma unroll
   for (int r = 0; r < VPL; ++r) {
     const int e = element_of<V>(r, lane);
-    if (e < E) row[e] = c[r];
+    if (e < p.E) row[e] = c[r];
   }
   __syncwarp();
   float best = -CUDART_INF_F, second = -CUDART_INF_F;
-  if (lane < G)
-    for (int i = 0; i < per; ++i) top_two(best, second, row[lane * per + i], -CUDART_INF_F);
-  const uint32_t keep = best_groups(group_score<SIG>(best, second), G, kept, lane);
+  if (lane < p.G)
+    for (int i = 0; i < p.per; ++i) top_two(best, second, row[lane * p.per + i], -CUDART_INF_F);
+  const uint32_t keep = best_groups(group_score<SIG>(best, second), p.G, p.kept, lane);
 #pragma unroll
   for (int r = 0; r < VPL; ++r) {
     const int e = element_of<V>(r, lane);
-    if (e < E && !((keep >> (e / per)) & 1u)) c[r] = -CUDART_INF_F;
+    if (e < p.E && !((keep >> (e * p.per_inverse >> 21)) & 1u)) c[r] = -CUDART_INF_F;
   }
   __syncwarp();
 }
@@ -427,7 +438,7 @@ __device__ __forceinline__ int route_token(const RouteParams& p, int t, int lane
     }
 #pragma unroll
     for (int r = 0; r < VPL; ++r) c[r] = x[r] == -CUDART_INF_F ? -CUDART_INF_F : s[r] + c[r];
-    if (p.G > 1) keep_groups<VPL, V, SIG>(c, row, p.E, p.G, p.kept, lane);
+    if (p.G > 1) keep_groups<VPL, V, SIG>(p, c, row, lane);
     best = c[0];
 #pragma unroll
     for (int r = 1; r < VPL; ++r) best = fmaxf(best, c[r]);
@@ -451,7 +462,7 @@ __device__ __forceinline__ int route_token(const RouteParams& p, int t, int lane
       float c[VPL];
 #pragma unroll
       for (int r = 0; r < VPL; ++r) c[r] = x[r];
-      keep_groups<VPL, V, SIG>(c, row, p.E, p.G, p.kept, lane);
+      keep_groups<VPL, V, SIG>(p, c, row, lane);
       best = c[0];
 #pragma unroll
       for (int r = 1; r < VPL; ++r) best = fmaxf(best, c[r]);
@@ -1116,6 +1127,13 @@ bool route_args(const ep_router_config* cfg, int32_t T, const void* d_logits, in
   p->G = cfg->num_groups;
   p->kept = cfg->topk_groups;
   if (p->kept == p->G) p->G = p->kept = 1;
+  p->per = p->E / p->G;
+  p->per_log2 = -1;
+  for (int i = 2; i <= 7; ++i)
+    if (p->per == 1 << i) p->per_log2 = i;
+  // floor(2^21 / per) + 1 is off by under 2^-21 of e < 2^11, less than the
+  // 1 / per that the quotient is from the next whole number (per <= 2^10)
+  p->per_inverse = (1u << 21) / uint32_t(p->per) + 1u;
   p->renorm = cfg->renormalize != 0;
   p->scale = cfg->route_scale;
   p->idx = d_idx;
