@@ -2,12 +2,13 @@
 // (ep_route), the same with the balance and z losses (ep_route_balance), and
 // the gradient of both by the logits (ep_route_backward).
 //
-// One warp owns one token at a time; lane `lane` holds VPL of its E logits
-// in registers (element_of below), so a token's row is read once and every
-// reduction over experts is a warp reduction.  The statistics of the losses
-// are summed in registers over a CTA's run of tokens, then once per (CTA,
-// sequence) in a fixed order: no floating-point atomics, so the same inputs
-// give the same bits.
+// A tile of 8, 16 or 32 lanes of a warp owns one token at a time and holds
+// its E logits in registers, so that a token's row is read once and every
+// sum over experts is a few shuffles; narrow tiles (few experts) put several
+// tokens in a warp, which shares the instructions that do not depend on the
+// number of experts.  The statistics of the losses are summed in registers
+// over a CTA's run of tokens, then once per (CTA, sequence), in a fixed
+// order: no floating-point atomics, so the same inputs give the same bits.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -25,6 +26,22 @@ constexpr int kRouteThreads = 256;
 constexpr int kRouteWarps = kRouteThreads / 32;
 constexpr int kMaxGroups = 32;
 constexpr unsigned kFull = 0xffffffffu;
+
+// A tile of `L` lanes with `N` fp32 or bf16 logits each, loaded in vectors of
+// `V` neighbours (1 or 4).
+template <int L, int N, int V, bool BF16>
+struct Shape {
+  static constexpr int kLanes = L, kValues = N, kVec = V;
+  static constexpr bool kBf16 = BF16;
+  static constexpr int kTiles = 32 / L;             // tokens of a warp
+  static constexpr int kRuns = 32 / L < N ? 32 / L : N;   // of a lane's logits, see choose()
+  static constexpr int kSlots = L == 8 ? 2 : 1;     // candidates a lane
+  static constexpr int kCandidates = L * kSlots;    // of a token
+  // logits that are loaded a token ahead: where two rows fit the registers
+  static constexpr bool kAhead = N <= 16;
+  // Expert of register r of lane l of the tile.
+  static __device__ __forceinline__ int expert(int r, int l) { return (r / V * L + l) * V + r % V; }
+};
 
 struct RouteParams {
   const void* logits;        // [T, ld] fp32 or bf16
@@ -50,72 +67,124 @@ struct RouteParams {
   unsigned* done;            // cleared for the second kernel
 };
 
-// Index of register r of this lane: one logit a load (V = 1), or V
-// neighbouring ones.
-template <int V>
-__device__ __forceinline__ int element_of(int r, int lane) {
-  return (r / V * 32 + lane) * V + r % V;
-}
+// ---- rows -----------------------------------------------------------------
 
-// A token's logits in registers, -inf past the last expert.
-template <int VPL, int V, bool BF16>
-__device__ __forceinline__ void load_row(const void* base, int64_t offset, int E, int lane,
-                                         float (&x)[VPL]) {
-#pragma unroll
-  for (int r = 0; r < VPL; r += V) {
-    const int e = element_of<V>(r, lane);
-    if constexpr (V == 1) {
-      if constexpr (BF16) {
-        x[r] = e < E ? __uint_as_float(uint32_t(static_cast<const uint16_t*>(base)[offset + e]) << 16)
-                     : -CUDART_INF_F;
-      } else {
-        x[r] = e < E ? static_cast<const float*>(base)[offset + e] : -CUDART_INF_F;
-      }
-    } else {
-      static_assert(V == 4, "vectors of four logits");
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[r + i] = -CUDART_INF_F;
-      if (e < E) {
-        if constexpr (BF16) {
-          const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) +
-                                                          offset + e);
-          x[r] = bf16_lo(v.x);
-          x[r + 1] = bf16_hi(v.x);
-          x[r + 2] = bf16_lo(v.y);
-          x[r + 3] = bf16_hi(v.y);
-        } else {
-          const float4 v =
-              *reinterpret_cast<const float4*>(static_cast<const float*>(base) + offset + e);
-          x[r] = v.x;
-          x[r + 1] = v.y;
-          x[r + 2] = v.z;
-          x[r + 3] = v.w;
-        }
-      }
-    }
-  }
-}
-
-template <bool BF16>
+template <class S>
 __device__ __forceinline__ float load_one(const void* base, int64_t at) {
-  if constexpr (BF16)
+  if constexpr (S::kBf16)
     return __uint_as_float(uint32_t(static_cast<const uint16_t*>(base)[at]) << 16);
   else
     return static_cast<const float*>(base)[at];
 }
 
-__device__ __forceinline__ float warp_sum(float v) {
+// A token's logits in registers, -inf past the last expert and, where !have,
+// throughout.
+template <class S>
+__device__ __forceinline__ void load_row(const void* base, int64_t offset, int E, int l, bool have,
+                                         float (&x)[S::kValues]) {
+  const int limit = have ? E : 0;
 #pragma unroll
-  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(kFull, v, d);
+  for (int r = 0; r < S::kValues; r += S::kVec) {
+    const int e = S::expert(r, l);
+#pragma unroll
+    for (int i = 0; i < S::kVec; ++i) x[r + i] = -CUDART_INF_F;
+    if (e >= limit) continue;
+    if constexpr (S::kVec == 1) {
+      x[r] = load_one<S>(base, offset + e);
+    } else if constexpr (S::kBf16) {
+      const uint2 v =
+          *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + offset + e);
+      x[r] = bf16_lo(v.x);
+      x[r + 1] = bf16_hi(v.x);
+      x[r + 2] = bf16_lo(v.y);
+      x[r + 3] = bf16_hi(v.y);
+    } else {
+      const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(base) + offset + e);
+      x[r] = v.x;
+      x[r + 1] = v.y;
+      x[r + 2] = v.z;
+      x[r + 3] = v.w;
+    }
+  }
+}
+
+template <class S>
+__device__ __forceinline__ void store_row(void* base, int64_t offset, int E, int l,
+                                          const float (&g)[S::kValues]) {
+#pragma unroll
+  for (int r = 0; r < S::kValues; r += S::kVec) {
+    const int e = S::expert(r, l);
+    if (e >= E) continue;
+    if constexpr (S::kVec == 1) {
+      if constexpr (S::kBf16)
+        static_cast<__nv_bfloat16*>(base)[offset + e] = __float2bfloat16_rn(g[r]);
+      else
+        static_cast<float*>(base)[offset + e] = g[r];
+    } else if constexpr (S::kBf16) {
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(base) + offset + e) =
+          make_uint2(pack_bf16x2(g[r], g[r + 1]), pack_bf16x2(g[r + 2], g[r + 3]));
+    } else {
+      *reinterpret_cast<float4*>(static_cast<float*>(base) + offset + e) =
+          make_float4(g[r], g[r + 1], g[r + 2], g[r + 3]);
+    }
+  }
+}
+
+// Floats of a row of E in shared memory: whole vectors of four.
+__host__ __device__ __forceinline__ int padded_row(int E) { return (E + 3) & ~3; }
+
+// A lane's values of a row of E floats in shared memory (16-byte aligned).
+template <class S>
+__device__ __forceinline__ void read_row(const float* row, int E, int l, float (&v)[S::kValues]) {
+#pragma unroll
+  for (int r = 0; r < S::kValues; r += S::kVec) {
+    const int e = S::expert(r, l);
+    if constexpr (S::kVec == 4) {
+      float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (e < E) f = *reinterpret_cast<const float4*>(row + e);
+      v[r] = f.x;
+      v[r + 1] = f.y;
+      v[r + 2] = f.z;
+      v[r + 3] = f.w;
+    } else {
+      v[r] = e < E ? row[e] : 0.0f;
+    }
+  }
+}
+
+// ---- tiles ----------------------------------------------------------------
+
+template <int L>
+__device__ __forceinline__ float tile_sum(float v) {
+#pragma unroll
+  for (int d = L / 2; d; d >>= 1) v += __shfl_xor_sync(kFull, v, d);
   return v;
 }
 
-// Largest of the lanes' values; a NaN counts only where all are NaN.
-__device__ __forceinline__ float warp_max(float v) {
-  float m;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
-  return m;
+// Largest of a tile's values; a NaN counts only where all are NaN.
+template <int L>
+__device__ __forceinline__ float tile_max(float v) {
+  if constexpr (L == 32) {
+    float m;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+    return m;
+  } else {
+#pragma unroll
+    for (int d = L / 2; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, d));
+    return v;
+  }
 }
+
+// Bits of a ballot that belong to this lane's tile, from bit 0.
+template <int L>
+__device__ __forceinline__ uint32_t tile_bits(uint32_t ballot, int lane) {
+  if constexpr (L == 32)
+    return ballot;
+  else
+    return ballot >> (lane & ~(L - 1)) & ((1u << L) - 1u);
+}
+
+// ---- scores ---------------------------------------------------------------
 
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -141,60 +210,68 @@ __device__ __forceinline__ float soft_score(float l, float top) {
   return fast_exp2((l - top) * kLog2e);
 }
 
+template <int N>
+__device__ __forceinline__ float largest(const float (&x)[N]) {
+  float m = x[0];
+#pragma unroll
+  for (int r = 1; r < N; ++r) m = fmaxf(m, x[r]);
+  return m;
+}
+
 // Softmax scores of a token before their division: s = exp(x - top), top the
 // row's maximum; returns their total.  -inf scores 0, and so does all of a
 // row of nothing else.
-template <int VPL>
-__device__ __forceinline__ float soft_scores(const float (&x)[VPL], float (&s)[VPL], float top) {
+template <class S>
+__device__ __forceinline__ float soft_scores(const float (&x)[S::kValues], float (&s)[S::kValues],
+                                             float top) {
   const float base = top == -CUDART_INF_F ? 0.0f : top;
   float total = 0.0f;
 #pragma unroll
-  for (int r = 0; r < VPL; ++r) {
+  for (int r = 0; r < S::kValues; ++r) {
     s[r] = soft_score(x[r], base);
     total += s[r];
   }
-  return warp_sum(total);
+  return tile_sum<S::kLanes>(total);
 }
 
-// Scores of a token as soft_scores or sigmoid has them, their total, and
+// Scores of a token, as soft_scores or sigmoid has them, their total, and
 // (softmax) the row's maximum.
-template <int VPL, bool SIG>
-__device__ __forceinline__ float scores(const float (&x)[VPL], float (&s)[VPL], float* top) {
+template <class S, bool SIG>
+__device__ __forceinline__ float scores(const float (&x)[S::kValues], float (&s)[S::kValues],
+                                        float* top) {
   if constexpr (SIG) {
     float total = 0.0f;
 #pragma unroll
-    for (int r = 0; r < VPL; ++r) {
+    for (int r = 0; r < S::kValues; ++r) {
       s[r] = sigmoid(x[r]);      // exp2(+inf) = inf, its reciprocal 0
       total += s[r];
     }
     *top = 0.0f;
-    return warp_sum(total);
+    return tile_sum<S::kLanes>(total);
   } else {
-    float m = x[0];
-#pragma unroll
-    for (int r = 1; r < VPL; ++r) m = fmaxf(m, x[r]);
-    *top = warp_max(m);
-    return soft_scores<VPL>(x, s, *top);
+    *top = tile_max<S::kLanes>(largest(x));
+    return soft_scores<S>(x, s, *top);
   }
 }
 
-// The `kept` best of G groups (G <= 32) by the scores that lanes g < G hold,
-// as a bit mask; equal scores go to the lower group, -inf is never kept.
+// ---- groups ---------------------------------------------------------------
+
+// The `kept` best of G groups by the scores that lanes l < G hold, as a bit
+// mask; equal scores go to the lower group, -inf is never kept.  No NaN
+// reaches this.
+template <class S>
 __device__ __forceinline__ uint32_t best_groups(float score, int G, int kept, int lane) {
-  uint32_t keep = 0;
-  float left = lane < G ? score : -CUDART_INF_F;
-  for (int i = 0; i < kept; ++i) {
-    const float top = warp_max(left);
-    const uint32_t at = __ballot_sync(kFull, left == top);
-    // no NaN reaches this, so that a lane always answers
-    const int g = __ffs(at) - 1;
-    keep |= top > -CUDART_INF_F ? 1u << g : 0u;
-    if (lane == g) left = -CUDART_INF_F;
+  const int l = lane % S::kLanes;
+  int before = 0;
+  for (int g = 0; g < G; ++g) {
+    const float o = __shfl_sync(kFull, score, g, S::kLanes);
+    before += o > score || (o == score && g < l) ? 1 : 0;
   }
-  return keep;
+  const bool in = l < G && before < kept && score > -CUDART_INF_F;
+  return tile_bits<S::kLanes>(__ballot_sync(kFull, in), lane);
 }
 
-// Adds (best, second) of another set to a running pair.
+// Adds (b, s) of another set to a running (best, second).
 __device__ __forceinline__ void top_two(float& best, float& second, float b, float s) {
   second = fmaxf(fminf(best, b), fmaxf(second, s));
   best = fmaxf(best, b);
@@ -208,28 +285,32 @@ __device__ __forceinline__ float group_score(float best, float second) {
 }
 
 // Clears the choice scores of every group but the best.  Groups of 4, 8, ...
-// 128 experts are whole aligned runs of lanes of one vector (V = 4), and
-// reduce by shuffles; other sizes go through this warp's shared scratch of E
-// floats.
-template <int VPL, int V, bool SIG>
-__device__ __forceinline__ void keep_groups(const RouteParams& p, float (&c)[VPL], float* row,
+// experts up to four a lane are whole aligned runs of the lanes of one
+// vector (V = 4), and reduce by shuffles; other sizes go through the tile's
+// shared scratch of E floats.
+template <class S, bool SIG>
+__device__ __forceinline__ void keep_groups(const RouteParams& p, float (&c)[S::kValues], float* row,
                                             int lane) {
+  constexpr int L = S::kLanes;
+  const int l = lane % L;
 #pragma unroll
-  for (int r = 0; r < VPL; ++r) c[r] = fmaxf(c[r], -CUDART_INF_F);      // a NaN is not chosen
-  if constexpr (V == 4) {
-    if (p.per_log2 > 0) {
-      // a group is 2^span lanes of a vector, a vector 2^(5 - span) groups
-      const int span = p.per_log2 - 2, local = lane >> span, of_vector = 5 - span;
-      const int at = (lane & ((1 << of_vector) - 1)) << span;      // where group `lane` begins
+  for (int r = 0; r < S::kValues; ++r) c[r] = fmaxf(c[r], -CUDART_INF_F);   // a NaN is not chosen
+  if constexpr (S::kVec == 4) {
+    constexpr int kLog = L == 8 ? 3 : L == 16 ? 4 : 5;
+    if (p.per_log2 > 0 && p.per_log2 - 2 <= kLog) {
+      // a group is 2^span lanes of a vector, a vector 2^(kLog - span) groups
+      const int span = p.per_log2 - 2, of_vector = kLog - span;
+      const int at = (l & ((1 << of_vector) - 1)) << span;      // where group l begins
       float mine = -CUDART_INF_F;
 #pragma unroll
-      for (int v = 0; v < VPL / 4; ++v) {
+      for (int v = 0; v < S::kValues / 4; ++v) {
         const float hi0 = fmaxf(c[4 * v], c[4 * v + 1]), lo0 = fminf(c[4 * v], c[4 * v + 1]);
-        const float hi1 = fmaxf(c[4 * v + 2], c[4 * v + 3]), lo1 = fminf(c[4 * v + 2], c[4 * v + 3]);
+        const float hi1 = fmaxf(c[4 * v + 2], c[4 * v + 3]);
+        const float lo1 = fminf(c[4 * v + 2], c[4 * v + 3]);
         float best = hi0, second = lo0;
         top_two(best, second, hi1, lo1);
 #pragma unroll
-        for (int i = 0; i < 5; ++i) {
+        for (int i = 0; i < kLog; ++i) {
           if (i >= span) break;
           const float b = __shfl_xor_sync(kFull, best, 1 << i);
           if constexpr (SIG) {
@@ -239,13 +320,13 @@ __device__ __forceinline__ void keep_groups(const RouteParams& p, float (&c)[VPL
             best = fmaxf(best, b);
           }
         }
-        const float score = __shfl_sync(kFull, group_score<SIG>(best, second), at);
-        if (lane >> of_vector == v) mine = score;
+        const float score = __shfl_sync(kFull, group_score<SIG>(best, second), at, L);
+        if (l >> of_vector == v) mine = score;
       }
-      const uint32_t keep = best_groups(mine, p.G, p.kept, lane);
+      const uint32_t keep = best_groups<S>(mine, p.G, p.kept, lane);
 #pragma unroll
-      for (int v = 0; v < VPL / 4; ++v) {
-        const int g = (v << of_vector) + local;
+      for (int v = 0; v < S::kValues / 4; ++v) {
+        const int g = (v << of_vector) + (l >> span);
         if (!((keep >> (g & 31)) & 1u)) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) c[4 * v + i] = -CUDART_INF_F;
@@ -255,66 +336,70 @@ __device__ __forceinline__ void keep_groups(const RouteParams& p, float (&c)[VPL
     }
   }
 #pragma unroll
-  for (int r = 0; r < VPL; ++r) {
-    const int e = element_of<V>(r, lane);
+  for (int r = 0; r < S::kValues; ++r) {
+    const int e = S::expert(r, l);
     if (e < p.E) row[e] = c[r];
   }
   __syncwarp();
   float best = -CUDART_INF_F, second = -CUDART_INF_F;
-  if (lane < p.G)
-    for (int i = 0; i < p.per; ++i) top_two(best, second, row[lane * p.per + i], -CUDART_INF_F);
-  const uint32_t keep = best_groups(group_score<SIG>(best, second), p.G, p.kept, lane);
+  if (l < p.G)
+    for (int i = 0; i < p.per; ++i) top_two(best, second, row[l * p.per + i], -CUDART_INF_F);
+  const uint32_t keep = best_groups<S>(group_score<SIG>(best, second), p.G, p.kept, lane);
 #pragma unroll
-  for (int r = 0; r < VPL; ++r) {
-    const int e = element_of<V>(r, lane);
+  for (int r = 0; r < S::kValues; ++r) {
+    const int e = S::expert(r, l);
     if (e < p.E && !((keep >> (e * p.per_inverse >> 21)) & 1u)) c[r] = -CUDART_INF_F;
   }
   __syncwarp();
 }
 
-// The K largest of a warp's choice scores one after another, equal ones by
-// ascending index: lane k returns the k-th expert or -1.
-template <int VPL, int V>
-__device__ __noinline__ int choose_in_turn(float (&c)[VPL], int K, int lane) {
+// ---- choice ---------------------------------------------------------------
+
+// The K largest of a tile's choice scores one after another, equal ones by
+// ascending index: lane k of the tile returns the k-th expert or -1.
+template <class S>
+__device__ __noinline__ int choose_in_turn(float (&c)[S::kValues], int K, int l) {
   int mine = -1;
   for (int k = 0; k < K; ++k) {
     float best = -CUDART_INF_F;
     int at = 0x7fffffff;
 #pragma unroll
-    for (int r = 0; r < VPL; ++r) {
+    for (int r = 0; r < S::kValues; ++r) {
       if (c[r] > best) {
         best = c[r];
-        at = element_of<V>(r, lane);
+        at = S::expert(r, l);
       }
     }
-    const float top = warp_max(best);
-    if (top == -CUDART_INF_F) break;
-    const int win = __reduce_min_sync(kFull, best == top ? at : 0x7fffffff);
+    const float top = tile_max<S::kLanes>(best);
+    int win = best == top && top > -CUDART_INF_F ? at : 0x7fffffff;
 #pragma unroll
-    for (int r = 0; r < VPL; ++r)
-      if (element_of<V>(r, lane) == win) c[r] = -CUDART_INF_F;
-    if (lane == k) mine = win;
+    for (int d = S::kLanes / 2; d; d >>= 1) win = min(win, __shfl_xor_sync(kFull, win, d));
+#pragma unroll
+    for (int r = 0; r < S::kValues; ++r)
+      if (S::expert(r, l) == win) c[r] = -CUDART_INF_F;
+    if (l == k && top > -CUDART_INF_F) mine = win;
   }
   return mine;
 }
 
-// A set of the registers 0 .. VPL - 1.
-template <int VPL>
+// A set of the registers 0 .. N - 1.
+template <int N>
 struct RegisterSet {
-  using Bits = std::conditional_t<(VPL > 32), unsigned long long, uint32_t>;
+  using Bits = std::conditional_t<(N > 32), unsigned long long, uint32_t>;
   Bits bits = 0;
   __device__ __forceinline__ void add(int r, bool in) { bits |= in ? Bits(1) << r : Bits(0); }
   __device__ __forceinline__ int first() const {
-    if constexpr (VPL > 32) return __ffsll(bits) - 1;
+    if constexpr (N > 32) return __ffsll(bits) - 1;
     return __ffs(bits) - 1;
   }
   __device__ __forceinline__ void drop_first() { bits &= bits - 1; }
 };
 
-// What a warp's lanes share while they choose: candidates, one a lane.
-struct Candidates {
-  int expert[32];
-  unsigned long long key[32];
+// What a tile's lanes share while they choose.
+template <class S>
+struct __align__(16) Candidates {
+  unsigned long long key[S::kCandidates];
+  int expert[S::kCandidates];
 };
 
 // Order of choice as one number: the higher score first, then the lower
@@ -327,250 +412,271 @@ __device__ __forceinline__ unsigned long long choice_key(float c, int e) {
 
 // A lane's share of a token's choice: expert e, with logit l, takes `rank`;
 // e = -1 where the rank stays empty, rank >= K where the lane has none.
+template <class S>
 struct Chosen {
-  int e, rank;
-  float l;
+  int e[S::kSlots], rank[S::kSlots];
+  float l[S::kSlots];
 };
 
-// Chooses the K largest of a warp's choice scores c, `best` the lane's
-// largest; -inf and NaN are never chosen.  The K-th largest of the lanes'
-// largest (equal ones taken together) is a bound that at least K scores
-// reach, where K can be chosen at all; with scores spread over the lanes few
-// more do.  Those become candidates, one a lane, that each count the
-// candidates before them.  More than 32 candidates (many equal scores, K
-// near 32) are chosen in turn.
-template <int VPL, int V, bool BF16, bool SIG>
-__device__ __forceinline__ Chosen choose(const RouteParams& p, const float (&c)[VPL], float best,
-                                         const void* logits, int64_t offset, int lane,
-                                         Candidates& cand) {
+// Chooses the K largest of a tile's choice scores c; -inf and NaN are never
+// chosen.  A lane's scores are taken as kRuns runs, 32 runs a token, and the
+// K-th largest of the runs' maxima (equal ones of different lanes taken
+// together) is a bound that at least K scores reach, where K can be chosen
+// at all; with the best scores spread over the runs few more do.  Those
+// become candidates that each count the candidates before them.  More than
+// kCandidates (many equal scores, K near the lanes) are chosen in turn.
+template <class S, bool SIG>
+__device__ __forceinline__ Chosen<S> choose(const RouteParams& p, const float (&c)[S::kValues],
+                                            int64_t offset, int lane, Candidates<S>& cand) {
+  constexpr int L = S::kLanes, kRun = S::kValues / S::kRuns;
+  const int l = lane % L;
+  float top[S::kRuns];      // the runs' maxima, in descending order
+#pragma unroll
+  for (int i = 0; i < S::kRuns; ++i) {
+    top[i] = -CUDART_INF_F;
+#pragma unroll
+    for (int r = 0; r < kRun; ++r) top[i] = fmaxf(top[i], c[i * kRun + r]);
+  }
+  const auto order = [&](int a, int b) {
+    const float hi = fmaxf(top[a], top[b]);
+    top[b] = fminf(top[a], top[b]);
+    top[a] = hi;
+  };
+  if constexpr (S::kRuns == 2) order(0, 1);
+  if constexpr (S::kRuns == 4) {
+    order(0, 1);
+    order(2, 3);
+    order(0, 2);
+    order(1, 3);
+    order(1, 2);
+  }
   float bound = -CUDART_INF_F;
 #pragma unroll 4
   for (int k = 0; k < p.K; ++k) {
-    bound = warp_max(best);
-    best = best == bound ? -CUDART_INF_F : best;
+    bound = tile_max<L>(top[0]);
+    const bool drop = top[0] == bound;
+#pragma unroll
+    for (int i = 0; i < S::kRuns - 1; ++i) top[i] = drop ? top[i + 1] : top[i];
+    top[S::kRuns - 1] = drop ? -CUDART_INF_F : top[S::kRuns - 1];
   }
   bound = fmaxf(bound, -3.402823466e38f);
-  RegisterSet<VPL> mine;
+  RegisterSet<S::kValues> mine;
 #pragma unroll
-  for (int r = 0; r < VPL; ++r) mine.add(r, c[r] >= bound);
-  const uint32_t before = lanemask_lt();
+  for (int r = 0; r < S::kValues; ++r) mine.add(r, c[r] >= bound);
+  const uint32_t before = (1u << l) - 1u;
   int n = 0;
   for (;;) {
-    const uint32_t who = __ballot_sync(kFull, mine.bits != 0);
-    if (who == 0) break;
+    const uint32_t all = __ballot_sync(kFull, mine.bits != 0);
+    if (all == 0) break;
+    const uint32_t who = tile_bits<L>(all, lane);
     const int at = n + __popc(who & before);
-    if (mine.bits != 0 && at < 32) cand.expert[at] = element_of<V>(mine.first(), lane);
+    if (mine.bits != 0 && at < S::kCandidates) cand.expert[at] = S::expert(mine.first(), l);
     mine.drop_first();
     n += __popc(who);
   }
   __syncwarp();
-  Chosen out = {-1, lane, 0.0f};
-  if (n > 32) {
-    float left[VPL];      // a copy: c itself then stays in registers
+  Chosen<S> out;
 #pragma unroll
-    for (int r = 0; r < VPL; ++r) left[r] = c[r];
-    out.e = choose_in_turn<VPL, V>(left, p.K, lane);
-    if (out.e >= 0) out.l = load_one<BF16>(logits, offset + out.e);
+  for (int i = 0; i < S::kSlots; ++i) {
+    out.e[i] = -1;
+    out.rank[i] = l + i * L;
+    out.l[i] = 0.0f;
+  }
+  if (__any_sync(kFull, n > S::kCandidates)) {
+    float left[S::kValues];      // a copy: c itself then stays in registers
+#pragma unroll
+    for (int r = 0; r < S::kValues; ++r) left[r] = c[r];
+    out.e[0] = choose_in_turn<S>(left, p.K, l);
+    if (out.e[0] >= 0) out.l[0] = load_one<S>(p.logits, offset + out.e[0]);
     return out;
   }
-  unsigned long long key = 0;
-  if (lane < n) {
-    out.e = cand.expert[lane];
-    out.l = load_one<BF16>(logits, offset + out.e);
-    float score = out.l;
-    if constexpr (SIG) score = sigmoid(out.l) + (p.bias != nullptr ? p.bias[out.e] : 0.0f);
-    key = choice_key(score, out.e);
-  }
-  cand.key[lane] = key;      // the rest come after any candidate
-  __syncwarp();
-  int rank = 0;
-  for (int i = 0; i < n; i += 4) {
+  unsigned long long key[S::kSlots];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) rank += cand.key[i + j] > key ? 1 : 0;
+  for (int i = 0; i < S::kSlots; ++i) {
+    key[i] = 0;      // past the candidates: after all of them
+    if (l + i * L < n) {
+      const int e = cand.expert[l + i * L];
+      out.e[i] = e;
+      out.l[i] = load_one<S>(p.logits, offset + e);
+      float score = out.l[i];
+      if constexpr (SIG) score = sigmoid(score) + (p.bias != nullptr ? p.bias[e] : 0.0f);
+      key[i] = choice_key(score, e);
+    }
+    cand.key[l + i * L] = key[i];
   }
   __syncwarp();
-  if (lane < n) out.rank = rank;
+  int rank[S::kSlots] = {};
+  for (int j = 0; j < n; j += 4) {
+    const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(cand.key + j);
+    const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(cand.key + j + 2);
+#pragma unroll
+    for (int i = 0; i < S::kSlots; ++i)
+      rank[i] += (a.x > key[i] ? 1 : 0) + (a.y > key[i] ? 1 : 0) + (b.x > key[i] ? 1 : 0) +
+                 (b.y > key[i] ? 1 : 0);
+  }
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < S::kSlots; ++i)
+    if (l + i * L < n) out.rank[i] = rank[i];
   return out;
 }
 
-// Floats of a row of E in shared memory: whole vectors of four.
-__host__ __device__ __forceinline__ int padded_row(int E) { return (E + 3) & ~3; }
+// ---- a token --------------------------------------------------------------
 
-// A lane's values of a row of E floats in shared memory (16-byte aligned).
-template <int VPL, int V>
-__device__ __forceinline__ void read_row(const float* row, int E, int lane, float (&v)[VPL]) {
-#pragma unroll
-  for (int r = 0; r < VPL; r += V) {
-    const int e = element_of<V>(r, lane);
-    if constexpr (V == 4) {
-      float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (e < E) f = *reinterpret_cast<const float4*>(row + e);
-      v[r] = f.x;
-      v[r + 1] = f.y;
-      v[r + 2] = f.z;
-      v[r + 3] = f.w;
-    } else {
-      v[r] = e < E ? row[e] : 0.0f;
-    }
-  }
-}
-
-// One token, given its logits: choice and gate weights.  Leaves the scores in
-// `s` with their total and the row's maximum; softmax needs those only for
-// statistics (STATS) or for weights that are not renormalised.  Returns the
-// lane's chosen expert or -1.
-template <int VPL, int V, bool BF16, bool SIG, bool STATS>
-__device__ __forceinline__ int route_token(const RouteParams& p, int t, int lane, float* row,
-                                           Candidates& cand, const float* bias,
-                                           const float (&x)[VPL], float (&s)[VPL], float* total,
-                                           float* top) {
-  float best, scale = p.scale;
+// One token of each tile, given its logits: choice and gate weights, written
+// where `live`.  Leaves the scores in `s` with their total and the row's
+// maximum; softmax needs those only for statistics (STATS) or for weights
+// that are not renormalised.  Returns the choice, e = -1 for what is not
+// taken.
+template <class S, bool SIG, bool STATS>
+__device__ __forceinline__ Chosen<S> route_token(const RouteParams& p, int t, bool live, int lane,
+                                                 float* row, Candidates<S>& cand,
+                                                 const float* bias, const float (&x)[S::kValues],
+                                                 float (&s)[S::kValues], float* total,
+                                                 float* top) {
+  constexpr int L = S::kLanes;
+  const int l = lane % L;
   const int64_t offset = int64_t(t) * p.ld;
-  Chosen mine;
+  float scale = p.scale;
+  float c[S::kValues];
   if constexpr (SIG) {
-    *total = scores<VPL, SIG>(x, s, top);
-    float c[VPL];
+    *total = scores<S, SIG>(x, s, top);
     if (p.bias != nullptr) {
-      read_row<VPL, V>(bias, p.E, lane, c);
+      read_row<S>(bias, p.E, l, c);
     } else {
 #pragma unroll
-      for (int r = 0; r < VPL; ++r) c[r] = 0.0f;
+      for (int r = 0; r < S::kValues; ++r) c[r] = 0.0f;
     }
 #pragma unroll
-    for (int r = 0; r < VPL; ++r) c[r] = x[r] == -CUDART_INF_F ? -CUDART_INF_F : s[r] + c[r];
-    if (p.G > 1) keep_groups<VPL, V, SIG>(p, c, row, lane);
-    best = c[0];
-#pragma unroll
-    for (int r = 1; r < VPL; ++r) best = fmaxf(best, c[r]);
-    mine = choose<VPL, V, BF16, SIG>(p, c, best, p.logits, offset, lane, cand);
+    for (int r = 0; r < S::kValues; ++r)
+      c[r] = x[r] == -CUDART_INF_F ? -CUDART_INF_F : s[r] + c[r];
   } else {
-    best = x[0];
-#pragma unroll
-    for (int r = 1; r < VPL; ++r) best = fmaxf(best, x[r]);
-    *top = warp_max(best);
+    *top = tile_max<L>(largest(x));
     if (STATS || !p.renorm) {
-      *total = soft_scores<VPL>(x, s, *top);
+      *total = soft_scores<S>(x, s, *top);
       if (!p.renorm) scale = scale / *total;
       if (*total != *total) scale = *total;
     } else {
-      bool nan = false;
+      // NaN where a logit is, or where -inf meets +inf, whose weights are NaN
+      float any = 0.0f;
 #pragma unroll
-      for (int r = 0; r < VPL; ++r) nan |= x[r] != x[r];
-      if (__any_sync(kFull, nan)) scale = CUDART_NAN_F;
+      for (int r = 0; r < S::kValues; ++r) any += x[r];
+      if (tile_bits<L>(__ballot_sync(kFull, any != any), lane) != 0) scale = CUDART_NAN_F;
     }
-    if (p.G > 1) {
-      float c[VPL];
 #pragma unroll
-      for (int r = 0; r < VPL; ++r) c[r] = x[r];
-      keep_groups<VPL, V, SIG>(p, c, row, lane);
-      best = c[0];
-#pragma unroll
-      for (int r = 1; r < VPL; ++r) best = fmaxf(best, c[r]);
-      mine = choose<VPL, V, BF16, SIG>(p, c, best, p.logits, offset, lane, cand);
-    } else {
-      mine = choose<VPL, V, BF16, SIG>(p, x, best, p.logits, offset, lane, cand);
-    }
+    for (int r = 0; r < S::kValues; ++r) c[r] = x[r];
   }
-  const bool taken = mine.e >= 0 && mine.rank < p.K;
-  float w = 0.0f;
-  if (taken) w = SIG ? sigmoid(mine.l) : soft_score(mine.l, *top);
+  if (p.G > 1) keep_groups<S, SIG>(p, c, row, lane);
+  Chosen<S> out = choose<S, SIG>(p, c, offset, lane, cand);
+  float w[S::kSlots], sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < S::kSlots; ++i) {
+    const bool taken = out.e[i] >= 0 && out.rank[i] < p.K;
+    w[i] = 0.0f;
+    if (taken) w[i] = SIG ? sigmoid(out.l[i]) : soft_score(out.l[i], *top);
+    sum += w[i];
+    if (!taken) out.e[i] = -1;
+  }
   if (p.renorm) {
-    const float sum = warp_sum(w);
+    sum = tile_sum<L>(sum);
     scale = sum == 0.0f ? 0.0f : scale / sum;
   }
-  if (mine.rank < p.K) {
-    const int64_t at = int64_t(t) * p.K + mine.rank;
-    p.idx[at] = mine.e;
-    p.w[at] = taken ? w * scale : 0.0f;
+#pragma unroll
+  for (int i = 0; i < S::kSlots; ++i) {
+    if (live && out.rank[i] < p.K) {
+      const int64_t at = int64_t(t) * p.K + out.rank[i];
+      p.idx[at] = out.e[i];
+      p.w[at] = out.e[i] >= 0 ? w[i] * scale : 0.0f;
+    }
   }
-  return taken ? mine.e : -1;
+  return out;
 }
 
-__device__ __forceinline__ void route_masked(const RouteParams& p, int t, int lane) {
-  if (lane < p.K) {
-    p.idx[int64_t(t) * p.K + lane] = -1;
-    p.w[int64_t(t) * p.K + lane] = 0.0f;
-  }
-}
+// CTAs of a per-token kernel that shall share an SM, for its register limit:
+// 32 or 24 warps with the widths of common layers.
+template <class S>
+constexpr int kRouteShare = S::kValues <= 8 ? 4 : S::kValues <= 16 ? 3 : 1;
 
-// Logits that a warp loads ahead of the token it works on: the next token's,
-// where two rows fit its registers.
-template <int VPL>
-constexpr bool kAhead = VPL <= 16;
-
-template <int VPL, int V, bool BF16, bool SIG>
-__global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteParams p) {
+template <class S, bool SIG>
+__global__ void __launch_bounds__(kRouteThreads, kRouteShare<S>) route_kernel(RouteParams p) {
   extern __shared__ __align__(16) float smem[];
-  __shared__ Candidates cands[kRouteWarps];
+  __shared__ Candidates<S> cands[kRouteWarps * S::kTiles];
   pdl_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const float* bias = smem;      // [E] padded to whole vectors, then the warps' rows
-  float* row = smem + (warp + 1) * padded_row(p.E);
+  const int lane = threadIdx.x & 31, l = lane % S::kLanes;
+  const int tile = threadIdx.x / S::kLanes;      // of the CTA
+  constexpr int kCtaTiles = kRouteWarps * S::kTiles;
+  const float* bias = smem;      // [E] padded to whole vectors, then the tiles' rows
+  float* row = smem + (tile + 1) * padded_row(p.E);
   if (SIG && p.bias != nullptr) {
     for (int e = threadIdx.x; e < p.E; e += kRouteThreads) smem[e] = p.bias[e];
     __syncthreads();
   }
-  const int stride = gridDim.x * kRouteWarps;
-  float x[VPL], s[VPL], total, top;
-  int t = blockIdx.x * kRouteWarps + warp;
-  if (kAhead<VPL> && t < p.T) load_row<VPL, V, BF16>(p.logits, int64_t(t) * p.ld, p.E, lane, x);
-  for (; t < p.T; t += stride) {
-    float next[VPL];
-    if constexpr (kAhead<VPL>) {
-      const int u = t + stride;
-      if (u < p.T) load_row<VPL, V, BF16>(p.logits, int64_t(u) * p.ld, p.E, lane, next);
-    } else {
-      load_row<VPL, V, BF16>(p.logits, int64_t(t) * p.ld, p.E, lane, x);
-    }
-    if (p.mask != nullptr && p.mask[t] == 0)
-      route_masked(p, t, lane);
+  const int stride = gridDim.x * kCtaTiles;
+  const auto load = [&](int t, float (&x)[S::kValues]) {
+    const bool have = t < p.T && (p.mask == nullptr || p.mask[t] != 0);
+    load_row<S>(p.logits, int64_t(t) * p.ld, p.E, l, have, x);
+  };
+  float x[S::kValues], s[S::kValues], total, top;
+  // a warp's tiles go through the same number of tokens
+  int t = blockIdx.x * kCtaTiles + tile, first = t - tile % S::kTiles;
+  if constexpr (S::kAhead) load(t, x);
+  for (; first < p.T; t += stride, first += stride) {
+    float next[S::kValues];
+    if constexpr (S::kAhead)
+      load(t + stride, next);
     else
-      route_token<VPL, V, BF16, SIG, false>(p, t, lane, row, cands[warp], bias, x, s, &total,
-                                            &top);
-    if constexpr (kAhead<VPL>) {
+      load(t, x);
+    route_token<S, SIG, false>(p, t, t < p.T, lane, row, cands[tile], bias, x, s, &total, &top);
+    if constexpr (S::kAhead) {
 #pragma unroll
-      for (int r = 0; r < VPL; ++r) x[r] = next[r];
+      for (int r = 0; r < S::kValues; ++r) x[r] = next[r];
     }
   }
 }
 
-// First sequence whose end lies past token t (the last one otherwise).
-__device__ __forceinline__ int sequence_of(const int32_t* seq_start, int B, int t) {
-  int lo = 0, hi = B - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi) / 2;
-    if (seq_start[mid + 1] > t)
-      hi = mid;
-    else
-      lo = mid + 1;
+// First sequence whose end lies past token t (the last one otherwise), by a
+// whole warp for one t: 32 ends at a time, so that two rounds of loads serve
+// a thousand sequences.
+__device__ __forceinline__ int sequence_of(const int32_t* seq_start, int B, int t, int lane) {
+  int lo = 0, n = B - 1;      // the answer is among lo .. lo + n
+  while (n > 0) {
+    const int step = (n + 31) / 32, i = lane * step;
+    const bool past = i + step - 1 >= n || seq_start[lo + i + step] > t;
+    const int skip = __ffs(__ballot_sync(kFull, past)) - 1;      // the last lane always answers
+    lo += skip * step;
+    n = min(step - 1, n - skip * step);
   }
   return lo;
 }
+
+// ---- balance --------------------------------------------------------------
+
+template <class S>
+constexpr int kBalanceThreads = S::kValues <= 16 ? 512 : 256;
+template <class S>
+constexpr int kBalanceShare = S::kValues <= 8 ? 2 : 1;
 
 // ep_route_balance, first kernel.  A CTA owns the tokens [c * R, (c + 1) * R)
 // and walks the sequences they belong to; the sums of (CTA c, sequence b) go
 // to partial row c + b, which no other pair uses (both only grow along the
 // tokens).
-template <int VPL>
-constexpr int kBalanceThreads = VPL <= 16 ? 512 : 256;
-template <int VPL>
-constexpr int kBalanceCtasPerSm = VPL <= 8 ? 2 : 1;
-
-template <int VPL, int V, bool BF16, bool SIG>
-__global__ void __launch_bounds__(kBalanceThreads<VPL>, kBalanceCtasPerSm<VPL>)
+template <class S, bool SIG>
+__global__ void __launch_bounds__(kBalanceThreads<S>, kBalanceShare<S>)
 balance_kernel(RouteParams p) {
-  constexpr int kThreads = kBalanceThreads<VPL>, kWarps = kThreads / 32;
+  constexpr int kThreads = kBalanceThreads<S>, kWarps = kThreads / 32;
+  constexpr int kCtaTiles = kThreads / S::kLanes;
   extern __shared__ __align__(16) float smem[];
   const int width = padded_row(p.E);
-  float* probs = smem;                                          // [kWarps][width]
-  float* bias = smem + kWarps * width;                          // [width]
+  float* rows = smem;                                           // [kCtaTiles][width]
+  float* bias = smem + kCtaTiles * width;                       // [width]
   int* counts = reinterpret_cast<int*>(bias + width);           // [width]
-  __shared__ Candidates cands[kWarps];
+  __shared__ Candidates<S> cands[kCtaTiles];
   __shared__ float warp_z[kWarps];
   __shared__ int warp_n[kWarps];
   pdl_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float* row = probs + warp * width;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % S::kLanes;
+  const int tile = threadIdx.x / S::kLanes;
+  float* row = rows + tile * width;
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.done = 0;
   for (int e = threadIdx.x; e < p.E; e += kThreads) counts[e] = 0;
   if (SIG && p.bias != nullptr)
@@ -578,78 +684,98 @@ balance_kernel(RouteParams p) {
   __syncthreads();
   const int first = blockIdx.x * p.tokens_per_cta;
   const int last = min(p.T, first + p.tokens_per_cta);
-  int b = p.B > 1 ? sequence_of(p.seq_start, p.B, first) : 0;
-  for (int t = first; t < last;) {
-    while (b < p.B - 1 && p.seq_start[b + 1] <= t) ++b;
-    const int end = b < p.B - 1 ? min(last, p.seq_start[b + 1]) : last;
-    float sum[VPL], z = 0.0f;
-    int n = 0;
+  int b = p.B > 1 ? sequence_of(p.seq_start, p.B, first, lane) : 0;
+  float sum[S::kValues], z = 0.0f;
+  int n = 0;
 #pragma unroll
-    for (int r = 0; r < VPL; ++r) sum[r] = 0.0f;
-    float x[VPL], s[VPL], total, top;
-    int u = t + warp;
-    if (kAhead<VPL> && u < end) load_row<VPL, V, BF16>(p.logits, int64_t(u) * p.ld, p.E, lane, x);
-    for (; u < end; u += kWarps) {
-      float next[VPL];
-      if constexpr (kAhead<VPL>) {
-        if (u + kWarps < end)
-          load_row<VPL, V, BF16>(p.logits, int64_t(u + kWarps) * p.ld, p.E, lane, next);
-      } else {
-        load_row<VPL, V, BF16>(p.logits, int64_t(u) * p.ld, p.E, lane, x);
-      }
-      if (p.mask != nullptr && p.mask[u] == 0) {
-        route_masked(p, u, lane);
-      } else {
-        const int mine = route_token<VPL, V, BF16, SIG, true>(p, u, lane, row, cands[warp], bias,
-                                                              x, s, &total, &top);
-        if (mine >= 0) atomicAdd(&counts[mine], 1);
+  for (int r = 0; r < S::kValues; ++r) sum[r] = 0.0f;
+  float x[S::kValues], s[S::kValues], total, top;
+  bool have, next_have = false;
+  const auto load = [&](int u, bool& have, float (&x)[S::kValues]) {
+    have = u < last && (p.mask == nullptr || p.mask[u] != 0);
+    load_row<S>(p.logits, int64_t(u) * p.ld, p.E, l, have, x);
+  };
+  if constexpr (S::kAhead) load(first + tile, have, x);
+  for (int t = first; t < last; t += kCtaTiles) {
+    const int u = t + tile;
+    float next[S::kValues];
+    if constexpr (S::kAhead)
+      load(u + kCtaTiles, next_have, next);
+    else
+      load(u, have, x);
+    const Chosen<S> mine = route_token<S, SIG, true>(p, u, u < last, lane, row, cands[tile], bias,
+                                                     x, s, &total, &top);
+    // all tiles' tokens are routed; the sequences they lie in, one by one
+    const int block_end = min(last, t + kCtaTiles);
+    for (int from = t; from < block_end;) {
+      while (b < p.B - 1 && p.seq_start[b + 1] <= from) ++b;
+      const int end = b < p.B - 1 ? min(last, p.seq_start[b + 1]) : last;
+      if (have && u >= from && u < end) {
+#pragma unroll
+        for (int i = 0; i < S::kSlots; ++i)
+          if (mine.e[i] >= 0) atomicAdd(&counts[mine.e[i]], 1);
         // total is 0 only where no expert is in service: the token adds nothing
         const float inv = total == 0.0f ? 0.0f : fast_reciprocal(total);
 #pragma unroll
-        for (int r = 0; r < VPL; ++r) sum[r] = fmaf(s[r], inv, sum[r]);
-        ++n;
-        if (!SIG && total != 0.0f) {
-          const float lse = top + __logf(total);
-          z += lse * lse;
+        for (int r = 0; r < S::kValues; ++r) sum[r] = fmaf(s[r], inv, sum[r]);
+        if (l == 0) {
+          ++n;
+          if (!SIG && total != 0.0f) {
+            const float lse = top + __logf(total);
+            z += lse * lse;
+          }
         }
       }
-      if constexpr (kAhead<VPL>) {
+      from = end;
+      if (end > block_end) continue;      // the sequence goes on in the next tokens
+      // the tiles of a warp, then the warps in order
+      __syncwarp();
 #pragma unroll
-        for (int r = 0; r < VPL; ++r) x[r] = next[r];
+      for (int d = 16; d >= S::kLanes; d >>= 1) {
+#pragma unroll
+        for (int r = 0; r < S::kValues; ++r) sum[r] += __shfl_xor_sync(kFull, sum[r], d);
       }
-    }
-    __syncwarp();
+      z = tile_sum<32>(z);
+      n = __reduce_add_sync(kFull, n);
 #pragma unroll
-    for (int r = 0; r < VPL; ++r) {
-      const int e = element_of<V>(r, lane);
-      if (e < p.E) row[e] = sum[r];
-    }
-    if (lane == 0) {
-      warp_z[warp] = z;
-      warp_n[warp] = n;
-    }
-    __syncthreads();
-    const int64_t part = int64_t(blockIdx.x) + b;
-    for (int e = threadIdx.x; e < p.E; e += kThreads) {
-      float acc = 0.0f;
-#pragma unroll
-      for (int v = 0; v < kWarps; ++v) acc += probs[v * width + e];
-      p.part_prob[part * p.E + e] = acc;
-      p.part_count[part * p.E + e] = counts[e];
-      counts[e] = 0;
-    }
-    if (threadIdx.x == 0) {
-      float zs = 0.0f;
-      int ns = 0;
-      for (int v = 0; v < kWarps; ++v) {
-        zs += warp_z[v];
-        ns += warp_n[v];
+      for (int r = 0; r < S::kValues; ++r) {
+        const int e = S::expert(r, l);
+        if (lane < S::kLanes && e < p.E) rows[warp * width + e] = sum[r];
+        sum[r] = 0.0f;
       }
-      p.part_z[part] = zs;
-      p.part_tokens[part] = ns;
+      if (lane == 0) {
+        warp_z[warp] = z;
+        warp_n[warp] = n;
+      }
+      z = 0.0f;
+      n = 0;
+      __syncthreads();
+      const int64_t part = int64_t(blockIdx.x) + b;
+      for (int e = threadIdx.x; e < p.E; e += kThreads) {
+        float acc = 0.0f;
+#pragma unroll
+        for (int v = 0; v < kWarps; ++v) acc += rows[v * width + e];
+        p.part_prob[part * p.E + e] = acc;
+        p.part_count[part * p.E + e] = counts[e];
+        counts[e] = 0;
+      }
+      if (threadIdx.x == 0) {
+        float zs = 0.0f;
+        int ns = 0;
+        for (int v = 0; v < kWarps; ++v) {
+          zs += warp_z[v];
+          ns += warp_n[v];
+        }
+        p.part_z[part] = zs;
+        p.part_tokens[part] = ns;
+      }
+      __syncthreads();
     }
-    __syncthreads();
-    t = end;
+    if constexpr (S::kAhead) {
+#pragma unroll
+      for (int r = 0; r < S::kValues; ++r) x[r] = next[r];
+      have = next_have;
+    }
   }
 }
 
@@ -673,17 +799,26 @@ struct BalanceParams {
   float* loss;             // [2]
 };
 
-// Sum over a block, in a fixed order, in every thread.  The block is whole
-// warps, at most 32 of them.
-template <typename T>
-__device__ T block_sum(T v, T* scratch) {
+// Sums of a float and two integers over a block of whole warps, in a fixed
+// order, in every thread.
+struct Sums {
+  float f;
+  int a, b;
+};
+__device__ Sums block_sum(Sums v, Sums* scratch) {
 #pragma unroll
-  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(kFull, v, d);
-  __syncthreads();
+  for (int d = 16; d; d >>= 1) v.f += __shfl_xor_sync(kFull, v.f, d);
+  v.a = __reduce_add_sync(kFull, v.a);
+  v.b = __reduce_add_sync(kFull, v.b);
   if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
   __syncthreads();
-  T s = T(0);
-  for (int i = 0; i < int(blockDim.x >> 5); ++i) s += scratch[i];
+  Sums s = {0.0f, 0, 0};
+#pragma unroll
+  for (int i = 0; i < kSumThreads / 32; ++i) {
+    s.f += scratch[i].f;
+    s.a += scratch[i].a;
+    s.b += scratch[i].b;
+  }
   return s;
 }
 
@@ -693,8 +828,7 @@ __device__ T block_sum(T v, T* scratch) {
 __global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(BalanceParams p) {
   __shared__ float probs[kSumRows][kSumExperts];
   __shared__ int counts[kSumRows][kSumExperts];
-  __shared__ float fscratch[32];
-  __shared__ int iscratch[32];
+  __shared__ Sums scratch[3][kSumThreads / 32];
   __shared__ bool is_last;
   pdl_wait();
   const int b = blockIdx.x, lane = threadIdx.x % kSumExperts, part = threadIdx.x / kSumExperts;
@@ -723,8 +857,9 @@ __global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(BalanceParams 
   }
   probs[part][lane] = prob;
   counts[part][lane] = count;
-  n = block_sum(n, iscratch);
-  z = block_sum(z, fscratch);
+  const Sums of_seq = block_sum({z, n, 0}, scratch[0]);
+  n = of_seq.a;
+  z = of_seq.f;
   if (threadIdx.x < 32) {      // lanes from kSumExperts on add nothing
     prob = 0.0f;
     count = 0;
@@ -742,7 +877,7 @@ __global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(BalanceParams 
         p.expert_count[int64_t(b) * p.E + e] = count;
       }
     }
-    const float dot = warp_sum(float(count) * inv_n * prob);
+    const float dot = tile_sum<32>(float(count) * inv_n * prob);
     if (threadIdx.x == 0) {
       p.dots[int64_t(b) * gridDim.y + blockIdx.y] = dot;
       if (blockIdx.y == 0) {
@@ -768,17 +903,17 @@ __global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(BalanceParams 
     full += m > 0 ? 1 : 0;
     z += __ldcg(p.seq_z + i);
   }
-  loss = block_sum(loss, fscratch);
-  z = block_sum(z, fscratch);
-  n = block_sum(n, iscratch);
-  full = block_sum(full, iscratch);
+  const Sums l = block_sum({loss, n, full}, scratch[1]);
+  const Sums zs = block_sum({z, 0, 0}, scratch[2]);
   if (threadIdx.x == 0) {
-    p.seq_tokens[p.B] = n;
-    p.seq_tokens[p.B + 1] = full;
-    p.loss[0] = full > 0 ? loss * (float(p.E) / float(p.K)) / float(full) : 0.0f;
-    p.loss[1] = n > 0 ? z / float(n) : 0.0f;
+    p.seq_tokens[p.B] = l.a;
+    p.seq_tokens[p.B + 1] = l.b;
+    p.loss[0] = l.b > 0 ? l.f * (float(p.E) / float(p.K)) / float(l.b) : 0.0f;
+    p.loss[1] = l.a > 0 ? zs.f / float(l.a) : 0.0f;
   }
 }
+
+// ---- backward -------------------------------------------------------------
 
 struct RouteBackwardParams {
   const void* logits;
@@ -797,158 +932,126 @@ struct RouteBackwardParams {
   int64_t ld_grad;
 };
 
-template <int VPL, int V, bool BF16>
-__device__ __forceinline__ void store_row(void* base, int64_t offset, int E, int lane,
-                                          const float (&g)[VPL]) {
-#pragma unroll
-  for (int r = 0; r < VPL; r += V) {
-    const int e = element_of<V>(r, lane);
-    if (e >= E) continue;
-    if constexpr (V == 1) {
-      if constexpr (BF16)
-        static_cast<__nv_bfloat16*>(base)[offset + e] = __float2bfloat16_rn(g[r]);
-      else
-        static_cast<float*>(base)[offset + e] = g[r];
-    } else {
-      if constexpr (BF16) {
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(base) + offset + e) =
-            make_uint2(pack_bf16x2(g[r], g[r + 1]), pack_bf16x2(g[r + 2], g[r + 3]));
-      } else {
-        *reinterpret_cast<float4*>(static_cast<float*>(base) + offset + e) =
-            make_float4(g[r], g[r + 1], g[r + 2], g[r + 3]);
-      }
-    }
-  }
-}
-
 // dL/dlogits of a token, all of it recomputed from its logits:
 //   dq_e = g0 c_be E / (K n_b^2 B')       balance loss by the normalised score
 //   ds_k = scale dw_k, or scale / S (dw_k - sum_j dw_j s_j / S)   gate weight
 //   softmax:  g = dq + ds,  dl = s (g - sum s g + g1 2 lse / N)
 //   sigmoid:  u = (dq - sum q dq) / sum s + ds,  dl = u s (1 - s)
-template <int VPL, int V, bool BF16, bool SIG>
-__global__ void __launch_bounds__(kRouteThreads) route_backward_kernel(RouteBackwardParams p) {
+// The next token's logits, choice and gate gradient are loaded ahead.
+template <class S, bool SIG>
+__global__ void __launch_bounds__(kRouteThreads, kRouteShare<S>)
+route_backward_kernel(RouteBackwardParams p) {
   extern __shared__ __align__(16) float smem[];
   pdl_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float* row = smem + warp * padded_row(p.E);
-  for (int e = lane; e < p.E; e += 32) row[e] = 0.0f;
+  constexpr int L = S::kLanes, kCtaTiles = kRouteThreads / L;
+  const int lane = threadIdx.x & 31, l = lane % L, tile = threadIdx.x / L;
+  float* row = smem + tile * padded_row(p.E);      // ds of the chosen, else 0
+  for (int e = l; e < p.E; e += L) row[e] = 0.0f;
   __syncwarp();
   const int first = blockIdx.x * p.tokens_per_cta;
   const int last = min(p.T, first + p.tokens_per_cta);
-  float dq[VPL];
+  float dq[S::kValues];
 #pragma unroll
-  for (int r = 0; r < VPL; ++r) dq[r] = 0.0f;
+  for (int r = 0; r < S::kValues; ++r) dq[r] = 0.0f;
   float dlse = 0.0f;
   const bool losses = p.expert_count != nullptr;
   if (losses && !SIG) {
     const int n = p.seq_tokens[p.B];
     dlse = n > 0 ? p.grad_loss[1] * 2.0f / float(n) : 0.0f;
   }
-  int b = -1;
-  // a token's logits, choice and gate gradient are loaded a token ahead
-  float x[VPL], s[VPL], top, dw = 0.0f;
-  int64_t choice = -1;
-  const bool selects = p.grad_w != nullptr && lane < p.K;
-  const auto load_choice = [&](int t, int64_t& e, float& g) {
-    e = p.idx[int64_t(t) * p.K + lane];
-    g = p.grad_w[int64_t(t) * p.K + lane];
+  struct Token {
+    float x[S::kValues], dw;
+    int choice;      // of lane k of the tile: its k-th, or -1
+    bool have;
   };
-  int t = first + warp;
-  if (t < last) {
-    if constexpr (kAhead<VPL>) load_row<VPL, V, BF16>(p.logits, int64_t(t) * p.ld, p.E, lane, x);
-    if (selects) load_choice(t, choice, dw);
-  }
-  for (; t < last; t += kRouteWarps) {
-    float next[VPL], next_dw = 0.0f;
-    int64_t next_choice = -1;
-    if (t + kRouteWarps < last) {
-      if constexpr (kAhead<VPL>)
-        load_row<VPL, V, BF16>(p.logits, int64_t(t + kRouteWarps) * p.ld, p.E, lane, next);
-      if (selects) load_choice(t + kRouteWarps, next_choice, next_dw);
+  const auto load = [&](int t, Token& k) {
+    k.have = t < last && (p.mask == nullptr || p.mask[t] != 0);
+    load_row<S>(p.logits, int64_t(t) * p.ld, p.E, l, k.have, k.x);
+    k.choice = -1;
+    k.dw = 0.0f;
+    if (p.grad_w != nullptr && k.have && l < p.K) {
+      const int64_t e = p.idx[int64_t(t) * p.K + l];
+      k.choice = e >= 0 && e < p.E ? int(e) : -1;
+      k.dw = p.grad_w[int64_t(t) * p.K + l];
     }
-    if constexpr (!kAhead<VPL>)
-      load_row<VPL, V, BF16>(p.logits, int64_t(t) * p.ld, p.E, lane, x);
-    float g[VPL];
-    if (p.mask != nullptr && p.mask[t] == 0) {
+  };
+  Token now, next;
+  int t = first + tile, warp_first = t - tile % S::kTiles;
+  int b = losses && p.B > 1 ? sequence_of(p.seq_start, p.B, warp_first, lane) : 0, was = -1;
+  if constexpr (S::kAhead) load(t, now);
+  for (; warp_first < last; t += kCtaTiles, warp_first += kCtaTiles) {
+    if constexpr (S::kAhead)
+      load(t + kCtaTiles, next);
+    else
+      load(t, now);
+    if (losses && t < last) {
+      while (b < p.B - 1 && p.seq_start[b + 1] <= t) ++b;
+      if (b != was) {
+        was = b;
+        const int n = p.seq_tokens[b], full = p.seq_tokens[p.B + 1];
+        const float each = n > 0 && full > 0 ? p.grad_loss[0] * (float(p.E) / float(p.K)) /
+                                                   (float(n) * float(n) * float(full))
+                                             : 0.0f;
 #pragma unroll
-      for (int r = 0; r < VPL; ++r) g[r] = 0.0f;
-    } else {
-      if (losses) {
-        const int was = b;
-        if (b < 0)
-          b = p.B > 1 ? sequence_of(p.seq_start, p.B, t) : 0;
-        else
-          while (b < p.B - 1 && p.seq_start[b + 1] <= t) ++b;
-        if (b != was) {
-          const int n = p.seq_tokens[b], full = p.seq_tokens[p.B + 1];
-          const float each = n > 0 && full > 0 ? p.grad_loss[0] * (float(p.E) / float(p.K)) /
-                                                     (float(n) * float(n) * float(full))
-                                               : 0.0f;
-#pragma unroll
-          for (int r = 0; r < VPL; ++r) {
-            const int e = element_of<V>(r, lane);
-            dq[r] = e < p.E ? each * float(p.expert_count[int64_t(b) * p.E + e]) : 0.0f;
-          }
+        for (int r = 0; r < S::kValues; ++r) {
+          const int e = S::expert(r, l);
+          dq[r] = e < p.E ? each * float(p.expert_count[int64_t(b) * p.E + e]) : 0.0f;
         }
-      }
-      // gate weights: lane k holds selection k
-      const int mine = choice >= 0 && choice < p.E ? int(choice) : -1;
-      const float l = mine >= 0 ? load_one<BF16>(p.logits, int64_t(t) * p.ld + mine) : 0.0f;
-      const float total = scores<VPL, SIG>(x, s, &top);
-      const float inv = total == 0.0f ? 0.0f : fast_reciprocal(total);
-      if (p.grad_w != nullptr) {
-        float ds = 0.0f, sk = 0.0f;
-        if (mine >= 0) {
-          sk = SIG ? sigmoid(l) : soft_score(l, top) * inv;
-          ds = dw * p.scale;
-        }
-        if (p.renorm) {
-          const float sum = warp_sum(sk);
-          const float is = sum == 0.0f ? 0.0f : fast_reciprocal(sum);
-          const float mean = warp_sum(ds * sk) * is;
-          ds = (ds - mean) * is;
-        }
-        if (mine >= 0) row[mine] = ds;
-        __syncwarp();
-        read_row<VPL, V>(row, p.E, lane, g);
-        __syncwarp();
-        if (mine >= 0) row[mine] = 0.0f;
-      } else {
-#pragma unroll
-        for (int r = 0; r < VPL; ++r) g[r] = 0.0f;
-      }
-      float dot = 0.0f;
-#pragma unroll
-      for (int r = 0; r < VPL; ++r) {
-        if constexpr (SIG) {
-          dot = fmaf(s[r], dq[r], dot);
-        } else {
-          s[r] *= inv;
-          g[r] += dq[r];
-          dot = fmaf(s[r], g[r], dot);
-        }
-      }
-      dot = warp_sum(dot);
-      if constexpr (SIG) {
-        dot *= inv;
-#pragma unroll
-        for (int r = 0; r < VPL; ++r)
-          g[r] = fmaf(dq[r] - dot, inv, g[r]) * (s[r] * (1.0f - s[r]));
-      } else {
-        const float z = total != 0.0f ? dlse * (top + __logf(total)) : 0.0f;
-#pragma unroll
-        for (int r = 0; r < VPL; ++r) g[r] = s[r] * (g[r] - (dot - z));
       }
     }
-    store_row<VPL, V, BF16>(p.grad, int64_t(t) * p.ld_grad, p.E, lane, g);
     __syncwarp();
-    choice = next_choice;
-    dw = next_dw;
-    if constexpr (kAhead<VPL>) {
+    const int mine = now.choice;
+    const float logit =
+        mine >= 0 ? load_one<S>(p.logits, int64_t(t) * p.ld + mine) : 0.0f;
+    float s[S::kValues], g[S::kValues], top;
+    const float total = scores<S, SIG>(now.x, s, &top);
+    const float inv = total == 0.0f ? 0.0f : fast_reciprocal(total);
+    if (p.grad_w != nullptr) {
+      float ds = 0.0f, sk = 0.0f;
+      if (mine >= 0) {
+        sk = SIG ? sigmoid(logit) : soft_score(logit, top) * inv;
+        ds = now.dw * p.scale;
+      }
+      if (p.renorm) {
+        const float sum = tile_sum<L>(sk);
+        const float is = sum == 0.0f ? 0.0f : fast_reciprocal(sum);
+        const float mean = tile_sum<L>(ds * sk) * is;
+        ds = (ds - mean) * is;
+      }
+      if (mine >= 0) row[mine] = ds;
+      __syncwarp();
+      read_row<S>(row, p.E, l, g);
+      __syncwarp();
+      if (mine >= 0) row[mine] = 0.0f;
+    } else {
 #pragma unroll
-      for (int r = 0; r < VPL; ++r) x[r] = next[r];
+      for (int r = 0; r < S::kValues; ++r) g[r] = 0.0f;
     }
+    float dot = 0.0f;
+#pragma unroll
+    for (int r = 0; r < S::kValues; ++r) {
+      if constexpr (SIG) {
+        dot = fmaf(s[r], dq[r], dot);
+      } else {
+        s[r] *= inv;
+        g[r] += dq[r];
+        dot = fmaf(s[r], g[r], dot);
+      }
+    }
+    dot = tile_sum<L>(dot);
+    if constexpr (SIG) {
+      dot *= inv;
+#pragma unroll
+      for (int r = 0; r < S::kValues; ++r)
+        g[r] = fmaf(dq[r] - dot, inv, g[r]) * (s[r] * (1.0f - s[r]));
+    } else {
+      const float z = total != 0.0f ? dlse * (top + __logf(total)) : 0.0f;
+#pragma unroll
+      for (int r = 0; r < S::kValues; ++r) g[r] = s[r] * (g[r] - (dot - z));
+    }
+    // a padding token's row was taken as -inf: all its scores are 0
+    if (t < last) store_row<S>(p.grad, int64_t(t) * p.ld_grad, p.E, l, g);
+    if constexpr (S::kAhead) now = next;
   }
 }
 
@@ -973,35 +1076,58 @@ bool router_ok(const ep_router_config* c) {
 
 constexpr int kMaxSequences = 1 << 20;
 
-// CTAs of the per-token kernels over `tokens` tokens: at most four an SM
-// (32 warps), each warp with a token at least.
-constexpr int kRouteCtasPerSm = 4;
-int route_ctas(int tokens) {
-  const int want = (tokens + kRouteWarps - 1) / kRouteWarps;
-  const int most = device_info().sm_count * kRouteCtasPerSm;
+// CTAs of a per-token kernel over `tokens` tokens, `tiles` of them at a time
+// in a CTA: at most `share` CTAs an SM, each tile with a token at least.
+int route_ctas(int tokens, int tiles, int share) {
+  const int want = (tokens + tiles - 1) / tiles;
+  const int most = device_info().sm_count * share;
   return want < most ? want : most;
 }
 
-// Calls f.template operator()<VPL, V, BF16, SIG>() for the smallest VPL that
-// holds E logits in a warp.  Rows whose vectors of four are aligned load
-// those; narrow rows keep more lanes busy with single loads.
-template <typename F>
-cudaError_t with_shape(int E, int64_t ld, bool bf16, bool sig, F&& f) {
-  const bool vec = E >= 128 && E <= 512 && E % 4 == 0 && ld % 4 == 0;
-  int vpl = vec ? 4 : 1;
-  while (vpl * 32 < E) vpl *= 2;
-#define EP_SHAPE(N, W)                                                    \
-  if (vpl == N && vec == (W == 4)) {                                      \
-    if (bf16) return sig ? f.template operator()<N, W, true, true>()      \
-                         : f.template operator()<N, W, true, false>();    \
-    return sig ? f.template operator()<N, W, false, true>()               \
-               : f.template operator()<N, W, false, false>();             \
+// Tokens a CTA when `tokens` are dealt to at most `ctas` CTAs in runs.
+int run_length(int tokens, int ctas) { return ctas > 0 ? (tokens + ctas - 1) / ctas : 1; }
+
+// Calls f.template operator()<Shape, SIG>() with the tile that suits E, K, G
+// and the number of tokens T.  Few tokens (a warp each at most) take a whole
+// warp, which is done soonest; many take narrow tiles where these measured
+// faster: 8 lanes up to 64 experts (ep_route of 8192 tokens by 64: 3.0 us, by
+// whole warps 4.6), 16 up to 128 (4.2, 5.3), but not 16 at 256 (11.1, 8.0 at
+// 16384 tokens: the same instructions a token less a third, yet half the
+// tokens in flight and longer chains of shuffles).  A tile needs a lane for
+// each group and rank, and candidates for K and a few more.  Rows whose
+// vectors of four logits are aligned are loaded as those.
+template <bool BF16, typename F>
+cudaError_t with_shape(int T, int E, int K, int G, int64_t ld, bool sig, F&& f) {
+  const bool vec = E % 4 == 0 && ld % 4 == 0;
+  const bool many = T > device_info().sm_count * 32;
+#define EP_SHAPE(L, N, V)                                                 \
+  return sig ? f.template operator()<Shape<L, N, V, BF16>, true>()        \
+             : f.template operator()<Shape<L, N, V, BF16>, false>()
+  if (many && vec && E <= 64 && K <= 8 && G <= 8) {
+    if (E <= 32) EP_SHAPE(8, 4, 4);
+    EP_SHAPE(8, 8, 4);
   }
-  EP_SHAPE(1, 1) EP_SHAPE(2, 1) EP_SHAPE(4, 1) EP_SHAPE(8, 1) EP_SHAPE(16, 1)
-  EP_SHAPE(32, 1) EP_SHAPE(64, 1)
-  EP_SHAPE(4, 4) EP_SHAPE(8, 4) EP_SHAPE(16, 4)
+  if (many && vec && E <= 128 && K <= 10 && G <= 16) EP_SHAPE(16, 8, 4);
+  if (E <= 32) EP_SHAPE(32, 1, 1);
+  if (E <= 64) EP_SHAPE(32, 2, 1);
+  if (E <= 128) EP_SHAPE(32, 4, 1);
+  if (E <= 256) {
+    if (vec) EP_SHAPE(32, 8, 4);
+    EP_SHAPE(32, 8, 1);
+  }
+  if (E <= 512) {
+    if (vec) EP_SHAPE(32, 16, 4);
+    EP_SHAPE(32, 16, 1);
+  }
+  EP_SHAPE(32, 64, 1);
 #undef EP_SHAPE
-  return cudaErrorInvalidValue;
+}
+
+template <typename F>
+cudaError_t with_shape(const ep_router_config* cfg, int T, int G, int64_t ld, F&& f) {
+  const bool sig = cfg->score == EP_SCORE_SIGMOID;
+  return cfg->logits_bf16 ? with_shape<true>(T, cfg->num_experts, cfg->num_topk, G, ld, sig, f)
+                          : with_shape<false>(T, cfg->num_experts, cfg->num_topk, G, ld, sig, f);
 }
 
 // Raises a kernel's dynamic shared-memory limit where `bytes` needs it (48 KiB
@@ -1014,16 +1140,17 @@ cudaError_t allow_smem(void (*kernel)(P...), size_t bytes) {
 
 struct LaunchRoute {
   RouteParams p;
-  int ctas;
   cudaStream_t stream;
-  template <int VPL, int V, bool BF16, bool SIG>
+  template <class S, bool SIG>
   cudaError_t operator()() const {
-    const size_t rows = p.G > 1 ? kRouteWarps + 1 : SIG ? 1 : 0;
+    constexpr int kCtaTiles = kRouteThreads / S::kLanes;
+    const size_t rows = p.G > 1 ? kCtaTiles + 1 : SIG ? 1 : 0;
     const size_t smem = sizeof(float) * rows * padded_row(p.E);
-    auto* kernel = route_kernel<VPL, V, BF16, SIG>;
+    auto* kernel = route_kernel<S, SIG>;
     const cudaError_t e = allow_smem(kernel, smem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kernel, dim3(ctas), dim3(kRouteThreads), smem, stream, p);
+    return launch_pdl(kernel, dim3(route_ctas(p.T, kCtaTiles, kRouteShare<S>)),
+                      dim3(kRouteThreads), smem, stream, p);
   }
 };
 
@@ -1034,17 +1161,15 @@ struct LaunchBalance {
   RouteParams p;
   BalanceParams q;      // of the second kernel
   cudaStream_t stream;
-  template <int VPL, int V, bool BF16, bool SIG>
+  template <class S, bool SIG>
   cudaError_t operator()() {
-    constexpr int kThreads = kBalanceThreads<VPL>, kWarps = kThreads / 32;
-    // each warp with a token at least; no tokens: one CTA still clears `done`
-    const int want = (p.T + kWarps - 1) / kWarps;
-    const int most = device_info().sm_count * kBalanceCtasPerSm<VPL>;
-    const int ctas = want < most ? (want > 1 ? want : 1) : most;
-    p.tokens_per_cta = q.tokens_per_cta = p.T > 0 ? (p.T + ctas - 1) / ctas : 1;
+    constexpr int kThreads = kBalanceThreads<S>, kCtaTiles = kThreads / S::kLanes;
+    const int ctas = route_ctas(p.T, kCtaTiles, kBalanceShare<S>);
+    p.tokens_per_cta = q.tokens_per_cta = run_length(p.T, ctas);
+    // no tokens: one CTA still clears `done`
     const int used = p.T > 0 ? (p.T + p.tokens_per_cta - 1) / p.tokens_per_cta : 1;
-    const size_t smem = sizeof(float) * (kWarps + 2) * padded_row(p.E);
-    auto* kernel = balance_kernel<VPL, V, BF16, SIG>;
+    const size_t smem = sizeof(float) * (kCtaTiles + 2) * padded_row(p.E);
+    auto* kernel = balance_kernel<S, SIG>;
     cudaError_t e = allow_smem(kernel, smem);
     if (e != cudaSuccess) return e;
     e = launch_pdl(kernel, dim3(used), dim3(kThreads), smem, stream, p);
@@ -1056,23 +1181,19 @@ struct LaunchBalance {
 
 struct LaunchBackward {
   RouteBackwardParams p;
-  int ctas;
   cudaStream_t stream;
-  template <int VPL, int V, bool BF16, bool SIG>
-  cudaError_t operator()() const {
-    const size_t smem = sizeof(float) * kRouteWarps * padded_row(p.E);
-    auto* kernel = route_backward_kernel<VPL, V, BF16, SIG>;
+  template <class S, bool SIG>
+  cudaError_t operator()() {
+    constexpr int kCtaTiles = kRouteThreads / S::kLanes;
+    p.tokens_per_cta = run_length(p.T, route_ctas(p.T, kCtaTiles, kRouteShare<S>));
+    const size_t smem = sizeof(float) * kCtaTiles * padded_row(p.E);
+    auto* kernel = route_backward_kernel<S, SIG>;
     const cudaError_t e = allow_smem(kernel, smem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kernel, dim3(ctas), dim3(kRouteThreads), smem, stream, p);
+    return launch_pdl(kernel, dim3((p.T + p.tokens_per_cta - 1) / p.tokens_per_cta),
+                      dim3(kRouteThreads), smem, stream, p);
   }
 };
-
-// Tokens per CTA of the kernels that give each CTA a run of tokens.
-int run_length(int T) {
-  const int ctas = route_ctas(T);
-  return ctas > 0 ? (T + ctas - 1) / ctas : 1;
-}
 
 struct BalanceWorkspace {
   float* prob;
@@ -1157,10 +1278,8 @@ int32_t ep_route(const ep_router_config* cfg, int32_t num_tokens, const void* d_
                   d_topk_weights, &l.p))
     return EP_ERR_INVALID_ARG;
   if (num_tokens == 0) return EP_OK;
-  l.ctas = route_ctas(num_tokens);
   l.stream = static_cast<cudaStream_t>(stream);
-  return status(with_shape(l.p.E, ld_logits, cfg->logits_bf16 != 0,
-                           cfg->score == EP_SCORE_SIGMOID, l));
+  return status(with_shape(cfg, num_tokens, l.p.G, ld_logits, l));
 }
 
 int64_t ep_route_workspace_bytes(const ep_router_config* cfg, int32_t num_seqs) {
@@ -1208,8 +1327,7 @@ int32_t ep_route_balance(const ep_router_config* cfg, int32_t num_tokens, const 
   l.q.seq_z = w.seq_z;
   l.q.done = w.done;
   l.q.loss = d_loss;
-  return status(with_shape(l.p.E, ld_logits, cfg->logits_bf16 != 0,
-                           cfg->score == EP_SCORE_SIGMOID, l));
+  return status(with_shape(cfg, num_tokens, l.p.G, ld_logits, l));
 }
 
 int32_t ep_route_backward(const ep_router_config* cfg, int32_t num_tokens, const void* d_logits,
@@ -1243,7 +1361,6 @@ int32_t ep_route_backward(const ep_router_config* cfg, int32_t num_tokens, const
   l.p.E = cfg->num_experts;
   l.p.K = cfg->num_topk;
   l.p.B = num_seqs;
-  l.p.tokens_per_cta = run_length(num_tokens);
   l.p.renorm = cfg->renormalize != 0;
   l.p.scale = cfg->route_scale;
   l.p.idx = d_topk_idx;
@@ -1254,11 +1371,10 @@ int32_t ep_route_backward(const ep_router_config* cfg, int32_t num_tokens, const
   l.p.grad_loss = d_grad_loss;
   l.p.grad = d_grad_logits;
   l.p.ld_grad = ld_grad;
-  l.ctas = (num_tokens + l.p.tokens_per_cta - 1) / l.p.tokens_per_cta;
   l.stream = static_cast<cudaStream_t>(stream);
   // both rows have to allow vectors for either to use them
   const int64_t ld = ld_logits % 4 == 0 ? ld_grad : ld_logits;
-  return status(with_shape(l.p.E, ld, cfg->logits_bf16 != 0, cfg->score == EP_SCORE_SIGMOID, l));
+  return status(with_shape(cfg, num_tokens, 1, ld, l));
 }
 
 }  // extern "C"
