@@ -19,6 +19,7 @@ from __future__ import annotations
 import ctypes
 import dataclasses
 import os
+from threading import get_ident as _get_ident
 from typing import Optional
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -805,6 +806,30 @@ def _stream_of(t, stream):
     return _torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
+# Scratch memory of the eager calls, by (device, stream, host thread): calls
+# of one thread on one stream run in order, so that they can share it.
+_workspaces = {}
+_outgrown = []      # kept: a stream other than the allocating one may use them still
+
+
+def _workspace_of(t, stream: int, size: int):
+    """At least `size` bytes on t's device for a call on this stream.  Kept
+    from call to call (asking the allocator each time costs more than the
+    kernels of a small batch); under stream capture, fresh memory that the
+    graph owns."""
+    if _torch.cuda.is_current_stream_capturing():
+        return _torch.empty(size, dtype=_torch.uint8, device=t.device)
+    key = t.get_device(), stream, _get_ident()
+    got = _workspaces.get(key)
+    if got is None or got.nbytes < size:
+        if got is not None:
+            _outgrown.append(got)
+            size = max(size, 2 * got.nbytes)      # so that they stay few
+        got = _workspaces[key] = _torch.empty(max(size, 1 << 20), dtype=_torch.uint8,
+                                              device=t.device)
+    return got
+
+
 class _LazyTorch:
     """torch, imported by the first call that needs it."""
 
@@ -882,8 +907,8 @@ def route_balance(cfg: RouterConfig, logits, bias=None, token_mask=None, seq_sta
     """ep_route_balance.  seq_start: int32 [B + 1] CUDA tensor, or None for one
     sequence.  Returns (topk_idx, topk_weights, expert_count int32 [B, E],
     expert_prob fp32 [B, E], seq_tokens int32 [B + 2], loss fp32 [2]), which
-    `out` may give; workspace: ep_route_workspace_bytes bytes (allocated when
-    None)."""
+    `out` may give; workspace: ep_route_workspace_bytes bytes (when None,
+    memory kept for the calls of this thread on this stream)."""
     c, T, ld = _logits_args(cfg, "route_balance", logits)
     B = 1 if seq_start is None else seq_start.shape[0] - 1
     E, K, dev = cfg.num_experts, cfg.num_topk, logits.device
@@ -899,8 +924,9 @@ def route_balance(cfg: RouterConfig, logits, bias=None, token_mask=None, seq_sta
     size = _lib.ep_route_workspace_bytes(c, B)
     if size < 0:
         _refuse("route_balance: config or number of sequences")
+    handle = _stream_of(logits, stream)
     if workspace is None:
-        workspace = _torch.empty(size, dtype=_torch.uint8, device=dev)
+        workspace = _workspace_of(logits, handle, size)
     if not (_flat(idx, _torch.int64, (T, K)) and _flat(w, f32, (T, K))
             and _flat(count, i32, (B, E)) and _flat(prob, f32, (B, E))
             and _flat(tokens, i32, (B + 2,)) and _flat(loss, f32, (2,))
@@ -911,7 +937,7 @@ def route_balance(cfg: RouterConfig, logits, bias=None, token_mask=None, seq_sta
     st = _lib.ep_route_balance(c, T, logits.data_ptr(), ld, _ptr(bias), _ptr(token_mask), B,
                                _ptr(seq_start), idx.data_ptr(), w.data_ptr(), count.data_ptr(),
                                prob.data_ptr(), tokens.data_ptr(), loss.data_ptr(),
-                               workspace.data_ptr(), _stream_of(logits, stream))
+                               workspace.data_ptr(), handle)
     if st:
         _check(st, "ep_route_balance")
     return idx, w, count, prob, tokens, loss

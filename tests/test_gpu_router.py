@@ -288,3 +288,24 @@ def test_torch_layer_refuses(ep):
         with pytest.raises(ep.EpError) as e:
             call()
         assert e.value.status == ep.EP_ERR_INVALID_ARG
+
+
+def test_calls_on_two_streams_keep_apart(ep):
+    """Each stream has its own scratch memory, and a larger call after a
+    smaller one gets more of it."""
+    cfg = ep.RouterConfig(512, 4)
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    xs = [torch.randn((3000 + 500 * i, 512), device="cuda", generator=gen) for i in range(2)]
+    seq = [torch.linspace(0, len(x), 2000 * i + 2, device="cuda").to(torch.int32)
+           for i, x in enumerate(xs)]
+    want = [ep.route_balance(cfg, x, seq_start=s) for x, s in zip(xs, seq)]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(20):
+        for x, s, st in zip(xs, seq, streams):
+            with torch.cuda.stream(st):
+                got.append(ep.route_balance(cfg, x, seq_start=s))
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(g, want[i % 2]))
