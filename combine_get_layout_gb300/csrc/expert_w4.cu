@@ -107,12 +107,14 @@ __device__ __forceinline__ void decode(uint32_t word, uint32_t even, uint32_t od
   }
 }
 
-// What decode takes off the even and odd pairs of a row with zero point z:
-// pairs of 1024 + z and 64 + z in f16, of 128 + z in bf16.
+// What decode takes off the even and odd pairs of the row whose zero point
+// (under 16) is byte i of z: pairs of 1024 + z and 64 + z in f16, of 128 + z
+// in bf16.  One byte permutation puts the zero point and the offset's upper
+// byte in both halves.
 template <bool FP8>
-__device__ __forceinline__ void offsets(uint32_t z, uint32_t* even, uint32_t* odd) {
-  *even = (FP8 ? 0x64006400u : 0x43004300u) + z * 0x00010001u;
-  *odd = 0x54005400u + z * 0x00100010u;
+__device__ __forceinline__ void offsets(uint32_t z, int i, uint32_t* even, uint32_t* odd) {
+  *even = __byte_perm(z, FP8 ? 0x64646464u : 0x43434343u, 0x4040u + 0x0101u * i);
+  *odd = __byte_perm(z << 4, 0x54545454u, 0x4040u + 0x0101u * i);
 }
 
 // Two E4M3 values as an f16 pair (exact).
@@ -339,13 +341,16 @@ __device__ __forceinline__ void multiply_unit(uint32_t stage, int lane, int tile
 #pragma unroll
   for (int s = 0; s < St::kGroups; ++s) {
     const uint4 sv = lds16(stage + St::kScales + s * 128 + g * 16);
-    uint2 zv = make_uint2(0x08080808u, 0x08080808u);
+    uint2 zv;
     if constexpr (ZEROS) zv = lds8(stage + St::kZeros + s * 64 + g * 8);
     if (!FP8 && 32 * kWords * s >= inputs) break;      // groups past H
     uint32_t even[8], odd[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      offsets<FP8>((i < 4 ? zv.x : zv.y) >> (8 * (i & 3)) & 0xFFu, &even[i], &odd[i]);
+    for (int i = 0; i < 8; ++i) {
+      even[i] = FP8 ? 0x64086408u : 0x43084308u;      // 1032, 136
+      odd[i] = 0x54805480u;                           // 72
+      if constexpr (ZEROS) offsets<FP8>(i < 4 ? zv.x : zv.y, i & 3, &even[i], &odd[i]);
+    }
     float d[NT][4][4];
 #pragma unroll
     for (int i = s * kWords; i < (s + 1) * kWords; ++i) {
