@@ -217,15 +217,16 @@ __device__ void count_chunks(const W4Params& p, int* pre) {
   __syncthreads();
 }
 
-// The expert whose chunks hold chunk c.
-__device__ __forceinline__ int expert_of(const int* pre, int E, int c) {
-  int lo = 0, hi = E - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi) / 2;
-    if (pre[mid + 1] > c)
-      hi = mid;
-    else
-      lo = mid + 1;
+// The expert whose chunks hold chunk c, by a whole warp: 32 experts' ends a
+// round, so that two rounds serve a thousand experts.
+__device__ __forceinline__ int expert_of(const int* pre, int E, int c, int lane) {
+  int lo = 0, n = E - 1;      // the answer is among lo .. lo + n
+  while (n > 0) {
+    const int step = (n >> 5) + 1, i = lane * step;
+    const bool past = i + step - 1 >= n || pre[lo + i + step] > c;
+    const int skip = __ffs(__ballot_sync(0xffffffffu, past)) - 1;      // the last lane answers
+    lo += skip * step;
+    n = min(step - 1, n - skip * step);
   }
   return lo;
 }
@@ -251,9 +252,9 @@ struct Walk {
 struct Item {
   int expert, tile, row0, rows;
   template <int kRows>
-  __device__ __forceinline__ void find(const W4Params& p, const int* pre, const Walk& at) {
+  __device__ __forceinline__ void find(const W4Params& p, const int* pre, const Walk& at, int lane) {
     tile = at.tile;
-    expert = expert_of(pre, p.E, at.chunk);
+    expert = expert_of(pre, p.E, at.chunk, lane);
     row0 = max(0, p.start[expert]) + (at.chunk - pre[expert]) * kRows;
     rows = min(kRows, min(p.cap, p.end[expert]) - row0);
   }
@@ -444,7 +445,7 @@ __global__ void __launch_bounds__(WARPS * 32) expert_w4_kernel(W4Params p, int s
   loader.kb = p.blocks;
   const auto enter = [&] {
     Item next;
-    next.find<8 * NT>(p, pre, ahead);
+    next.find<8 * NT>(p, pre, ahead, lane);
     loader.start(p, next, slice, lane);
   };
   if (!ahead.done()) enter();
@@ -464,7 +465,7 @@ __global__ void __launch_bounds__(WARPS * 32) expert_w4_kernel(W4Params p, int s
   uint32_t stage = base, idle = base + (STAGES - 1) * St::kBytes;
   for (; !now.done(); now.advance(p)) {
     Item it;
-    it.find<8 * NT>(p, pre, now);
+    it.find<8 * NT>(p, pre, now, lane);
     const int used = (it.rows + 7) >> 3;
     float acc[NT][4][4];
 #pragma unroll

@@ -640,7 +640,7 @@ __global__ void __launch_bounds__(kRouteThreads, kRouteShare<S>) route_kernel(Ro
 __device__ __forceinline__ int sequence_of(const int32_t* seq_start, int B, int t, int lane) {
   int lo = 0, n = B - 1;      // the answer is among lo .. lo + n
   while (n > 0) {
-    const int step = (n + 31) / 32, i = lane * step;
+    const int step = n / 32 + 1, i = lane * step;
     const bool past = i + step - 1 >= n || seq_start[lo + i + step] > t;
     const int skip = __ffs(__ballot_sync(kFull, past)) - 1;      // the last lane always answers
     lo += skip * step;

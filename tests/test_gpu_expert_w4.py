@@ -89,6 +89,8 @@ CASES = [
     dict(counts=[4, 24], H=2080, N=72, group=32), dict(counts=[1], H=8192, N=62, gated=True),
     dict(counts=[0, 1] * 40 + [3], H=64, N=130, group=64),
     dict(counts=[5, 6], H=640, N=2050, group=128, gated=True, zeros=True),
+    dict(counts=[0] * 32 + [9], H=64, N=64, group=32), dict(counts=[3] * 33, H=64, N=64, group=64),
+    dict(counts=[1, 0, 0] * 352 + [2], H=32, N=32, group=32),
 ]
 
 

@@ -156,6 +156,8 @@ BALANCE = [
                                                   groups=8, kept=4, scale=2.5),
     dict(T=40, E=2048, K=32, B=2), dict(T=64, E=130, K=6, B=2, score="sigmoid", dead=4),
     dict(T=7, E=32, K=3, B=1, masked=1.1),
+    dict(T=200, E=8, K=2, B=33), dict(T=150, E=8, K=1, B=65), dict(T=90, E=16, K=2, B=1057),
+    dict(T=6000, E=24, K=2, B=97, masked=0.02),
 ]
 
 
