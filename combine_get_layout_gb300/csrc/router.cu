@@ -262,13 +262,27 @@ __device__ __forceinline__ float scores(const float (&x)[S::kValues], float (&s)
 template <class S>
 __device__ __forceinline__ uint32_t best_groups(float score, int G, int kept, int lane) {
   const int l = lane % S::kLanes;
-  int before = 0;
-  for (int g = 0; g < G; ++g) {
-    const float o = __shfl_sync(kFull, score, g, S::kLanes);
-    before += o > score || (o == score && g < l) ? 1 : 0;
+  if constexpr (S::kLanes == 32) {      // a maximum is one instruction: one after another
+    uint32_t keep = 0;
+    float left = l < G ? score : -CUDART_INF_F;
+    for (int i = 0; i < kept; ++i) {
+      const float top = tile_max<32>(left);
+      const uint32_t first = __ballot_sync(kFull, left == top);
+      const uint32_t one = first & (0u - first);
+      keep |= one;
+      if (one >> l & 1u) left = -CUDART_INF_F;
+    }
+    // groups of no score answer last, if at all
+    return keep & __ballot_sync(kFull, l < G && score > -CUDART_INF_F);
+  } else {
+    int before = 0;
+    for (int g = 0; g < G; ++g) {
+      const float o = __shfl_sync(kFull, score, g, S::kLanes);
+      before += o > score || (o == score && g < l) ? 1 : 0;
+    }
+    const bool in = l < G && before < kept && score > -CUDART_INF_F;
+    return tile_bits<S::kLanes>(__ballot_sync(kFull, in), lane);
   }
-  const bool in = l < G && before < kept && score > -CUDART_INF_F;
-  return tile_bits<S::kLanes>(__ballot_sync(kFull, in), lane);
 }
 
 // Adds (b, s) of another set to a running (best, second).
@@ -293,8 +307,10 @@ __device__ __forceinline__ void keep_groups(const RouteParams& p, float (&c)[S::
                                             int lane) {
   constexpr int L = S::kLanes;
   const int l = lane % L;
+  if constexpr (!SIG) {      // a NaN is not chosen; sigmoid choice scores have none
 #pragma unroll
-  for (int r = 0; r < S::kValues; ++r) c[r] = fmaxf(c[r], -CUDART_INF_F);   // a NaN is not chosen
+    for (int r = 0; r < S::kValues; ++r) c[r] = fmaxf(c[r], -CUDART_INF_F);
+  }
   if constexpr (S::kVec == 4) {
     constexpr int kLog = L == 8 ? 3 : L == 16 ? 4 : 5;
     if (p.per_log2 > 0 && p.per_log2 - 2 <= kLog) {
@@ -537,7 +553,7 @@ __device__ __forceinline__ Chosen<S> route_token(const RouteParams& p, int t, bo
   constexpr int L = S::kLanes;
   const int l = lane % L;
   const int64_t offset = int64_t(t) * p.ld;
-  float scale = p.scale;
+  float inv = 1.0f;      // what the chosen scores are multiplied by, but for p.scale
   float c[S::kValues];
   if constexpr (SIG) {
     *total = scores<S, SIG>(x, s, top);
@@ -549,19 +565,19 @@ __device__ __forceinline__ Chosen<S> route_token(const RouteParams& p, int t, bo
     }
 #pragma unroll
     for (int r = 0; r < S::kValues; ++r)
-      c[r] = x[r] == -CUDART_INF_F ? -CUDART_INF_F : s[r] + c[r];
+      c[r] = x[r] > -CUDART_INF_F ? s[r] + c[r] : -CUDART_INF_F;      // NaN too
   } else {
     *top = tile_max<L>(largest(x));
     if (STATS || !p.renorm) {
       *total = soft_scores<S>(x, s, *top);
-      if (!p.renorm) scale = scale / *total;
-      if (*total != *total) scale = *total;
+      if (!p.renorm) inv = fast_reciprocal(*total);
+      if (*total != *total) inv = *total;
     } else {
       // NaN where a logit is, or where -inf meets +inf, whose weights are NaN
       float any = 0.0f;
 #pragma unroll
       for (int r = 0; r < S::kValues; ++r) any += x[r];
-      if (tile_bits<L>(__ballot_sync(kFull, any != any), lane) != 0) scale = CUDART_NAN_F;
+      if (tile_bits<L>(__ballot_sync(kFull, any != any), lane) != 0) inv = CUDART_NAN_F;
     }
 #pragma unroll
     for (int r = 0; r < S::kValues; ++r) c[r] = x[r];
@@ -579,14 +595,14 @@ __device__ __forceinline__ Chosen<S> route_token(const RouteParams& p, int t, bo
   }
   if (p.renorm) {
     sum = tile_sum<L>(sum);
-    scale = sum == 0.0f ? 0.0f : scale / sum;
+    inv = sum == 0.0f ? 0.0f : inv * fast_reciprocal(sum);
   }
 #pragma unroll
   for (int i = 0; i < S::kSlots; ++i) {
     if (live && out.rank[i] < p.K) {
       const int64_t at = int64_t(t) * p.K + out.rank[i];
       p.idx[at] = out.e[i];
-      p.w[at] = out.e[i] >= 0 ? w[i] * scale : 0.0f;
+      p.w[at] = out.e[i] >= 0 ? w[i] * inv * p.scale : 0.0f;
     }
   }
   return out;
