@@ -126,18 +126,26 @@ __device__ __forceinline__ uint32_t e4m3_pair(uint32_t two) {
 
 // ---- the product ----------------------------------------------------------------
 
-// A warp's stage in shared memory: one block (128 inputs) of its tile and
-// chunk.  x rows are swizzled in units of the fragments' reads, so that the
-// eight lanes (FP8: sixteen) of one shared-memory pass meet different banks.
-template <bool FP8, int GROUP, bool ZEROS, int NT>
-struct Stage {
-  static constexpr int kGroups = kBlockIn / GROUP;
+// How a kernel takes its columns: NT tiles of eight rows of x, staged with the
+// codes or read straight into registers (DIRECT).
+template <bool FP8_, int GROUP_, bool ZEROS_, int NT_, bool DIRECT_>
+struct Kind {
+  static constexpr bool FP8 = FP8_, ZEROS = ZEROS_, DIRECT = DIRECT_;
+  static constexpr int GROUP = GROUP_, NT = NT_;
+  static constexpr int kChunk = 8 * NT;                      // rows of an item at most
+  static constexpr int kGroups = kBlockIn / GROUP;           // scale groups a block
+  static constexpr int kWords = GROUP / 32;                  // words of a lane a group
+
+  // A warp's stage in shared memory: one unit, a block (128 inputs) of its
+  // tile and chunk.  x rows are swizzled in units of the fragments' reads, so
+  // that the eight lanes (FP8: sixteen) of one shared-memory pass meet
+  // different banks.
   static constexpr int kRowBytes = FP8 ? 128 : 256;
-  static constexpr int kX = kTileRows * kBlockIn / 2;              // after the codes
-  static constexpr int kScales = kX + 8 * NT * kRowBytes;
+  static constexpr int kX = kTileRows * kBlockIn / 2;        // after the codes
+  static constexpr int kScales = kX + (DIRECT ? 0 : kChunk * kRowBytes);
   static constexpr int kZeros = kScales + kGroups * kTileRows * 2;
   static constexpr int kXScale = kZeros + (ZEROS ? kGroups * kTileRows : 0);
-  static constexpr int kBytes = kXScale + (FP8 ? 8 * NT * 4 : 0);
+  static constexpr int kBytes = kXScale + (FP8 && !DIRECT ? kChunk * 4 : 0);
   static_assert(kBytes % 16 == 0);
 
   // Byte offset of 16-byte piece c of row t of x.
@@ -172,6 +180,11 @@ __device__ __forceinline__ uint2 lds8(uint32_t at) {
   asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
   return v;
 }
+__device__ __forceinline__ uint32_t lds2(uint32_t at) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at));
+  return v;
+}
 __device__ __forceinline__ uint32_t lds4(uint32_t at) {
   uint32_t v;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at));
@@ -188,7 +201,7 @@ __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) {
 template <int kRows>
 __device__ void count_chunks(const W4Params& p, int* pre) {
   __shared__ int warp_sum[32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int each = (p.E + blockDim.x - 1) / blockDim.x;
   const int e0 = min(p.E, int(threadIdx.x) * each), e1 = min(p.E, e0 + each);
   int mine = 0;
@@ -251,21 +264,20 @@ struct Walk {
 // A tile of 64 packed weight rows by a chunk of up to kRows rows of x.
 struct Item {
   int expert, tile, row0, rows;
-  template <int kRows>
-  __device__ __forceinline__ void find(const W4Params& p, const int* pre, const Walk& at, int lane) {
-    tile = at.tile;
-    expert = expert_of(pre, p.E, at.chunk, lane);
-    row0 = max(0, p.start[expert]) + (at.chunk - pre[expert]) * kRows;
-    rows = min(kRows, min(p.cap, p.end[expert]) - row0);
-  }
 };
+
+template <int kRows>
+__device__ __forceinline__ Item item_at(const W4Params& p, const int* pre, const Walk& at, int lane) {
+  const int e = expert_of(pre, p.E, at.chunk, lane);
+  const int row0 = max(0, p.start[e]) + (at.chunk - pre[e]) * kRows;
+  return {e, at.tile, row0, min(kRows, min(p.cap, p.end[e]) - row0)};
+}
 
 // A lane's share of the copies of an item's units, one unit after another.
 // Columns past the item's rows and inputs past H are not copied: what a
 // stage holds there meets only columns that are not stored, and is skipped.
-template <bool FP8, int GROUP, bool ZEROS, int NT>
+template <class Kd>
 struct Loader {
-  using St = Stage<FP8, GROUP, ZEROS, NT>;
   const char *codes, *scales, *x, *x_scale, *zeros;
   int rows;      // left of the lane's first row
   int k;         // first input of the lane's pieces of x
@@ -274,15 +286,18 @@ struct Loader {
   __device__ __forceinline__ void start(const W4Params& p, const Item& it, int slice, int lane) {
     const int64_t unit = (int64_t(it.expert) * p.tiles + it.tile) * p.blocks + slice;
     codes = reinterpret_cast<const char*>(p.codes) + unit * 4096 + lane * 16;
-    scales = reinterpret_cast<const char*>(p.scales) + unit * (St::kGroups * kTileRows * 2) + lane * 16;
-    if constexpr (ZEROS)
-      zeros = reinterpret_cast<const char*>(p.zeros) + unit * (St::kGroups * kTileRows) + lane * 16;
-    const int t = FP8 ? lane >> 3 : lane >> 4, c = FP8 ? lane & 7 : lane & 15;
-    rows = it.rows - t;
-    k = slice * kBlockIn + c * (FP8 ? 16 : 8);
-    x = static_cast<const char*>(p.x) + (int64_t(it.row0 + t) * p.H + k) * (FP8 ? 1 : 2);
-    if constexpr (FP8)
-      x_scale = reinterpret_cast<const char*>(p.x_scale + int64_t(it.row0 + lane) * p.blocks + slice);
+    scales = reinterpret_cast<const char*>(p.scales) + unit * (Kd::kGroups * kTileRows * 2) + lane * 16;
+    if constexpr (Kd::ZEROS)
+      zeros = reinterpret_cast<const char*>(p.zeros) + unit * (Kd::kGroups * kTileRows) + lane * 16;
+    if constexpr (!Kd::DIRECT) {
+      const int t = Kd::FP8 ? lane >> 3 : lane >> 4, c = Kd::FP8 ? lane & 7 : lane & 15;
+      rows = it.rows - t;
+      k = slice * kBlockIn + c * (Kd::FP8 ? 16 : 8);
+      x = static_cast<const char*>(p.x) + (int64_t(it.row0 + t) * p.H + k) * (Kd::FP8 ? 1 : 2);
+      if constexpr (Kd::FP8)
+        x_scale =
+            reinterpret_cast<const char*>(p.x_scale + int64_t(it.row0 + lane) * p.blocks + slice);
+    }
     kb = slice;
   }
 
@@ -290,117 +305,215 @@ struct Loader {
 #pragma unroll
     for (int i = 0; i < 8; ++i) cp_async<16>(stage + i * 512 + lane * 16, codes + i * 512);
     codes += split * 4096;
-    if constexpr (FP8) {
+    if constexpr (Kd::DIRECT) {
+      // the columns go another way
+    } else if constexpr (Kd::FP8) {
       const int t = lane >> 3, c = lane & 7;
 #pragma unroll
-      for (int i = 0; i < 2 * NT; ++i)
-        if (4 * i < rows) cp_async<16>(stage + St::x_piece(4 * i + t, c), x + int64_t(4 * i) * p.H);
-      if (lane < 8 * NT && lane < rows + t) cp_async<4>(stage + St::kXScale + lane * 4, x_scale);
+      for (int i = 0; i < 2 * Kd::NT; ++i)
+        if (4 * i < rows) cp_async<16>(stage + Kd::x_piece(4 * i + t, c), x + int64_t(4 * i) * p.H);
+      if (lane < Kd::kChunk && lane < rows + t) cp_async<4>(stage + Kd::kXScale + lane * 4, x_scale);
       x += split * kBlockIn;
       x_scale += split * 4;
     } else {
       const int t = lane >> 4, c = lane & 15;
 #pragma unroll
-      for (int i = 0; i < 4 * NT; ++i)
+      for (int i = 0; i < 4 * Kd::NT; ++i)
         if (2 * i < rows && k < p.H)
-          cp_async<16>(stage + St::x_piece(2 * i + t, c), x + int64_t(4 * i) * p.H);
+          cp_async<16>(stage + Kd::x_piece(2 * i + t, c), x + int64_t(4 * i) * p.H);
       x += split * kBlockIn * 2;
       k += split * kBlockIn;
     }
-    if (lane < St::kGroups * 8) cp_async<16>(stage + St::kScales + lane * 16, scales);
-    scales += split * (St::kGroups * kTileRows * 2);
-    if constexpr (ZEROS) {
-      if (lane < St::kGroups * 4) cp_async<16>(stage + St::kZeros + lane * 16, zeros);
-      zeros += split * (St::kGroups * kTileRows);
+    if (lane < Kd::kGroups * 8) cp_async<16>(stage + Kd::kScales + lane * 16, scales);
+    scales += split * (Kd::kGroups * kTileRows * 2);
+    if constexpr (Kd::ZEROS) {
+      if (lane < Kd::kGroups * 4) cp_async<16>(stage + Kd::kZeros + lane * 16, zeros);
+      zeros += split * (Kd::kGroups * kTileRows);
     }
     kb += split;
   }
 };
 
-// acc += the unit in a stage.  Lane (g = lane / 4, q = lane % 4) holds packed
-// rows 8 g .. 8 g + 7 (piece 2 r + h is row g + 8 h of the r-th 16-row
-// operand) and columns 8 t + 2 q, + 1: acc[t][r][2 h + c].
-template <bool FP8, int GROUP, bool ZEROS, int NT>
-__device__ __forceinline__ void multiply_unit(uint32_t stage, int lane, int tiles_used, int inputs,
-                                              float (&acc)[NT][4][4]) {
-  using St = Stage<FP8, GROUP, ZEROS, NT>;
-  constexpr int kWords = GROUP / 32;              // words of a lane a group
-  const int g = lane >> 2, q = lane & 3;
+// The columns of the product: lane (g, q) multiplies with inputs 32 i + 8 q
+// .. + 7 (word i) of rows 8 t + g.  DIRECT (bf16) reads a unit's words into
+// registers through L1, where the warps of an SM that work on other tiles of
+// the same rows find them.
+template <class Kd>
+struct Columns {
+  static_assert(!(Kd::DIRECT && Kd::FP8), "E4M3 rows are staged");
+  uint4 v[Kd::DIRECT ? Kd::NT : 1][4];
+  const char* x[Kd::NT];
+
+  __device__ __forceinline__ void start(const W4Params& p, const Item& it, int slice, int lane) {
+    if constexpr (Kd::DIRECT) {
+      // a row past the item's reads its last one: nothing of it is stored
+#pragma unroll
+      for (int t = 0; t < Kd::NT; ++t)
+        x[t] = static_cast<const char*>(p.x) +
+               (int64_t(it.row0 + min(8 * t + (lane >> 2), it.rows - 1)) * p.H +
+                slice * kBlockIn + 8 * (lane & 3)) * 2;
+    }
+  }
+
+  // The next unit's, of which `inputs` lie before H; moves on by `split`.
+  template <int USED>
+  __device__ __forceinline__ void load(int inputs, int split) {
+    if constexpr (Kd::DIRECT) {
+#pragma unroll
+      for (int t = 0; t < USED; ++t) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (32 * i < inputs) v[t][i] = __ldg(reinterpret_cast<const uint4*>(x[t] + 64 * i));
+        x[t] += split * kBlockIn * 2;
+      }
+    }
+  }
+
+  // Word i as four 16-bit float pairs, inputs 2 j and 2 j + 1 in pair j.
+  __device__ __forceinline__ void word(uint32_t stage, int lane, int t, int i,
+                                       uint32_t (&b)[4]) const {
+    const int g = lane >> 2, q = lane & 3;
+    if constexpr (Kd::FP8) {
+      const uint2 w = lds8(stage + Kd::x_piece(8 * t + g, 2 * i + (q >> 1)) + (q & 1) * 8);
+      b[0] = e4m3_pair(w.x);
+      b[1] = e4m3_pair(w.x >> 16);
+      b[2] = e4m3_pair(w.y);
+      b[3] = e4m3_pair(w.y >> 16);
+    } else {
+      uint4 w;
+      if constexpr (Kd::DIRECT)
+        w = v[t][i];
+      else
+        w = lds16(stage + Kd::x_piece(8 * t + g, 4 * i + q));
+      b[0] = w.x;
+      b[1] = w.y;
+      b[2] = w.z;
+      b[3] = w.w;
+    }
+  }
+
+  // The scales of columns 8 t + 2 q and + 1.
+  static __device__ __forceinline__ float2 scale(uint32_t stage, int lane, int t) {
+    if constexpr (Kd::FP8) {
+      const uint2 s = lds8(stage + Kd::kXScale + (8 * t + 2 * (lane & 3)) * 4);
+      return make_float2(__uint_as_float(s.x), __uint_as_float(s.y));
+    }
+    return make_float2(1.0f, 1.0f);
+  }
+};
+
+// acc += a group's sums d, rows scaled by the bf16 pair sw, columns by sx.
+template <class Kd>
+__device__ __forceinline__ void add_group(float (&acc)[4], const float (&d)[4], uint32_t sw,
+                                          float2 sx) {
+  const float s0 = bf16_lo(sw), s1 = bf16_hi(sw);
+  acc[0] = fmaf(d[0], Kd::FP8 ? s0 * sx.x : s0, acc[0]);
+  acc[1] = fmaf(d[1], Kd::FP8 ? s0 * sx.y : s0, acc[1]);
+  acc[2] = fmaf(d[2], Kd::FP8 ? s1 * sx.x : s1, acc[2]);
+  acc[3] = fmaf(d[3], Kd::FP8 ? s1 * sx.y : s1, acc[3]);
+}
+
+// d (+)= word i of weight rows lo, hi by the columns' b.
+template <class Kd>
+__device__ __forceinline__ void multiply_word(float (&d)[4], bool first, const uint32_t (&lo)[4],
+                                              const uint32_t (&hi)[4], const uint32_t (&b)[4]) {
+  if (first)
+    mma_first<Kd::FP8>(d, lo[0], hi[0], lo[1], hi[1], b[0], b[1]);
+  else
+    mma<Kd::FP8>(d, lo[0], hi[0], lo[1], hi[1], b[0], b[1]);
+  mma<Kd::FP8>(d, lo[2], hi[2], lo[3], hi[3], b[2], b[3]);
+}
+
+// What a code without a zero point carries, as decode() wants it.
+template <bool FP8>
+constexpr uint32_t kEven = FP8 ? 0x64086408u : 0x43084308u;      // 1024 + 8, 128 + 8
+constexpr uint32_t kOdd = 0x54805480u;                           // 64 + 8
+
+// acc += the unit in a stage, one column tile.  Lane (g = lane / 4, q = lane
+// % 4) holds packed rows 8 g .. 8 g + 7 (piece 2 r + h is row g + 8 h of the
+// r-th 16-row operand) and columns 2 q, 2 q + 1: acc[r][2 h + c].  The four
+// operands' chains of sums run side by side.
+template <class Kd>
+__device__ __forceinline__ void multiply_one(uint32_t stage, int lane, int inputs,
+                                             const Columns<Kd>& cols, float (&acc)[4][4]) {
+  const int g = lane >> 2;
   uint4 w[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) w[i] = lds16(stage + i * 512 + lane * 16);
-  float sx[NT][2];
+  const float2 sx = Columns<Kd>::scale(stage, lane, 0);
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    sx[t][0] = sx[t][1] = 1.0f;
-    if constexpr (FP8) {
-      const uint2 v = lds8(stage + St::kXScale + (8 * t + 2 * q) * 4);
-      sx[t][0] = __uint_as_float(v.x);
-      sx[t][1] = __uint_as_float(v.y);
-    }
-  }
-#pragma unroll
-  for (int s = 0; s < St::kGroups; ++s) {
-    const uint4 sv = lds16(stage + St::kScales + s * 128 + g * 16);
+  for (int s = 0; s < Kd::kGroups; ++s) {
+    if (!Kd::FP8 && Kd::GROUP * s >= inputs) break;      // groups past H
+    const uint4 sv = lds16(stage + Kd::kScales + s * 128 + g * 16);
     uint2 zv;
-    if constexpr (ZEROS) zv = lds8(stage + St::kZeros + s * 64 + g * 8);
-    if (!FP8 && 32 * kWords * s >= inputs) break;      // groups past H
+    if constexpr (Kd::ZEROS) zv = lds8(stage + Kd::kZeros + s * 64 + g * 8);
     uint32_t even[8], odd[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      even[i] = FP8 ? 0x64086408u : 0x43084308u;      // 1032, 136
-      odd[i] = 0x54805480u;                           // 72
-      if constexpr (ZEROS) offsets<FP8>(i < 4 ? zv.x : zv.y, i & 3, &even[i], &odd[i]);
+      even[i] = kEven<Kd::FP8>;
+      odd[i] = kOdd;
+      if constexpr (Kd::ZEROS) offsets<Kd::FP8>(i < 4 ? zv.x : zv.y, i & 3, &even[i], &odd[i]);
     }
-    float d[NT][4][4];
+    float d[4][4];
 #pragma unroll
-    for (int i = s * kWords; i < (s + 1) * kWords; ++i) {
-      uint32_t b[NT][4];
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        if (NT > 1 && t >= tiles_used) continue;
-        if constexpr (FP8) {
-          const uint2 v = lds8(stage + St::x_piece(8 * t + g, 2 * i + (q >> 1)) + (q & 1) * 8);
-          b[t][0] = e4m3_pair(v.x);
-          b[t][1] = e4m3_pair(v.x >> 16);
-          b[t][2] = e4m3_pair(v.y);
-          b[t][3] = e4m3_pair(v.y >> 16);
-        } else {
-          const uint4 v = lds16(stage + St::x_piece(8 * t + g, 4 * i + q));
-          b[t][0] = v.x;
-          b[t][1] = v.y;
-          b[t][2] = v.z;
-          b[t][3] = v.w;
-        }
-      }
+    for (int i = s * Kd::kWords; i < (s + 1) * Kd::kWords; ++i) {
+      uint32_t b[4];
+      cols.word(stage, lane, 0, i, b);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         uint32_t lo[4], hi[4];
-        decode<FP8>(word_of(w[2 * r], i), even[2 * r], odd[2 * r], lo);
-        decode<FP8>(word_of(w[2 * r + 1], i), even[2 * r + 1], odd[2 * r + 1], hi);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          if (NT > 1 && t >= tiles_used) continue;
-          if (i == s * kWords)
-            mma_first<FP8>(d[t][r], lo[0], hi[0], lo[1], hi[1], b[t][0], b[t][1]);
-          else
-            mma<FP8>(d[t][r], lo[0], hi[0], lo[1], hi[1], b[t][0], b[t][1]);
-          mma<FP8>(d[t][r], lo[2], hi[2], lo[3], hi[3], b[t][2], b[t][3]);
-        }
+        decode<Kd::FP8>(word_of(w[2 * r], i), even[2 * r], odd[2 * r], lo);
+        decode<Kd::FP8>(word_of(w[2 * r + 1], i), even[2 * r + 1], odd[2 * r + 1], hi);
+        multiply_word<Kd>(d[r], i == s * Kd::kWords, lo, hi, b);
       }
     }
     const uint32_t sw[4] = {sv.x, sv.y, sv.z, sv.w};
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const float s0 = bf16_lo(sw[r]), s1 = bf16_hi(sw[r]);
+    for (int r = 0; r < 4; ++r) add_group<Kd>(acc[r], d[r], sw[r], sx);
+  }
+}
+
+// The same for all NT column tiles: a decoded word serves each of them.  One
+// operand after another, so that the sums of NT tiles fit the registers.
+template <class Kd>
+__device__ __forceinline__ void multiply_all(uint32_t stage, int lane, int inputs,
+                                             const Columns<Kd>& cols,
+                                             float (&acc)[Kd::NT][4][4]) {
+  const int g = lane >> 2;
+  uint32_t b[Kd::NT][4][4];
+  float2 sx[Kd::NT];
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        if (NT > 1 && t >= tiles_used) continue;
-        acc[t][r][0] = fmaf(d[t][r][0], FP8 ? s0 * sx[t][0] : s0, acc[t][r][0]);
-        acc[t][r][1] = fmaf(d[t][r][1], FP8 ? s0 * sx[t][1] : s0, acc[t][r][1]);
-        acc[t][r][2] = fmaf(d[t][r][2], FP8 ? s1 * sx[t][0] : s1, acc[t][r][2]);
-        acc[t][r][3] = fmaf(d[t][r][3], FP8 ? s1 * sx[t][1] : s1, acc[t][r][3]);
+  for (int t = 0; t < Kd::NT; ++t) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) cols.word(stage, lane, t, i, b[t][i]);
+    sx[t] = Columns<Kd>::scale(stage, lane, t);
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const uint4 w0 = lds16(stage + (2 * r) * 512 + lane * 16);
+    const uint4 w1 = lds16(stage + (2 * r + 1) * 512 + lane * 16);
+#pragma unroll
+    for (int s = 0; s < Kd::kGroups; ++s) {
+      if (!Kd::FP8 && Kd::GROUP * s >= inputs) break;      // groups past H
+      const uint32_t sw = lds4(stage + Kd::kScales + s * 128 + g * 16 + r * 4);
+      uint32_t even[2] = {kEven<Kd::FP8>, kEven<Kd::FP8>}, odd[2] = {kOdd, kOdd};
+      if constexpr (Kd::ZEROS) {
+        const uint32_t z = lds2(stage + Kd::kZeros + s * 64 + g * 8 + 2 * r);
+        offsets<Kd::FP8>(z, 0, &even[0], &odd[0]);
+        offsets<Kd::FP8>(z, 1, &even[1], &odd[1]);
       }
+      float d[Kd::NT][4];
+#pragma unroll
+      for (int i = s * Kd::kWords; i < (s + 1) * Kd::kWords; ++i) {
+        uint32_t lo[4], hi[4];
+        decode<Kd::FP8>(word_of(w0, i), even[0], odd[0], lo);
+        decode<Kd::FP8>(word_of(w1, i), even[1], odd[1], hi);
+#pragma unroll
+        for (int t = 0; t < Kd::NT; ++t)
+          multiply_word<Kd>(d[t], i == s * Kd::kWords, lo, hi, b[t][i]);
+      }
+#pragma unroll
+      for (int t = 0; t < Kd::NT; ++t) add_group<Kd>(acc[t][r], d[t], sw, sx[t]);
     }
   }
 }
@@ -423,30 +536,40 @@ __device__ __forceinline__ void store_pair(const W4Params& p, const Item& it, in
 
 // WARPS warps a CTA in groups of `split`: a group shares an item, warp j of
 // it taking the blocks j, j + split, ...; the warps of a group add up their
-// sums in shared memory.  Each warp keeps STAGES units on their way in
-// shared memory of its own (cp.async, so no barrier and no flag).
-template <bool FP8, int GROUP, bool ZEROS, int NT, int WARPS, int STAGES>
+// sums in shared memory, in the order of the warps.  Each warp keeps STAGES
+// units on their way in shared memory of its own (cp.async, so no barrier
+// and no flag), across the ends of items too.  One CTA an SM.
+//
+// What bounds it.  Few rows: reading the weights.  128 tokens, 8 of 256
+// experts, 4096 x 7168 gated, E4M3 rows: 3.82 GB in 562 us = 6.8 TB/s, 1.02
+// of the measured copy rate.  One such token (120 MB): 24.8 us = 4.8 TB/s;
+// its 512 items are 3.4 an SM, so that some SMs have four, and about 4 us
+// are launch, table of chunks, first load and last sum.  One row by 7168 x
+// 2048: 5.3 us, all latency.  Sixteen warps and not eight (659 us for the
+// 128 tokens) because a unit is some 450 instructions that depend on each
+// other closely: integer operations (half rate) to decode, about 230.  That
+// is also what bounds many rows, with the tensor cores at a third; one
+// decoding for two column tiles then pays.
+template <class Kd, int WARPS, int STAGES>
 __global__ void __launch_bounds__(WARPS * 32) expert_w4_kernel(W4Params p, int split) {
-  using St = Stage<FP8, GROUP, ZEROS, NT>;
-  static_assert(St::kBytes >= NT * 2048, "a stage holds a warp's sums");
+  constexpr int NT = Kd::NT;
+  static_assert(Kd::kBytes >= NT * 2048, "a stage holds a warp's sums");
   extern __shared__ __align__(16) char smem[];
-  int* const pre = reinterpret_cast<int*>(smem + WARPS * STAGES * St::kBytes);
+  int* const pre = reinterpret_cast<int*>(smem + WARPS * STAGES * Kd::kBytes);
   __shared__ uint32_t sums_at[WARPS];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const uint32_t base = smem_addr(smem) + warp * (STAGES * St::kBytes);
+  const uint32_t base = smem_addr(smem) + warp * (STAGES * Kd::kBytes);
   pdl_wait();
-  count_chunks<8 * NT>(p, pre);
+  count_chunks<Kd::kChunk>(p, pre);
   // groups are numbered across the CTAs first: a last partial round of items
   // then spreads over all SMs
   const int group = warp / split, slice = warp % split;
   Walk now(p, group * gridDim.x + blockIdx.x, gridDim.x * (WARPS / split), pre[p.E]);
   Walk ahead = now;      // the item of the unit to load next
-  Loader<FP8, GROUP, ZEROS, NT> loader;
+  Loader<Kd> loader;
   loader.kb = p.blocks;
   const auto enter = [&] {
-    Item next;
-    next.find<8 * NT>(p, pre, ahead, lane);
-    loader.start(p, next, slice, lane);
+    loader.start(p, item_at<Kd::kChunk>(p, pre, ahead, lane), slice, lane);
   };
   if (!ahead.done()) enter();
   const auto load_next = [&](uint32_t stage) {
@@ -460,13 +583,14 @@ __global__ void __launch_bounds__(WARPS * 32) expert_w4_kernel(W4Params p, int s
     cp_async_commit();
   };
 #pragma unroll
-  for (int i = 0; i < STAGES - 1; ++i) load_next(base + i * St::kBytes);
+  for (int i = 0; i < STAGES - 1; ++i) load_next(base + i * Kd::kBytes);
 
-  uint32_t stage = base, idle = base + (STAGES - 1) * St::kBytes;
+  Columns<Kd> cols = {};
+  uint32_t stage = base, idle = base + (STAGES - 1) * Kd::kBytes;
   for (; !now.done(); now.advance(p)) {
-    Item it;
-    it.find<8 * NT>(p, pre, now, lane);
+    const Item it = item_at<Kd::kChunk>(p, pre, now, lane);
     const int used = (it.rows + 7) >> 3;
+    cols.start(p, it, slice, lane);
     float acc[NT][4][4];
 #pragma unroll
     for (int t = 0; t < NT; ++t)
@@ -475,12 +599,23 @@ __global__ void __launch_bounds__(WARPS * 32) expert_w4_kernel(W4Params p, int s
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[t][r][i] = 0.0f;
     for (int kb = slice; kb < p.blocks; kb += split) {
+      const int inputs = p.H - kb * kBlockIn;
+      // one branch a unit: inside the products it would split the stream of
+      // multiplications (measured 1.4 times slower)
+      const bool all = NT > 1 && used > 1;
+      if (all)
+        cols.template load<NT>(inputs, split);
+      else
+        cols.template load<1>(inputs, split);
       cp_async_wait<STAGES - 2>();
       __syncwarp();      // the unit is there, and the idle stage was read by all
       load_next(idle);
-      multiply_unit<FP8, GROUP, ZEROS, NT>(stage, lane, used, p.H - kb * kBlockIn, acc);
+      if (all)
+        multiply_all<Kd>(stage, lane, inputs, cols, acc);
+      else
+        multiply_one<Kd>(stage, lane, inputs, cols, acc[0]);
       idle = stage;
-      stage = stage == base + (STAGES - 1) * St::kBytes ? base : stage + St::kBytes;
+      stage = stage == base + (STAGES - 1) * Kd::kBytes ? base : stage + Kd::kBytes;
     }
     const int g = lane >> 2, q = lane & 3;
     if (split == 1) {
@@ -625,12 +760,13 @@ double expected_chunks(int rows, int E, int size) {
   return active > full ? active : full;
 }
 
-template <bool FP8, int GROUP, bool ZEROS>
-cudaError_t launch_w4(const W4Params& p, int num_rows, cudaStream_t stream) {
-  constexpr int NT = 1, WARPS = 16;
-  constexpr int STAGES = kSmemBudget / (WARPS * Stage<FP8, GROUP, ZEROS, NT>::kBytes);
-  static_assert(STAGES >= 2);
-  const double items = expected_chunks(num_rows, p.E, 8 * NT) * p.tiles;
+template <class Kd>
+cudaError_t launch_kind(const W4Params& p, int num_rows, cudaStream_t stream) {
+  constexpr int WARPS = 16;
+  // two stages; a third measured no faster, and leaves less of L1
+  constexpr int STAGES = 2;
+  static_assert(WARPS * STAGES * Kd::kBytes <= kSmemBudget);
+  const double items = expected_chunks(num_rows, p.E, Kd::kChunk) * p.tiles;
   const int sms = device_info().sm_count;
   // Units one warp works through: rounds of items times its blocks of each,
   // and about one unit's time to add up a group's sums.
@@ -645,11 +781,11 @@ cudaError_t launch_w4(const W4Params& p, int num_rows, cudaStream_t stream) {
     }
   }
   // an upper bound of the items: an expert's last chunk may be short
-  const int64_t chunks = int64_t(num_rows) / (8 * NT) + (num_rows < p.E ? num_rows : p.E);
+  const int64_t chunks = int64_t(num_rows) / (Kd::kChunk) + (num_rows < p.E ? num_rows : p.E);
   const int64_t want = (chunks * p.tiles + WARPS / split - 1) / (WARPS / split);
   const int grid = int(want < sms ? want : sms);
-  const size_t smem = WARPS * STAGES * Stage<FP8, GROUP, ZEROS, NT>::kBytes + sizeof(int) * (p.E + 1);
-  auto* kernel = expert_w4_kernel<FP8, GROUP, ZEROS, NT, WARPS, STAGES>;
+  const size_t smem = WARPS * STAGES * Kd::kBytes + sizeof(int) * (p.E + 1);
+  auto* kernel = expert_w4_kernel<Kd, WARPS, STAGES>;
   // once per kernel and device: the limit for any number of experts
   static std::atomic<uint64_t> raised{0};
   int dev = 0;
@@ -661,6 +797,20 @@ cudaError_t launch_w4(const W4Params& p, int num_rows, cudaStream_t stream) {
     if (dev < 64) raised.fetch_or(uint64_t(1) << dev, std::memory_order_release);
   }
   return launch_pdl(kernel, dim3(grid), dim3(WARPS * 32), smem, stream, p, split);
+}
+
+// One column tile (8 rows) an item, or two where the experts in use have
+// over seven rows on average.  64 experts of 2048 x 4096, one tile and two:
+// bf16 rows 54 and 59 us at 4 rows an expert, 74 and 70 at 8, 122 and 103 at
+// 16, 383 and 270 at 64; E4M3 50 and 54, 67 and 67, 113 and 99, 353 and 276.
+// Two tiles of bf16 rows do not fit the stages of 16 warps and are read
+// directly (staged, with 12 warps: 132 us at 16).
+template <bool FP8, int GROUP, bool ZEROS>
+cudaError_t launch_w4(const W4Params& p, int num_rows, cudaStream_t s) {
+  const double active = p.E * (1.0 - pow(1.0 - 1.0 / p.E, num_rows));
+  if (num_rows > 7.0 * active)
+    return launch_kind<Kind<FP8, GROUP, ZEROS, 2, !FP8>>(p, num_rows, s);
+  return launch_kind<Kind<FP8, GROUP, ZEROS, 1, false>>(p, num_rows, s);
 }
 
 template <bool FP8, int GROUP>
