@@ -1,4 +1,5 @@
-"""Python binding of libep_gb300.so (MoE dispatch / combine layout on GB300).
+"""Python binding of libep_gb300.so (MoE dispatch / combine layout on GB300,
+with the router gate before it and experts' 4-bit products inside).
 
 Two layers, both argument marshalling only -- every step of layout, dispatch
 and combine runs in the library's CUDA kernels:
@@ -6,7 +7,7 @@ and combine runs in the library's CUDA kernels:
 * ``ep_*`` functions with the C ABI's names and arguments (include/ep.h),
   taking ``EpConfig`` / ``EpLayout`` ctypes structures and raw pointers.
 * A torch layer (``Config``, ``Layout``, ``get_layout``, ``dispatch``,
-  ``combine``) that allocates device buffers with torch, passes
+  ``combine``, ``route``, ``expert_w4``, ...) that allocates device buffers with torch, passes
   ``tensor.data_ptr()`` and the current CUDA stream, and raises ``EpError``
   on a non-zero status.  torch provides memory and streams, nothing else.
 

@@ -10,6 +10,13 @@
  *   ep_dispatch   : token-major x       -> expert-major rows (bf16 or FP8)
  *   ep_combine    : expert-major rows   -> token-major y (gate-weighted)
  *
+ * with what stands before and between them in a layer:
+ *
+ *   ep_route      : router logits       -> topk_idx, gate weights (losses,
+ *                                          gradient: ep_route_balance,
+ *                                          ep_route_backward)
+ *   ep_expert_w4  : expert-major rows   -> rows times 4-bit expert weights
+ *
  * Sources (page title, section):
  *  "GPU Microarchitecture: DeepEP from First Principles" -- 1.1 and 1.2
  *  (dispatch token-major -> destination-major -> expert-major; combine back,
@@ -557,8 +564,8 @@ EP_API int64_t ep_route_workspace_bytes(const ep_router_config *cfg, int32_t num
 
 /* ep_route together with the balance statistics and losses of its tokens.
  *
- * The tokens form num_seqs (B in [1, 2^20]) sequences: d_seq_start (device int32 [B + 1],
- * NULL when B = 1) ascends from 0 to T, sequence b owns tokens
+ * The tokens form B = num_seqs (1 to 2^20) sequences: d_seq_start (device
+ * int32 [B + 1], NULL when B = 1) ascends from 0 to T, sequence b owns tokens
  * [seq_start[b], seq_start[b+1]) and may be empty.  Masked tokens count
  * nowhere.  With n_b the tokens of sequence b, c_be their selections of
  * expert e, and p_te = s_te / (sum of s_t over the experts):
@@ -650,7 +657,7 @@ EP_API int32_t ep_w4_pack(const ep_w4_config *cfg, const uint8_t *d_codes,
 
 /* The product.  cap: rows that d_x and d_out hold.  num_rows: how many rows
  * the experts have together, at most (T * K of the layout's call; it sizes
- * the launch, and more rows are still computed).
+ * the launch, and more rows are still computed; 0 launches nothing).
  * d_x: device [cap, H] bf16, or E4M3 bytes with d_x_scale (device fp32
  *   [cap, H / 128]), as ep_dispatch writes them.
  * d_expert_start, d_expert_end: device int32 [E] at least, a layout's: expert
@@ -658,7 +665,8 @@ EP_API int32_t ep_w4_pack(const ep_w4_config *cfg, const uint8_t *d_codes,
  * d_out: device bf16 [cap, N] ([cap, N/2] when gated); rows of no expert
  *   are not written.
  * Products and sums are fp32 (codes and inputs enter them exactly), rounded
- * once at the end.  Returns EP_OK or an error. */
+ * once at the end; the same call gives the same bits.  A value of x that is
+ * not finite shows in its own row alone.  Returns EP_OK or an error. */
 EP_API int32_t ep_expert_w4(const ep_w4_config *cfg, int32_t cap, int32_t num_rows,
                             const void *d_x, const float *d_x_scale, const void *d_codes,
                             const void *d_scales, const uint8_t *d_zeros,
