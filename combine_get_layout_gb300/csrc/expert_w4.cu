@@ -780,10 +780,10 @@ cudaError_t launch_kind(const W4Params& p, int num_rows, cudaStream_t stream) {
       least = cost;
     }
   }
-  // an upper bound of the items: an expert's last chunk may be short
-  const int64_t chunks = int64_t(num_rows) / (Kd::kChunk) + (num_rows < p.E ? num_rows : p.E);
-  const int64_t want = (chunks * p.tiles + WARPS / split - 1) / (WARPS / split);
-  const int grid = int(want < sms ? want : sms);
+  // every SM that can have an item (an upper bound of them: an expert's last
+  // chunk may be short), rather than as few as hold all groups
+  const int64_t chunks = int64_t(num_rows) / Kd::kChunk + (num_rows < p.E ? num_rows : p.E);
+  const int grid = int(chunks * p.tiles < sms ? chunks * p.tiles : sms);
   const size_t smem = WARPS * STAGES * Kd::kBytes + sizeof(int) * (p.E + 1);
   auto* kernel = expert_w4_kernel<Kd, WARPS, STAGES>;
   // once per kernel and device: the limit for any number of experts
