@@ -792,8 +792,8 @@ def _refuse(what: str):
 
 def _flat(t, dtype, shape) -> bool:
     """t is None, or a contiguous CUDA tensor of this type and shape."""
-    return t is None or (t.dtype is dtype and t.shape == shape and t.is_contiguous()
-                         and t.is_cuda)
+    return t is None or (t.dtype is dtype and t.is_cuda and t.is_contiguous()
+                         and t.shape == shape)
 
 
 def _mask_ok(t, T: int) -> bool:
@@ -894,7 +894,8 @@ def route(cfg: RouterConfig, logits, bias=None, token_mask=None, topk_idx=None,
     if topk_weights is None:
         topk_weights = _torch.empty(shape, dtype=_torch.float32, device=logits.device)
     if not (_flat(topk_idx, _torch.int64, shape) and _flat(topk_weights, _torch.float32, shape)
-            and _flat(bias, _torch.float32, (cfg.num_experts,)) and _mask_ok(token_mask, T)):
+            and (bias is None or _flat(bias, _torch.float32, (cfg.num_experts,)))
+            and (token_mask is None or _mask_ok(token_mask, T))):
         _refuse("route: type, shape or place of a tensor")
     st = _lib.ep_route(c, T, logits.data_ptr(), ld, _ptr(bias), _ptr(token_mask),
                        topk_idx.data_ptr(), topk_weights.data_ptr(), _stream_of(logits, stream))

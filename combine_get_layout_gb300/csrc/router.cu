@@ -201,6 +201,14 @@ __device__ __forceinline__ float fast_reciprocal(float x) {
   return r;
 }
 
+// a / b for 0 <= a <= b, given 1 / b to within a few roundings: the product,
+// and its residual as one correction (Newton's step for a quotient).  a / a
+// is 1: the correction of 1 - 2^-24 or 1 + 2^-23 rounds to it.
+__device__ __forceinline__ float quotient(float a, float b, float inv_b) {
+  const float q = a * inv_b;
+  return fmaf(fmaf(-q, b, a), inv_b, q);
+}
+
 __device__ __forceinline__ float sigmoid(float x) {
   return fast_reciprocal(1.0f + fast_exp2(-kLog2e * x));
 }
@@ -553,7 +561,7 @@ __device__ __forceinline__ Chosen<S> route_token(const RouteParams& p, int t, bo
   constexpr int L = S::kLanes;
   const int l = lane % L;
   const int64_t offset = int64_t(t) * p.ld;
-  float inv = 1.0f;      // what the chosen scores are multiplied by, but for p.scale
+  float divisor = 1.0f;      // of the chosen scores
   float c[S::kValues];
   if constexpr (SIG) {
     *total = scores<S, SIG>(x, s, top);
@@ -570,14 +578,13 @@ __device__ __forceinline__ Chosen<S> route_token(const RouteParams& p, int t, bo
     *top = tile_max<L>(largest(x));
     if (STATS || !p.renorm) {
       *total = soft_scores<S>(x, s, *top);
-      if (!p.renorm) inv = fast_reciprocal(*total);
-      if (*total != *total) inv = *total;
+      if (!p.renorm || *total != *total) divisor = *total;
     } else {
       // NaN where a logit is, or where -inf meets +inf, whose weights are NaN
       float any = 0.0f;
 #pragma unroll
       for (int r = 0; r < S::kValues; ++r) any += x[r];
-      if (tile_bits<L>(__ballot_sync(kFull, any != any), lane) != 0) inv = CUDART_NAN_F;
+      if (tile_bits<L>(__ballot_sync(kFull, any != any), lane) != 0) divisor = CUDART_NAN_F;
     }
 #pragma unroll
     for (int r = 0; r < S::kValues; ++r) c[r] = x[r];
@@ -595,14 +602,15 @@ __device__ __forceinline__ Chosen<S> route_token(const RouteParams& p, int t, bo
   }
   if (p.renorm) {
     sum = tile_sum<L>(sum);
-    inv = sum == 0.0f ? 0.0f : inv * fast_reciprocal(sum);
+    if (divisor == divisor) divisor = sum;      // the mark of a row with a NaN stays
   }
+  const float inv = fast_reciprocal(divisor);
 #pragma unroll
   for (int i = 0; i < S::kSlots; ++i) {
     if (live && out.rank[i] < p.K) {
       const int64_t at = int64_t(t) * p.K + out.rank[i];
       p.idx[at] = out.e[i];
-      p.w[at] = out.e[i] >= 0 ? w[i] * inv * p.scale : 0.0f;
+      p.w[at] = out.e[i] >= 0 && divisor != 0.0f ? quotient(w[i], divisor, inv) * p.scale : 0.0f;
     }
   }
   return out;
@@ -1051,7 +1059,8 @@ route_backward_kernel(RouteBackwardParams p) {
       if (p.renorm) {
         const float sum = tile_sum<L>(sk);
         const float is = sum == 0.0f ? 0.0f : fast_reciprocal(sum);
-        const float mean = tile_sum<L>(ds * sk) * is;
+        // a single choice weighs exactly 1, and passes nothing on
+        const float mean = tile_sum<L>(ds * quotient(sk, sum, is));
         ds = (ds - mean) * is;
       }
       if (mine >= 0) row[mine] = ds;
@@ -1111,6 +1120,7 @@ bool router_ok(const ep_router_config* c) {
 }
 
 constexpr int kMaxSequences = 1 << 20;
+constexpr int kMaxTokens = 1 << 30;      // token numbers and strides stay under 2^31
 
 // CTAs of a per-token kernel over `tokens` tokens, `tiles` of them at a time
 // in a CTA: at most `share` CTAs an SM, each tile with a token at least.
@@ -1269,7 +1279,7 @@ int32_t status(cudaError_t e) { return note_cuda(e) == cudaSuccess ? EP_OK : EP_
 bool route_args(const ep_router_config* cfg, int32_t T, const void* d_logits, int64_t ld,
                 const float* d_bias, const uint8_t* d_mask, int64_t* d_idx, float* d_w,
                 RouteParams* p) {
-  if (!router_ok(cfg) || T < 0 || ld < cfg->num_experts) return false;
+  if (!router_ok(cfg) || T < 0 || T > kMaxTokens || ld < cfg->num_experts) return false;
   if (d_bias != nullptr && cfg->score != EP_SCORE_SIGMOID) return false;
   if (!aligned_or_null(d_bias) || !aligned_or_null(d_mask)) return false;
   if (T > 0 && (!aligned(d_logits) || !aligned(d_idx) || !aligned(d_w))) return false;
@@ -1372,7 +1382,7 @@ int32_t ep_route_backward(const ep_router_config* cfg, int32_t num_tokens, const
                           const int32_t* d_seq_start, const int32_t* d_expert_count,
                           const int32_t* d_seq_tokens, const float* d_grad_loss,
                           void* d_grad_logits, int64_t ld_grad, void* stream) {
-  if (!router_ok(cfg) || num_tokens < 0) return EP_ERR_INVALID_ARG;
+  if (!router_ok(cfg) || num_tokens < 0 || num_tokens > kMaxTokens) return EP_ERR_INVALID_ARG;
   if (ld_logits < cfg->num_experts || ld_grad < cfg->num_experts) return EP_ERR_INVALID_ARG;
   if (num_seqs < 1 || num_seqs > kMaxSequences) return EP_ERR_INVALID_ARG;
   if (num_tokens > 0 && (!aligned(d_logits) || !aligned(d_grad_logits)))

@@ -546,7 +546,7 @@ typedef struct {
   float route_scale;     /* factor of every gate weight                     */
 } ep_router_config;
 
-/* Choice and gate weights of num_tokens tokens.
+/* Choice and gate weights of num_tokens (T, at most 2^30) tokens.
  * d_logits: device [T, ld_logits] fp32 or bf16, ld_logits >= E (entries past
  *   E are not read).
  * d_bias: device fp32 [E] or NULL; sigmoid scores only.

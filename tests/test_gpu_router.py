@@ -212,6 +212,19 @@ def test_balance_and_backward(ep, case):
             (abs(only_w) + abs(only_l)) + 1e-38).all()
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_a_single_renormalised_choice_weighs_one(ep, score):
+    """w = s / s is 1 to the bit, and passes no gradient on."""
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    for E in (1, 8, 60, 256, 1000):
+        cfg = ep.RouterConfig(E, 1, score, route_scale=2.5)
+        x = 3 * torch.randn((6000, E), device="cuda", generator=gen)
+        idx, w = ep.route(cfg, x)
+        assert (w == 2.5).all()
+        g = ep.route_backward(cfg, x, idx, torch.randn(w.shape, device="cuda", generator=gen))
+        assert (g == 0).all()
+
+
 def test_no_tokens(ep):
     cfg = ep.RouterConfig(16, 2)
     x = torch.empty((0, 16), device="cuda")

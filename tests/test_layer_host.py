@@ -56,7 +56,7 @@ def test_router_configs_rejected(ep, bad):
 def test_router_arguments_rejected(ep):
     c = router(ep)
     good = [c, 2, A, 64, None, None, A, A, None]
-    for at, v in ((1, -1), (2, None), (2, M), (3, 63), (4, A), (4, M), (5, M), (6, None), (6, M),
+    for at, v in ((1, -1), (1, (1 << 30) + 1), (2, None), (2, M), (3, 63), (4, A), (4, M), (5, M), (6, None), (6, M),
                   (7, None), (7, M)):
         a = list(good)
         a[at] = v
@@ -68,7 +68,7 @@ def test_router_arguments_rejected(ep):
         a[at] = v
         assert ep.ep_route_balance(*a) == ep.EP_ERR_INVALID_ARG, (at, v)
     good = [c, 2, A, 64, None, A, A, 2, A, A, A, A, A, 64, None]
-    for at, v in ((1, -1), (2, M), (3, 63), (4, M), (5, None), (6, M), (7, 0), (8, None),
+    for at, v in ((1, -1), (1, (1 << 30) + 1), (2, M), (3, 63), (4, M), (5, None), (6, M), (7, 0), (8, None),
                   (9, None), (10, None), (11, None), (11, M), (12, None), (13, 63)):
         a = list(good)
         a[at] = v
