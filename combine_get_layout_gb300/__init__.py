@@ -10,6 +10,8 @@ and combine runs in the library's CUDA kernels:
   ``combine``, ``route``, ``expert_w4``, ...) that allocates device buffers with torch, passes
   ``tensor.data_ptr()`` and the current CUDA stream, and raises ``EpError``
   on a non-zero status.  torch provides memory and streams, nothing else.
+  The calls of the router gate and of the experts' products go through a
+  small compiled extension (ep_torch_calls) instead of ctypes.
 
 There is no fallback: if the shared library is missing, importing this
 package raises.  Build it with ``python combine_get_layout_gb300/build_lib.py``.
@@ -782,12 +784,49 @@ def combine_ranks(cfg: Config, layout: Layout, rank_y, y=None, stream=None):
 
 
 # ---- router gate -----------------------------------------------------------------
-# The wrappers below sit in decode loops where a call is a few microseconds:
-# they build their ABI configs once, test each tensor with one expression and
-# read the current stream's handle directly.
+# The calls below sit in decode loops where a kernel takes a few microseconds:
+# their ABI configs are built once, and a compiled extension (ep_torch_calls,
+# csrc/torch_calls.cpp) checks the tensors and calls the library in one step.
 
 def _refuse(what: str):
     raise EpError(EP_ERR_INVALID_ARG, what)
+
+
+def _done(status: int, what: str):
+    if status < 0:
+        _refuse(f"{what}: type, shape or place of a tensor")
+    _check(status, f"ep_{what}")
+
+
+class _LazyCalls:
+    """ep_torch_calls, loaded with torch by the first call that needs it."""
+
+    def __getattr__(self, name):
+        global _calls
+        import glob
+        import importlib.machinery
+        import importlib.metadata
+        import importlib.util
+        import sys
+
+        import torch  # noqa: F401  (its libraries have to be there first)
+
+        path = os.path.join(_PKG, "_lib", "ep_torch_calls.%s.torch%s.so" % (
+            sys.implementation.cache_tag,
+            importlib.metadata.version("torch").replace("+", ".")))
+        if not os.path.exists(path):
+            raise ImportError(
+                f"{path} is missing (there: {glob.glob(path[:path.index('.cp')] + '*')}): "
+                "build it with `python combine_get_layout_gb300/build_lib.py`")
+        loader = importlib.machinery.ExtensionFileLoader("ep_torch_calls", path)
+        mod = importlib.util.module_from_spec(
+            importlib.util.spec_from_loader("ep_torch_calls", loader))
+        loader.exec_module(mod)
+        _calls = mod
+        return getattr(mod, name)
+
+
+_calls = _LazyCalls()
 
 
 def _flat(t, dtype, shape) -> bool:
@@ -796,52 +835,33 @@ def _flat(t, dtype, shape) -> bool:
                          and t.shape == shape)
 
 
-def _mask_ok(t, T: int) -> bool:
-    return t is None or _flat(t, _torch.bool, (T,)) or _flat(t, _torch.uint8, (T,))
-
-
-def _stream_of(t, stream):
-    """The stream's handle; the current stream of t's device when None."""
-    if stream is not None:
-        return stream.cuda_stream
-    return _torch._C._cuda_getCurrentRawStream(t.get_device())
-
-
 # Scratch memory of the eager calls, by (device, stream, host thread): calls
 # of one thread on one stream run in order, so that they can share it.
 _workspaces = {}
 _outgrown = []      # kept: a stream other than the allocating one may use them still
 
 
-def _workspace_of(t, stream: int, size: int):
-    """At least `size` bytes on t's device for a call on this stream.  Kept
-    from call to call (asking the allocator each time costs more than the
-    kernels of a small batch); under stream capture, fresh memory that the
-    graph owns."""
-    if _torch.cuda.is_current_stream_capturing():
-        return _torch.empty(size, dtype=_torch.uint8, device=t.device)
-    key = t.get_device(), stream, _get_ident()
+def _workspace_of(t, stream, size: int):
+    """At least `size` bytes on t's device for a call on this stream (None:
+    the current one).  Kept from call to call (asking the allocator each time
+    costs more than the kernels of a small batch); under stream capture, fresh
+    memory that the graph owns."""
+    import torch
+
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(size, dtype=torch.uint8, device=t.device)
+    dev = t.get_device()
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    key = dev, stream, _get_ident()
     got = _workspaces.get(key)
     if got is None or got.nbytes < size:
         if got is not None:
             _outgrown.append(got)
             size = max(size, 2 * got.nbytes)      # so that they stay few
-        got = _workspaces[key] = _torch.empty(max(size, 1 << 20), dtype=_torch.uint8,
-                                              device=t.device)
+        got = _workspaces[key] = torch.empty(max(size, 1 << 20), dtype=torch.uint8,
+                                             device=t.device)
     return got
-
-
-class _LazyTorch:
-    """torch, imported by the first call that needs it."""
-
-    def __getattr__(self, name):
-        global _torch
-        import torch as _torch
-
-        return getattr(_torch, name)
-
-
-_torch = _LazyTorch()
 
 
 @dataclasses.dataclass(frozen=True)
@@ -860,26 +880,15 @@ class RouterConfig:
     def __post_init__(self):
         if self.score not in ("softmax", "sigmoid"):
             _refuse(f"RouterConfig: score {self.score!r}")
-        both = tuple(EpRouterConfig(self.num_experts, self.num_topk,
-                                    int(self.score == "sigmoid"), self.num_groups,
-                                    self.topk_groups, int(self.renormalize), bf16,
-                                    self.route_scale) for bf16 in (0, 1))
+        both = (EpRouterConfig * 2)(*(
+            EpRouterConfig(self.num_experts, self.num_topk, int(self.score == "sigmoid"),
+                           self.num_groups, self.topk_groups, int(self.renormalize), bf16,
+                           self.route_scale) for bf16 in (0, 1)))
         object.__setattr__(self, "_c", both)
+        object.__setattr__(self, "_at", ctypes.addressof(both))
 
     def c(self, bf16: bool = False) -> EpRouterConfig:
-        return self._c[bf16]
-
-
-def _logits_args(cfg: RouterConfig, what: str, logits):
-    """(ABI config, T, row stride) of a [T, E] tensor with unit column stride."""
-    dtype = logits.dtype
-    if dtype is not _torch.float32 and dtype is not _torch.bfloat16:
-        _refuse(f"{what}: logits are {dtype}")
-    T, E = logits.shape
-    row, col = logits.stride()
-    if E != cfg.num_experts or (col != 1 and E != 1) or not logits.is_cuda:
-        _refuse(f"{what}: logits are not CUDA [T, {cfg.num_experts}] with unit column stride")
-    return cfg._c[dtype is _torch.bfloat16], T, row if T > 1 else E
+        return self._c[int(bf16)]
 
 
 def route(cfg: RouterConfig, logits, bias=None, token_mask=None, topk_idx=None,
@@ -887,20 +896,18 @@ def route(cfg: RouterConfig, logits, bias=None, token_mask=None, topk_idx=None,
     """ep_route.  logits: fp32 or bf16 CUDA tensor [T, E], rows may be strided;
     bias: fp32 [E]; token_mask: uint8 or bool [T].  Returns (topk_idx int64
     [T, K], topk_weights fp32 [T, K])."""
-    c, T, ld = _logits_args(cfg, "route", logits)
-    shape = (T, cfg.num_topk)
-    if topk_idx is None:
-        topk_idx = _torch.empty(shape, dtype=_torch.int64, device=logits.device)
-    if topk_weights is None:
-        topk_weights = _torch.empty(shape, dtype=_torch.float32, device=logits.device)
-    if not (_flat(topk_idx, _torch.int64, shape) and _flat(topk_weights, _torch.float32, shape)
-            and (bias is None or _flat(bias, _torch.float32, (cfg.num_experts,)))
-            and (token_mask is None or _mask_ok(token_mask, T))):
-        _refuse("route: type, shape or place of a tensor")
-    st = _lib.ep_route(c, T, logits.data_ptr(), ld, _ptr(bias), _ptr(token_mask),
-                       topk_idx.data_ptr(), topk_weights.data_ptr(), _stream_of(logits, stream))
+    if topk_idx is None or topk_weights is None:
+        import torch
+
+        shape, dev = (logits.shape[0], cfg.num_topk), logits.device
+        if topk_idx is None:
+            topk_idx = torch.empty(shape, dtype=torch.int64, device=dev)
+        if topk_weights is None:
+            topk_weights = torch.empty(shape, dtype=torch.float32, device=dev)
+    st = _calls.route(cfg._at, logits, bias, token_mask, topk_idx, topk_weights,
+                      stream if stream is None else stream.cuda_stream)
     if st:
-        _check(st, "ep_route")
+        _done(st, "route")
     return topk_idx, topk_weights
 
 
@@ -911,37 +918,28 @@ def route_balance(cfg: RouterConfig, logits, bias=None, token_mask=None, seq_sta
     expert_prob fp32 [B, E], seq_tokens int32 [B + 2], loss fp32 [2]), which
     `out` may give; workspace: ep_route_workspace_bytes bytes (when None,
     memory kept for the calls of this thread on this stream)."""
-    c, T, ld = _logits_args(cfg, "route_balance", logits)
     B = 1 if seq_start is None else seq_start.shape[0] - 1
-    E, K, dev = cfg.num_experts, cfg.num_topk, logits.device
-    i32, f32 = _torch.int32, _torch.float32
     if out is None:
-        out = (_torch.empty((T, K), dtype=_torch.int64, device=dev),
-               _torch.empty((T, K), dtype=f32, device=dev),
-               _torch.empty((B, E), dtype=i32, device=dev),
-               _torch.empty((B, E), dtype=f32, device=dev),
-               _torch.empty((B + 2,), dtype=i32, device=dev),
-               _torch.empty((2,), dtype=f32, device=dev))
-    idx, w, count, prob, tokens, loss = out
-    size = _lib.ep_route_workspace_bytes(c, B)
-    if size < 0:
-        _refuse("route_balance: config or number of sequences")
-    handle = _stream_of(logits, stream)
+        import torch
+
+        T, E, K, dev = logits.shape[0], cfg.num_experts, cfg.num_topk, logits.device
+        out = (torch.empty((T, K), dtype=torch.int64, device=dev),
+               torch.empty((T, K), dtype=torch.float32, device=dev),
+               torch.empty((B, E), dtype=torch.int32, device=dev),
+               torch.empty((B, E), dtype=torch.float32, device=dev),
+               torch.empty((B + 2,), dtype=torch.int32, device=dev),
+               torch.empty((2,), dtype=torch.float32, device=dev))
+    size = _lib.ep_route_workspace_bytes(cfg._c[0], B)
+    if size < 0 or not logits.is_cuda:
+        _refuse("route_balance: config, number of sequences or place of the logits")
+    handle = None if stream is None else stream.cuda_stream
     if workspace is None:
         workspace = _workspace_of(logits, handle, size)
-    if not (_flat(idx, _torch.int64, (T, K)) and _flat(w, f32, (T, K))
-            and _flat(count, i32, (B, E)) and _flat(prob, f32, (B, E))
-            and _flat(tokens, i32, (B + 2,)) and _flat(loss, f32, (2,))
-            and _flat(bias, f32, (E,)) and _mask_ok(token_mask, T)
-            and _flat(seq_start, i32, (B + 1,))
-            and workspace.is_cuda and workspace.nbytes >= size):
-        _refuse("route_balance: type, shape or place of a tensor")
-    st = _lib.ep_route_balance(c, T, logits.data_ptr(), ld, _ptr(bias), _ptr(token_mask), B,
-                               _ptr(seq_start), idx.data_ptr(), w.data_ptr(), count.data_ptr(),
-                               prob.data_ptr(), tokens.data_ptr(), loss.data_ptr(),
-                               workspace.data_ptr(), handle)
+    idx, w, count, prob, tokens, loss = out
+    st = _calls.route_balance(cfg._at, logits, bias, token_mask, seq_start, idx, w, count, prob,
+                              tokens, loss, workspace, size, handle)
     if st:
-        _check(st, "ep_route_balance")
+        _done(st, "route_balance")
     return idx, w, count, prob, tokens, loss
 
 
@@ -951,24 +949,15 @@ def route_backward(cfg: RouterConfig, logits, topk_idx=None, grad_w=None, token_
     """ep_route_backward.  grad_w: the gate weights' gradient (combine_backward
     returns it); expert_count, seq_tokens: route_balance's; grad_loss: fp32 [2]
     CUDA tensor.  Returns grad_logits [T, E] of the logits' type."""
-    c, T, ld = _logits_args(cfg, "route_backward", logits)
-    B = 1 if seq_start is None else seq_start.shape[0] - 1
-    E, K = cfg.num_experts, cfg.num_topk
-    i32, f32 = _torch.int32, _torch.float32
     if grad_logits is None:
-        grad_logits = _torch.empty((T, E), dtype=logits.dtype, device=logits.device)
-    c_grad, Tg, ld_grad = _logits_args(cfg, "route_backward", grad_logits)
-    if not (c_grad is c and Tg == T and _mask_ok(token_mask, T)
-            and _flat(topk_idx, _torch.int64, (T, K)) and _flat(grad_w, f32, (T, K))
-            and _flat(seq_start, i32, (B + 1,)) and _flat(expert_count, i32, (B, E))
-            and _flat(seq_tokens, i32, (B + 2,)) and _flat(grad_loss, f32, (2,))):
-        _refuse("route_backward: type, shape or place of a tensor")
-    st = _lib.ep_route_backward(c, T, logits.data_ptr(), ld, _ptr(token_mask), _ptr(topk_idx),
-                                _ptr(grad_w), B, _ptr(seq_start), _ptr(expert_count),
-                                _ptr(seq_tokens), _ptr(grad_loss), grad_logits.data_ptr(),
-                                ld_grad, _stream_of(logits, stream))
+        import torch
+
+        grad_logits = torch.empty(tuple(logits.shape), dtype=logits.dtype, device=logits.device)
+    st = _calls.route_backward(cfg._at, logits, topk_idx, grad_w, token_mask, seq_start,
+                               expert_count, seq_tokens, grad_loss, grad_logits,
+                               stream if stream is None else stream.cuda_stream)
     if st:
-        _check(st, "ep_route_backward")
+        _done(st, "route_backward")
     return grad_logits
 
 
@@ -993,7 +982,7 @@ class W4Config:
         if min(sizes) < 0:
             _refuse("W4Config")
         object.__setattr__(self, "_c", c)
-        object.__setattr__(self, "_sizes", sizes)
+        object.__setattr__(self, "_at", ctypes.addressof(c))
         object.__setattr__(self, "_width",
                            self.out_features // 2 if self.gated else self.out_features)
 
@@ -1010,27 +999,21 @@ def w4_pack(cfg: W4Config, codes, scales, zeros=None, stream=None):
     [E, N, H / group]; zeros: uint8, as the scales.  Returns the packed (codes
     int32 [E, tiles, blocks, 8, 32, 4], scales bf16 [E, tiles, groups, 64],
     zeros uint8 or None)."""
+    import torch
+
     E, N, H, g = cfg.num_experts, cfg.out_features, cfg.in_features, cfg.group_size
-    if not (_flat(codes, _torch.uint8, (E, N, H // 2))
-            and _flat(scales, _torch.bfloat16, (E, N, H // g))
-            and _flat(zeros, _torch.uint8, (E, N, H // g))):
+    if not (_flat(codes, torch.uint8, (E, N, H // 2))
+            and _flat(scales, torch.bfloat16, (E, N, H // g))
+            and _flat(zeros, torch.uint8, (E, N, H // g))):
         _refuse("w4_pack: type, shape or place of a tensor")
     tiles, blocks, dev = -(-cfg._width // (32 if cfg.gated else 64)), -(-H // 128), codes.device
-    pc = _torch.empty((E, tiles, blocks, 8, 32, 4), dtype=_torch.int32, device=dev)
-    ps = _torch.empty((E, tiles, blocks * 128 // g, 64), dtype=_torch.bfloat16, device=dev)
-    pz = _torch.empty(ps.shape, dtype=_torch.uint8, device=dev) if cfg.has_zeros else None
+    pc = torch.empty((E, tiles, blocks, 8, 32, 4), dtype=torch.int32, device=dev)
+    ps = torch.empty((E, tiles, blocks * 128 // g, 64), dtype=torch.bfloat16, device=dev)
+    pz = torch.empty(ps.shape, dtype=torch.uint8, device=dev) if cfg.has_zeros else None
     st = ep_w4_pack(cfg._c, codes.data_ptr(), scales.data_ptr(), _ptr(zeros), pc.data_ptr(),
-                    ps.data_ptr(), _ptr(pz), _stream_of(codes, stream))
+                    ps.data_ptr(), _ptr(pz), _stream(stream))
     _check(st, "ep_w4_pack")
     return pc, ps, pz
-
-
-def _packed(t, size: int) -> bool:
-    return t.nbytes == size and t.is_contiguous() and t.is_cuda
-
-
-def _segments(t, E: int) -> bool:
-    return t.dtype is _torch.int32 and t.shape[0] >= E and t.is_contiguous() and t.is_cuda
 
 
 def expert_w4(cfg: W4Config, x, codes, scales, expert_start, expert_end, num_rows, zeros=None,
@@ -1039,20 +1022,12 @@ def expert_w4(cfg: W4Config, x, codes, scales, expert_start, expert_end, num_row
     [cap, H / 128]; codes, scales, zeros: w4_pack's; expert_start, expert_end:
     a Layout's; num_rows: rows of all experts together at most (T * K).
     Returns out, bf16 [cap, N] ([cap, N / 2] when gated)."""
-    H, E, sizes = cfg.in_features, cfg.num_experts, cfg._sizes
-    cap, shape = x.shape[0], (x.shape[0], cfg._width)
     if out is None:
-        out = _torch.empty(shape, dtype=_torch.bfloat16, device=x.device)
-    if not (_flat(x, _torch.uint8 if cfg.x_fp8 else _torch.bfloat16, (cap, H))
-            and (x_scale is None or _flat(x_scale, _torch.float32, (cap, H // 128)))
-            and _flat(out, _torch.bfloat16, shape)
-            and _packed(codes, sizes[0]) and _packed(scales, sizes[1])
-            and (zeros is None or _packed(zeros, sizes[2]))
-            and _segments(expert_start, E) and _segments(expert_end, E)):
-        _refuse("expert_w4: type, shape or place of a tensor")
-    st = _lib.ep_expert_w4(cfg._c, cap, num_rows, x.data_ptr(), _ptr(x_scale), codes.data_ptr(),
-                           scales.data_ptr(), _ptr(zeros), expert_start.data_ptr(),
-                           expert_end.data_ptr(), out.data_ptr(), _stream_of(x, stream))
+        import torch
+
+        out = torch.empty((x.shape[0], cfg._width), dtype=torch.bfloat16, device=x.device)
+    st = _calls.expert_w4(cfg._at, x, codes, scales, expert_start, expert_end, num_rows, zeros,
+                          x_scale, out, stream if stream is None else stream.cuda_stream)
     if st:
-        _check(st, "ep_expert_w4")
+        _done(st, "expert_w4")
     return out

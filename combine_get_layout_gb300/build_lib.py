@@ -1,8 +1,11 @@
-"""Builds libep_gb300.so in-tree for sm_103a with nvcc.
+"""Builds libep_gb300.so in-tree for sm_103a with nvcc, and the torch layer's
+compiled calls beside it.
 
 Each .cu file is compiled in its own nvcc process (in parallel), then the
 objects are linked into one shared library with the CUDA runtime linked
-statically.  Usage: ``python combine_get_layout_gb300/build_lib.py [--force]``.
+statically.  ep_torch_calls (csrc/torch_calls.cpp) is a Python extension for
+the installed torch, compiled by the host compiler and linked to that
+library.  Usage: ``python combine_get_layout_gb300/build_lib.py [--force]``.
 This file is standalone (it never imports the package, whose import needs the
 built library).
 """
@@ -10,10 +13,13 @@ built library).
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.metadata
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -21,6 +27,10 @@ CSRC = os.path.join(PKG, "csrc")
 OUT_DIR = os.path.join(PKG, "_lib")
 BUILD_DIR = os.path.join(PKG, "_build_obj")
 LIB = os.path.join(OUT_DIR, "libep_gb300.so")
+CALLS_SRC = os.path.join(CSRC, "torch_calls.cpp")
+# one file a Python and torch, whose binary interfaces it follows
+CALLS = os.path.join(OUT_DIR, "ep_torch_calls.%s.torch%s.so" % (
+    sys.implementation.cache_tag, importlib.metadata.version("torch").replace("+", ".")))
 HEADERS = [os.path.join(ROOT, "include", "ep.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -51,8 +61,49 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
+def calls_up_to_date() -> bool:
+    if not os.path.exists(CALLS):
+        return False
+    t = os.path.getmtime(CALLS)
+    return all(os.path.getmtime(d) <= t for d in [CALLS_SRC, *HEADERS])
+
+
+def compile_calls() -> str:
+    """The object file of ep_torch_calls; linked after the library."""
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(shutil.which(nvcc()) or nvcc())))
+    inc = [os.path.join(torch_dir, "include"),
+           os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    obj = os.path.join(BUILD_DIR, "torch_calls.o")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-c", CALLS_SRC, "-o", obj]
+    for d in inc:
+        cmd += ["-isystem", d]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {CALLS_SRC}:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def link_calls(obj: str) -> None:
+    torch_lib = os.path.join(os.path.dirname(importlib.util.find_spec("torch").origin), "lib")
+    tmp = CALLS + f".tmp{os.getpid()}"
+    # torch's own libraries are loaded before the extension is, this one from
+    # beside it
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L" + OUT_DIR, "-l:" + os.path.basename(LIB),
+           "-Wl,-rpath,$ORIGIN", "-L" + torch_lib, "-lc10", "-lc10_cuda", "-ltorch_cpu",
+           "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"linking {CALLS} failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS)
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     if not force and up_to_date():
+        if not calls_up_to_date():
+            os.makedirs(BUILD_DIR, exist_ok=True)
+            link_calls(compile_calls())
         return LIB
     os.makedirs(OUT_DIR, exist_ok=True)
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -69,14 +120,17 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         return obj
 
     srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=max(1, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(srcs) + 1) as ex:
+        calls = ex.submit(compile_calls)
         objs = list(ex.map(compile_one, srcs))
+        calls_obj = calls.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    link_calls(calls_obj)
     return LIB
 
 

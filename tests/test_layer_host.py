@@ -156,3 +156,31 @@ def test_reference_gradient_against_differences():
                     d[t, e] = 1e-5
                     slope = (ref.objective(l + d, *a) - ref.objective(l - d, *a)) / 2e-5
                     assert abs(slope - g[t, e]) < 1e-8
+
+
+def test_compiled_calls_refuse_before_they_call(ep):
+    """Tensors on the CPU, of the wrong kind or count: no kernel is reached."""
+    import torch
+
+    cfg = ep.RouterConfig(8, 2)
+    x = torch.zeros((3, 8))
+    w4 = ep.W4Config(1, 128, 64)
+    codes, scales = torch.zeros((1, 1, 1, 8, 32, 4), dtype=torch.int32), torch.zeros((1, 1, 1, 64))
+    seg = torch.zeros(2, dtype=torch.int32)
+    bad = [
+        lambda: ep.route(cfg, x), lambda: ep.route_balance(cfg, x),
+        lambda: ep.route_backward(cfg, x),
+        lambda: ep.expert_w4(w4, torch.zeros((1, 128), dtype=torch.bfloat16), codes,
+                             scales.bfloat16(), seg, seg, 1),
+    ]
+    for call in bad:
+        with pytest.raises(ep.EpError) as e:
+            call()
+        assert e.value.status == ep.EP_ERR_INVALID_ARG
+    assert ep._calls.route(cfg._at, "logits", None, None, None, None, None) == -1
+    with pytest.raises(TypeError):
+        ep._calls.route(cfg._at, x)
+    with pytest.raises(TypeError):
+        ep._calls.route("config", x, None, None, None, None, None)
+    with pytest.raises(ep.EpError):
+        ep.RouterConfig(8, 2, score="tanh")
