@@ -230,6 +230,27 @@ __device__ void count_chunks(const W4Params& p, int* pre) {
   __syncthreads();
 }
 
+// The same for up to 32 experts, an expert a lane: every warp counts for
+// itself and writes the same values, so that none waits for another (one row
+// of one matrix: 5.3 -> 4.8 us).
+template <int kRows>
+__device__ __forceinline__ void count_few_chunks(const W4Params& p, int* pre, int lane) {
+  int n = 0;
+  if (lane < p.E) {
+    const int lo = max(0, p.start[lane]), hi = min(p.cap, p.end[lane]);
+    n = hi > lo ? (hi - lo + kRows - 1) / kRows : 0;
+  }
+  int end = n;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int up = __shfl_up_sync(0xffffffffu, end, d);
+    if (lane >= d) end += up;
+  }
+  if (lane < p.E) pre[lane + 1] = end;
+  if (lane == 0) pre[0] = 0;
+  __syncwarp();
+}
+
 // The expert whose chunks hold chunk c, by a whole warp: 32 experts' ends a
 // round, so that two rounds serve a thousand experts.
 __device__ __forceinline__ int expert_of(const int* pre, int E, int c, int lane) {
@@ -266,6 +287,7 @@ struct Item {
   int expert, tile, row0, rows;
 };
 
+// Of a chunk below the total, by a whole warp.
 template <int kRows>
 __device__ __forceinline__ Item item_at(const W4Params& p, const int* pre, const Walk& at, int lane) {
   const int e = expert_of(pre, p.E, at.chunk, lane);
@@ -560,7 +582,10 @@ __global__ void __launch_bounds__(WARPS * 32) expert_w4_kernel(W4Params p, int s
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t base = smem_addr(smem) + warp * (STAGES * Kd::kBytes);
   pdl_wait();
-  count_chunks<Kd::kChunk>(p, pre);
+  if (p.E <= 32)
+    count_few_chunks<Kd::kChunk>(p, pre, lane);
+  else
+    count_chunks<Kd::kChunk>(p, pre);
   // groups are numbered across the CTAs first: a last partial round of items
   // then spreads over all SMs
   const int group = warp / split, slice = warp % split;

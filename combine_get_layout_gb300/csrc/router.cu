@@ -839,41 +839,19 @@ struct BalanceParams {
   float* loss;             // [2]
 };
 
-// Sums of a float and two integers over a block of whole warps, in a fixed
-// order, in every thread.
-struct Sums {
-  float f;
-  int a, b;
-};
-__device__ Sums block_sum(Sums v, Sums* scratch) {
-#pragma unroll
-  for (int d = 16; d; d >>= 1) v.f += __shfl_xor_sync(kFull, v.f, d);
-  v.a = __reduce_add_sync(kFull, v.a);
-  v.b = __reduce_add_sync(kFull, v.b);
-  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
-  __syncthreads();
-  Sums s = {0.0f, 0, 0};
-#pragma unroll
-  for (int i = 0; i < kSumThreads / 32; ++i) {
-    s.f += scratch[i].f;
-    s.a += scratch[i].a;
-    s.b += scratch[i].b;
-  }
-  return s;
-}
-
 // Second kernel: CTA (b, i) adds up the partial rows of sequence b for the
 // experts from kSumExperts i on, kSumRows rows at a time, in a fixed order;
-// the CTA that finishes last forms the losses from what all have written.
-// Latency alone: a handful of dependent loads, sums and one atomic.
+// the first warp of the CTA that finishes last forms the losses from what all
+// have written.  Latency alone: a handful of dependent loads, sums and one
+// atomic.
 __global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(BalanceParams p) {
-  __shared__ float probs[kSumRows][kSumExperts];
-  __shared__ int counts[kSumRows][kSumExperts];
-  __shared__ Sums scratch[3][kSumThreads / 32];
-  __shared__ bool is_last;
+  constexpr int kWarps = kSumThreads / 32;
+  __shared__ float probs[kWarps][kSumExperts], zs[kWarps];
+  __shared__ int counts[kWarps][kSumExperts], ns[kWarps];
   pdl_wait();
-  const int b = blockIdx.x, lane = threadIdx.x % kSumExperts, part = threadIdx.x / kSumExperts;
-  int e = blockIdx.y * kSumExperts + lane;
+  const int b = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int part = threadIdx.x / kSumExperts;
+  const int e = blockIdx.y * kSumExperts + threadIdx.x % kSumExperts;
   const int lo = b == 0 ? 0 : min(max(p.seq_start[b], 0), p.T);
   const int hi = b == p.B - 1 ? p.T : min(max(p.seq_start[b + 1], 0), p.T);
   int c0 = 0, c1 = 0;
@@ -896,61 +874,86 @@ __global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(BalanceParams 
     n += p.part_tokens[c + b];
     z += p.part_z[c + b];
   }
-  probs[part][lane] = prob;
-  counts[part][lane] = count;
-  const Sums of_seq = block_sum({z, n, 0}, scratch[0]);
-  n = of_seq.a;
-  z = of_seq.f;
-  if (threadIdx.x < 32) {      // lanes from kSumExperts on add nothing
-    prob = 0.0f;
-    count = 0;
-    e = blockIdx.y * kSumExperts + threadIdx.x;
-    const float inv_n = n > 0 ? 1.0f / float(n) : 0.0f;
-    if (threadIdx.x < kSumExperts) {
+  // the four rows of a warp, then the warps
 #pragma unroll
-      for (int r = 0; r < kSumRows; ++r) {
-        prob += probs[r][threadIdx.x];
-        count += counts[r][threadIdx.x];
-      }
-      prob *= inv_n;
-      if (e < p.E) {
-        p.expert_prob[int64_t(b) * p.E + e] = prob;
-        p.expert_count[int64_t(b) * p.E + e] = count;
-      }
-    }
-    const float dot = tile_sum<32>(float(count) * inv_n * prob);
-    if (threadIdx.x == 0) {
-      p.dots[int64_t(b) * gridDim.y + blockIdx.y] = dot;
-      if (blockIdx.y == 0) {
-        p.seq_tokens[b] = n;
-        p.seq_z[b] = z;
-      }
-      __threadfence();
-      is_last = atomicAdd(p.done, 1u) == gridDim.x * gridDim.y - 1;
-    }
+  for (int d = kSumExperts; d < 32; d <<= 1) {
+    prob += __shfl_xor_sync(kFull, prob, d);
+    count += __shfl_xor_sync(kFull, count, d);
+  }
+  z = tile_sum<32>(z);
+  n = __reduce_add_sync(kFull, n);
+  if (lane < kSumExperts) {
+    probs[warp][lane] = prob;
+    counts[warp][lane] = count;
+  }
+  if (lane == 0) {
+    zs[warp] = z;
+    ns[warp] = n;
   }
   __syncthreads();
-  if (!is_last) return;
+  if (warp != 0) return;
+  prob = 0.0f;
+  count = 0;
+  z = lane < kWarps ? zs[lane] : 0.0f;
+  n = lane < kWarps ? ns[lane] : 0;
+  if (lane < kSumExperts) {
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      prob += probs[w][lane];
+      count += counts[w][lane];
+    }
+  }
+  z = tile_sum<32>(z);
+  n = __reduce_add_sync(kFull, n);
+  const float inv_n = n > 0 ? 1.0f / float(n) : 0.0f;
+  prob *= inv_n;
+  if (lane < kSumExperts && e < p.E) {
+    p.expert_prob[int64_t(b) * p.E + e] = prob;
+    p.expert_count[int64_t(b) * p.E + e] = count;
+  }
+  const float dot = tile_sum<32>(float(count) * inv_n * prob);      // lanes past the experts: 0
+  unsigned before = 0;
+  if (lane == 0) {
+    p.dots[int64_t(b) * gridDim.y + blockIdx.y] = dot;
+    if (blockIdx.y == 0) {
+      p.seq_tokens[b] = n;
+      p.seq_z[b] = z;
+    }
+    __threadfence();
+    before = atomicAdd(p.done, 1u);
+  }
+  before = __shfl_sync(kFull, before, 0);
+  if (before != gridDim.x * gridDim.y - 1) return;
   __threadfence();
+  // every term is there: 32 at a time, in a fixed order
   float loss = 0.0f;
   int full = 0;
   n = 0;
   z = 0.0f;
-  for (int64_t i = threadIdx.x; i < int64_t(p.B) * gridDim.y; i += kSumThreads)
-    loss += __ldcg(p.dots + i);
-  for (int i = threadIdx.x; i < p.B; i += kSumThreads) {
+  const int64_t dots = int64_t(p.B) * gridDim.y;
+  for (int64_t i = lane; i < dots; i += 32 * 16) {
+    float v[16];      // all on their way at once
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] = i + 32 * j < dots ? __ldcg(p.dots + i + 32 * j) : 0.0f;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) loss += v[j];
+  }
+#pragma unroll 4
+  for (int i = lane; i < p.B; i += 32) {
     const int m = __ldcg(p.seq_tokens + i);
     n += m;
     full += m > 0 ? 1 : 0;
     z += __ldcg(p.seq_z + i);
   }
-  const Sums l = block_sum({loss, n, full}, scratch[1]);
-  const Sums zs = block_sum({z, 0, 0}, scratch[2]);
-  if (threadIdx.x == 0) {
-    p.seq_tokens[p.B] = l.a;
-    p.seq_tokens[p.B + 1] = l.b;
-    p.loss[0] = l.b > 0 ? l.f * (float(p.E) / float(p.K)) / float(l.b) : 0.0f;
-    p.loss[1] = l.a > 0 ? zs.f / float(l.a) : 0.0f;
+  loss = tile_sum<32>(loss);
+  z = tile_sum<32>(z);
+  n = __reduce_add_sync(kFull, n);
+  full = __reduce_add_sync(kFull, full);
+  if (lane == 0) {
+    p.seq_tokens[p.B] = n;
+    p.seq_tokens[p.B + 1] = full;
+    p.loss[0] = full > 0 ? loss * (float(p.E) / float(p.K)) / float(full) : 0.0f;
+    p.loss[1] = n > 0 ? z / float(n) : 0.0f;
   }
 }
 
