@@ -567,7 +567,7 @@ __device__ __forceinline__ void store_pair(const W4Params& p, const Item& it, in
 // of the measured copy rate.  One such token (120 MB): 24.8 us = 4.8 TB/s;
 // its 512 items are 3.4 an SM, so that some SMs have four, and about 4 us
 // are launch, table of chunks, first load and last sum.  One row by 7168 x
-// 2048: 5.3 us, all latency.  Sixteen warps and not eight (659 us for the
+// 2048: 4.9 us, all latency.  Sixteen warps and not eight (659 us for the
 // 128 tokens) because a unit is some 450 instructions that depend on each
 // other closely: integer operations (half rate) to decode, about 230.  That
 // is also what bounds many rows, with the tensor cores at a third; one

@@ -690,10 +690,10 @@ constexpr int kBalanceShare = S::kValues <= 8 ? 2 : 1;
 
 // ep_route_balance, first kernel: what bounds it is what bounds ep_route, and
 // the flush of a CTA's sums.  16384 tokens by 256 experts, sigmoid, groups, 4
-// sequences: 23.8 us for both kernels, the bytes 2.8; 4096 by softmax 10.7;
-// 8191 by 64 in 37 ragged sequences 11.3.  512 threads, two CTAs an SM at 64
+// sequences: 23.6 us for both kernels, the bytes 2.8; 4096 by softmax 9.5;
+// 8191 by 64 in 37 ragged sequences 10.7.  512 threads, two CTAs an SM at 64
 // registers, against 256 threads at 97: 26.8 and 32.0 us at 16384 tokens.
-// About 5 us are the second kernel and its launch; starting it early
+// About 4 us are the second kernel and its launch; starting it early
 // (launch_dependents) measured no better.
 //
 // A CTA owns the tokens [c * R, (c + 1) * R)
@@ -819,9 +819,12 @@ balance_kernel(RouteParams p) {
   }
 }
 
-constexpr int kSumExperts = 8;       // of a CTA of the second kernel: a 32-byte sector of a row
-constexpr int kSumRows = 32;         // partial rows it adds at a time
-constexpr int kSumThreads = kSumExperts * kSumRows;
+constexpr int kSumThreads = 256;     // of a CTA of the second kernel
+// Experts of such a CTA: 8 (a 32-byte sector of a row; 32 partial rows at a
+// time) where sequences have many partial rows, 64 (four at a time) where
+// they have few, so that many sequences make fewer CTAs: 4096 tokens of 64
+// sequences by 256 experts 17.7 and 11.8 us.
+constexpr int kSumExperts = 8, kSumExpertsMany = 64;
 
 struct BalanceParams {
   const int32_t* seq_start;
@@ -840,18 +843,19 @@ struct BalanceParams {
 };
 
 // Second kernel: CTA (b, i) adds up the partial rows of sequence b for the
-// experts from kSumExperts i on, kSumRows rows at a time, in a fixed order;
+// experts from EX i on, kSumThreads / EX rows at a time, in a fixed order;
 // the first warp of the CTA that finishes last forms the losses from what all
 // have written.  Latency alone: a handful of dependent loads, sums and one
 // atomic.
+template <int EX>
 __global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(BalanceParams p) {
-  constexpr int kWarps = kSumThreads / 32;
-  __shared__ float probs[kWarps][kSumExperts], zs[kWarps];
-  __shared__ int counts[kWarps][kSumExperts], ns[kWarps];
+  constexpr int kWarps = kSumThreads / 32, kRows = kSumThreads / EX;
+  constexpr int kSums = EX < 32 ? kWarps : kRows;      // of an expert, through shared memory
+  __shared__ float probs[kSums][EX], zs[kWarps];
+  __shared__ int counts[kSums][EX], ns[kWarps];
   pdl_wait();
   const int b = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int part = threadIdx.x / kSumExperts;
-  const int e = blockIdx.y * kSumExperts + threadIdx.x % kSumExperts;
+  const int part = threadIdx.x / EX, first = blockIdx.y * EX, e = first + threadIdx.x % EX;
   const int lo = b == 0 ? 0 : min(max(p.seq_start[b], 0), p.T);
   const int hi = b == p.B - 1 ? p.T : min(max(p.seq_start[b + 1], 0), p.T);
   int c0 = 0, c1 = 0;
@@ -865,7 +869,7 @@ __global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(BalanceParams 
     const float* fp = p.part_prob + int64_t(c0 + b) * p.E + e;
     const int32_t* ip = p.part_count + int64_t(c0 + b) * p.E + e;
 #pragma unroll 8
-    for (int c = part; c < c1 - c0; c += kSumRows) {
+    for (int c = part; c < c1 - c0; c += kRows) {
       prob += fp[int64_t(c) * p.E];
       count += ip[int64_t(c) * p.E];
     }
@@ -874,17 +878,22 @@ __global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(BalanceParams 
     n += p.part_tokens[c + b];
     z += p.part_z[c + b];
   }
-  // the four rows of a warp, then the warps
+  // the rows of a warp, then the warps
 #pragma unroll
-  for (int d = kSumExperts; d < 32; d <<= 1) {
+  for (int d = EX; d < 32; d <<= 1) {
     prob += __shfl_xor_sync(kFull, prob, d);
     count += __shfl_xor_sync(kFull, count, d);
   }
   z = tile_sum<32>(z);
   n = __reduce_add_sync(kFull, n);
-  if (lane < kSumExperts) {
-    probs[warp][lane] = prob;
-    counts[warp][lane] = count;
+  if constexpr (EX < 32) {
+    if (lane < EX) {
+      probs[warp][lane] = prob;
+      counts[warp][lane] = count;
+    }
+  } else {
+    probs[part][threadIdx.x % EX] = prob;
+    counts[part][threadIdx.x % EX] = count;
   }
   if (lane == 0) {
     zs[warp] = z;
@@ -892,26 +901,27 @@ __global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(BalanceParams 
   }
   __syncthreads();
   if (warp != 0) return;
-  prob = 0.0f;
-  count = 0;
-  z = lane < kWarps ? zs[lane] : 0.0f;
-  n = lane < kWarps ? ns[lane] : 0;
-  if (lane < kSumExperts) {
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      prob += probs[w][lane];
-      count += counts[w][lane];
-    }
-  }
-  z = tile_sum<32>(z);
-  n = __reduce_add_sync(kFull, n);
+  z = tile_sum<32>(lane < kWarps ? zs[lane] : 0.0f);
+  n = __reduce_add_sync(kFull, lane < kWarps ? ns[lane] : 0);
   const float inv_n = n > 0 ? 1.0f / float(n) : 0.0f;
-  prob *= inv_n;
-  if (lane < kSumExperts && e < p.E) {
-    p.expert_prob[int64_t(b) * p.E + e] = prob;
-    p.expert_count[int64_t(b) * p.E + e] = count;
+  float dot = 0.0f;
+#pragma unroll
+  for (int i = lane; i < EX; i += 32) {
+    prob = 0.0f;
+    count = 0;
+#pragma unroll
+    for (int w = 0; w < kSums; ++w) {
+      prob += probs[w][i];
+      count += counts[w][i];
+    }
+    prob *= inv_n;
+    if (first + i < p.E) {
+      p.expert_prob[int64_t(b) * p.E + first + i] = prob;
+      p.expert_count[int64_t(b) * p.E + first + i] = count;
+    }
+    dot += float(count) * inv_n * prob;
   }
-  const float dot = tile_sum<32>(float(count) * inv_n * prob);      // lanes past the experts: 0
+  dot = tile_sum<32>(dot);
   unsigned before = 0;
   if (lane == 0) {
     p.dots[int64_t(b) * gridDim.y + blockIdx.y] = dot;
@@ -984,7 +994,7 @@ struct RouteBackwardParams {
 // The next token's logits, choice and gate gradient are loaded ahead.
 //
 // What bounds it: instructions again, about 400 a token of 256 experts; 16384
-// tokens, bf16, sigmoid: 8.5 us (bytes: 2.8), 4096, fp32, softmax: 3.8 (1.3).
+// tokens, bf16, sigmoid: 8.7 us (bytes: 2.8), 4096, fp32, softmax: 3.9 (1.3).
 template <class S, bool SIG>
 __global__ void __launch_bounds__(kRouteThreads, kRouteShare<S>)
 route_backward_kernel(RouteBackwardParams p) {
@@ -1203,7 +1213,7 @@ struct LaunchRoute {
   }
 };
 
-// CTAs of the second kernel along the experts.
+// CTAs of the second kernel along the experts, at most.
 int sum_ctas(int E) { return (E + kSumExperts - 1) / kSumExperts; }
 
 struct LaunchBalance {
@@ -1223,8 +1233,12 @@ struct LaunchBalance {
     if (e != cudaSuccess) return e;
     e = launch_pdl(kernel, dim3(used), dim3(kThreads), smem, stream, p);
     if (e != cudaSuccess) return e;
-    return launch_pdl(balance_sum_kernel, dim3(p.B, sum_ctas(p.E)), dim3(kSumThreads), 0, stream,
-                      q);
+    if (used < 16 * int64_t(p.B))
+      return launch_pdl(balance_sum_kernel<kSumExpertsMany>,
+                        dim3(p.B, (p.E + kSumExpertsMany - 1) / kSumExpertsMany),
+                        dim3(kSumThreads), 0, stream, q);
+    return launch_pdl(balance_sum_kernel<kSumExperts>, dim3(p.B, sum_ctas(p.E)),
+                      dim3(kSumThreads), 0, stream, q);
   }
 };
 
