@@ -685,14 +685,13 @@ __device__ __forceinline__ int sequence_of(const int32_t* seq_start, int B, int 
 
 template <class S>
 constexpr int kBalanceThreads = S::kValues <= 16 ? 512 : 256;
-template <class S>
-constexpr int kBalanceShare = S::kValues <= 8 ? 2 : 1;
 
 // ep_route_balance, first kernel: what bounds it is what bounds ep_route, and
 // the flush of a CTA's sums.  16384 tokens by 256 experts, sigmoid, groups, 4
-// sequences: 23.6 us for both kernels, the bytes 2.8; 4096 by softmax 9.5;
-// 8191 by 64 in 37 ragged sequences 10.7.  512 threads, two CTAs an SM at 64
-// registers, against 256 threads at 97: 26.8 and 32.0 us at 16384 tokens.
+// sequences: 22.3 us for both kernels, the bytes 2.8; 4096 by softmax 10.1;
+// 8191 by 64 in 37 ragged sequences 10.3.  One CTA of 512 threads an SM, with
+// the registers it likes: two at 64 registers 23.4, 10.4 and 10.8 us; 768
+// threads 21.4, 10.7 and 11.6; two of 256 threads 23.0, 11.1 and 10.9.
 // About 4 us are the second kernel and its launch; starting it early
 // (launch_dependents) measured no better.
 //
@@ -701,7 +700,7 @@ constexpr int kBalanceShare = S::kValues <= 8 ? 2 : 1;
 // to partial row c + b, which no other pair uses (both only grow along the
 // tokens).
 template <class S, bool SIG>
-__global__ void __launch_bounds__(kBalanceThreads<S>, kBalanceShare<S>)
+__global__ void __launch_bounds__(kBalanceThreads<S>, 1)
 balance_kernel(RouteParams p) {
   constexpr int kThreads = kBalanceThreads<S>, kWarps = kThreads / 32;
   constexpr int kCtaTiles = kThreads / S::kLanes;
@@ -1223,7 +1222,7 @@ struct LaunchBalance {
   template <class S, bool SIG>
   cudaError_t operator()() {
     constexpr int kThreads = kBalanceThreads<S>, kCtaTiles = kThreads / S::kLanes;
-    const int ctas = route_ctas(p.T, kCtaTiles, kBalanceShare<S>);
+    const int ctas = route_ctas(p.T, kCtaTiles, 1);
     p.tokens_per_cta = q.tokens_per_cta = run_length(p.T, ctas);
     // no tokens: one CTA still clears `done`
     const int used = p.T > 0 ? (p.T + p.tokens_per_cta - 1) / p.tokens_per_cta : 1;
@@ -1269,9 +1268,9 @@ struct BalanceWorkspace {
   int64_t bytes;
 };
 
-// The first kernel has at most two CTAs an SM, whatever T.
+// The first kernel has at most one CTA an SM, whatever T.
 BalanceWorkspace carve(void* base, int E, int B) {
-  const int64_t rows = int64_t(device_info().sm_count) * 2 + B;
+  const int64_t rows = int64_t(device_info().sm_count) + B;
   char* at = static_cast<char*>(base);
   auto take = [&](int64_t n) {
     char* p = at;
