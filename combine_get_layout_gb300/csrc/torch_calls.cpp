@@ -12,6 +12,8 @@
 
 #include <c10/cuda/CUDAStream.h>
 
+#include <exception>
+
 #include "../../include/ep.h"
 
 namespace {
@@ -30,10 +32,11 @@ struct Arg {
     fits = THPVariable_Check(o);
     if (fits) t = &THPVariable_Unpack(o);
   }
-  // present, on the GPU, contiguous, of this type and shape
+  // present, strided and on the GPU
+  bool here() const { return t != nullptr && t->is_cuda() && t->layout() == at::kStrided; }
+  // and contiguous, of this type and shape
   bool is(ScalarType type, at::IntArrayRef shape) const {
-    return t != nullptr && t->scalar_type() == type && t->is_cuda() && t->is_contiguous() &&
-           t->sizes() == shape;
+    return here() && t->scalar_type() == type && t->is_contiguous() && t->sizes() == shape;
   }
   bool is_or_absent(ScalarType type, at::IntArrayRef shape) const {
     return fits && (t == nullptr || is(type, shape));
@@ -43,7 +46,7 @@ struct Arg {
   }
   // of so many bytes, whatever its type and shape
   bool holds(int64_t bytes) const {
-    return t != nullptr && t->is_cuda() && t->is_contiguous() && int64_t(t->nbytes()) >= bytes;
+    return here() && t->is_contiguous() && int64_t(t->nbytes()) >= bytes;
   }
   template <typename T>
   T* ptr() const {
@@ -58,7 +61,7 @@ struct Logits {
   int64_t T = 0, ld = 0;
 
   Logits(const Arg& a, int64_t E) {
-    if (a.t == nullptr || !a.t->is_cuda() || a.t->dim() != 2 || a.t->size(1) != E) return;
+    if (!a.here() || a.t->dim() != 2 || a.t->size(1) != E) return;
     bf16 = a.t->scalar_type() == ScalarType::BFloat16;
     if (!bf16 && a.t->scalar_type() != ScalarType::Float) return;
     if (a.t->stride(1) != 1 && E != 1) return;
@@ -83,13 +86,32 @@ const ep_router_config* router_config(PyObject* o) {
   return static_cast<const ep_router_config*>(PyLong_AsVoidPtr(o));
 }
 
+// Lets other host threads run, until the end of the scope by whatever way.
+struct Released {
+  PyThreadState* state = PyEval_SaveThread();
+  ~Released() { PyEval_RestoreThread(state); }
+};
+
 template <typename F>
 PyObject* status_of(F&& call) {
   int32_t status;
-  Py_BEGIN_ALLOW_THREADS;
-  status = call();
-  Py_END_ALLOW_THREADS;
+  {
+    Released others;
+    status = call();
+  }
   return PyLong_FromLong(status);
+}
+
+// A function as Python calls it; what torch throws (a tensor without
+// storage, say) becomes a RuntimeError.
+template <PyObject* (*F)(PyObject* const*, Py_ssize_t)>
+PyObject* guarded(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  try {
+    return F(args, n);
+  } catch (const std::exception& e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+    return nullptr;
+  }
 }
 
 PyObject* unfit() { return PyLong_FromLong(kUnfit); }
@@ -101,7 +123,7 @@ bool arity(Py_ssize_t got, Py_ssize_t want) {
 }
 
 // route(configs, logits, bias, mask, idx, w, stream)
-PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
+PyObject* route(PyObject* const* a, Py_ssize_t n) {
   if (!arity(n, 7)) return nullptr;
   const ep_router_config* cfg = router_config(a[0]);
   if (cfg == nullptr) return nullptr;
@@ -121,7 +143,7 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // route_balance(configs, logits, bias, mask, seq_start, idx, w, count, prob,
 // tokens, loss, workspace, workspace_bytes, stream)
-PyObject* route_balance(PyObject*, PyObject* const* a, Py_ssize_t n) {
+PyObject* route_balance(PyObject* const* a, Py_ssize_t n) {
   if (!arity(n, 14)) return nullptr;
   const ep_router_config* cfg = router_config(a[0]);
   if (cfg == nullptr) return nullptr;
@@ -153,7 +175,7 @@ PyObject* route_balance(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // route_backward(configs, logits, idx, grad_w, mask, seq_start, count, tokens,
 // grad_loss, grad_logits, stream)
-PyObject* route_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+PyObject* route_backward(PyObject* const* a, Py_ssize_t n) {
   if (!arity(n, 11)) return nullptr;
   const ep_router_config* cfg = router_config(a[0]);
   if (cfg == nullptr) return nullptr;
@@ -185,7 +207,7 @@ PyObject* route_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // expert_w4(config, x, codes, scales, start, end, num_rows, zeros, x_scale,
 // out, stream)
-PyObject* expert_w4(PyObject*, PyObject* const* a, Py_ssize_t n) {
+PyObject* expert_w4(PyObject* const* a, Py_ssize_t n) {
   if (!arity(n, 11)) return nullptr;
   const auto* cfg = static_cast<const ep_w4_config*>(PyLong_AsVoidPtr(a[0]));
   if (cfg == nullptr) return nullptr;
@@ -198,8 +220,8 @@ PyObject* expert_w4(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (x.t == nullptr || x.t->dim() != 2) return unfit();
   const int64_t cap = x.t->size(0);
   const auto segments = [E](const Arg& s) {
-    return s.t != nullptr && s.t->scalar_type() == ScalarType::Int && s.t->is_cuda() &&
-           s.t->is_contiguous() && s.t->dim() == 1 && s.t->size(0) >= E;
+    return s.here() && s.t->scalar_type() == ScalarType::Int && s.t->is_contiguous() &&
+           s.t->dim() == 1 && s.t->size(0) >= E;
   };
   if (cap > INT32_MAX || num_rows > INT32_MAX || num_rows < INT32_MIN ||
       !x.is(cfg->x_fp8 ? ScalarType::Byte : ScalarType::BFloat16, {cap, H}) ||
@@ -219,8 +241,11 @@ PyObject* expert_w4(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-#define EP_CALL(f) \
-  { #f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr }
+#define EP_CALL(f)                                                                      \
+  {                                                                                     \
+    #f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(guarded<f>)),        \
+        METH_FASTCALL, nullptr                                                          \
+  }
 PyMethodDef methods[] = {EP_CALL(route), EP_CALL(route_balance), EP_CALL(route_backward),
                          EP_CALL(expert_w4), {nullptr, nullptr, 0, nullptr}};
 #undef EP_CALL

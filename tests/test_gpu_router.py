@@ -287,7 +287,10 @@ def test_torch_layer_refuses(ep):
         lambda: ep.route(cfg, x.double()),
         lambda: ep.route(cfg, x[:, :15]),
         lambda: ep.route(cfg, x.T.contiguous().T),
-        lambda: ep.route(cfg, x.cpu()),
+        lambda: ep.route(cfg, x.cpu()), lambda: ep.route(cfg, x.to_sparse()),
+        lambda: ep.route(cfg, x, topk_idx=torch.zeros((4, 2), dtype=torch.int64,
+                                                      device="cuda").to_sparse()),
+        lambda: ep.route(cfg, x.to("meta")),
         lambda: ep.route(cfg, x, torch.zeros(16, device="cuda")),             # bias: sigmoid only
         lambda: ep.route(ep.RouterConfig(16, 2, "sigmoid"), x, torch.zeros(15, device="cuda")),
         lambda: ep.route(cfg, x, None, torch.ones(3, dtype=torch.uint8, device="cuda")),
