@@ -767,7 +767,9 @@ balance_kernel(RouteParams p) {
       }
       from = end;
       if (end > block_end) continue;      // the sequence goes on in the next tokens
-      // the tiles of a warp, then the warps in order
+      // the tiles of a warp, then the warps in order.  A warp's sums go to the
+      // row of its first tile: other rows may still hold the choice scores of
+      // groups of warps that have not come here yet.
       __syncwarp();
 #pragma unroll
       for (int d = 16; d >= S::kLanes; d >>= 1) {
@@ -779,7 +781,7 @@ balance_kernel(RouteParams p) {
 #pragma unroll
       for (int r = 0; r < S::kValues; ++r) {
         const int e = S::expert(r, l);
-        if (lane < S::kLanes && e < p.E) rows[warp * width + e] = sum[r];
+        if (lane < S::kLanes && e < p.E) rows[warp * S::kTiles * width + e] = sum[r];
         sum[r] = 0.0f;
       }
       if (lane == 0) {
@@ -793,7 +795,7 @@ balance_kernel(RouteParams p) {
       for (int e = threadIdx.x; e < p.E; e += kThreads) {
         float acc = 0.0f;
 #pragma unroll
-        for (int v = 0; v < kWarps; ++v) acc += rows[v * width + e];
+        for (int v = 0; v < kWarps; ++v) acc += rows[v * S::kTiles * width + e];
         p.part_prob[part * p.E + e] = acc;
         p.part_count[part * p.E + e] = counts[e];
         counts[e] = 0;
