@@ -864,8 +864,16 @@ def _workspace_of(t, stream, size: int):
     return got
 
 
+class _AbiConfig:
+    """A config that keeps its ABI struct and the struct's address.  Copies and
+    pickles carry the fields alone: each object has a struct of its own."""
+
+    def __reduce__(self):
+        return type(self), tuple(getattr(self, f.name) for f in dataclasses.fields(self))
+
+
 @dataclasses.dataclass(frozen=True)
-class RouterConfig:
+class RouterConfig(_AbiConfig):
     """Mirror of ep_router_config (see include/ep.h); the logits' type is
     taken from the tensors."""
 
@@ -964,7 +972,7 @@ def route_backward(cfg: RouterConfig, logits, topk_idx=None, grad_w=None, token_
 # ---- experts' products with 4-bit weights ----------------------------------------
 
 @dataclasses.dataclass(frozen=True)
-class W4Config:
+class W4Config(_AbiConfig):
     """Mirror of ep_w4_config (see include/ep.h)."""
 
     num_experts: int
