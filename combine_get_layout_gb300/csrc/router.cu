@@ -175,6 +175,13 @@ __device__ __forceinline__ float tile_max(float v) {
   }
 }
 
+// The larger, or NaN if either is.
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
+}
+
 // Bits of a ballot that belong to this lane's tile, from bit 0.
 template <int L>
 __device__ __forceinline__ uint32_t tile_bits(uint32_t ballot, int lane) {
@@ -580,10 +587,11 @@ __device__ __forceinline__ Chosen<S> route_token(const RouteParams& p, int t, bo
       *total = soft_scores<S>(x, s, *top);
       if (!p.renorm || *total != *total) divisor = *total;
     } else {
-      // NaN where a logit is, or where -inf meets +inf, whose weights are NaN
-      float any = 0.0f;
+      // NaN where a logit is (a +inf makes its own weight and so all NaN).
+      // Not a sum: finite logits' may overflow, and meet -inf.
+      float any = x[0];
 #pragma unroll
-      for (int r = 0; r < S::kValues; ++r) any += x[r];
+      for (int r = 1; r < S::kValues; ++r) any = max_or_nan(any, x[r]);
       if (tile_bits<L>(__ballot_sync(kFull, any != any), lane) != 0) divisor = CUDART_NAN_F;
     }
 #pragma unroll

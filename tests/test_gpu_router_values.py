@@ -1,0 +1,53 @@
+"""The router gate on values at the ends of their types: the gate weights of
+finite logits are finite, and ep_route agrees with ep_route_balance."""
+
+import numpy as np
+import pytest
+import torch
+
+import layer_ref as ref
+from test_gpu_router import ep  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+INF = float("inf")
+# (tokens, experts): a warp a token with and without vectors and padding, and
+# several tokens a warp
+SIZES = [(6, 256), (6, 200), (6, 45), (6, 600), (5000, 60), (5000, 128)]
+
+
+@pytest.mark.parametrize("T,E", SIZES)
+@pytest.mark.parametrize("bf16", [False, True])
+def test_huge_finite_logits_beside_minus_infinity(ep, T, E, bf16):  # noqa: F811
+    """Sums of a few of a row's logits overflow; their softmax does not."""
+    big = 3.0e38
+    l = np.zeros((T, E))
+    l[:, ::3] = -INF
+    l[0::3, [1, 2, 4, 5]] = big
+    l[1::3, 1:] = -big
+    l[2::3] = np.where(np.isinf(l[2::3]), -INF, big)
+    dt = torch.bfloat16 if bf16 else torch.float32
+    x = torch.from_numpy(l).to(dt).cuda()
+    cfg = ep.RouterConfig(E, 4)
+    idx, w = ep.route(cfg, x)
+    full = x[:6].double().cpu().numpy()
+    want, ww = ref.route(full, 4)
+    assert np.array_equal(idx[:6].cpu().numpy(), want)
+    # shares of equal or vanishing scores: a quotient of small whole numbers
+    np.testing.assert_allclose(w[:6].cpu().numpy(), ww, rtol=4 * ref.EPS, atol=0)
+    assert torch.equal(w[:3].repeat(-(-T // 3), 1)[:T], w)
+    assert torch.equal(idx[:3].repeat(-(-T // 3), 1)[:T], idx)
+    got = ep.route_balance(cfg, x)
+    assert torch.equal(got[0], idx) and torch.equal(got[1], w)
+
+
+@pytest.mark.parametrize("T,E", SIZES)
+def test_nan_and_plus_infinity_still_show(ep, T, E):  # noqa: F811
+    l = np.zeros((T, E))
+    l[0::3, E - 1] = np.nan
+    l[1::3, 7] = INF
+    l[1::3, 8] = -INF
+    x = torch.from_numpy(l).float().cuda()
+    idx, w = ep.route(ep.RouterConfig(E, 4), x)
+    assert torch.isnan(w[0::3]).all() and torch.isnan(w[1::3]).all()
+    assert (w[2::3] == 0.25).all()
+    assert (idx[0::3] != E - 1).all() and (idx[1::3, 0] == 7).all()
