@@ -161,6 +161,10 @@ __device__ __forceinline__ float tile_sum(float v) {
   return v;
 }
 
+// A choice bias as the kernels keep it: NaN takes its expert out of the choice,
+// as -inf does, so that no choice score is NaN.
+__device__ __forceinline__ float clean_bias(float b) { return fmaxf(b, -CUDART_INF_F); }
+
 // Largest of a tile's values; a NaN counts only where all are NaN.
 template <int L>
 __device__ __forceinline__ float tile_max(float v) {
@@ -648,7 +652,7 @@ __global__ void __launch_bounds__(kRouteThreads, kRouteShare<S>) route_kernel(Ro
   const float* bias = smem;      // [E] padded to whole vectors, then the tiles' rows
   float* row = smem + (tile + 1) * padded_row(p.E);
   if (SIG && p.bias != nullptr) {
-    for (int e = threadIdx.x; e < p.E; e += kRouteThreads) smem[e] = p.bias[e];
+    for (int e = threadIdx.x; e < p.E; e += kRouteThreads) smem[e] = clean_bias(p.bias[e]);
     __syncthreads();
   }
   const int stride = gridDim.x * kCtaTiles;
@@ -727,7 +731,7 @@ balance_kernel(RouteParams p) {
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.done = 0;
   for (int e = threadIdx.x; e < p.E; e += kThreads) counts[e] = 0;
   if (SIG && p.bias != nullptr)
-    for (int e = threadIdx.x; e < p.E; e += kThreads) bias[e] = p.bias[e];
+    for (int e = threadIdx.x; e < p.E; e += kThreads) bias[e] = clean_bias(p.bias[e]);
   __syncthreads();
   const int first = blockIdx.x * p.tokens_per_cta;
   const int last = min(p.T, first + p.tokens_per_cta);

@@ -521,7 +521,8 @@ EP_API int32_t ep_selftest_layout_timeout(const ep_config *cfg, int32_t num_toke
  *
  * Score s_te of token t for expert e: softmax over e of the logits l_te, or
  * sigmoid(l_te).  Choice score: l_te itself (softmax; the same order), or
- * s_te + bias_e (sigmoid; the bias orders, it never enters a weight).  A
+ * s_te + bias_e (sigmoid; the bias orders, it never enters a weight; a bias
+ * of -inf or NaN takes its expert out of the choice, not out of the scores).  A
  * logit of -inf takes its expert out of service for that token (score 0,
  * never chosen); a NaN logit is never chosen either and its row's softmax
  * scores are NaN.  With num_groups > 1, groups of E / num_groups consecutive

@@ -1,5 +1,5 @@
-"""The router gate on values at the ends of their types: the gate weights of
-finite logits are finite, and ep_route agrees with ep_route_balance."""
+"""The router gate on values at the ends of their types: weights of finite
+logits are finite, with and without statistics; a bias that is not a number."""
 
 import numpy as np
 import pytest
@@ -51,3 +51,31 @@ def test_nan_and_plus_infinity_still_show(ep, T, E):  # noqa: F811
     assert torch.isnan(w[0::3]).all() and torch.isnan(w[1::3]).all()
     assert (w[2::3] == 0.25).all()
     assert (idx[0::3] != E - 1).all() and (idx[1::3, 0] == 7).all()
+
+
+@pytest.mark.parametrize("T,E,groups,kept,K", [
+    (40, 256, 8, 3, 8), (40, 60, 4, 2, 4), (40, 160, 8, 3, 6), (40, 64, 32, 5, 4),
+    (5000, 64, 8, 3, 4), (5000, 60, 4, 2, 4), (5000, 128, 16, 4, 8), (40, 256, 1, 1, 8),
+])
+def test_an_expert_whose_bias_is_nan_is_out_of_the_choice(ep, T, E, groups, kept, K):  # noqa: F811
+    """As with a bias of -inf: neither chosen nor counted for its group."""
+    rng = np.random.default_rng(6)
+    l = np.stack([rng.permutation(E) for _ in range(40)]) / 32.0 - 4.0
+    bias = rng.integers(-40, 41, E) / 1024.0
+    out = rng.permutation(E)[:E // 2]
+    bias[out] = np.nan
+    kill = np.where(np.isnan(bias), -INF, bias)
+    x = torch.from_numpy(np.tile(l, (T // 40, 1))).float().cuda()
+    cfg = ep.RouterConfig(E, K, "sigmoid", groups, kept)
+    idx, w = ep.route(cfg, x, torch.from_numpy(bias).float().cuda())
+    want, ww = ref.route(l, K, "sigmoid", kill, groups, kept)
+    assert np.array_equal(idx[:40].cpu().numpy(), want) and not np.isin(want, out).any()
+    # a score of at most 2^-1 to 1 and a sum of K: E / 32 + 5 steps cover both
+    rt = ref.EPS * (2 * (E / 32 + 5) + 40)
+    np.testing.assert_allclose(w[:40].cpu().numpy(), ww, rtol=rt)
+    assert torch.equal(idx, idx[:40].repeat(T // 40, 1))
+    idx2, w2 = ep.route(cfg, x, torch.from_numpy(kill).float().cuda())
+    assert torch.equal(idx, idx2) and torch.equal(w, w2)
+    got = ep.route_balance(cfg, x, torch.from_numpy(bias).float().cuda())
+    assert torch.equal(got[0], idx)
+    np.testing.assert_allclose(got[1][:40].cpu().numpy(), ww, rtol=rt)
