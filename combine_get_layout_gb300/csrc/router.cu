@@ -13,6 +13,7 @@
 #include <cuda_runtime.h>
 #include <math_constants.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "../../include/ep.h"
@@ -1203,11 +1204,23 @@ cudaError_t with_shape(const ep_router_config* cfg, int T, int G, int64_t ld, F&
 }
 
 // Raises a kernel's dynamic shared-memory limit where `bytes` needs it (48 KiB
-// with the static arrays, which are under 8, need no leave).
-template <typename... P>
-cudaError_t allow_smem(void (*kernel)(P...), size_t bytes) {
-  if (bytes <= 40 * 1024) return cudaSuccess;
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+// with the static arrays, which are under 13, need no leave): once per kernel
+// and device, to what the most experts need, because host threads that launch
+// the same kernel with other numbers of experts share the limit.
+constexpr size_t kMostSmem = 10 * 2048 * sizeof(float);      // the balance kernel's rows
+
+template <auto kKernel, class S, int kRows>
+cudaError_t allow_smem(size_t bytes) {
+  static_assert(kRows * S::kLanes * S::kValues * sizeof(float) <= kMostSmem);
+  if (bytes <= 32 * 1024) return cudaSuccess;
+  static std::atomic<uint64_t> raised{0};      // a bit a device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && (raised.load(std::memory_order_acquire) >> dev & 1)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMostSmem));
+  if (e == cudaSuccess && dev < 64) raised.fetch_or(uint64_t(1) << dev, std::memory_order_release);
+  return e;
 }
 
 struct LaunchRoute {
@@ -1218,8 +1231,8 @@ struct LaunchRoute {
     constexpr int kCtaTiles = kRouteThreads / S::kLanes;
     const size_t rows = p.G > 1 ? kCtaTiles + 1 : SIG ? 1 : 0;
     const size_t smem = sizeof(float) * rows * padded_row(p.E);
-    auto* kernel = route_kernel<S, SIG>;
-    const cudaError_t e = allow_smem(kernel, smem);
+    constexpr auto* kernel = route_kernel<S, SIG>;
+    const cudaError_t e = allow_smem<kernel, S, kCtaTiles + 1>(smem);
     if (e != cudaSuccess) return e;
     return launch_pdl(kernel, dim3(route_ctas(p.T, kCtaTiles, kRouteShare<S>)),
                       dim3(kRouteThreads), smem, stream, p);
@@ -1241,8 +1254,8 @@ struct LaunchBalance {
     // no tokens: one CTA still clears `done`
     const int used = p.T > 0 ? (p.T + p.tokens_per_cta - 1) / p.tokens_per_cta : 1;
     const size_t smem = sizeof(float) * (kCtaTiles + 2) * padded_row(p.E);
-    auto* kernel = balance_kernel<S, SIG>;
-    cudaError_t e = allow_smem(kernel, smem);
+    constexpr auto* kernel = balance_kernel<S, SIG>;
+    cudaError_t e = allow_smem<kernel, S, kCtaTiles + 2>(smem);
     if (e != cudaSuccess) return e;
     e = launch_pdl(kernel, dim3(used), dim3(kThreads), smem, stream, p);
     if (e != cudaSuccess) return e;
@@ -1263,8 +1276,8 @@ struct LaunchBackward {
     constexpr int kCtaTiles = kRouteThreads / S::kLanes;
     p.tokens_per_cta = run_length(p.T, route_ctas(p.T, kCtaTiles, kRouteShare<S>));
     const size_t smem = sizeof(float) * kCtaTiles * padded_row(p.E);
-    auto* kernel = route_backward_kernel<S, SIG>;
-    const cudaError_t e = allow_smem(kernel, smem);
+    constexpr auto* kernel = route_backward_kernel<S, SIG>;
+    const cudaError_t e = allow_smem<kernel, S, kCtaTiles + 1>(smem);
     if (e != cudaSuccess) return e;
     return launch_pdl(kernel, dim3((p.T + p.tokens_per_cta - 1) / p.tokens_per_cta),
                       dim3(kRouteThreads), smem, stream, p);
