@@ -843,17 +843,20 @@ _outgrown = []      # kept: a stream other than the allocating one may use them 
 
 def _workspace_of(t, stream, size: int):
     """At least `size` bytes on t's device for a call on this stream (None:
-    the current one).  Kept from call to call (asking the allocator each time
-    costs more than the kernels of a small batch); under stream capture, fresh
-    memory that the graph owns."""
+    the current one), made under it, so that nothing else that the memory was
+    or will be used for overlaps.  Kept from call to call (asking the
+    allocator each time costs more than the kernels of a small batch); where
+    that stream is being captured, fresh memory that the graph owns."""
     import torch
 
+    dev = t.get_device()
+    handle = torch._C._cuda_getCurrentRawStream(dev)
+    if stream is not None and stream.cuda_stream != handle:
+        with torch.cuda.stream(stream):
+            return _workspace_of(t, None, size)
     if torch.cuda.is_current_stream_capturing():
         return torch.empty(size, dtype=torch.uint8, device=t.device)
-    dev = t.get_device()
-    if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(dev)
-    key = dev, stream, _get_ident()
+    key = dev, handle, _get_ident()
     got = _workspaces.get(key)
     if got is None or got.nbytes < size:
         if got is not None:
@@ -940,12 +943,12 @@ def route_balance(cfg: RouterConfig, logits, bias=None, token_mask=None, seq_sta
     size = _lib.ep_route_workspace_bytes(cfg._c[0], B)
     if size < 0 or not logits.is_cuda:
         _refuse("route_balance: config, number of sequences or place of the logits")
-    handle = None if stream is None else stream.cuda_stream
     if workspace is None:
-        workspace = _workspace_of(logits, handle, size)
+        workspace = _workspace_of(logits, stream, size)
     idx, w, count, prob, tokens, loss = out
     st = _calls.route_balance(cfg._at, logits, bias, token_mask, seq_start, idx, w, count, prob,
-                              tokens, loss, workspace, size, handle)
+                              tokens, loss, workspace, size,
+                              stream if stream is None else stream.cuda_stream)
     if st:
         _done(st, "route_balance")
     return idx, w, count, prob, tokens, loss

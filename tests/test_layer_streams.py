@@ -1,0 +1,105 @@
+"""Which stream the router's scratch memory and the outputs are allocated
+for, on a stand-in for torch's streams and allocator.  No GPU."""
+
+import contextlib
+import types
+
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def ep():
+    from conftest import load_build_module
+
+    load_build_module().build()
+    import combine_get_layout_gb300 as ep
+
+    return ep
+
+
+class Streams:
+    """The current stream, those under capture, and every allocation (stream,
+    bytes, tensor)."""
+
+    def __init__(self, monkeypatch):
+        self.current, self.capturing, self.made = self.stream(1), set(), []
+        empty = torch.empty
+
+        def make(shape, dtype=None, device=None):
+            t = empty(shape, dtype=dtype, device="cpu")
+            self.made.append((self.current.cuda_stream, t.nbytes, t))
+            return t
+
+        @contextlib.contextmanager
+        def under(stream):
+            was, self.current = self.current, stream
+            yield
+            self.current = was
+
+        monkeypatch.setattr(torch, "empty", make)
+        monkeypatch.setattr(torch.cuda, "stream", under)
+        monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: self.current)
+        monkeypatch.setattr(torch.cuda, "is_current_stream_capturing",
+                            lambda: self.current.cuda_stream in self.capturing)
+        monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream",
+                            lambda dev: self.current.cuda_stream, raising=False)
+
+    @staticmethod
+    def stream(handle):
+        return types.SimpleNamespace(cuda_stream=handle)
+
+
+@pytest.fixture
+def streams(monkeypatch, ep):
+    monkeypatch.setattr(ep, "_workspaces", {})
+    return Streams(monkeypatch)
+
+
+class Logits:
+    is_cuda, shape, device = True, (8, 16), torch.device("cuda", 0)
+
+    def get_device(self):
+        return 0
+
+
+def balance(ep, monkeypatch, stream, B=1, experts=16):
+    """The scratch memory that one call hands to the library."""
+    used = []
+    monkeypatch.setattr(ep, "_calls", types.SimpleNamespace(
+        route_balance=lambda *a: used.append((a[11], a[12], a[13])) or 0))
+    seq = None if B == 1 else types.SimpleNamespace(shape=(B + 1,))
+    ep.route_balance(ep.RouterConfig(experts, 2), Logits(), seq_start=seq, out=(None,) * 6,
+                     stream=stream)
+    (memory, size, handle), = used
+    assert memory.nbytes >= size and handle == (None if stream is None else stream.cuda_stream)
+    return memory
+
+
+def made_for(streams, memory):
+    return next(s for s, _, t in streams.made if t is memory)
+
+
+def test_scratch_memory_is_made_for_the_stream_that_uses_it(ep, streams, monkeypatch):
+    s = streams.stream(2)
+    assert made_for(streams, balance(ep, monkeypatch, None)) == 1
+    mine = balance(ep, monkeypatch, s)
+    assert made_for(streams, mine) == 2 and streams.current.cuda_stream == 1
+    assert balance(ep, monkeypatch, s) is mine                  # kept
+    streams.current = s
+    assert balance(ep, monkeypatch, None) is mine               # the same stream
+    assert balance(ep, monkeypatch, streams.stream(1)) is not mine
+
+
+def test_a_capturing_stream_gets_memory_that_its_graph_owns(ep, streams, monkeypatch):
+    s = streams.stream(2)
+    kept = balance(ep, monkeypatch, s), balance(ep, monkeypatch, None)
+    streams.capturing = {2}                     # the given stream alone
+    a, b = balance(ep, monkeypatch, s), balance(ep, monkeypatch, s)
+    assert a is not b and all(t is not k for t in (a, b) for k in kept)
+    assert made_for(streams, a) == made_for(streams, b) == 2
+    streams.capturing = {1, 2}                  # and the current one, which it joined
+    c = balance(ep, monkeypatch, s)
+    assert all(c is not k for k in (a, b, *kept)) and made_for(streams, c) == 2
+    streams.capturing = {1}                     # the given one is not part of it
+    assert balance(ep, monkeypatch, s) is kept[0]
