@@ -22,7 +22,7 @@ from __future__ import annotations
 import ctypes
 import dataclasses
 import os
-from threading import get_ident as _get_ident
+from threading import Lock as _Lock, get_ident as _get_ident
 from typing import Optional
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -836,9 +836,12 @@ def _flat(t, dtype, shape) -> bool:
 
 
 # Scratch memory of the eager calls, by (device, stream, host thread): calls
-# of one thread on one stream run in order, so that they can share it.
+# of one thread on one stream run in order, so that they can share it.  A
+# block that leaves the table goes back to its stream's memory, which later
+# work of that stream alone takes it from.
 _workspaces = {}
-_outgrown = []      # kept: a stream other than the allocating one may use them still
+_workspaces_lock = _Lock()
+_MOST_WORKSPACES = 32
 
 
 def _workspace_of(t, stream, size: int):
@@ -859,11 +862,12 @@ def _workspace_of(t, stream, size: int):
     key = dev, handle, _get_ident()
     got = _workspaces.get(key)
     if got is None or got.nbytes < size:
-        if got is not None:
-            _outgrown.append(got)
-            size = max(size, 2 * got.nbytes)      # so that they stay few
-        got = _workspaces[key] = torch.empty(max(size, 1 << 20), dtype=torch.uint8,
-                                             device=t.device)
+        got = torch.empty(max(size, 1 << 20), dtype=torch.uint8, device=t.device)
+        with _workspaces_lock:
+            _workspaces.pop(key, None)
+            while len(_workspaces) >= _MOST_WORKSPACES:      # the first that was made
+                del _workspaces[next(iter(_workspaces))]
+            _workspaces[key] = got
     return got
 
 

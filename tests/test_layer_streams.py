@@ -72,6 +72,7 @@ def balance(ep, monkeypatch, stream, B=1, experts=16):
     ep.route_balance(ep.RouterConfig(experts, 2), Logits(), seq_start=seq, out=(None,) * 6,
                      stream=stream)
     (memory, size, handle), = used
+    used.clear()
     assert memory.nbytes >= size and handle == (None if stream is None else stream.cuda_stream)
     return memory
 
@@ -103,3 +104,49 @@ def test_a_capturing_stream_gets_memory_that_its_graph_owns(ep, streams, monkeyp
     assert all(c is not k for k in (a, b, *kept)) and made_for(streams, c) == 2
     streams.capturing = {1}                     # the given one is not part of it
     assert balance(ep, monkeypatch, s) is kept[0]
+
+
+def test_kept_memory_is_bounded_and_what_is_outgrown_is_released(ep, streams, monkeypatch):
+    import gc
+    import weakref
+
+    small = balance(ep, monkeypatch, None)
+    ref, size = weakref.ref(small), small.nbytes
+    del small
+    large = balance(ep, monkeypatch, None, B=4000, experts=512)
+    assert large.nbytes > size
+    streams.made.clear()
+    gc.collect()
+    assert ref() is None                        # the larger block took its place
+    assert balance(ep, monkeypatch, None) is large
+    refs = []
+    for handle in range(100, 400):
+        refs.append(weakref.ref(balance(ep, monkeypatch, streams.stream(handle))))
+        streams.made.clear()
+    gc.collect()
+    alive = sum(r() is not None for r in refs)
+    assert 16 <= alive <= 64 and refs[-1]() is not None
+
+
+def test_the_table_turns_over_while_other_threads_use_it(ep, streams, monkeypatch):
+    import itertools
+    import threading
+
+    number, said = itertools.count(), []
+    monkeypatch.setattr(ep, "_get_ident", lambda: next(number))
+
+    def work():
+        try:
+            for _ in range(2000):
+                assert ep._workspace_of(Logits(), None, 100).nbytes >= 100
+                streams.made.clear()
+        except Exception as e:
+            said.append(repr(e))
+
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not said, said[0]
+    assert len(ep._workspaces) <= 64
