@@ -835,6 +835,25 @@ def _flat(t, dtype, shape) -> bool:
                          and t.shape == shape)
 
 
+def _outputs(stream, device, *wanted):
+    """Uninitialised tensors, one for each (shape, type), for a call on this
+    stream (None: the current one): made under it, so that what their memory
+    was used for is over, and recorded on the current one, on which the
+    caller may go on with them."""
+    import torch
+
+    here = None
+    if stream is not None and device.type == "cuda":      # other places are refused later
+        here = torch.cuda.current_stream(device)
+    if here is None or here.cuda_stream == stream.cuda_stream:
+        return tuple(torch.empty(shape, dtype=dtype, device=device) for shape, dtype in wanted)
+    with torch.cuda.stream(stream):
+        made = tuple(torch.empty(shape, dtype=dtype, device=device) for shape, dtype in wanted)
+    for t in made:
+        t.record_stream(here)
+    return made
+
+
 # Scratch memory of the eager calls, by (device, stream, host thread): calls
 # of one thread on one stream run in order, so that they can share it.  A
 # block that leaves the table goes back to its stream's memory, which later
@@ -916,9 +935,9 @@ def route(cfg: RouterConfig, logits, bias=None, token_mask=None, topk_idx=None,
 
         shape, dev = (logits.shape[0], cfg.num_topk), logits.device
         if topk_idx is None:
-            topk_idx = torch.empty(shape, dtype=torch.int64, device=dev)
+            topk_idx, = _outputs(stream, dev, (shape, torch.int64))
         if topk_weights is None:
-            topk_weights = torch.empty(shape, dtype=torch.float32, device=dev)
+            topk_weights, = _outputs(stream, dev, (shape, torch.float32))
     st = _calls.route(cfg._at, logits, bias, token_mask, topk_idx, topk_weights,
                       stream if stream is None else stream.cuda_stream)
     if st:
@@ -938,12 +957,9 @@ def route_balance(cfg: RouterConfig, logits, bias=None, token_mask=None, seq_sta
         import torch
 
         T, E, K, dev = logits.shape[0], cfg.num_experts, cfg.num_topk, logits.device
-        out = (torch.empty((T, K), dtype=torch.int64, device=dev),
-               torch.empty((T, K), dtype=torch.float32, device=dev),
-               torch.empty((B, E), dtype=torch.int32, device=dev),
-               torch.empty((B, E), dtype=torch.float32, device=dev),
-               torch.empty((B + 2,), dtype=torch.int32, device=dev),
-               torch.empty((2,), dtype=torch.float32, device=dev))
+        out = _outputs(stream, dev, ((T, K), torch.int64), ((T, K), torch.float32),
+                       ((B, E), torch.int32), ((B, E), torch.float32), ((B + 2,), torch.int32),
+                       ((2,), torch.float32))
     size = _lib.ep_route_workspace_bytes(cfg._c[0], B)
     if size < 0 or not logits.is_cuda:
         _refuse("route_balance: config, number of sequences or place of the logits")
@@ -965,9 +981,7 @@ def route_backward(cfg: RouterConfig, logits, topk_idx=None, grad_w=None, token_
     returns it); expert_count, seq_tokens: route_balance's; grad_loss: fp32 [2]
     CUDA tensor.  Returns grad_logits [T, E] of the logits' type."""
     if grad_logits is None:
-        import torch
-
-        grad_logits = torch.empty(tuple(logits.shape), dtype=logits.dtype, device=logits.device)
+        grad_logits, = _outputs(stream, logits.device, (tuple(logits.shape), logits.dtype))
     st = _calls.route_backward(cfg._at, logits, topk_idx, grad_w, token_mask, seq_start,
                                expert_count, seq_tokens, grad_loss, grad_logits,
                                stream if stream is None else stream.cuda_stream)
@@ -1022,9 +1036,10 @@ def w4_pack(cfg: W4Config, codes, scales, zeros=None, stream=None):
             and _flat(zeros, torch.uint8, (E, N, H // g))):
         _refuse("w4_pack: type, shape or place of a tensor")
     tiles, blocks, dev = -(-cfg._width // (32 if cfg.gated else 64)), -(-H // 128), codes.device
-    pc = torch.empty((E, tiles, blocks, 8, 32, 4), dtype=torch.int32, device=dev)
-    ps = torch.empty((E, tiles, blocks * 128 // g, 64), dtype=torch.bfloat16, device=dev)
-    pz = torch.empty(ps.shape, dtype=torch.uint8, device=dev) if cfg.has_zeros else None
+    packed = (E, tiles, blocks * 128 // g, 64)
+    pc, ps = _outputs(stream, dev, ((E, tiles, blocks, 8, 32, 4), torch.int32),
+                      (packed, torch.bfloat16))
+    pz, = _outputs(stream, dev, (packed, torch.uint8)) if cfg.has_zeros else (None,)
     st = ep_w4_pack(cfg._c, codes.data_ptr(), scales.data_ptr(), _ptr(zeros), pc.data_ptr(),
                     ps.data_ptr(), _ptr(pz), _stream(stream))
     _check(st, "ep_w4_pack")
@@ -1040,7 +1055,7 @@ def expert_w4(cfg: W4Config, x, codes, scales, expert_start, expert_end, num_row
     if out is None:
         import torch
 
-        out = torch.empty((x.shape[0], cfg._width), dtype=torch.bfloat16, device=x.device)
+        out, = _outputs(stream, x.device, ((x.shape[0], cfg._width), torch.bfloat16))
     st = _calls.expert_w4(cfg._at, x, codes, scales, expert_start, expert_end, num_rows, zeros,
                           x_scale, out, stream if stream is None else stream.cuda_stream)
     if st:

@@ -37,3 +37,22 @@ def test_a_forked_branch_of_a_capture_and_eager_calls_beside_its_replays(ep):  #
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out_x, want_x))
         assert all(torch.equal(a, b) for a, b in zip(out_y, want_y))
+
+
+def test_outputs_of_a_given_stream(ep):  # noqa: F811
+    """Made by the calls themselves, read on the current stream after it."""
+    cfg = ep.RouterConfig(64, 6, "sigmoid")
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.randn((2000, 64), device="cuda", generator=gen)
+    want = ep.route_balance(cfg, x)
+    grad = ep.route_backward(cfg, x, want[0], want[1])
+    side = torch.cuda.Stream()
+    for _ in range(20):
+        torch.empty(1 << 22, device="cuda").fill_(7.0)      # freed while in flight
+        side.wait_stream(torch.cuda.current_stream())
+        got = ep.route_balance(cfg, x, stream=side)
+        g = ep.route_backward(cfg, x, *ep.route(cfg, x, stream=side), stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        assert all(torch.equal(a, b) for a, b in zip(got, want)) and torch.equal(g, grad)
+    with pytest.raises(ep.EpError):
+        ep.route(cfg, x.cpu(), stream=side)

@@ -150,3 +150,57 @@ def test_the_table_turns_over_while_other_threads_use_it(ep, streams, monkeypatc
         t.join()
     assert not said, said[0]
     assert len(ep._workspaces) <= 64
+
+
+class Fake:
+    """A CUDA tensor as far as the Python layer looks at one."""
+
+    is_cuda, device = True, torch.device("cuda", 0)
+
+    def __init__(self, shape, dtype):
+        self.shape, self.dtype = torch.Size(shape), dtype
+
+    def is_contiguous(self):
+        return True
+
+    def get_device(self):
+        return 0
+
+    def data_ptr(self):
+        return 0x10000
+
+
+def calls_that_allocate(ep):
+    router, w4 = ep.RouterConfig(16, 2), ep.W4Config(2, 128, 64, has_zeros=True)
+    x, rows = Fake((8, 16), torch.float32), Fake((4, 128), torch.bfloat16)
+    codes, scales = Fake((2, 64, 64), torch.uint8), Fake((2, 64, 1), torch.bfloat16)
+    zeros = Fake((2, 64, 1), torch.uint8)
+    return {
+        "route": (2, lambda s: ep.route(router, x, stream=s)),
+        "route_balance": (6, lambda s: ep.route_balance(router, x, workspace=x, stream=s)),
+        "route_backward": (1, lambda s: (ep.route_backward(router, x, stream=s),)),
+        "expert_w4": (1, lambda s: (ep.expert_w4(w4, rows, *[None] * 4, 4, stream=s),)),
+        "w4_pack": (3, lambda s: ep.w4_pack(w4, codes, scales, zeros, stream=s)),
+    }
+
+
+@pytest.mark.parametrize("name", ["route", "route_balance", "route_backward", "expert_w4",
+                                  "w4_pack"])
+def test_outputs_are_made_for_the_stream_that_writes_them(ep, streams, monkeypatch, name):
+    """And recorded on the current one, on which the caller goes on."""
+    recorded = []
+    monkeypatch.setattr(torch.Tensor, "record_stream",
+                        lambda t, s: recorded.append((t, s.cuda_stream)), raising=False)
+    monkeypatch.setattr(ep, "_calls", types.SimpleNamespace(**{
+        n: lambda *a: 0 for n in ("route", "route_balance", "route_backward", "expert_w4")}))
+    monkeypatch.setattr(ep, "ep_w4_pack", lambda *a: 0)
+    many, call = calls_that_allocate(ep)[name]
+    for stream, made_on in ((streams.stream(2), 2), (streams.stream(1), 1), (None, 1)):
+        streams.made.clear()
+        recorded.clear()
+        out = call(stream)
+        assert len(out) == many and [s for s, _, _ in streams.made] == [made_on] * many
+        assert all(any(t is o for _, _, t in streams.made) for o in out)
+        marks = [(t, s) for t, s in recorded]
+        assert len(marks) == (many if made_on == 2 else 0) and all(s == 1 for _, s in marks)
+        assert streams.current.cuda_stream == 1
