@@ -829,6 +829,18 @@ class _LazyCalls:
 _calls = _LazyCalls()
 
 
+def _on_current_gpu(*tensors) -> bool:
+    """Whether the tensors (None left out) are all on the current GPU, the one
+    that the library launches on."""
+    import torch
+
+    try:
+        gpu = torch._C._cuda_getDevice()
+    except (AttributeError, RuntimeError):      # torch without CUDA, no GPU here
+        return False
+    return all(t is None or t.get_device() == gpu for t in tensors)
+
+
 def _flat(t, dtype, shape) -> bool:
     """t is None, or a contiguous CUDA tensor of this type and shape."""
     return t is None or (t.dtype is dtype and t.is_cuda and t.is_contiguous()
@@ -872,6 +884,8 @@ def _workspace_of(t, stream, size: int):
     import torch
 
     dev = t.get_device()
+    if not _on_current_gpu(t):
+        _refuse("route_balance: the logits are on another GPU than the current one")
     handle = torch._C._cuda_getCurrentRawStream(dev)
     if stream is not None and stream.cuda_stream != handle:
         with torch.cuda.stream(stream):
@@ -1033,7 +1047,7 @@ def w4_pack(cfg: W4Config, codes, scales, zeros=None, stream=None):
     E, N, H, g = cfg.num_experts, cfg.out_features, cfg.in_features, cfg.group_size
     if not (_flat(codes, torch.uint8, (E, N, H // 2))
             and _flat(scales, torch.bfloat16, (E, N, H // g))
-            and _flat(zeros, torch.uint8, (E, N, H // g))):
+            and _flat(zeros, torch.uint8, (E, N, H // g)) and _on_current_gpu(codes, scales, zeros)):
         _refuse("w4_pack: type, shape or place of a tensor")
     tiles, blocks, dev = -(-cfg._width // (32 if cfg.gated else 64)), -(-H // 128), codes.device
     packed = (E, tiles, blocks * 128 // g, 64)

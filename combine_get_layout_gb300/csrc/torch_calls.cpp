@@ -10,9 +10,11 @@
 #define PY_SSIZE_T_CLEAN
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 
 #include <exception>
+#include <initializer_list>
 
 #include "../../include/ep.h"
 
@@ -32,7 +34,7 @@ struct Arg {
     fits = THPVariable_Check(o);
     if (fits) t = &THPVariable_Unpack(o);
   }
-  // present, strided and on the GPU
+  // present, strided and on a GPU
   bool here() const { return t != nullptr && t->is_cuda() && t->layout() == at::kStrided; }
   // and contiguous, of this type and shape
   bool is(ScalarType type, at::IntArrayRef shape) const {
@@ -54,6 +56,16 @@ struct Arg {
   }
 };
 
+// Whether the present tensors are all on the current GPU: the one that the
+// library launches on, and whose memory a launch may use.
+bool on_current_gpu(std::initializer_list<const Arg*> args) {
+  c10::DeviceIndex gpu = -1;
+  if (c10::cuda::GetDevice(&gpu) != cudaSuccess) return false;
+  for (const Arg* a : args)
+    if (a->t != nullptr && (!a->t->is_cuda() || a->t->get_device() != gpu)) return false;
+  return true;
+}
+
 // Router logits or their gradient: [T, E] of fp32 or bf16, columns of unit
 // stride.
 struct Logits {
@@ -71,10 +83,10 @@ struct Logits {
   }
 };
 
-// A stream handle, or the current stream of a tensor's device for None.
-bool stream_of(PyObject* o, const Arg& a, void** stream) {
+// A stream handle, or the current stream for None.
+bool stream_of(PyObject* o, void** stream) {
   if (o == Py_None) {
-    *stream = c10::cuda::getCurrentCUDAStream(a.t->get_device()).stream();
+    *stream = c10::cuda::getCurrentCUDAStream().stream();
     return true;
   }
   *stream = PyLong_AsVoidPtr(o);
@@ -131,10 +143,11 @@ PyObject* route(PyObject* const* a, Py_ssize_t n) {
   const Arg logits(a[1]), bias(a[2]), mask(a[3]), idx(a[4]), w(a[5]);
   const Logits l(logits, E);
   if (!l.fits || !bias.is_or_absent(ScalarType::Float, {E}) || !mask.is_mask_or_absent(l.T) ||
-      !idx.is(ScalarType::Long, {l.T, K}) || !w.is(ScalarType::Float, {l.T, K}))
+      !idx.is(ScalarType::Long, {l.T, K}) || !w.is(ScalarType::Float, {l.T, K}) ||
+      !on_current_gpu({&logits, &bias, &mask, &idx, &w}))
     return unfit();
   void* stream;
-  if (!stream_of(a[6], logits, &stream)) return nullptr;
+  if (!stream_of(a[6], &stream)) return nullptr;
   return status_of([&] {
     return ep_route(cfg + l.bf16, int32_t(l.T), logits.ptr<void>(), l.ld, bias.ptr<float>(),
                     mask.ptr<uint8_t>(), idx.ptr<int64_t>(), w.ptr<float>(), stream);
@@ -160,10 +173,12 @@ PyObject* route_balance(PyObject* const* a, Py_ssize_t n) {
       !idx.is(ScalarType::Long, {l.T, K}) || !w.is(ScalarType::Float, {l.T, K}) ||
       !count.is(ScalarType::Int, {B, E}) || !prob.is(ScalarType::Float, {B, E}) ||
       !tokens.is(ScalarType::Int, {B + 2}) || !loss.is(ScalarType::Float, {2}) ||
-      !workspace.holds(bytes))
+      !workspace.holds(bytes) ||
+      !on_current_gpu({&logits, &bias, &mask, &seq, &idx, &w, &count, &prob, &tokens, &loss,
+                       &workspace}))
     return unfit();
   void* stream;
-  if (!stream_of(a[13], logits, &stream)) return nullptr;
+  if (!stream_of(a[13], &stream)) return nullptr;
   return status_of([&] {
     return ep_route_balance(cfg + l.bf16, int32_t(l.T), logits.ptr<void>(), l.ld,
                             bias.ptr<float>(), mask.ptr<uint8_t>(), int32_t(B),
@@ -192,10 +207,11 @@ PyObject* route_backward(PyObject* const* a, Py_ssize_t n) {
       !grad_w.is_or_absent(ScalarType::Float, {l.T, K}) ||
       !count.is_or_absent(ScalarType::Int, {B, E}) ||
       !tokens.is_or_absent(ScalarType::Int, {B + 2}) ||
-      !grad_loss.is_or_absent(ScalarType::Float, {2}))
+      !grad_loss.is_or_absent(ScalarType::Float, {2}) ||
+      !on_current_gpu({&logits, &idx, &grad_w, &mask, &seq, &count, &tokens, &grad_loss, &grad}))
     return unfit();
   void* stream;
-  if (!stream_of(a[10], logits, &stream)) return nullptr;
+  if (!stream_of(a[10], &stream)) return nullptr;
   return status_of([&] {
     return ep_route_backward(cfg + l.bf16, int32_t(l.T), logits.ptr<void>(), l.ld,
                              mask.ptr<uint8_t>(), idx.ptr<int64_t>(), grad_w.ptr<float>(),
@@ -229,10 +245,11 @@ PyObject* expert_w4(PyObject* const* a, Py_ssize_t n) {
       !out.is(ScalarType::BFloat16, {cap, N}) || !segments(start) || !segments(end) ||
       !codes.holds(ep_w4_codes_bytes(cfg)) || !scales.holds(ep_w4_scales_bytes(cfg)) ||
       scales.t->scalar_type() != ScalarType::BFloat16 || !zeros.fits ||
-      (zeros.t != nullptr && !zeros.holds(ep_w4_zeros_bytes(cfg))))
+      (zeros.t != nullptr && !zeros.holds(ep_w4_zeros_bytes(cfg))) ||
+      !on_current_gpu({&x, &codes, &scales, &start, &end, &zeros, &x_scale, &out}))
     return unfit();
   void* stream;
-  if (!stream_of(a[10], x, &stream)) return nullptr;
+  if (!stream_of(a[10], &stream)) return nullptr;
   return status_of([&] {
     return ep_expert_w4(cfg, int32_t(cap), int32_t(num_rows), x.ptr<void>(),
                         x_scale.ptr<float>(), codes.ptr<void>(), scales.ptr<void>(),

@@ -44,6 +44,7 @@ class Streams:
                             lambda: self.current.cuda_stream in self.capturing)
         monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream",
                             lambda dev: self.current.cuda_stream, raising=False)
+        monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
 
     @staticmethod
     def stream(handle):
