@@ -1,5 +1,5 @@
-"""Builds libep_gb300.so in-tree for sm_103a with nvcc, and the torch layer's
-compiled calls beside it.
+"""Builds libep_gb300.so in-tree for sm_103a with nvcc, and beside it, where torch
+is installed, the torch layer's compiled calls.
 
 Each .cu file is compiled in its own nvcc process (in parallel), then the
 objects are linked into one shared library with the CUDA runtime linked
@@ -28,9 +28,6 @@ OUT_DIR = os.path.join(PKG, "_lib")
 BUILD_DIR = os.path.join(PKG, "_build_obj")
 LIB = os.path.join(OUT_DIR, "libep_gb300.so")
 CALLS_SRC = os.path.join(CSRC, "torch_calls.cpp")
-# one file a Python and torch, whose binary interfaces it follows
-CALLS = os.path.join(OUT_DIR, "ep_torch_calls.%s.torch%s.so" % (
-    sys.implementation.cache_tag, importlib.metadata.version("torch").replace("+", ".")))
 HEADERS = [os.path.join(ROOT, "include", "ep.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -61,19 +58,35 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
-def calls_up_to_date() -> bool:
-    if not os.path.exists(CALLS):
+def torch_dir() -> str:
+    return os.path.dirname(importlib.util.find_spec("torch").origin)
+
+
+def calls_path():
+    """ep_torch_calls for the installed torch, or None without one (with CUDA):
+    one file a Python and torch, whose binary interfaces it follows."""
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        return None
+    if not os.path.exists(os.path.join(torch_dir(), "lib", "libc10_cuda.so")):
+        return None
+    return os.path.join(OUT_DIR, "ep_torch_calls.%s.torch%s.so" % (
+        sys.implementation.cache_tag, version.replace("+", ".")))
+
+
+def calls_up_to_date(calls: str) -> bool:
+    if not os.path.exists(calls):
         return False
-    t = os.path.getmtime(CALLS)
+    t = os.path.getmtime(calls)
     return all(os.path.getmtime(d) <= t for d in [CALLS_SRC, *HEADERS])
 
 
 def compile_calls() -> str:
     """The object file of ep_torch_calls; linked after the library."""
-    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(shutil.which(nvcc()) or nvcc())))
-    inc = [os.path.join(torch_dir, "include"),
-           os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+    inc = [os.path.join(torch_dir(), "include"),
+           os.path.join(torch_dir(), "include", "torch", "csrc", "api", "include"),
            sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
     obj = os.path.join(BUILD_DIR, "torch_calls.o")
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-c", CALLS_SRC, "-o", obj]
@@ -85,9 +98,9 @@ def compile_calls() -> str:
     return obj
 
 
-def link_calls(obj: str) -> None:
-    torch_lib = os.path.join(os.path.dirname(importlib.util.find_spec("torch").origin), "lib")
-    tmp = CALLS + f".tmp{os.getpid()}"
+def link_calls(obj: str, calls: str) -> None:
+    torch_lib = os.path.join(torch_dir(), "lib")
+    tmp = calls + f".tmp{os.getpid()}"
     # torch's own libraries are loaded before the extension is, this one from
     # beside it
     cmd = ["g++", "-shared", "-o", tmp, obj, "-L" + OUT_DIR, "-l:" + os.path.basename(LIB),
@@ -95,15 +108,16 @@ def link_calls(obj: str) -> None:
            "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"linking {CALLS} failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, CALLS)
+        raise RuntimeError(f"linking {calls} failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, calls)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
+    calls = calls_path()
     if not force and up_to_date():
-        if not calls_up_to_date():
+        if calls is not None and not calls_up_to_date(calls):
             os.makedirs(BUILD_DIR, exist_ok=True)
-            link_calls(compile_calls())
+            link_calls(compile_calls(), calls)
         return LIB
     os.makedirs(OUT_DIR, exist_ok=True)
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -121,16 +135,16 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
 
     srcs = sources()
     with cf.ThreadPoolExecutor(max_workers=len(srcs) + 1) as ex:
-        calls = ex.submit(compile_calls)
+        calls_obj = ex.submit(compile_calls) if calls is not None else None
         objs = list(ex.map(compile_one, srcs))
-        calls_obj = calls.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    link_calls(calls_obj)
+    if calls_obj is not None:
+        link_calls(calls_obj.result(), calls)
     return LIB
 
 
