@@ -180,10 +180,16 @@ __device__ __forceinline__ float tile_max(float v) {
   }
 }
 
-// The larger, or NaN if either is.
+// The larger and the smaller, or NaN if either is.
 __device__ __forceinline__ float max_or_nan(float a, float b) {
   float m;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
+}
+
+__device__ __forceinline__ float min_or_nan(float a, float b) {
+  float m;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
   return m;
 }
 
@@ -198,10 +204,9 @@ __device__ __forceinline__ uint32_t tile_bits(uint32_t ballot, int lane) {
 
 // ---- scores ---------------------------------------------------------------
 
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// 2^x and 1 / x to 2^-22 of the value: what a score is rounded to anyway
-// once 32-bit sums and products have passed over it.
+// 2^x and 1 / x to 2^-22 of the value, or 0 below 2^-126.
 __device__ __forceinline__ float fast_exp2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -213,6 +218,14 @@ __device__ __forceinline__ float fast_reciprocal(float x) {
   return r;
 }
 
+// exp(d) for -128 <= d <= 88.  t = d log2 e is rounded to up to 2^-17 of an
+// exponent near 128, so that 2^t would be off by up to 4e-6 of its value;
+// d - t ln 2 is what the rounding left out, and exp of it 1 + itself.
+__device__ __forceinline__ float exponential(float d) {
+  const float t = d * kLog2e, e = fast_exp2(t);
+  return fmaf(e, fmaf(-t, kLn2, d), e);
+}
+
 // a / b for 0 <= a <= b, given 1 / b to within a few roundings: the product,
 // and its residual as one correction (Newton's step for a quotient).  a / a
 // is 1: the correction of 1 - 2^-24 or 1 + 2^-23 rounds to it.
@@ -221,13 +234,16 @@ __device__ __forceinline__ float quotient(float a, float b, float inv_b) {
   return fmaf(fmaf(-q, b, a), inv_b, q);
 }
 
+// Under 2^-126 (x below -87.3) it is 0.
 __device__ __forceinline__ float sigmoid(float x) {
-  return fast_reciprocal(1.0f + fast_exp2(-kLog2e * x));
+  const float d = min_or_nan(max_or_nan(-x, -128.0f), 88.0f);
+  return fast_reciprocal(1.0f + exponential(d));
 }
 
-// exp(l - top); the difference first, so that no size of logit overflows.
+// exp(l - top), 0 under 2^-126; the difference first, so that no size of
+// logit overflows.
 __device__ __forceinline__ float soft_score(float l, float top) {
-  return fast_exp2((l - top) * kLog2e);
+  return exponential(max_or_nan(l - top, -128.0f));
 }
 
 template <int N>
