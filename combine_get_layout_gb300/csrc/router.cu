@@ -1137,7 +1137,12 @@ route_backward_kernel(RouteBackwardParams p) {
 #pragma unroll
       for (int r = 0; r < S::kValues; ++r) g[r] = s[r] * (g[r] - (dot - z));
     }
-    // a padding token's row was taken as -inf: all its scores are 0
+    // a padding token's row was taken as -inf: all its scores are 0, but not
+    // their products with a coefficient that is not finite
+    if (!now.have) {
+#pragma unroll
+      for (int r = 0; r < S::kValues; ++r) g[r] = 0.0f;
+    }
     if (t < last) store_row<S>(p.grad, int64_t(t) * p.ld_grad, p.E, l, g);
     if constexpr (S::kAhead) now = next;
   }

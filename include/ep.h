@@ -598,7 +598,8 @@ EP_API int32_t ep_route_balance(const ep_router_config *cfg, int32_t num_tokens,
  *   fp32 [2]): all three, or all NULL (no loss terms).  grad_loss[1] is not
  *   used with sigmoid scores.
  * d_grad_logits: device [T, ld_grad], the type of the logits; columns past E
- *   are not written.  Masked tokens and experts out of service get 0.
+ *   are not written.  Masked tokens get 0, and so do experts out of service
+ *   where their token's gradients and coefficients are finite.
  * Everything else is recomputed from the logits.  Returns EP_OK or an
  * error. */
 EP_API int32_t ep_route_backward(const ep_router_config *cfg, int32_t num_tokens,

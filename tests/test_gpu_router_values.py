@@ -79,3 +79,23 @@ def test_an_expert_whose_bias_is_nan_is_out_of_the_choice(ep, T, E, groups, kept
     got = ep.route_balance(cfg, x, torch.from_numpy(bias).float().cuda())
     assert torch.equal(got[0], idx)
     np.testing.assert_allclose(got[1][:40].cpu().numpy(), ww, rtol=rt)
+
+
+@pytest.mark.parametrize("T,E", [(40, 256), (40, 60), (6000, 60), (6000, 128), (40, 1000)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("bad", [INF, np.nan])
+def test_masked_tokens_get_no_gradient_whatever_comes_in(ep, T, E, score, bad):  # noqa: F811
+    """Coefficients and gate gradients that are not finite, NaN in masked rows."""
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn((T, E), device="cuda", generator=gen)
+    mask = torch.rand(T, device="cuda", generator=gen) > 0.4
+    x[~mask] = float("nan")
+    cfg = ep.RouterConfig(E, 4, score)
+    idx, w, count, _, tokens, _ = ep.route_balance(cfg, x, None, mask)
+    gl = torch.tensor([bad, bad], device="cuda")
+    gw = torch.where(mask[:, None], torch.randn((T, 4), device="cuda", generator=gen), bad)
+    g = ep.route_backward(cfg, x, idx, gw, mask, None, count, tokens, gl)
+    assert (g[~mask] == 0).all() and torch.isnan(g[mask]).any(1).all()
+    gl.zero_()
+    g = ep.route_backward(cfg, x, idx, gw, mask, None, count, tokens, gl)
+    assert (g[~mask] == 0).all() and torch.isfinite(g).all()
