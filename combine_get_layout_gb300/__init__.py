@@ -911,6 +911,12 @@ class _AbiConfig:
     def __reduce__(self):
         return type(self), tuple(getattr(self, f.name) for f in dataclasses.fields(self))
 
+    def _same_numbers(self, c) -> bool:
+        """Whether the struct holds the fields' whole numbers: ctypes drops the
+        bits that do not fit."""
+        return all(getattr(c, f.name) == getattr(self, f.name) for f in dataclasses.fields(self)
+                   if f.type == "int")
+
 
 @dataclasses.dataclass(frozen=True)
 class RouterConfig(_AbiConfig):
@@ -932,6 +938,8 @@ class RouterConfig(_AbiConfig):
             EpRouterConfig(self.num_experts, self.num_topk, int(self.score == "sigmoid"),
                            self.num_groups, self.topk_groups, int(self.renormalize), bf16,
                            self.route_scale) for bf16 in (0, 1)))
+        if not self._same_numbers(both[0]):
+            _refuse("RouterConfig: a number of over 32 bits")
         object.__setattr__(self, "_c", both)
         object.__setattr__(self, "_at", ctypes.addressof(both))
 
@@ -1022,7 +1030,7 @@ class W4Config(_AbiConfig):
         c = EpW4Config(self.num_experts, self.in_features, self.out_features, self.group_size,
                        int(self.x_fp8), int(self.gated), int(self.has_zeros))
         sizes = ep_w4_codes_bytes(c), ep_w4_scales_bytes(c), ep_w4_zeros_bytes(c)
-        if min(sizes) < 0:
+        if min(sizes) < 0 or not self._same_numbers(c):
             _refuse("W4Config")
         object.__setattr__(self, "_c", c)
         object.__setattr__(self, "_at", ctypes.addressof(c))

@@ -71,3 +71,17 @@ def test_another_process_gets_a_struct_of_its_own(ep, kind):
                        text=True, env=env, cwd=ROOT, timeout=300)
     assert r.returncode == 0, r.stderr
     assert r.stdout.strip() == str(fields_of(c))
+
+
+@pytest.mark.parametrize("make_one", [
+    lambda ep: ep.RouterConfig(2**32 + 16, 2), lambda ep: ep.RouterConfig(16, 2**32 + 2),
+    lambda ep: ep.RouterConfig(16, 2, num_groups=2**32 + 1),
+    lambda ep: ep.RouterConfig(16, 2, topk_groups=1 - 2**32),
+    lambda ep: ep.W4Config(2**32 + 1, 128, 64), lambda ep: ep.W4Config(1, 2**32 + 128, 64),
+    lambda ep: ep.W4Config(1, 128, 2**40 + 64), lambda ep: ep.W4Config(1, 128, 64, 128 - 2**32),
+])
+def test_numbers_that_a_field_does_not_hold_are_refused(ep, make_one):
+    """A field of 32 bits keeps the lower ones of a larger number."""
+    with pytest.raises(ep.EpError) as e:
+        make_one(ep)
+    assert e.value.status == ep.EP_ERR_INVALID_ARG
