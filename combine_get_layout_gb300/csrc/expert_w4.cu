@@ -198,7 +198,7 @@ __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) {
 // Chunks of kRows rows that rows lo .. hi - 1 make, for any 0 <= lo, hi < 2^31.
 template <int kRows>
 __host__ __device__ constexpr int chunks_of(int lo, int hi) {
-  return hi > lo ? (hi - lo - 1) / kRows + 1 : 0;
+  return hi > lo ? int((unsigned(hi) - unsigned(lo) + (kRows - 1)) / kRows) : 0;
 }
 static_assert(chunks_of<8>(0, 0x7fffffff) == 1 << 28 && chunks_of<16>(5, 0x7fffffff) == 1 << 27);
 static_assert(chunks_of<8>(3, 3) == 0 && chunks_of<8>(4, 3) == 0 && chunks_of<8>(0, 1) == 1 &&
@@ -324,10 +324,10 @@ struct Loader {
       const int t = Kd::FP8 ? lane >> 3 : lane >> 4, c = Kd::FP8 ? lane & 7 : lane & 15;
       rows = it.rows - t;
       k = slice * kBlockIn + c * (Kd::FP8 ? 16 : 8);
-      x = static_cast<const char*>(p.x) + ((int64_t(it.row0) + t) * p.H + k) * (Kd::FP8 ? 1 : 2);
+      x = static_cast<const char*>(p.x) + (int64_t(unsigned(it.row0) + t) * p.H + k) * (Kd::FP8 ? 1 : 2);
       if constexpr (Kd::FP8)
         x_scale =
-            reinterpret_cast<const char*>(p.x_scale + (int64_t(it.row0) + lane) * p.blocks + slice);
+            reinterpret_cast<const char*>(p.x_scale + int64_t(unsigned(it.row0) + lane) * p.blocks + slice);
     }
     kb = slice;
   }
@@ -381,7 +381,7 @@ struct Columns {
 #pragma unroll
       for (int t = 0; t < Kd::NT; ++t)
         x[t] = static_cast<const char*>(p.x) +
-               ((int64_t(it.row0) + min(8 * t + (lane >> 2), it.rows - 1)) * p.H +
+               (int64_t(it.row0 + min(8 * t + (lane >> 2), it.rows - 1)) * p.H +
                 slice * kBlockIn + 8 * (lane & 3)) * 2;
     }
   }
@@ -554,7 +554,7 @@ __device__ __forceinline__ void multiply_all(uint32_t stage, int lane, int input
 __device__ __forceinline__ void store_pair(const W4Params& p, const Item& it, int g, int i, int col,
                                            float lo, float hi) {
   if (col >= it.rows) return;
-  __nv_bfloat16* o = p.out + (int64_t(it.row0) + col) * p.N;
+  __nv_bfloat16* o = p.out + int64_t(it.row0 + col) * p.N;
   if (p.gated) {
     const int n = it.tile * 32 + 4 * g + i;
     if (n < p.N) o[n] = __float2bfloat16_rn(lo / (1.0f + expf(-lo)) * hi);
