@@ -787,6 +787,8 @@ def combine_ranks(cfg: Config, layout: Layout, rank_y, y=None, stream=None):
 # The calls below sit in decode loops where a kernel takes a few microseconds:
 # their ABI configs are built once, and a compiled extension (ep_torch_calls,
 # csrc/torch_calls.cpp) checks the tensors and calls the library in one step.
+# All tensors of a call are on the current GPU.  With `stream`, the caller lets
+# that stream wait for the inputs, and whoever reads the outputs for it.
 
 def _refuse(what: str):
     raise EpError(EP_ERR_INVALID_ARG, what)

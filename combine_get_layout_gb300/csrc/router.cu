@@ -649,7 +649,7 @@ __device__ __forceinline__ Chosen<S> route_token(const RouteParams& p, int t, bo
 //
 // What bounds it: instructions, about 400 a token of 256 experts by softmax
 // with top-8 (300 of them with top-1: loads, scores, reductions, addresses)
-// and 670 by sigmoid with groups, at 2.5 a cycle and SM with 28 warps.  16384
+// and 690 by sigmoid with groups, at 2.5 a cycle and SM with 28 warps.  16384
 // tokens, bf16: 8.3 us, where the bytes would take 1.5; 128 tokens 3.1 us
 // and one 2.7, of which an empty launch is about 1.7.
 //
@@ -717,10 +717,12 @@ constexpr int kBalanceThreads = S::kValues <= 16 ? 512 : 256;
 
 // ep_route_balance, first kernel: what bounds it is what bounds ep_route, and
 // the flush of a CTA's sums.  16384 tokens by 256 experts, sigmoid, groups, 4
-// sequences: 22.3 us for both kernels, the bytes 2.8; 4096 by softmax 10.1;
-// 8191 by 64 in 37 ragged sequences 10.3.  One CTA of 512 threads an SM, with
-// the registers it likes: two at 64 registers 23.4, 10.4 and 10.8 us; 768
-// threads 21.4, 10.7 and 11.6; two of 256 threads 23.0, 11.1 and 10.9.
+// sequences: 23.0 us for both kernels (745 instructions a token), the bytes
+// 2.8; 4096 by softmax 10.5; 8191 by 64 in 37 ragged sequences 10.6.  One CTA
+// of 512 threads an SM, with the registers it likes.  Measured with one
+// rounding an exponential less, when this took 22.3, 10.1 and 10.3 us: two at
+// 64 registers 23.4, 10.4 and 10.8; 768 threads 21.4, 10.7 and 11.6; two of
+// 256 threads 23.0, 11.1 and 10.9.
 // About 4 us are the second kernel and its launch; starting it early
 // (launch_dependents) measured no better.
 //
@@ -1023,8 +1025,8 @@ struct RouteBackwardParams {
 //   sigmoid:  u = (dq - sum q dq) / sum s + ds,  dl = u s (1 - s)
 // The next token's logits, choice and gate gradient are loaded ahead.
 //
-// What bounds it: instructions again, about 400 a token of 256 experts; 16384
-// tokens, bf16, sigmoid: 8.7 us (bytes: 2.8), 4096, fp32, softmax: 3.9 (1.3).
+// What bounds it: instructions again, about 460 a token of 256 experts; 16384
+// tokens, bf16, sigmoid: 9.4 us (bytes: 2.8), 4096, fp32, softmax: 4.0 (1.3).
 template <class S, bool SIG>
 __global__ void __launch_bounds__(kRouteThreads, kRouteShare<S>)
 route_backward_kernel(RouteBackwardParams p) {

@@ -1,8 +1,8 @@
 // The torch layer's calls whose kernels take a few microseconds: checks of the
 // tensors and the C ABI call in one step, for a Python wrapper each in
 // __init__.py.  A call of ep_route for one token from Python, one after another:
-// 3.0 us, and 5.4 with the same checks in Python and ctypes; of
-// ep_route_backward for 4096, 3.9 and 7.4.
+// 2.9 to 3.0 us, and 5.4 with the same checks in Python and ctypes; of
+// ep_route_backward for 4096, 4.0 and 7.4.
 //
 // Every function returns the entry point's status, or -1 where a tensor's
 // type, shape, layout or place does not fit (nothing is called then).  The

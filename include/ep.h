@@ -533,7 +533,8 @@ EP_API int32_t ep_selftest_layout_timeout(const ep_config *cfg, int32_t num_toke
  * index.  w_tk = route_scale * s of choice k, divided by the sum of the
  * chosen s when renormalize is set (0 where that sum is 0).  Where fewer than
  * K experts can be chosen, and for masked tokens, idx = -1 and w = 0 (an
- * unused selection of ep_get_layout). */
+ * unused selection of ep_get_layout).  A score under 2^-126 is taken as 0;
+ * its expert can be chosen all the same. */
 enum { EP_SCORE_SOFTMAX = 0, EP_SCORE_SIGMOID = 1 };
 
 typedef struct {
