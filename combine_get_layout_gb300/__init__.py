@@ -37,6 +37,10 @@ EP_ERR_CUDA = 5
 EP_ERR_TIMEOUT = 6
 EP_ERR_TIMEOUT_PENDING = 7
 
+EP_GRAD_BF16 = 0
+EP_GRAD_FP32 = 1
+EP_GRAD_FP32_ADD = 2
+
 # The entry points include/ep.h declares (kept in sync by a test).
 ABI_SYMBOLS = (
     "ep_recv_capacity",
@@ -66,6 +70,10 @@ ABI_SYMBOLS = (
     "ep_w4_zeros_bytes",
     "ep_w4_pack",
     "ep_expert_w4",
+    "ep_expert_mm",
+    "ep_expert_mm_backward",
+    "ep_act_save",
+    "ep_act_backward",
     "ep_check_error",
     "ep_selftest_wait_timeout",
     "ep_selftest_layout_timeout",
@@ -134,6 +142,16 @@ class EpW4Config(ctypes.Structure):
     ]
 
 
+class EpExpertConfig(ctypes.Structure):
+    _fields_ = [
+        ("num_experts", ctypes.c_int32),
+        ("in_features", ctypes.c_int32),
+        ("out_features", ctypes.c_int32),
+        ("x_fp8", ctypes.c_int32),
+        ("gated", ctypes.c_int32),
+    ]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -197,6 +215,15 @@ def _load():
     L.ep_w4_pack.argtypes = [P(EpW4Config), vp, vp, vp, vp, vp, vp, vp]
     L.ep_expert_w4.restype = i32
     L.ep_expert_w4.argtypes = [P(EpW4Config), i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    L.ep_expert_mm.restype = i32
+    L.ep_expert_mm.argtypes = [P(EpExpertConfig), i32, i32, vp, vp, vp, vp, vp, vp, vp, vp]
+    L.ep_expert_mm_backward.restype = i32
+    L.ep_expert_mm_backward.argtypes = [P(EpExpertConfig), i32, i32, vp, vp, vp, vp, vp, vp, vp,
+                                        vp, i32, vp, vp]
+    L.ep_act_save.restype = i32
+    L.ep_act_save.argtypes = [i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp]
+    L.ep_act_backward.restype = i32
+    L.ep_act_backward.argtypes = [i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp]
     L.ep_check_error.restype = i32
     L.ep_check_error.argtypes = [P(EpLayout), vp]
     L.ep_selftest_fp8_quotient.restype = i32
@@ -378,6 +405,31 @@ def ep_expert_w4(cfg, cap, num_rows, d_x, d_x_scale, d_codes, d_scales, d_zeros,
                  d_expert_start, d_expert_end, d_out, stream) -> int:
     return _lib.ep_expert_w4(cfg, cap, num_rows, d_x, d_x_scale, d_codes, d_scales, d_zeros,
                              d_expert_start, d_expert_end, d_out, stream)
+
+
+def ep_expert_mm(cfg, cap, num_rows, d_x, d_x_scale, d_w, d_expert_start, d_expert_end, d_out,
+                 d_err, stream) -> int:
+    return _lib.ep_expert_mm(cfg, cap, num_rows, d_x, d_x_scale, d_w, d_expert_start,
+                             d_expert_end, d_out, d_err, stream)
+
+
+def ep_expert_mm_backward(cfg, cap, num_rows, d_grad_out, d_w, d_x, d_x_scale, d_expert_start,
+                          d_expert_end, d_grad_x, d_grad_w, grad_w_type, d_err, stream) -> int:
+    return _lib.ep_expert_mm_backward(cfg, cap, num_rows, d_grad_out, d_w, d_x, d_x_scale,
+                                      d_expert_start, d_expert_end, d_grad_x, d_grad_w,
+                                      grad_w_type, d_err, stream)
+
+
+def ep_act_save(num_experts, width, cap, num_rows, d_h, d_expert_start, d_expert_end, d_a, d_q,
+                d_scale, stream) -> int:
+    return _lib.ep_act_save(num_experts, width, cap, num_rows, d_h, d_expert_start, d_expert_end,
+                            d_a, d_q, d_scale, stream)
+
+
+def ep_act_backward(num_experts, width, cap, num_rows, d_grad_a, d_q, d_scale, d_expert_start,
+                    d_expert_end, d_grad_h, d_a, stream) -> int:
+    return _lib.ep_act_backward(num_experts, width, cap, num_rows, d_grad_a, d_q, d_scale,
+                                d_expert_start, d_expert_end, d_grad_h, d_a, stream)
 
 
 def ep_check_error(layout, stream) -> int:
@@ -1085,3 +1137,127 @@ def expert_w4(cfg: W4Config, x, codes, scales, expert_start, expert_end, num_row
     if st:
         _done(st, "expert_w4")
     return out
+
+
+# ---- experts' products with bf16 weights -------------------------------------------
+
+@dataclasses.dataclass(frozen=True)
+class ExpertConfig(_AbiConfig):
+    """Mirror of ep_expert_config (see include/ep.h)."""
+
+    num_experts: int
+    in_features: int
+    out_features: int
+    x_fp8: bool = False
+    gated: bool = False
+
+    def __post_init__(self):
+        c = EpExpertConfig(self.num_experts, self.in_features, self.out_features,
+                           int(self.x_fp8), int(self.gated))
+        # a call without rows checks the config alone
+        at = 16
+        if not self._same_numbers(c) or ep_expert_mm(c, 0, 0, None, None, at, at, at, None, None,
+                                                     None) != EP_OK:
+            _refuse("ExpertConfig")
+        object.__setattr__(self, "_c", c)
+        object.__setattr__(self, "_at", ctypes.addressof(c))
+        object.__setattr__(self, "_width",
+                           self.out_features // 2 if self.gated else self.out_features)
+
+    def c(self) -> EpExpertConfig:
+        return self._c
+
+    @property
+    def out_width(self) -> int:
+        return self._width
+
+
+def expert_mm(cfg: ExpertConfig, x, w, expert_start, expert_end, num_rows, x_scale=None, out=None,
+              err=None, stream=None):
+    """ep_expert_mm.  x: bf16 [cap, H], or uint8 (E4M3 bits) with x_scale fp32
+    [cap, H / 128]; w: bf16 [E, N, H]; expert_start, expert_end: a Layout's;
+    num_rows: rows of all experts together at most (T * K); err: a Layout's,
+    or None.  Returns out, bf16 [cap, N] ([cap, N / 2] when gated)."""
+    if out is None:
+        import torch
+
+        out, = _outputs(stream, x.device, ((x.shape[0], cfg._width), torch.bfloat16))
+    st = _calls.expert_mm(cfg._at, x, w, expert_start, expert_end, num_rows, x_scale, out, err,
+                          stream if stream is None else stream.cuda_stream)
+    if st:
+        _done(st, "expert_mm")
+    return out
+
+
+def expert_mm_backward(cfg: ExpertConfig, grad_out, expert_start, expert_end, num_rows, w=None,
+                       x=None, x_scale=None, grad_x=None, grad_w=None, grad_w_dtype=None,
+                       accumulate: bool = False, err=None, stream=None):
+    """ep_expert_mm_backward.  grad_out: bf16 [cap, N].  With w (the forward
+    call's) the gradient by the rows is computed, with x (and x_scale) the
+    gradient by the weights: grad_w [E, N, H] of grad_w's type, or of
+    grad_w_dtype (bf16 by default, or fp32) where it is None; accumulate: adds
+    to grad_w (fp32).  Returns (grad_x bf16 [cap, H] or None, grad_w or
+    None)."""
+    if w is not None and grad_x is None:
+        import torch
+
+        grad_x, = _outputs(stream, grad_out.device,
+                           ((grad_out.shape[0], cfg.in_features), torch.bfloat16))
+    if x is not None and grad_w is None:
+        import torch
+
+        if accumulate:
+            _refuse("expert_mm_backward: accumulate without grad_w")
+        grad_w, = _outputs(stream, grad_out.device,
+                           ((cfg.num_experts, cfg.out_features, cfg.in_features),
+                            grad_w_dtype or torch.bfloat16))
+    st = _calls.expert_mm_backward(cfg._at, grad_out, expert_start, expert_end, num_rows, w, x,
+                                   x_scale, grad_x, grad_w, bool(accumulate), err,
+                                   stream if stream is None else stream.cuda_stream)
+    if st:
+        _done(st, "expert_mm_backward")
+    return grad_x, grad_w
+
+
+# ---- gated activation with its input kept in 8 bits ----------------------------------
+
+def act_save(h, expert_start, expert_end, num_rows, a=None, h_q=None, h_scale=None, stream=None):
+    """ep_act_save.  h: bf16 [cap, 2 I], gate and up values side by side;
+    expert_start (int32 [E + 1], or [E]), expert_end (int32 [E]), num_rows: as in expert_mm.
+    Returns (a bf16 [cap, I], h_q uint8 (E4M3 bits) [cap, 2 I], h_scale fp32
+    [cap, 2 ceil(I / 128)])."""
+    if a is None or h_q is None or h_scale is None:
+        import torch
+
+        cap, width, dev = h.shape[0], h.shape[1] // 2, h.device
+        if a is None:
+            a, = _outputs(stream, dev, ((cap, width), torch.bfloat16))
+        if h_q is None:
+            h_q, = _outputs(stream, dev, ((cap, 2 * width), torch.uint8))
+        if h_scale is None:
+            h_scale, = _outputs(stream, dev, ((cap, 2 * -(-width // 128)), torch.float32))
+    st = _calls.act_save(h, expert_start, expert_end, num_rows, a, h_q, h_scale,
+                         stream if stream is None else stream.cuda_stream)
+    if st:
+        _done(st, "act_save")
+    return a, h_q, h_scale
+
+
+def act_backward(grad_a, h_q, h_scale, expert_start, expert_end, num_rows, grad_h=None, a=None,
+                 want_a: bool = True, stream=None):
+    """ep_act_backward.  grad_a: bf16 [cap, I]; h_q, h_scale: act_save's.
+    Returns (grad_h bf16 [cap, 2 I], a bf16 [cap, I] or None)."""
+    want_a = want_a or a is not None
+    if grad_h is None or (a is None and want_a):
+        import torch
+
+        cap, width, dev = grad_a.shape[0], grad_a.shape[1], grad_a.device
+        if grad_h is None:
+            grad_h, = _outputs(stream, dev, ((cap, 2 * width), torch.bfloat16))
+        if a is None and want_a:
+            a, = _outputs(stream, dev, ((cap, width), torch.bfloat16))
+    st = _calls.act_backward(grad_a, h_q, h_scale, expert_start, expert_end, num_rows, grad_h, a,
+                             stream if stream is None else stream.cuda_stream)
+    if st:
+        _done(st, "act_backward")
+    return grad_h, a

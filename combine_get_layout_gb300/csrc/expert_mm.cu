@@ -1,0 +1,765 @@
+// Products grouped by expert (ep_expert_mm) and their gradients
+// (ep_expert_mm_backward) on the 5th-generation tensor cores.
+//
+// With x the rows of one expert (its segment [start, end) of the layout), W its
+// matrix [N, H] and dy the gradient by the outputs:
+//   forward   y  = x W^T      reduction over H    (gated: silu(y_g) * y_u)
+//   by rows   dx = dy W       reduction over N
+//   by W      dW = dy^T x     reduction over the segment's rows
+//
+// The first two put the weights on the product's M side (128 features a CTA)
+// and the rows on its N side: N is any multiple of 16 up to 256, so an
+// expert's ragged rows cost no more than 15 idle columns, where rows on the M
+// side would be rounded up to 128.  The accumulator then holds a feature a
+// lane and a row a column, and the epilogue transposes it through shared
+// memory.  dW is dense in both directions: 128 features of dy by 256 of x.
+//
+// One persistent CTA an SM, warps in roles: four read accumulators out, one
+// issues tensor copies (TMA), one the products, and four turn E4M3 rows into
+// bf16 operands where the rows are in 8 bits.  Operand tiles, 64 of the
+// reduction each, pass through a ring of stages in shared memory; two
+// accumulators alternate in tensor memory, so that one tile's epilogue runs
+// beside the next one's products.
+//
+// E4M3 rows enter as bf16(q * scale), one rounding (2^-9 of the value at most,
+// as rows that were never quantised have): the scale changes along the
+// reduction (every 128 inputs), so it cannot be applied to a sum.  Sums are
+// fp32 in tensor memory, rounded once on the way out.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+
+#include "../../include/ep.h"
+#include "ep_internal.h"
+#include "tcgen05.cuh"
+
+namespace ep {
+namespace {
+
+enum Mode { kForward, kByRows, kByWeights };
+
+constexpr int kLanes = 128;        // features of the M side a tile
+constexpr int kMaxCols = 256;      // columns of an accumulator
+constexpr int kDepth = 64;         // reduction a stage: 128 bytes of bf16
+constexpr int kStages = 4;
+constexpr int kABytes = kLanes * kDepth * 2;
+constexpr int kBBytes = kMaxCols * kDepth * 2;
+constexpr int kPanel = 64 * kDepth * 2;         // 64 features by 64 rows
+constexpr int kStaging = 4096;                  // bytes an epilogue warp
+constexpr int kRowGroup = 8;                    // row tiles that share weight tiles in L2
+
+constexpr int kEpilogueWarps = 4, kCopyWarp = 4, kMmaWarp = 5, kConvertWarps = 4;
+constexpr int kFirstConvertWarp = 6;
+
+struct MmParams {
+  int E, cap;
+  int M;              // features of the M side an expert (outputs when gated)
+  int depth;          // reduction (by weights: unused)
+  int cols;           // by weights: features of the N side
+  int m_tiles;
+  int n_tiles;        // by weights
+  const int32_t *start, *end;
+  __nv_bfloat16* out;
+  const uint8_t* xq;
+  const float* xs;
+  int x_width;        // features of an E4M3 row
+  int32_t* err;
+  bool add;           // by weights: to what is there
+};
+
+struct MmMaps {
+  CUtensorMap a;
+  CUtensorMap b[4];   // rows: boxes of 16, 32, 64 and 128; by weights: b[0]
+  CUtensorMap out;    // by weights
+};
+
+struct Smem {
+  uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drained;
+  uint32_t tmem;
+  int failed;
+};
+
+struct Item {
+  int e, m0;          // expert, first feature of the M side
+  int row0, rows;     // rows of the segment
+  int c0, cols;       // by weights: first feature of the N side; columns of the product
+  int blocks;         // steps of 64 along the reduction
+};
+
+// The segment of expert e, clipped to the rows that there are.
+__device__ __forceinline__ void segment(const MmParams& p, int e, int& row0, int& rows) {
+  const int s = min(max(__ldg(p.start + e), 0), p.cap);
+  rows = max(min(__ldg(p.end + e), p.cap) - s, 0);
+  row0 = s;
+}
+
+__device__ __forceinline__ int round16(int n) { return (n + 15) & ~15; }
+
+template <Mode MODE, bool GATED>
+__device__ __forceinline__ Item item_at(const MmParams& p, const int* table, int64_t idx) {
+  Item it;
+  constexpr int kFeatures = GATED ? kLanes / 2 : kLanes;
+  if (MODE == kByWeights) {
+    const int tiles = p.m_tiles * p.n_tiles;
+    it.e = int(idx / tiles);
+    const int local = int(idx - int64_t(it.e) * tiles);
+    it.m0 = local / p.n_tiles * kFeatures;
+    it.c0 = local % p.n_tiles * kMaxCols;
+    it.cols = min(kMaxCols, round16(p.cols - it.c0));
+    segment(p, it.e, it.row0, it.rows);
+    it.blocks = int((int64_t(it.rows) + kDepth - 1) / kDepth);
+    return it;
+  }
+  // the expert by its first row tile, then features outside, row tiles inside
+  const int q = int(idx / p.m_tiles);
+  int lo = 0, hi = p.E;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (table[mid] <= q)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  it.e = lo;
+  const int tiles = table[lo + 1] - table[lo];
+  int64_t local = idx - int64_t(table[lo]) * p.m_tiles;
+  const int group = int(local / (int64_t(kRowGroup) * p.m_tiles));
+  local -= int64_t(group) * kRowGroup * p.m_tiles;
+  const int in_group = min(kRowGroup, tiles - group * kRowGroup);
+  it.m0 = int(local) / in_group * kFeatures;
+  const int tile = group * kRowGroup + int(local) % in_group;
+  int row0, rows;
+  segment(p, lo, row0, rows);
+  const int per = round16(int((int64_t(rows) + tiles - 1) / tiles));
+  it.row0 = row0 + tile * per;
+  it.rows = min(per, rows - tile * per);
+  it.cols = round16(max(it.rows, 1));
+  it.c0 = 0;
+  it.blocks = (p.depth + kDepth - 1) / kDepth;
+  return it;
+}
+
+__device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
+
+// 16 E4M3 values times their scale, as bf16.
+__device__ __forceinline__ void widen16(uint4 q, float scale, uint4& lo, uint4& hi) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+  uint32_t r[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint16_t two = uint16_t(w[i / 2] >> (16 * (i % 2)));
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(two));
+    float a, b;
+    asm("{\n\t.reg .f16 l, u;\n\tmov.b32 {l, u}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, u;\n\t}"
+        : "=f"(a), "=f"(b)
+        : "r"(h));
+    r[i] = pack_bf16x2(a * scale, b * scale);
+  }
+  lo = make_uint4(r[0], r[1], r[2], r[3]);
+  hi = make_uint4(r[4], r[5], r[6], r[7]);
+}
+
+template <Mode MODE, bool FP8, bool GATED, bool OUT32>
+__global__ void __launch_bounds__(32 * (kFirstConvertWarp + (FP8 ? kConvertWarps : 0)), 1)
+    expert_mm_kernel(const __grid_constant__ MmMaps maps, const MmParams p) {
+  extern __shared__ uint8_t raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* staging = ring + kStages * (kABytes + kBBytes);
+  Smem& sm = *reinterpret_cast<Smem*>(staging + kEpilogueWarps * kStaging);
+  int* table = reinterpret_cast<int*>(&sm + 1);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  constexpr bool kAByFeature = MODE != kForward;      // inner dimension of A: features
+  constexpr bool kBByFeature = MODE == kByWeights;
+
+  if (warp == kCopyWarp && lane == 0) {
+    prefetch_map(&maps.a);
+    if (!FP8) prefetch_map(&maps.b[0]);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&sm.full[s], FP8 ? 1 + kConvertWarps : 1);
+      mbar_init(&sm.empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sm.acc_full[b], 1);
+      mbar_init(&sm.acc_empty[b], kEpilogueWarps);
+    }
+    mbar_init(&sm.drained, 1);
+    sm.failed = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) tmem_alloc(&sm.tmem, 2 * kMaxCols);
+  pdl_wait();
+  int64_t items;
+  if (MODE == kByWeights) {
+    items = int64_t(p.E) * p.m_tiles * p.n_tiles;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+  } else {
+    // row tiles of the experts before each one
+    for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
+      int row0, rows;
+      segment(p, e, row0, rows);
+      table[e + 1] = int((int64_t(rows) + kMaxCols - 1) / kMaxCols);
+    }
+    __syncthreads();
+    if (warp == 0) {
+      int64_t sum = 0;
+      for (int e0 = 0; e0 < p.E; e0 += 32) {
+        int64_t v = e0 + lane < p.E ? table[e0 + lane + 1] : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+          const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+          if (lane >= o) v += u;
+        }
+        if (e0 + lane < p.E) table[e0 + lane + 1] = int(min(sum + v, int64_t(INT32_MAX)));
+        sum += __shfl_sync(0xffffffffu, v, 31);
+      }
+      if (lane == 0) table[0] = 0;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    items = int64_t(table[p.E]) * p.m_tiles;
+  }
+  const uint32_t tmem = sm.tmem;
+
+  if (warp == kCopyWarp) {
+    if (lane == 0) {
+      uint32_t n = 0;      // stages filled so far
+      bool ok = true;
+      for (int64_t idx = blockIdx.x; ok && idx < items; idx += gridDim.x) {
+        const Item it = item_at<MODE, GATED>(p, table, idx);
+        for (int kb = 0; kb < it.blocks; ++kb, ++n) {
+          const int s = n % kStages;
+          ok = mbar_wait(&sm.empty[s], (n / kStages & 1) ^ 1, kWaitTimeoutNs);
+          if (!ok) break;
+          const uint32_t a = smem_addr(ring + s * (kABytes + kBBytes)), b = a + kABytes;
+          const uint32_t bar = smem_addr(&sm.full[s]);
+          const int k0 = kb * kDepth;
+          const int b_bytes = FP8 ? 0
+                              : kBByFeature ? (it.cols + 63) / 64 * kPanel
+                                            : it.cols * kDepth * 2;
+          mbar_arrive_expect_tx(&sm.full[s], kABytes + b_bytes);
+          if (MODE == kForward) {
+            if (GATED)
+              tma_load_5d(a, &maps.a, bar, k0, 0, 0, it.m0 / 16, it.e);
+            else
+              tma_load_3d(a, &maps.a, bar, k0, it.m0, it.e);
+          } else if (MODE == kByRows) {
+            tma_load_3d(a, &maps.a, bar, it.m0, k0, it.e);
+            tma_load_3d(a + kPanel, &maps.a, bar, it.m0 + 64, k0, it.e);
+          } else {
+            tma_load_2d(a, &maps.a, bar, it.m0, it.row0 + k0);
+            tma_load_2d(a + kPanel, &maps.a, bar, it.m0 + 64, it.row0 + k0);
+          }
+          if (FP8) continue;
+          if (kBByFeature) {
+            for (int c = 0; c < it.cols; c += 64)
+              tma_load_2d(b + c / 64 * kPanel, &maps.b[0], bar, it.c0 + c, it.row0 + k0);
+          } else {
+            // 256 = 128 + 128; else the boxes of its binary digits
+            int r = 0;
+            for (; it.cols - r >= 128; r += 128)
+              tma_load_2d(b + r * 128, &maps.b[3], bar, k0, it.row0 + r);
+#pragma unroll
+            for (int i = 2; i >= 0; --i)
+              if ((it.cols - r) & (16 << i)) {
+                tma_load_2d(b + r * 128, &maps.b[i], bar, k0, it.row0 + r);
+                r += 16 << i;
+              }
+          }
+        }
+      }
+      if (!ok) {
+        // its own copies in flight land before the CTA may end
+        bool landed = true;
+        for (uint32_t i = n < kStages ? 0 : n - kStages; i < n; ++i)
+          landed &= mbar_wait(&sm.full[i % kStages], i / kStages & 1, kWaitTimeoutNs);
+        record_error(p.err, landed ? ERRBIT_TIMEOUT : ERRBIT_TIMEOUT_PENDING);
+      }
+    }
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    uint32_t n = 0, tile = 0;
+    bool ok = true;
+    for (int64_t idx = blockIdx.x; ok && idx < items; idx += gridDim.x) {
+      const Item it = item_at<MODE, GATED>(p, table, idx);
+      if (it.blocks == 0) continue;
+      const uint32_t idesc = instr_desc(kLanes, it.cols, kAByFeature, kBByFeature);
+      const uint32_t buf = tile & 1, acc = tmem + buf * kMaxCols;
+      ok = mbar_wait(&sm.acc_empty[buf], (tile / 2 & 1) ^ 1, kWaitTimeoutNs);
+      if (!ok) break;
+      tc_fence_after();
+      for (int kb = 0; kb < it.blocks; ++kb, ++n) {
+        const int s = n % kStages;
+        ok = mbar_wait(&sm.full[s], n / kStages & 1, kWaitTimeoutNs);
+        if (!ok) break;
+        tc_fence_after();
+        uint8_t* a = ring + s * (kABytes + kBBytes);
+        int steps = kDepth / 16;
+        if (MODE == kByWeights) {
+          // rows past the segment's end are another's, or nobody's: products
+          // in steps of 16 rows, zeros up to a step's end
+          const int left = it.rows - kb * kDepth;
+          if (left < kDepth) {
+            steps = (left + 15) / 16;
+            const int panels = (FP8 ? 0 : (it.cols + 63) / 64) + 2;
+            const int pieces = (steps * 16 - left) * 8;
+            for (int i = lane; i < panels * pieces; i += 32) {
+              const int panel = i / pieces, at = i % pieces;
+              *reinterpret_cast<uint4*>(a + panel * kPanel + left * 128 + at * 16) =
+                  make_uint4(0, 0, 0, 0);
+            }
+            fence_async_shared();
+            __syncwarp();
+          }
+        }
+        if (lane == 0) {
+          const uint32_t at = smem_addr(a), bt = at + kABytes;
+          const uint64_t da = smem_desc(at, kAByFeature ? kPanel : 16, 1024);
+          const uint64_t db = smem_desc(bt, kBByFeature ? kPanel : 16, 1024);
+          // 16 of the reduction further: 32 bytes of a row, or 16 rows
+          const uint32_t as = (kAByFeature ? 2048 : 32) >> 4, bs = (kBByFeature ? 2048 : 32) >> 4;
+          for (int i = 0; i < steps; ++i)
+            mma_bf16(acc, da + i * as, db + i * bs, idesc, kb > 0 || i > 0);
+          mma_commit(smem_addr(&sm.empty[s]));
+          if (kb == it.blocks - 1) mma_commit(smem_addr(&sm.acc_full[buf]));
+        }
+        __syncwarp();
+      }
+      ++tile;
+    }
+    if (!ok) {
+      // products in flight end before the tensor memory is given back
+      if (lane == 0) {
+        mma_commit(smem_addr(&sm.drained));
+        mbar_wait(&sm.drained, 0, kWaitTimeoutNs);
+        record_error(p.err, ERRBIT_TIMEOUT);
+      }
+      __syncwarp();
+    }
+  } else if (FP8 && warp >= kFirstConvertWarp) {
+    const int t = threadIdx.x - kFirstConvertWarp * 32;
+    const int scales = p.x_width / 128;
+    uint32_t n = 0;
+    bool ok = true;
+    for (int64_t idx = blockIdx.x; ok && idx < items; idx += gridDim.x) {
+      const Item it = item_at<MODE, GATED>(p, table, idx);
+      for (int kb = 0; kb < it.blocks; ++kb, ++n) {
+        // pieces of 16 values: forward, 4 of each of the rows of this block's
+        // 64 inputs; by weights, 16 of each of its 64 rows
+        uint4 q[8];
+        float sc[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int row = kBByFeature ? t / 16 + 8 * i : t / 4 + 32 * i;
+          const int x = kBByFeature ? it.c0 + t % 16 * 16 : kb * kDepth + t % 4 * 16;
+          const int r = kBByFeature ? kb * kDepth + row : row;
+          q[i] = make_uint4(0, 0, 0, 0);
+          sc[i] = 0.0f;
+          if (r < it.rows && x < p.x_width) {
+            const int64_t at = int64_t(it.row0) + r;
+            q[i] = __ldg(reinterpret_cast<const uint4*>(p.xq + at * p.x_width + x));
+            sc[i] = __ldg(p.xs + at * scales + x / 128);
+          }
+        }
+        const int s = n % kStages;
+        ok = mbar_wait(&sm.empty[s], (n / kStages & 1) ^ 1, kWaitTimeoutNs);
+        if (!ok) break;
+        uint8_t* b = ring + s * (kABytes + kBBytes) + kABytes;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int row = kBByFeature ? t / 16 + 8 * i : t / 4 + 32 * i;
+          if (!kBByFeature && row >= it.cols) break;
+          if (kBByFeature && t % 16 * 16 >= it.cols) break;
+          uint4 lo, hi;
+          widen16(q[i], sc[i], lo, hi);
+          uint8_t* to = b + (kBByFeature ? t % 16 / 4 * kPanel : 0) + row * 128;
+          const int c = 2 * (t % 4);
+          *reinterpret_cast<uint4*>(to + ((c ^ (row & 7)) * 16)) = lo;
+          *reinterpret_cast<uint4*>(to + (((c + 1) ^ (row & 7)) * 16)) = hi;
+        }
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sm.full[s]));
+      }
+    }
+    if (!ok && lane == 0) record_error(p.err, ERRBIT_TIMEOUT);
+    __syncwarp();
+  } else if (warp < kEpilogueWarps) {
+    uint8_t* mine = staging + warp * kStaging;
+    const uint32_t mine_at = smem_addr(mine);
+    uint32_t tile = 0;
+    bool ok = true;
+    for (int64_t idx = blockIdx.x; ok && idx < items; idx += gridDim.x) {
+      const Item it = item_at<MODE, GATED>(p, table, idx);
+      const uint32_t buf = tile & 1;
+      const uint32_t acc = tmem + buf * kMaxCols + (uint32_t(warp * 32) << 16);
+      if (it.blocks > 0) {
+        // a tile's whole reduction may pass before: under 4 us a step
+        ok = mbar_wait(&sm.acc_full[buf], tile / 2 & 1,
+                       kWaitTimeoutNs + uint64_t(it.blocks) * 4000);
+        if (!ok) break;
+        tc_fence_after();
+      }
+      if (MODE == kByWeights) {
+        constexpr int kWide = OUT32 ? 32 : 64;      // columns of 128 bytes
+        for (int c = 0; c < it.cols; c += kWide) {
+          if (it.c0 + c >= p.cols || it.m0 + warp * 32 >= p.M) break;
+          uint32_t r[kWide / 32][32];
+#pragma unroll
+          for (int h = 0; h < kWide / 32; ++h) {
+            if (it.blocks > 0) {
+              tmem_load_32x32(acc + c + h * 32, r[h]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) r[h][i] = 0;
+            }
+          }
+          tmem_wait_load();
+          if (lane == 0) tma_store_wait_read<0>();
+          __syncwarp();
+#pragma unroll
+          for (int v = 0; v < 8; ++v) {
+            uint4 w;
+            if (OUT32) {
+              w = make_uint4(r[0][4 * v], r[0][4 * v + 1], r[0][4 * v + 2], r[0][4 * v + 3]);
+            } else {
+              const uint32_t* u = &r[(8 * v / 32) % (kWide / 32)][8 * v % 32];
+              w = make_uint4(pack_bf16x2(__uint_as_float(u[0]), __uint_as_float(u[1])),
+                             pack_bf16x2(__uint_as_float(u[2]), __uint_as_float(u[3])),
+                             pack_bf16x2(__uint_as_float(u[4]), __uint_as_float(u[5])),
+                             pack_bf16x2(__uint_as_float(u[6]), __uint_as_float(u[7])));
+            }
+            *reinterpret_cast<uint4*>(mine + lane * 128 + ((v ^ (lane & 7)) * 16)) = w;
+          }
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0) {
+            if (OUT32 && p.add)
+              tma_add_3d(&maps.out, mine_at, it.c0 + c, it.m0 + warp * 32, it.e);
+            else
+              tma_store_3d(&maps.out, mine_at, it.c0 + c, it.m0 + warp * 32, it.e);
+            tma_store_commit();
+          }
+        }
+      } else {
+        constexpr int kWidth = GATED ? 16 : 32;             // features of this warp
+        constexpr int kPitch = GATED ? 48 : 80;             // bytes of a staged row
+        const int m = it.m0 + warp * kWidth;
+        for (int c = 0; c < it.cols; c += 32) {
+          if (m >= p.M) break;
+          uint32_t r0[16], r1[16];
+          tmem_load_16x32(acc + c, r0);
+          tmem_load_16x32(acc + c + (16u << 16), r1);
+          tmem_wait_load();
+          // matrices of 8 features by 8 rows, transposed on the way
+          const uint32_t at = mine_at + (lane % 8 + lane / 16 * 8) * kPitch + (lane / 8 % 2) * 16;
+          if (GATED) {
+            float y[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              y[i] = silu(__uint_as_float(r0[i])) * __uint_as_float(r1[i]);
+#pragma unroll
+            for (int j = 0; j < 4; j += 2)
+              stmatrix_t4(at + j * 8 * kPitch, pack_bf16x2(y[4 * j], y[4 * j + 1]),
+                          pack_bf16x2(y[4 * j + 2], y[4 * j + 3]),
+                          pack_bf16x2(y[4 * j + 4], y[4 * j + 5]),
+                          pack_bf16x2(y[4 * j + 6], y[4 * j + 7]));
+          } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int j = 0; j < 4; j += 2) {
+                uint32_t w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  w[i] = pack_bf16x2(__uint_as_float(h ? r1[4 * j + 2 * i] : r0[4 * j + 2 * i]),
+                                     __uint_as_float(h ? r1[4 * j + 2 * i + 1]
+                                                       : r0[4 * j + 2 * i + 1]));
+                stmatrix_t4(at + j * 8 * kPitch + h * 32, w[0], w[1], w[2], w[3]);
+              }
+          }
+          __syncwarp();
+          constexpr int kVecs = kWidth / 8;                 // 16-byte pieces of a row
+#pragma unroll
+          for (int i = 0; i < kVecs; ++i) {
+            const int row = lane / kVecs + i * (32 / kVecs), v = lane % kVecs;
+            if (c + row < it.rows && m + v * 8 < p.M) {
+              const uint4 w = *reinterpret_cast<const uint4*>(mine + row * kPitch + v * 16);
+              *reinterpret_cast<uint4*>(p.out + (int64_t(it.row0) + c + row) * p.M + m + v * 8) = w;
+            }
+          }
+          __syncwarp();
+        }
+      }
+      if (it.blocks > 0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sm.acc_empty[buf]));
+        ++tile;
+      }
+    }
+    if (MODE == kByWeights && lane == 0) tma_store_wait<0>();
+    if (!ok && lane == 0) record_error(p.err, ERRBIT_TIMEOUT);
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMmaWarp) tmem_free(tmem, 2 * kMaxCols);
+}
+
+// ---- host ---------------------------------------------------------------------
+
+bool aligned(const void* p) { return p != nullptr && reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+bool config_ok(const ep_expert_config* c) {
+  if (c == nullptr || c->num_experts < 1 || c->num_experts > 2048) return false;
+  if (c->in_features < 8 || c->in_features > (1 << 20) || c->in_features % 8 != 0) return false;
+  if (c->out_features < 8 || c->out_features > (1 << 20) || c->out_features % 8 != 0) return false;
+  if (c->x_fp8 != 0 && c->x_fp8 != 1) return false;
+  if (c->gated != 0 && c->gated != 1) return false;
+  if (c->x_fp8 && c->in_features % 128 != 0) return false;
+  if (c->gated && c->out_features % 32 != 0) return false;
+  // strides of the tensor copies
+  return int64_t(c->in_features) * c->out_features < (int64_t(1) << 38);
+}
+
+int32_t status(cudaError_t e) { return note_cuda(e) == cudaSuccess ? EP_OK : EP_ERR_CUDA; }
+
+using EncodeFn = decltype(&cuTensorMapEncodeTiled);
+
+cudaError_t encoder(EncodeFn* fn) {
+  static std::atomic<EncodeFn> found{nullptr};
+  *fn = found.load(std::memory_order_acquire);
+  if (*fn != nullptr) return cudaSuccess;
+  void* at = nullptr;
+  cudaDriverEntryPointQueryResult how;
+  const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &at, 12000,
+                                                         cudaEnableDefault, &how);
+  if (e != cudaSuccess) return e;
+  if (how != cudaDriverEntryPointSuccess || at == nullptr) return cudaErrorNotSupported;
+  *fn = reinterpret_cast<EncodeFn>(at);
+  found.store(*fn, std::memory_order_release);
+  return cudaSuccess;
+}
+
+// A map of bf16 (or fp32) values, innermost dimension first, boxes of 128
+// bytes by `box`; strides in elements, of all dimensions but the first.
+template <int D>
+cudaError_t encode(CUtensorMap* m, bool f32, const void* base, const uint64_t (&dims)[D],
+                   const uint64_t (&strides)[D - 1], const uint32_t (&box)[D]) {
+  EncodeFn fn;
+  cudaError_t e = encoder(&fn);
+  if (e != cudaSuccess) return e;
+  cuuint64_t n[D], s[D - 1];
+  cuuint32_t b[D], step[D];
+  for (int i = 0; i < D; ++i) {
+    n[i] = dims[i];
+    b[i] = box[i];
+    step[i] = 1;
+    if (i > 0) s[i - 1] = strides[i - 1] * (f32 ? 4 : 2);
+  }
+  const CUresult r = fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                        D, const_cast<void*>(base), n, s, b, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// [rows, width] in boxes of 64 columns by `high` rows.
+cudaError_t encode_rows(CUtensorMap* m, const void* base, int rows, int width, int high) {
+  return encode<2>(m, false, base, {uint64_t(width), uint64_t(rows)}, {uint64_t(width)},
+                   {64, uint32_t(high)});
+}
+
+// [E, N, H] in boxes of 128 bytes by `high` rows.
+cudaError_t encode_weights(CUtensorMap* m, bool f32, const void* base, int E, int N, int H,
+                           int high) {
+  return encode<3>(m, f32, base, {uint64_t(H), uint64_t(N), uint64_t(E)},
+                   {uint64_t(H), uint64_t(N) * H}, {f32 ? 32u : 64u, uint32_t(high), 1});
+}
+
+size_t smem_bytes(int table) {
+  return 1024 + kStages * (kABytes + kBBytes) + kEpilogueWarps * kStaging + sizeof(Smem) +
+         sizeof(int) * table;
+}
+
+template <Mode MODE, bool FP8, bool GATED, bool OUT32>
+cudaError_t launch(const MmMaps& maps, const MmParams& p, int64_t most_items, cudaStream_t s) {
+  auto* kernel = expert_mm_kernel<MODE, FP8, GATED, OUT32>;
+  // once per kernel and device: the limit for any number of experts
+  static std::atomic<uint64_t> raised{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !(raised.load(std::memory_order_acquire) >> dev & 1)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             int(smem_bytes(2049)));
+    if (e != cudaSuccess) return e;
+    if (dev < 64) raised.fetch_or(uint64_t(1) << dev, std::memory_order_release);
+  }
+  const int sms = device_info().sm_count;
+  const int grid = int(most_items < sms ? most_items : sms);
+  return launch_pdl(kernel, dim3(grid), dim3(32 * (kFirstConvertWarp + (FP8 ? kConvertWarps : 0))),
+                    smem_bytes(MODE == kByWeights ? 0 : p.E + 1), s, maps, p);
+}
+
+// Tiles that `rows` rows of E experts can make, at most, by feature tiles.
+int64_t most_row_tiles(int rows, int E) {
+  return int64_t(rows) / kMaxCols + (rows < E ? rows : E);
+}
+
+MmParams params(const ep_expert_config* cfg, int cap, const int32_t* start, const int32_t* end,
+                int32_t* err) {
+  MmParams p = {};
+  p.E = cfg->num_experts;
+  p.cap = cap;
+  p.start = start;
+  p.end = end;
+  p.err = err;
+  return p;
+}
+
+cudaError_t forward(const ep_expert_config* c, int cap, int num_rows, const void* x,
+                    const float* x_scale, const void* w, const int32_t* start, const int32_t* end,
+                    void* out, int32_t* err, cudaStream_t s) {
+  MmParams p = params(c, cap, start, end, err);
+  const int H = c->in_features, N = c->out_features, I = N / 2;
+  const int features = c->gated ? kLanes / 2 : kLanes;
+  p.M = c->gated ? I : N;
+  p.depth = H;
+  p.m_tiles = (p.M + features - 1) / features;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  MmMaps maps;
+  cudaError_t e;
+  if (c->gated) {
+    // 16 gate rows, the 16 up rows that belong to them, and so on: an epilogue
+    // warp finds both in its lanes
+    e = encode<5>(&maps.a, false, w,
+                  {uint64_t(H), 16, 2, uint64_t(I / 16), uint64_t(c->num_experts)},
+                  {uint64_t(H), uint64_t(I) * H, uint64_t(16) * H, uint64_t(N) * H},
+                  {64, 16, 2, 4, 1});
+  } else {
+    e = encode_weights(&maps.a, false, w, c->num_experts, N, H, kLanes);
+  }
+  if (c->x_fp8) {
+    p.xq = static_cast<const uint8_t*>(x);
+    p.xs = x_scale;
+    p.x_width = H;
+  } else {
+    for (int i = 0; i < 4 && e == cudaSuccess; ++i)
+      e = encode_rows(&maps.b[i], x, cap, H, 16 << i);
+  }
+  if (e != cudaSuccess) return e;
+  const int64_t items = most_row_tiles(num_rows, p.E) * p.m_tiles;
+  if (c->gated)
+    return c->x_fp8 ? launch<kForward, true, true, false>(maps, p, items, s)
+                    : launch<kForward, false, true, false>(maps, p, items, s);
+  return c->x_fp8 ? launch<kForward, true, false, false>(maps, p, items, s)
+                  : launch<kForward, false, false, false>(maps, p, items, s);
+}
+
+cudaError_t by_rows(const ep_expert_config* c, int cap, int num_rows, const void* dy,
+                    const void* w, const int32_t* start, const int32_t* end, void* dx,
+                    int32_t* err, cudaStream_t s) {
+  MmParams p = params(c, cap, start, end, err);
+  p.M = c->in_features;
+  p.depth = c->out_features;
+  p.m_tiles = (p.M + kLanes - 1) / kLanes;
+  p.out = static_cast<__nv_bfloat16*>(dx);
+  MmMaps maps;
+  cudaError_t e = encode_weights(&maps.a, false, w, c->num_experts, c->out_features,
+                                 c->in_features, kDepth);
+  for (int i = 0; i < 4 && e == cudaSuccess; ++i)
+    e = encode_rows(&maps.b[i], dy, cap, c->out_features, 16 << i);
+  if (e != cudaSuccess) return e;
+  return launch<kByRows, false, false, false>(maps, p, most_row_tiles(num_rows, p.E) * p.m_tiles,
+                                              s);
+}
+
+cudaError_t by_weights(const ep_expert_config* c, int cap, const void* dy, const void* x,
+                       const float* x_scale, const int32_t* start, const int32_t* end, void* dw,
+                       int type, int32_t* err, cudaStream_t s) {
+  MmParams p = params(c, cap, start, end, err);
+  const bool f32 = type != EP_GRAD_BF16;
+  p.M = c->out_features;
+  p.cols = c->in_features;
+  p.m_tiles = (p.M + kLanes - 1) / kLanes;
+  p.n_tiles = (p.cols + kMaxCols - 1) / kMaxCols;
+  p.add = type == EP_GRAD_FP32_ADD;
+  const int64_t size = int64_t(p.E) * p.M * p.cols * (f32 ? 4 : 2);
+  if (cap == 0) return p.add ? cudaSuccess : cudaMemsetAsync(dw, 0, size, s);
+  MmMaps maps;
+  cudaError_t e = encode_rows(&maps.a, dy, cap, p.M, kDepth);
+  if (e == cudaSuccess) e = encode_weights(&maps.out, f32, dw, p.E, p.M, p.cols, 32);
+  if (c->x_fp8) {
+    p.xq = static_cast<const uint8_t*>(x);
+    p.xs = x_scale;
+    p.x_width = p.cols;
+  } else if (e == cudaSuccess) {
+    e = encode_rows(&maps.b[0], x, cap, p.cols, kDepth);
+  }
+  if (e != cudaSuccess) return e;
+  const int64_t items = int64_t(p.E) * p.m_tiles * p.n_tiles;
+  if (f32)
+    return c->x_fp8 ? launch<kByWeights, true, false, true>(maps, p, items, s)
+                    : launch<kByWeights, false, false, true>(maps, p, items, s);
+  return c->x_fp8 ? launch<kByWeights, true, false, false>(maps, p, items, s)
+                  : launch<kByWeights, false, false, false>(maps, p, items, s);
+}
+
+}  // namespace
+}  // namespace ep
+
+using namespace ep;
+
+extern "C" {
+
+int32_t ep_expert_mm(const ep_expert_config* cfg, int32_t cap, int32_t num_rows, const void* d_x,
+                     const float* d_x_scale, const void* d_w, const int32_t* d_expert_start,
+                     const int32_t* d_expert_end, void* d_out, int32_t* d_err, void* stream) {
+  if (!config_ok(cfg) || cap < 0 || num_rows < 0) return EP_ERR_INVALID_ARG;
+  if (!aligned(d_w) || !aligned(d_expert_start) || !aligned(d_expert_end))
+    return EP_ERR_INVALID_ARG;
+  if (d_err != nullptr && !aligned(d_err)) return EP_ERR_INVALID_ARG;
+  if (cap > 0 && (!aligned(d_x) || !aligned(d_out))) return EP_ERR_INVALID_ARG;
+  if (cfg->x_fp8 ? cap > 0 && !aligned(d_x_scale) : d_x_scale != nullptr)
+    return EP_ERR_INVALID_ARG;
+  if (cap == 0 || num_rows == 0) return EP_OK;
+  return status(forward(cfg, cap, num_rows, d_x, d_x_scale, d_w, d_expert_start, d_expert_end,
+                        d_out, d_err, static_cast<cudaStream_t>(stream)));
+}
+
+int32_t ep_expert_mm_backward(const ep_expert_config* cfg, int32_t cap, int32_t num_rows,
+                              const void* d_grad_out, const void* d_w, const void* d_x,
+                              const float* d_x_scale, const int32_t* d_expert_start,
+                              const int32_t* d_expert_end, void* d_grad_x, void* d_grad_w,
+                              int32_t grad_w_type, int32_t* d_err, void* stream) {
+  if (!config_ok(cfg) || cfg->gated || cap < 0 || num_rows < 0) return EP_ERR_INVALID_ARG;
+  if (!aligned(d_expert_start) || !aligned(d_expert_end)) return EP_ERR_INVALID_ARG;
+  if (d_err != nullptr && !aligned(d_err)) return EP_ERR_INVALID_ARG;
+  if (cap > 0 && !aligned(d_grad_out)) return EP_ERR_INVALID_ARG;
+  if (d_grad_x == nullptr && d_grad_w == nullptr) return EP_ERR_INVALID_ARG;
+  if (d_grad_x != nullptr && (!aligned(d_grad_x) || !aligned(d_w))) return EP_ERR_INVALID_ARG;
+  if (grad_w_type < EP_GRAD_BF16 || grad_w_type > EP_GRAD_FP32_ADD) return EP_ERR_INVALID_ARG;
+  if (d_grad_w != nullptr) {
+    if (!aligned(d_grad_w) || (cap > 0 && !aligned(d_x))) return EP_ERR_INVALID_ARG;
+    if (cfg->x_fp8 ? cap > 0 && !aligned(d_x_scale) : d_x_scale != nullptr)
+      return EP_ERR_INVALID_ARG;
+  }
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+  if (d_grad_x != nullptr && cap > 0 && num_rows > 0)
+    e = by_rows(cfg, cap, num_rows, d_grad_out, d_w, d_expert_start, d_expert_end, d_grad_x, d_err,
+                s);
+  if (e == cudaSuccess && d_grad_w != nullptr)
+    e = by_weights(cfg, cap, d_grad_out, d_x, d_x_scale, d_expert_start, d_expert_end, d_grad_w,
+                   grad_w_type, d_err, s);
+  return status(e);
+}
+
+}  // extern "C"

@@ -221,6 +221,12 @@ PyObject* route_backward(PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// A layout's segments: int32, at least E entries.
+bool segments_of(const Arg& s, int64_t E) {
+  return s.here() && s.t->scalar_type() == ScalarType::Int && s.t->is_contiguous() &&
+         s.t->dim() == 1 && s.t->size(0) >= E;
+}
+
 // expert_w4(config, x, codes, scales, start, end, num_rows, zeros, x_scale,
 // out, stream)
 PyObject* expert_w4(PyObject* const* a, Py_ssize_t n) {
@@ -235,14 +241,10 @@ PyObject* expert_w4(PyObject* const* a, Py_ssize_t n) {
   const int64_t N = cfg->gated ? cfg->out_features / 2 : cfg->out_features;
   if (x.t == nullptr || x.t->dim() != 2) return unfit();
   const int64_t cap = x.t->size(0);
-  const auto segments = [E](const Arg& s) {
-    return s.here() && s.t->scalar_type() == ScalarType::Int && s.t->is_contiguous() &&
-           s.t->dim() == 1 && s.t->size(0) >= E;
-  };
   if (cap > INT32_MAX || num_rows > INT32_MAX || num_rows < INT32_MIN ||
       !x.is(cfg->x_fp8 ? ScalarType::Byte : ScalarType::BFloat16, {cap, H}) ||
       !x_scale.is_or_absent(ScalarType::Float, {cap, H / 128}) ||
-      !out.is(ScalarType::BFloat16, {cap, N}) || !segments(start) || !segments(end) ||
+      !out.is(ScalarType::BFloat16, {cap, N}) || !segments_of(start, E) || !segments_of(end, E) ||
       !codes.holds(ep_w4_codes_bytes(cfg)) || !scales.holds(ep_w4_scales_bytes(cfg)) ||
       scales.t->scalar_type() != ScalarType::BFloat16 || !zeros.fits ||
       (zeros.t != nullptr && !zeros.holds(ep_w4_zeros_bytes(cfg))) ||
@@ -258,13 +260,142 @@ PyObject* expert_w4(PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// A layout's error word, or absent.
+bool error_word(const Arg& err) {
+  return err.fits &&
+         (err.t == nullptr || (err.holds(4) && err.t->scalar_type() == ScalarType::Int));
+}
+
+// A number of rows that a 32-bit argument holds.
+bool rows_of(PyObject* o, long long* rows) {
+  *rows = PyLong_AsLongLong(o);
+  return !(*rows == -1 && PyErr_Occurred());
+}
+
+bool in_32_bits(long long n) { return n <= INT32_MAX && n >= INT32_MIN; }
+
+// expert_mm(config, x, w, start, end, num_rows, x_scale, out, err, stream)
+PyObject* expert_mm(PyObject* const* a, Py_ssize_t n) {
+  if (!arity(n, 10)) return nullptr;
+  const auto* cfg = static_cast<const ep_expert_config*>(PyLong_AsVoidPtr(a[0]));
+  if (cfg == nullptr) return nullptr;
+  const Arg x(a[1]), w(a[2]), start(a[3]), end(a[4]), x_scale(a[6]), out(a[7]), err(a[8]);
+  long long num_rows;
+  if (!rows_of(a[5], &num_rows)) return nullptr;
+  const int64_t E = cfg->num_experts, H = cfg->in_features, N = cfg->out_features;
+  if (x.t == nullptr || x.t->dim() != 2) return unfit();
+  const int64_t cap = x.t->size(0);
+  if (cap > INT32_MAX || !in_32_bits(num_rows) ||
+      !x.is(cfg->x_fp8 ? ScalarType::Byte : ScalarType::BFloat16, {cap, H}) ||
+      !x_scale.is_or_absent(ScalarType::Float, {cap, H / 128}) ||
+      !w.is(ScalarType::BFloat16, {E, N, H}) ||
+      !out.is(ScalarType::BFloat16, {cap, cfg->gated ? N / 2 : N}) || !segments_of(start, E) ||
+      !segments_of(end, E) || !error_word(err) ||
+      !on_current_gpu({&x, &w, &start, &end, &x_scale, &out, &err}))
+    return unfit();
+  void* stream;
+  if (!stream_of(a[9], &stream)) return nullptr;
+  return status_of([&] {
+    return ep_expert_mm(cfg, int32_t(cap), int32_t(num_rows), x.ptr<void>(), x_scale.ptr<float>(),
+                        w.ptr<void>(), start.ptr<int32_t>(), end.ptr<int32_t>(), out.ptr<void>(),
+                        err.ptr<int32_t>(), stream);
+  });
+}
+
+// expert_mm_backward(config, grad_out, start, end, num_rows, w, x, x_scale,
+// grad_x, grad_w, accumulate, err, stream)
+PyObject* expert_mm_backward(PyObject* const* a, Py_ssize_t n) {
+  if (!arity(n, 13)) return nullptr;
+  const auto* cfg = static_cast<const ep_expert_config*>(PyLong_AsVoidPtr(a[0]));
+  if (cfg == nullptr) return nullptr;
+  const Arg dy(a[1]), start(a[2]), end(a[3]), w(a[5]), x(a[6]), x_scale(a[7]), dx(a[8]), dw(a[9]),
+      err(a[11]);
+  long long num_rows;
+  if (!rows_of(a[4], &num_rows)) return nullptr;
+  const int64_t E = cfg->num_experts, H = cfg->in_features, N = cfg->out_features;
+  if (dy.t == nullptr || dy.t->dim() != 2) return unfit();
+  const int64_t cap = dy.t->size(0);
+  const bool f32 = dw.t != nullptr && dw.t->scalar_type() == ScalarType::Float;
+  const bool add = a[10] == Py_True;
+  if (cap > INT32_MAX || !in_32_bits(num_rows) || !dy.is(ScalarType::BFloat16, {cap, N}) ||
+      !w.is_or_absent(ScalarType::BFloat16, {E, N, H}) ||
+      !x.is_or_absent(cfg->x_fp8 ? ScalarType::Byte : ScalarType::BFloat16, {cap, H}) ||
+      !x_scale.is_or_absent(ScalarType::Float, {cap, H / 128}) ||
+      !dx.is_or_absent(ScalarType::BFloat16, {cap, H}) ||
+      !dw.is_or_absent(f32 ? ScalarType::Float : ScalarType::BFloat16, {E, N, H}) ||
+      (w.t == nullptr) != (dx.t == nullptr) || (x.t == nullptr) != (dw.t == nullptr) ||
+      (add && !f32) || !segments_of(start, E) || !segments_of(end, E) || !error_word(err) ||
+      !on_current_gpu({&dy, &start, &end, &w, &x, &x_scale, &dx, &dw, &err}))
+    return unfit();
+  void* stream;
+  if (!stream_of(a[12], &stream)) return nullptr;
+  return status_of([&] {
+    return ep_expert_mm_backward(cfg, int32_t(cap), int32_t(num_rows), dy.ptr<void>(),
+                                 w.ptr<void>(), x.ptr<void>(), x_scale.ptr<float>(),
+                                 start.ptr<int32_t>(), end.ptr<int32_t>(), dx.ptr<void>(),
+                                 dw.ptr<void>(),
+                                 add ? EP_GRAD_FP32_ADD : f32 ? EP_GRAD_FP32 : EP_GRAD_BF16,
+                                 err.ptr<int32_t>(), stream);
+  });
+}
+
+// act_save(h, start, end, num_rows, a, q, scale, stream)
+PyObject* act_save(PyObject* const* v, Py_ssize_t n) {
+  if (!arity(n, 8)) return nullptr;
+  const Arg h(v[0]), start(v[1]), end(v[2]), a(v[4]), q(v[5]), scale(v[6]);
+  long long num_rows;
+  if (!rows_of(v[3], &num_rows)) return nullptr;
+  if (h.t == nullptr || h.t->dim() != 2 || end.t == nullptr || end.t->dim() != 1) return unfit();
+  const int64_t cap = h.t->size(0), I = h.t->size(1) / 2, E = end.t->size(0);
+  if (cap > INT32_MAX || E > INT32_MAX || I > INT32_MAX || !in_32_bits(num_rows) ||
+      !h.is(ScalarType::BFloat16, {cap, 2 * I}) || !a.is(ScalarType::BFloat16, {cap, I}) ||
+      !q.is(ScalarType::Byte, {cap, 2 * I}) ||
+      !scale.is(ScalarType::Float, {cap, 2 * ((I + 127) / 128)}) || !segments_of(start, E) ||
+      !segments_of(end, E) || !on_current_gpu({&h, &start, &end, &a, &q, &scale}))
+    return unfit();
+  void* stream;
+  if (!stream_of(v[7], &stream)) return nullptr;
+  return status_of([&] {
+    return ep_act_save(int32_t(E), int32_t(I), int32_t(cap), int32_t(num_rows), h.ptr<void>(),
+                       start.ptr<int32_t>(), end.ptr<int32_t>(), a.ptr<void>(), q.ptr<uint8_t>(),
+                       scale.ptr<float>(), stream);
+  });
+}
+
+// act_backward(grad_a, q, scale, start, end, num_rows, grad_h, a, stream)
+PyObject* act_backward(PyObject* const* v, Py_ssize_t n) {
+  if (!arity(n, 9)) return nullptr;
+  const Arg da(v[0]), q(v[1]), scale(v[2]), start(v[3]), end(v[4]), dh(v[6]), a(v[7]);
+  long long num_rows;
+  if (!rows_of(v[5], &num_rows)) return nullptr;
+  if (da.t == nullptr || da.t->dim() != 2 || end.t == nullptr || end.t->dim() != 1)
+    return unfit();
+  const int64_t cap = da.t->size(0), I = da.t->size(1), E = end.t->size(0);
+  if (cap > INT32_MAX || E > INT32_MAX || I > INT32_MAX || !in_32_bits(num_rows) ||
+      !da.is(ScalarType::BFloat16, {cap, I}) || !q.is(ScalarType::Byte, {cap, 2 * I}) ||
+      !scale.is(ScalarType::Float, {cap, 2 * ((I + 127) / 128)}) ||
+      !dh.is(ScalarType::BFloat16, {cap, 2 * I}) ||
+      !a.is_or_absent(ScalarType::BFloat16, {cap, I}) || !segments_of(start, E) ||
+      !segments_of(end, E) || !on_current_gpu({&da, &q, &scale, &start, &end, &dh, &a}))
+    return unfit();
+  void* stream;
+  if (!stream_of(v[8], &stream)) return nullptr;
+  return status_of([&] {
+    return ep_act_backward(int32_t(E), int32_t(I), int32_t(cap), int32_t(num_rows),
+                           da.ptr<void>(), q.ptr<uint8_t>(), scale.ptr<float>(),
+                           start.ptr<int32_t>(), end.ptr<int32_t>(), dh.ptr<void>(),
+                           a.ptr<void>(), stream);
+  });
+}
+
 #define EP_CALL(f)                                                                      \
   {                                                                                     \
     #f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(guarded<f>)),        \
         METH_FASTCALL, nullptr                                                          \
   }
 PyMethodDef methods[] = {EP_CALL(route), EP_CALL(route_balance), EP_CALL(route_backward),
-                         EP_CALL(expert_w4), {nullptr, nullptr, 0, nullptr}};
+                         EP_CALL(expert_w4), EP_CALL(expert_mm), EP_CALL(expert_mm_backward),
+                         EP_CALL(act_save), EP_CALL(act_backward), {nullptr, nullptr, 0, nullptr}};
 #undef EP_CALL
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "ep_torch_calls", nullptr, -1, methods,

@@ -16,6 +16,10 @@
  *                                          gradient: ep_route_balance,
  *                                          ep_route_backward)
  *   ep_expert_w4  : expert-major rows   -> rows times 4-bit expert weights
+ *   ep_expert_mm  : expert-major rows   -> rows times bf16 expert weights
+ *                                          (gradients: ep_expert_mm_backward)
+ *   ep_act_save   : gate and up values  -> gated activation, its input kept
+ *                                          in 8 bits for ep_act_backward
  *
  * Sources (page title, section):
  *  "GPU Microarchitecture: DeepEP from First Principles" -- 1.1 and 1.2
@@ -675,6 +679,98 @@ EP_API int32_t ep_expert_w4(const ep_w4_config *cfg, int32_t cap, int32_t num_ro
                             const void *d_scales, const uint8_t *d_zeros,
                             const int32_t *d_expert_start, const int32_t *d_expert_end,
                             void *d_out, void *stream);
+
+/* ---- Experts' products with bf16 weights -------------------------------------
+ * y_r = W_e x_r for the rows r of every expert e, between ep_dispatch and
+ * ep_combine, with W_e [N, H] in bf16, and the gradients by the rows and by
+ * the weights: for prompts, training, and decode with unquantised weights.
+ * Any number of rows an expert, none among them.  Sums are fp32, rounded once
+ * at the end; E4M3 rows enter as bf16(value * scale).  The same call gives the
+ * same bits. */
+typedef struct {
+  int32_t num_experts;   /* E in [1, 2048]                                   */
+  int32_t in_features;   /* H: a multiple of 8 (of 128 when x_fp8), <= 2^20  */
+  int32_t out_features;  /* N: a multiple of 8 (of 32 when gated), <= 2^20;
+                            H * N < 2^38                                     */
+  int32_t x_fp8;         /* 0: bf16 rows; 1: E4M3 rows with 1x128 fp32 scales */
+  int32_t gated;         /* 1: W_e stacks gate and up, y = silu(gate) * up   */
+} ep_expert_config;
+
+/* The product.  cap: rows that d_x and d_out hold.  num_rows: how many rows
+ * the experts have together, at most (T * K of the layout's call; it sizes
+ * the launch, and more rows are still computed; 0 launches nothing).
+ * d_x: device [cap, H] bf16, or E4M3 bytes with d_x_scale (device fp32
+ *   [cap, H / 128]), as ep_dispatch writes them.
+ * d_w: device bf16 [E, N, H]; when gated, rows [0, N/2) are the gate's and
+ *   rows [N/2, N) the up matrix's.
+ * d_expert_start, d_expert_end: device int32 [E] at least, a layout's: expert
+ *   e owns rows [start[e], end[e]), clipped to [0, cap); none when empty.
+ * d_out: device bf16 [cap, N] ([cap, N/2] when gated); rows of no expert
+ *   are not written.
+ * d_err: a layout's error word (device int32), or NULL: a wait inside the
+ *   kernel that gave up is recorded there (EP_ERR_TIMEOUT by
+ *   ep_check_error; the outputs are then undefined).
+ * A value of x that is not finite shows in its own row alone.  Returns EP_OK
+ * or an error. */
+EP_API int32_t ep_expert_mm(const ep_expert_config *cfg, int32_t cap, int32_t num_rows,
+                            const void *d_x, const float *d_x_scale, const void *d_w,
+                            const int32_t *d_expert_start, const int32_t *d_expert_end,
+                            void *d_out, int32_t *d_err, void *stream);
+
+/* Types of the weights' gradient. */
+#define EP_GRAD_BF16 0
+#define EP_GRAD_FP32 1
+#define EP_GRAD_FP32_ADD 2   /* added to what d_grad_w holds */
+
+/* Gradients of ep_expert_mm (gated = 0; ep_act_backward is the gated
+ * activation's) for d_grad_out, device bf16 [cap, N].  Either or both:
+ * d_grad_x: device bf16 [cap, H] or NULL: grad_out_r W_e, of every row of an
+ *   expert (rows of no expert are not written); needs d_w.
+ * d_grad_w: device [E, N, H] of grad_w_type or NULL: the sum over expert e's
+ *   rows of grad_out_r x_r^T, 0 for an expert without rows (with
+ *   EP_GRAD_FP32_ADD: what it holds stays); needs the rows d_x (and
+ *   d_x_scale) of the forward call.  Rows of no expert are not read into it.
+ * num_rows sizes the launch for d_grad_x as in ep_expert_mm; d_grad_w is
+ * written whatever it is.  d_grad_x and d_grad_w overlap no input.  Returns
+ * EP_OK or an error. */
+EP_API int32_t ep_expert_mm_backward(const ep_expert_config *cfg, int32_t cap, int32_t num_rows,
+                                     const void *d_grad_out, const void *d_w, const void *d_x,
+                                     const float *d_x_scale, const int32_t *d_expert_start,
+                                     const int32_t *d_expert_end, void *d_grad_x, void *d_grad_w,
+                                     int32_t grad_w_type, int32_t *d_err, void *stream);
+
+/* ---- Gated activation with its input kept in 8 bits ----------------------------
+ * Between an expert's two products in training: a = silu(g) * u of the gate
+ * and up values h = [g, u], 2 I wide, and the checkpoint of h that the
+ * backward pass reads in place of h: E4M3 with one fp32 scale for each block
+ * of 128 columns of g and of u (scale = amax / 448, codes of value / scale to
+ * nearest even; 0 for a block of zeros), ceil(I / 128) blocks a side, the
+ * last one maybe short.  Where 128 divides I these are rows as an FP8
+ * dispatch writes them, and ep_expert_mm takes them. */
+
+/* d_h: device bf16 [cap, 2 I]; d_a: device bf16 [cap, I]; d_q: device E4M3
+ * bytes [cap, 2 I]; d_scale: device fp32 [cap, 2 ceil(I / 128)].  I (width):
+ * a multiple of 8, <= 2^19.  num_experts in [1, 2048], cap, num_rows and the
+ * segments as in ep_expert_mm; rows of no expert are not written.  d_a is
+ * computed from h itself, in fp32, rounded once.  Returns EP_OK or an
+ * error. */
+EP_API int32_t ep_act_save(int32_t num_experts, int32_t width, int32_t cap, int32_t num_rows,
+                           const void *d_h, const int32_t *d_expert_start,
+                           const int32_t *d_expert_end, void *d_a, uint8_t *d_q, float *d_scale,
+                           void *stream);
+
+/* The gradient by h at the checkpoint's values g, u, for d_grad_a (device
+ * bf16 [cap, I]), c = 1 / (1 + exp(-g)):
+ *   d_grad_h (device bf16 [cap, 2 I]) = [grad_a u c (1 + g (1 - c)),
+ *                                        grad_a g c]
+ *   d_a (device bf16 [cap, I] or NULL) = g c u, the activation again, which
+ *     the weight gradient of the product behind it needs
+ * in fp32, rounded once.  Sizes as in ep_act_save.  Returns EP_OK or an
+ * error. */
+EP_API int32_t ep_act_backward(int32_t num_experts, int32_t width, int32_t cap, int32_t num_rows,
+                               const void *d_grad_a, const uint8_t *d_q, const float *d_scale,
+                               const int32_t *d_expert_start, const int32_t *d_expert_end,
+                               void *d_grad_h, void *d_a, void *stream);
 
 /* The cudaError_t of the last CUDA runtime call of this library that failed
  * in the calling thread (0 if none since the previous query); reading it
