@@ -6,8 +6,10 @@
 // the gradient of a, and writes the gradient of h and a again.  A few
 // operations a byte: memory bounds both.
 //
-// A warp takes four blocks of g and the same four of u of one row: 8 lanes a
-// block, 16 columns a lane, so that a block's maximum is three shuffles.
+// A warp walks along a row, 256 columns of g and the same of u in a step, 8
+// adjacent columns a lane, so that every access of a warp is one contiguous
+// piece; 16 lanes hold one block of 128, whose maximum is four shuffles.  The
+// loads of a warp's next step are issued before the present one is computed.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -19,12 +21,13 @@ namespace ep {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kCtasPerSm = 4;     // 64 registers a thread
 constexpr int kBlock = 128;
-constexpr int kSpan = 512;        // columns of g a warp takes at a time
+constexpr int kStep = 256;        // columns of g a warp takes in one step
 
 struct ActParams {
   int E, I, cap;
-  int spans;                      // kSpan pieces of a row
+  int parts, part;                // a row is walked in `parts` of `part` columns
   const int32_t *start, *end;
   const uint8_t* h;               // bf16 (save)
   const uint8_t* grad_a;          // bf16 (backward)
@@ -33,7 +36,7 @@ struct ActParams {
   float* scale;
 };
 
-// Rows of the experts before each one, in shared memory: table[E + 1].
+// Rows of the experts before each one: table[E + 1] in shared memory.
 __device__ void count_rows(const ActParams& p, int* table) {
   const int lane = threadIdx.x % 32;
   for (int e = threadIdx.x; e < p.E; e += kThreads) {
@@ -58,18 +61,48 @@ __device__ void count_rows(const ActParams& p, int* table) {
   __syncthreads();
 }
 
-// The buffer row of the r-th row of all experts.
-__device__ __forceinline__ int64_t row_of(const ActParams& p, const int* table, int r) {
-  int lo = 0, hi = p.E;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (table[mid] <= r)
-      lo = mid;
-    else
-      hi = mid;
+// A warp's walk over the parts of all experts' rows, a step at a time.
+struct Walk {
+  int64_t r;             // row among the experts' rows
+  int64_t row;           // in the buffers
+  int part, col, end;    // part of it, first column of the step, end of the part
+  int e = -1;
+  int first;             // buffer row of the expert's first
+
+  __device__ __forceinline__ bool enter(const ActParams& p, const int* table) {
+    if (r >= table[p.E]) return false;
+    if (e < 0 || r < table[e] || r >= table[e + 1]) {
+      int lo = 0, hi = p.E;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (table[mid] <= r)
+          lo = mid;
+        else
+          hi = mid;
+      }
+      e = lo;
+      first = min(max(__ldg(p.start + e), 0), p.cap);
+    }
+    row = int64_t(first) + (r - table[e]);
+    col = part * p.part;
+    end = min(col + p.part, p.I);
+    return true;
   }
-  return min(max(__ldg(p.start + lo), 0), p.cap) + (r - table[lo]);
-}
+  __device__ __forceinline__ bool begin(const ActParams& p, const int* table) {
+    const int at = blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
+    r = at / p.parts;
+    part = at % p.parts;
+    return enter(p, table);
+  }
+  __device__ __forceinline__ bool next(const ActParams& p, const int* table) {
+    col += kStep;
+    if (col < end) return true;
+    const int at = part + gridDim.x * (kThreads / 32);
+    r += at / p.parts;
+    part = at % p.parts;
+    return enter(p, table);
+  }
+};
 
 __device__ __forceinline__ void unpack(uint4 v, float* f) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -102,96 +135,147 @@ __device__ __forceinline__ void unpack8(uint2 v, float scale, float* f) {
   }
 }
 
-__device__ __forceinline__ uint4 load16(const uint8_t* p, bool there) {
-  return there ? ld_stream_u4(p) : make_uint4(0, 0, 0, 0);
+// 1 / (1 + exp(-x)) by the hardware's exponential and reciprocal: within
+// (2 + |x|) 2^-22 of itself, far inside the rounding to bf16 behind it, at a
+// quarter of the instructions that expf and a division take (which bound the
+// kernels: save of 32768 rows 146 us with them).
+__device__ __forceinline__ float sigmoid(float x) {
+  float r;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.0f + __expf(-x)));
+  return r;
 }
 
-__global__ void __launch_bounds__(kThreads) act_save_kernel(const ActParams p) {
+// The larger of two pairs of magnitudes; NaN is not larger.
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// The codes of eight values f (packed: v) of a block that 16 aligned lanes
+// hold, and the block's scale: amax / 448 and the codes of the quotients as
+// in quantize_group16.  All 32 lanes call.
+__device__ __forceinline__ uint2 quantize8(uint4 v, const float* f, float* scale) {
+  constexpr uint32_t kMagnitude = 0x7fff7fff;
+  uint32_t m = max2(max2(v.x & kMagnitude, v.y & kMagnitude),
+                    max2(v.z & kMagnitude, v.w & kMagnitude));
+#pragma unroll
+  for (int o = 8; o >= 1; o >>= 1) m = max2(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float amax = fmaxf(fmaxf(bf16_lo(m), bf16_hi(m)), 0.0f);
+  *scale = 0.0f;
+  if (amax == 0.0f) return make_uint2(0, 0);
+  const float s = __fdiv_rn(amax, 448.0f);
+  *scale = s;
+  const BlockQuotient div(s);
+  uint32_t c[4];
+  if (div.fast) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      c[j] = pack_e4m3x2(scaled_quotient(f[2 * j], s, div.y),
+                         scaled_quotient(f[2 * j + 1], s, div.y));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      c[j] = pack_e4m3x2(__fdiv_rn(f[2 * j], s), __fdiv_rn(f[2 * j + 1], s));
+  }
+  return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+}
+
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) act_save_kernel(const ActParams p) {
   extern __shared__ int table[];
   pdl_wait();
   count_rows(p, table);
   const int lane = threadIdx.x % 32;
-  const int64_t items = int64_t(table[p.E]) * p.spans;
   const int blocks = (p.I + kBlock - 1) / kBlock;
-  const int64_t step = int64_t(gridDim.x) * (kThreads / 32);
-  for (int64_t i = int64_t(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32; i < items; i += step) {
-    const int r = int(i / p.spans);
-    const int c = int(i - int64_t(r) * p.spans) * kSpan + lane * 16;     // first column
-    const int64_t row = row_of(p, table, r);
-    const bool lo = c < p.I, hi = c + 8 < p.I;
-    const uint8_t* g = p.h + (row * 2 * p.I + c) * 2;
-    const uint8_t* u = g + int64_t(p.I) * 2;
-    const uint4 g0 = load16(g, lo), g1 = load16(g + 16, hi);
-    const uint4 u0 = load16(u, lo), u1 = load16(u + 16, hi);
-    float x[16], y[16];
-    unpack(g0, x);
-    unpack(g1, x + 8);
-    unpack(u0, y);
-    unpack(u1, y + 8);
+  Walk w;
+  uint4 g, u;
+  const auto load = [&] {
+    const int c = w.col + lane * 8;
+    const uint8_t* h = p.h + (w.row * 2 * p.I + c) * 2;
+    g = u = make_uint4(0, 0, 0, 0);
+    if (c < w.end) {
+      g = ld_stream_u4(h);
+      u = ld_stream_u4(h + int64_t(p.I) * 2);
+    }
+  };
+  bool there = w.begin(p, table);
+  if (there) load();
+  while (there) {
+    const uint4 gv = g, uv = u;
+    const int64_t row = w.row;
+    const int c = w.col + lane * 8;
+    const bool in = c < w.end;
+    there = w.next(p, table);
+    if (there) load();
+    float x[8], y[8], x_scale, y_scale;
+    unpack(gv, x);
+    unpack(uv, y);
+    const uint2 xq = quantize8(gv, x, &x_scale), yq = quantize8(uv, y, &y_scale);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) y[j] *= x[j] / (1.0f + expf(-x[j]));
-    uint8_t* a = p.a + (row * p.I + c) * 2;
-    if (lo) *reinterpret_cast<uint4*>(a) = pack(y);
-    if (hi) *reinterpret_cast<uint4*>(a + 16) = pack(y + 8);
-    uint4 gq, uq;
-    float gs, us;
-    quantize_group16(g0, g1, &gq, &gs);
-    quantize_group16(u0, u1, &uq, &us);
-    uint8_t* q = p.q + row * 2 * p.I + c;
-    if (lo) {
-      *reinterpret_cast<uint2*>(q) = make_uint2(gq.x, gq.y);
-      *reinterpret_cast<uint2*>(q + p.I) = make_uint2(uq.x, uq.y);
-    }
-    if (hi) {
-      *reinterpret_cast<uint2*>(q + 8) = make_uint2(gq.z, gq.w);
-      *reinterpret_cast<uint2*>(q + p.I + 8) = make_uint2(uq.z, uq.w);
-    }
-    if (lo && lane % 8 == 0) {
-      float* s = p.scale + row * 2 * blocks + c / kBlock;
-      s[0] = gs;
-      s[blocks] = us;
+    for (int j = 0; j < 8; ++j) y[j] *= x[j] * sigmoid(x[j]);
+    if (in) {
+      *reinterpret_cast<uint4*>(p.a + (row * p.I + c) * 2) = pack(y);
+      uint8_t* q = p.q + row * 2 * p.I + c;
+      *reinterpret_cast<uint2*>(q) = xq;
+      *reinterpret_cast<uint2*>(q + p.I) = yq;
+      if (lane % 16 == 0) {
+        float* s = p.scale + row * 2 * blocks + c / kBlock;
+        s[0] = x_scale;
+        s[blocks] = y_scale;
+      }
     }
   }
 }
 
-__global__ void __launch_bounds__(kThreads) act_backward_kernel(const ActParams p) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) act_backward_kernel(const ActParams p) {
   extern __shared__ int table[];
   pdl_wait();
   count_rows(p, table);
   const int lane = threadIdx.x % 32;
-  const int64_t items = int64_t(table[p.E]) * p.spans;
   const int blocks = (p.I + kBlock - 1) / kBlock;
-  const int64_t step = int64_t(gridDim.x) * (kThreads / 32);
-  for (int64_t i = int64_t(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32; i < items; i += step) {
-    const int r = int(i / p.spans);
-    const int c0 = int(i - int64_t(r) * p.spans) * kSpan;
-    const int64_t row = row_of(p, table, r);
+  Walk w;
+  uint4 d;
+  uint2 gq, uq;
+  float gs, us;
+  const auto load = [&] {
+    const int c = w.col + lane * 8;
+    if (c >= w.end) return;
+    const uint8_t* q = p.q + w.row * 2 * p.I + c;
+    const float* s = p.scale + w.row * 2 * blocks + c / kBlock;
+    d = ld_stream_u4(p.grad_a + (w.row * p.I + c) * 2);
+    gq = __ldg(reinterpret_cast<const uint2*>(q));
+    uq = __ldg(reinterpret_cast<const uint2*>(q + p.I));
+    gs = __ldg(s);
+    us = __ldg(s + blocks);
+  };
+  bool there = w.begin(p, table);
+  if (there) load();
+  while (there) {
+    float x[8], y[8], da[8], dg[8];
+    const uint4 dv = d;
+    const uint2 gv = gq, uv = uq;
+    const float g_scale = gs, u_scale = us;
+    const int64_t row = w.row;
+    const int c = w.col + lane * 8;
+    const bool in = c < w.end;
+    there = w.next(p, table);
+    if (there) load();
+    if (!in) continue;
+    unpack(dv, da);
+    unpack8(gv, g_scale, x);
+    unpack8(uv, u_scale, y);
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      // eight columns a lane
-      const int c = c0 + half * (kSpan / 2) + lane * 8;
-      if (c >= p.I) continue;
-      const uint8_t* q = p.q + row * 2 * p.I + c;
-      const float* s = p.scale + row * 2 * blocks + c / kBlock;
-      float g[8], u[8], d[8], dg[8], du[8], a[8];
-      const uint2 gq = __ldg(reinterpret_cast<const uint2*>(q));
-      const uint2 uq = __ldg(reinterpret_cast<const uint2*>(q + p.I));
-      unpack(ld_stream_u4(p.grad_a + (row * p.I + c) * 2), d);
-      unpack8(gq, __ldg(s), g);
-      unpack8(uq, __ldg(s + blocks), u);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float t = 1.0f / (1.0f + expf(-g[j]));
-        const float act = g[j] * t;
-        dg[j] = d[j] * u[j] * t * (1.0f + g[j] * (1.0f - t));
-        du[j] = d[j] * act;
-        a[j] = act * u[j];
-      }
-      uint8_t* h = p.grad_h + (row * 2 * p.I + c) * 2;
-      *reinterpret_cast<uint4*>(h) = pack(dg);
-      *reinterpret_cast<uint4*>(h + int64_t(p.I) * 2) = pack(du);
-      if (p.a != nullptr) *reinterpret_cast<uint4*>(p.a + (row * p.I + c) * 2) = pack(a);
+    for (int j = 0; j < 8; ++j) {
+      const float t = sigmoid(x[j]);
+      const float act = x[j] * t;
+      dg[j] = da[j] * y[j] * t * (1.0f + x[j] * (1.0f - t));
+      da[j] *= act;
+      y[j] *= act;
     }
+    uint8_t* h = p.grad_h + (row * 2 * p.I + c) * 2;
+    *reinterpret_cast<uint4*>(h) = pack(dg);
+    *reinterpret_cast<uint4*>(h + int64_t(p.I) * 2) = pack(da);
+    if (p.a != nullptr) *reinterpret_cast<uint4*>(p.a + (row * p.I + c) * 2) = pack(y);
   }
 }
 
@@ -202,9 +286,16 @@ bool sizes_ok(int32_t E, int32_t I, int32_t cap, int32_t num_rows) {
          num_rows >= 0;
 }
 
-int32_t launch(void (*kernel)(ActParams), const ActParams& p, int num_rows, void* stream) {
-  const int64_t items = int64_t(num_rows) * p.spans;
-  const int64_t most = int64_t(device_info().sm_count) * 8;
+int32_t launch(void (*kernel)(ActParams), ActParams p, int num_rows, void* stream) {
+  // a row a warp, or its steps spread over warps where the rows are few
+  const int64_t most = int64_t(device_info().sm_count) * kCtasPerSm;
+  const int steps = (p.I + kStep - 1) / kStep;
+  const int64_t warps = most * (kThreads / 32);
+  const int64_t wanted = (warps + num_rows - 1) / num_rows;
+  const int parts = int(wanted < steps ? wanted : steps);
+  p.part = (steps + parts - 1) / parts * kStep;
+  p.parts = (p.I + p.part - 1) / p.part;
+  const int64_t items = int64_t(num_rows) * p.parts;
   const int64_t ctas = (items + kThreads / 32 - 1) / (kThreads / 32);
   return note_cuda(launch_pdl(kernel, dim3(unsigned(ctas < most ? ctas : most)), dim3(kThreads),
                               sizeof(int) * (p.E + 1), static_cast<cudaStream_t>(stream), p)) ==
@@ -218,7 +309,6 @@ ActParams params(int32_t E, int32_t I, int32_t cap, const int32_t* start, const 
   p.E = E;
   p.I = I;
   p.cap = cap;
-  p.spans = (I + kSpan - 1) / kSpan;
   p.start = start;
   p.end = end;
   return p;

@@ -7,28 +7,40 @@
 //   by rows   dx = dy W       reduction over N
 //   by W      dW = dy^T x     reduction over the segment's rows
 //
-// The first two put the weights on the product's M side (128 features a CTA)
+// The first two put the weights on the product's M side (256 features a tile)
 // and the rows on its N side: N is any multiple of 16 up to 256, so an
 // expert's ragged rows cost no more than 15 idle columns, where rows on the M
-// side would be rounded up to 128.  The accumulator then holds a feature a
-// lane and a row a column, and the epilogue transposes it through shared
-// memory.  dW is dense in both directions: 128 features of dy by 256 of x.
+// side would be rounded up to 128 or 256.  The accumulator then holds a
+// feature a lane and a row a column, and the epilogue transposes it through
+// shared memory.  dW is dense in both directions: 256 features of dy by 256
+// of x.
 //
-// One persistent CTA an SM, warps in roles: four read accumulators out, one
-// issues tensor copies (TMA), one the products, and four turn E4M3 rows into
-// bf16 operands where the rows are in 8 bits.  Operand tiles, 64 of the
-// reduction each, pass through a ring of stages in shared memory; two
-// accumulators alternate in tensor memory, so that one tile's epilogue runs
-// beside the next one's products.
+// A pair of CTAs (cluster of two) works on a tile together: each holds half of
+// the features and half of the columns in its shared memory, so that an
+// operand byte is read from there half as often, and its half of the
+// features' accumulator.  One persistent pair on two SMs, warps in roles: four
+// read accumulators out, one issues tensor copies (TMA), one (of the first
+// CTA) the products, four turn E4M3 rows into bf16 operands where the rows are
+// in 8 bits, and one clears what a last step along the rows must not see.
+// Operand tiles, 64 of the reduction each, pass through a ring of stages in
+// shared memory, as many as fit for the columns that the experts' rows need;
+// two accumulators alternate in tensor memory, so that one tile's epilogue
+// runs beside the next one's products.
 //
-// E4M3 rows enter as bf16(q * scale), one rounding (2^-9 of the value at most,
-// as rows that were never quantised have): the scale changes along the
-// reduction (every 128 inputs), so it cannot be applied to a sum.  Sums are
-// fp32 in tensor memory, rounded once on the way out.
+// E4M3 rows: the scale changes along the reduction (every 128 inputs), so it
+// cannot be applied to a sum.  Forward, value * scale enters as two bf16
+// parts, the nearest and the rest (16 bits of it together): the first CTA's
+// columns are the first parts, the second's the rests, and the epilogue adds
+// the two sums.  That halves the rows a tile holds; the weights are what costs
+// at the sizes that prompts and decode have.  dW takes bf16(value * scale)
+// alone, one rounding of 2^-9 of the value at most, as rows have that were
+// never quantised: there the products cost, and two parts would double them.
+// Sums are fp32 in tensor memory, rounded once on the way out.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cmath>
 
 #include "../../include/ep.h"
 #include "ep_internal.h"
@@ -39,18 +51,25 @@ namespace {
 
 enum Mode { kForward, kByRows, kByWeights };
 
-constexpr int kLanes = 128;        // features of the M side a tile
+constexpr int kLanes = 128;        // features of the M side a CTA
 constexpr int kMaxCols = 256;      // columns of an accumulator
 constexpr int kDepth = 64;         // reduction a stage: 128 bytes of bf16
-constexpr int kStages = 4;
+constexpr int kMaxStages = 12;
 constexpr int kABytes = kLanes * kDepth * 2;
-constexpr int kBBytes = kMaxCols * kDepth * 2;
+constexpr int kBBytes = kMaxCols / 2 * kDepth * 2;      // a CTA's half, at most
 constexpr int kPanel = 64 * kDepth * 2;         // 64 features by 64 rows
-constexpr int kStaging = 4096;                  // bytes an epilogue warp
 constexpr int kRowGroup = 8;                    // row tiles that share weight tiles in L2
 
-constexpr int kEpilogueWarps = 4, kCopyWarp = 4, kMmaWarp = 5, kConvertWarps = 4;
-constexpr int kFirstConvertWarp = 6;
+constexpr int kEpilogueWarps = 4, kCopyWarp = 4, kMmaWarp = 5, kClearWarp = 6;
+constexpr int kFirstConvertWarp = 7, kConvertWarps = 4;
+constexpr int kPieces = 4;         // of 16 values a converting thread has in a step
+constexpr int kAhead = 4;          // steps that it loads ahead
+
+__host__ __device__ constexpr int threads_of(bool fp8) { return 32 * (kFirstConvertWarp + (fp8 ? kConvertWarps : 0)); }
+// Bytes that the epilogue's warps stage a tile's pieces in.
+__host__ __device__ constexpr int staging_of(Mode m) { return kEpilogueWarps * (m == kByWeights ? 8192 : 2560); }
+// Rows of a tile: two columns each for E4M3 rows of a forward product.
+__host__ __device__ constexpr int rows_of(bool fp8) { return fp8 ? kMaxCols / 2 : kMaxCols; }
 
 struct MmParams {
   int E, cap;
@@ -64,26 +83,33 @@ struct MmParams {
   const uint8_t* xq;
   const float* xs;
   int x_width;        // features of an E4M3 row
+  int ring_bytes;     // of the stages
   int32_t* err;
   bool add;           // by weights: to what is there
 };
 
 struct MmMaps {
   CUtensorMap a;
-  CUtensorMap b[4];   // rows: boxes of 16, 32, 64 and 128; by weights: b[0]
+  CUtensorMap b[5];   // rows: boxes of 8, 16, 32, 64 and 128; by weights: b[0]
   CUtensorMap out;    // by weights
 };
 
 struct Smem {
-  uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drained;
+  uint64_t full[kMaxStages];       // of the first CTA: both CTAs' operands are there
+  uint64_t empty[kMaxStages];      // the products have read this CTA's
+  uint64_t last[kMaxStages];       // a last step along the rows has landed here
+  uint64_t acc_full[2];
+  uint64_t acc_empty[2];           // of the first CTA: both have read it out
+  uint64_t drained;
   uint32_t tmem;
-  int failed;
+  int most;                        // rows of a tile, at most
 };
 
 struct Item {
   int e, m0;          // expert, first feature of the M side
   int row0, rows;     // rows of the segment
-  int c0, cols;       // by weights: first feature of the N side; columns of the product
+  int c0;             // by weights: first feature of the N side
+  int cols;           // columns of the product
   int blocks;         // steps of 64 along the reduction
 };
 
@@ -96,17 +122,29 @@ __device__ __forceinline__ void segment(const MmParams& p, int e, int& row0, int
 
 __device__ __forceinline__ int round16(int n) { return (n + 15) & ~15; }
 
-template <Mode MODE, bool GATED>
+// Place in the ring of stages.
+struct Ring {
+  int s = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++s == stages) {
+      s = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+template <Mode MODE, bool FP8, bool GATED>
 __device__ __forceinline__ Item item_at(const MmParams& p, const int* table, int64_t idx) {
   Item it;
-  constexpr int kFeatures = GATED ? kLanes / 2 : kLanes;
+  constexpr int kFeatures = GATED ? kLanes : 2 * kLanes;      // of a pair
   if (MODE == kByWeights) {
     const int tiles = p.m_tiles * p.n_tiles;
     it.e = int(idx / tiles);
     const int local = int(idx - int64_t(it.e) * tiles);
     it.m0 = local / p.n_tiles * kFeatures;
     it.c0 = local % p.n_tiles * kMaxCols;
-    it.cols = min(kMaxCols, round16(p.cols - it.c0));
+    it.cols = p.cols - it.c0 > kMaxCols / 2 ? kMaxCols : kMaxCols / 2;
     segment(p, it.e, it.row0, it.rows);
     it.blocks = int((int64_t(it.rows) + kDepth - 1) / kDepth);
     return it;
@@ -134,7 +172,7 @@ __device__ __forceinline__ Item item_at(const MmParams& p, const int* table, int
   const int per = round16(int((int64_t(rows) + tiles - 1) / tiles));
   it.row0 = row0 + tile * per;
   it.rows = min(per, rows - tile * per);
-  it.cols = round16(max(it.rows, 1));
+  it.cols = round16(max(it.rows, 1)) * (FP8 ? 2 : 1);
   it.c0 = 0;
   it.blocks = (p.depth + kDepth - 1) / kDepth;
   return it;
@@ -142,7 +180,8 @@ __device__ __forceinline__ Item item_at(const MmParams& p, const int* table, int
 
 __device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
 
-// 16 E4M3 values times their scale, as bf16.
+// 16 E4M3 values times their scale as bf16, or what that rounding left.
+template <bool REST>
 __device__ __forceinline__ void widen16(uint4 q, float scale, uint4& lo, uint4& hi) {
   const uint32_t w[4] = {q.x, q.y, q.z, q.w};
   uint32_t r[8];
@@ -155,54 +194,67 @@ __device__ __forceinline__ void widen16(uint4 q, float scale, uint4& lo, uint4& 
     asm("{\n\t.reg .f16 l, u;\n\tmov.b32 {l, u}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, u;\n\t}"
         : "=f"(a), "=f"(b)
         : "r"(h));
-    r[i] = pack_bf16x2(a * scale, b * scale);
+    a *= scale;
+    b *= scale;
+    r[i] = pack_bf16x2(a, b);
+    if (REST) {
+      // 0 beside an infinity, which would leave inf - inf
+      const float x = bf16_lo(r[i]), y = bf16_hi(r[i]);
+      r[i] = pack_bf16x2(fabsf(x) < INFINITY ? a - x : 0.0f, fabsf(y) < INFINITY ? b - y : 0.0f);
+    }
   }
   lo = make_uint4(r[0], r[1], r[2], r[3]);
   hi = make_uint4(r[4], r[5], r[6], r[7]);
 }
 
 template <Mode MODE, bool FP8, bool GATED, bool OUT32>
-__global__ void __launch_bounds__(32 * (kFirstConvertWarp + (FP8 ? kConvertWarps : 0)), 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
     expert_mm_kernel(const __grid_constant__ MmMaps maps, const MmParams p) {
   extern __shared__ uint8_t raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* staging = ring + kStages * (kABytes + kBBytes);
-  Smem& sm = *reinterpret_cast<Smem*>(staging + kEpilogueWarps * kStaging);
+  uint8_t* staging = ring + p.ring_bytes;
+  Smem& sm = *reinterpret_cast<Smem*>(staging + staging_of(MODE));
   int* table = reinterpret_cast<int*>(&sm + 1);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t rank = cluster_rank();
   constexpr bool kAByFeature = MODE != kForward;      // inner dimension of A: features
   constexpr bool kBByFeature = MODE == kByWeights;
+  constexpr int kRows = rows_of(FP8);
 
   if (warp == kCopyWarp && lane == 0) {
     prefetch_map(&maps.a);
     if (!FP8) prefetch_map(&maps.b[0]);
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(&sm.full[s], FP8 ? 1 + kConvertWarps : 1);
+    for (int s = 0; s < kMaxStages; ++s) {
+      mbar_init(&sm.full[s], FP8 ? 2 + 2 * kConvertWarps : 2);
       mbar_init(&sm.empty[s], 1);
+      mbar_init(&sm.last[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sm.acc_full[b], 1);
-      mbar_init(&sm.acc_empty[b], kEpilogueWarps);
+      mbar_init(&sm.acc_empty[b], 2 * kEpilogueWarps);
     }
     mbar_init(&sm.drained, 1);
-    sm.failed = 0;
+    sm.most = 0;
     fence_mbar_init();
   }
   if (warp == kMmaWarp) tmem_alloc(&sm.tmem, 2 * kMaxCols);
   pdl_wait();
   int64_t items;
+  int stage_bytes = kABytes + kBBytes;
   if (MODE == kByWeights) {
     items = int64_t(p.E) * p.m_tiles * p.n_tiles;
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
   } else {
-    // row tiles of the experts before each one
+    // row tiles of the experts before each one, and the largest tile
+    __syncthreads();
+    int most = 0;
     for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
       int row0, rows;
       segment(p, e, row0, rows);
-      table[e + 1] = int((int64_t(rows) + kMaxCols - 1) / kMaxCols);
+      table[e + 1] = int((int64_t(rows) + kRows - 1) / kRows);
+      most = max(most, min(rows, kRows));
     }
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0) atomicMax(&sm.most, most);
     __syncthreads();
     if (warp == 0) {
       int64_t sum = 0;
@@ -218,196 +270,229 @@ __global__ void __launch_bounds__(32 * (kFirstConvertWarp + (FP8 ? kConvertWarps
       }
       if (lane == 0) table[0] = 0;
     }
-    tc_fence_before();
     __syncthreads();
-    tc_fence_after();
     items = int64_t(table[p.E]) * p.m_tiles;
+    // E4M3: all rows in each CTA, else half of them; in groups of eight
+    const int rows = round16(sm.most) / (FP8 ? 1 : 2);
+    stage_bytes = kABytes + rows * (kDepth * 2);
   }
+  const int stages = min(kMaxStages, p.ring_bytes / stage_bytes);
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
   const uint32_t tmem = sm.tmem;
+  const int64_t pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+  Ring at;
 
   if (warp == kCopyWarp) {
     if (lane == 0) {
-      uint32_t n = 0;      // stages filled so far
       bool ok = true;
-      for (int64_t idx = blockIdx.x; ok && idx < items; idx += gridDim.x) {
-        const Item it = item_at<MODE, GATED>(p, table, idx);
-        for (int kb = 0; kb < it.blocks; ++kb, ++n) {
-          const int s = n % kStages;
-          ok = mbar_wait(&sm.empty[s], (n / kStages & 1) ^ 1, kWaitTimeoutNs);
+      uint64_t n = 0;      // stages filled so far
+      for (int64_t idx = pair; ok && idx < items; idx += pairs) {
+        const Item it = item_at<MODE, FP8, GATED>(p, table, idx);
+        const int half = it.cols / 2;
+        // bytes of this CTA's copies into a stage
+        const int bytes = kABytes + (FP8 ? 0 : half * kDepth * 2);
+        const int m0 = it.m0 + int(rank) * (GATED ? kLanes / 2 : kLanes);
+        const int col0 = int(rank) * half;
+        for (int kb = 0; kb < it.blocks; ++kb, ++n, at.next(stages)) {
+          ok = mbar_wait(&sm.empty[at.s], at.phase ^ 1, kWaitTimeoutNs);
           if (!ok) break;
-          const uint32_t a = smem_addr(ring + s * (kABytes + kBBytes)), b = a + kABytes;
-          const uint32_t bar = smem_addr(&sm.full[s]);
+          const uint32_t a = smem_addr(ring + at.s * stage_bytes), b = a + kABytes;
           const int k0 = kb * kDepth;
-          const int b_bytes = FP8 ? 0
-                              : kBByFeature ? (it.cols + 63) / 64 * kPanel
-                                            : it.cols * kDepth * 2;
-          mbar_arrive_expect_tx(&sm.full[s], kABytes + b_bytes);
+          uint32_t bar = at_rank(smem_addr(&sm.full[at.s]), 0);
+          if (MODE == kByWeights && it.rows - k0 < kDepth) {
+            // cleared past the segment's end before it counts as full
+            bar = smem_addr(&sm.last[at.s]);
+            mbar_arrive_expect_tx(&sm.last[at.s], bytes);
+          } else if (rank == 0) {
+            mbar_arrive_expect_tx(&sm.full[at.s], 2 * bytes);
+          } else {
+            mbar_arrive_cluster(bar);
+          }
           if (MODE == kForward) {
             if (GATED)
-              tma_load_5d(a, &maps.a, bar, k0, 0, 0, it.m0 / 16, it.e);
+              tma_load_5d(a, &maps.a, bar, k0, 0, 0, m0 / 16, it.e);
             else
-              tma_load_3d(a, &maps.a, bar, k0, it.m0, it.e);
+              tma_load_3d(a, &maps.a, bar, k0, m0, it.e);
           } else if (MODE == kByRows) {
-            tma_load_3d(a, &maps.a, bar, it.m0, k0, it.e);
-            tma_load_3d(a + kPanel, &maps.a, bar, it.m0 + 64, k0, it.e);
+            tma_load_3d(a, &maps.a, bar, m0, k0, it.e);
+            tma_load_3d(a + kPanel, &maps.a, bar, m0 + 64, k0, it.e);
           } else {
-            tma_load_2d(a, &maps.a, bar, it.m0, it.row0 + k0);
-            tma_load_2d(a + kPanel, &maps.a, bar, it.m0 + 64, it.row0 + k0);
+            tma_load_2d(a, &maps.a, bar, m0, it.row0 + k0);
+            tma_load_2d(a + kPanel, &maps.a, bar, m0 + 64, it.row0 + k0);
           }
           if (FP8) continue;
           if (kBByFeature) {
-            for (int c = 0; c < it.cols; c += 64)
-              tma_load_2d(b + c / 64 * kPanel, &maps.b[0], bar, it.c0 + c, it.row0 + k0);
+            for (int c = 0; c < half; c += 64)
+              tma_load_2d(b + c / 64 * kPanel, &maps.b[0], bar, it.c0 + col0 + c, it.row0 + k0);
           } else {
-            // 256 = 128 + 128; else the boxes of its binary digits
+            // boxes of the binary digits of the CTA's rows
             int r = 0;
-            for (; it.cols - r >= 128; r += 128)
-              tma_load_2d(b + r * 128, &maps.b[3], bar, k0, it.row0 + r);
 #pragma unroll
-            for (int i = 2; i >= 0; --i)
-              if ((it.cols - r) & (16 << i)) {
-                tma_load_2d(b + r * 128, &maps.b[i], bar, k0, it.row0 + r);
-                r += 16 << i;
+            for (int i = 4; i >= 0; --i)
+              if (half & (8 << i)) {
+                tma_load_2d(b + r * 128, &maps.b[i], bar, k0, it.row0 + col0 + r);
+                r += 8 << i;
               }
           }
         }
       }
       if (!ok) {
-        // its own copies in flight land before the CTA may end
-        bool landed = true;
-        for (uint32_t i = n < kStages ? 0 : n - kStages; i < n; ++i)
-          landed &= mbar_wait(&sm.full[i % kStages], i / kStages & 1, kWaitTimeoutNs);
-        record_error(p.err, landed ? ERRBIT_TIMEOUT : ERRBIT_TIMEOUT_PENDING);
+        record_error(p.err, ERRBIT_TIMEOUT);
+        // the first CTA's barriers count the copies of both, which land before
+        // the pair may end (the second CTA waits for the first one's end)
+        for (uint64_t i = n < uint64_t(stages) ? 0 : n - stages; rank == 0 && i < n; ++i)
+          if (!mbar_wait(&sm.full[i % stages], i / stages & 1, kWaitTimeoutNs))
+            record_error(p.err, ERRBIT_TIMEOUT_PENDING);
       }
     }
     __syncwarp();
-  } else if (warp == kMmaWarp) {
-    uint32_t n = 0, tile = 0;
-    bool ok = true;
-    for (int64_t idx = blockIdx.x; ok && idx < items; idx += gridDim.x) {
-      const Item it = item_at<MODE, GATED>(p, table, idx);
-      if (it.blocks == 0) continue;
-      const uint32_t idesc = instr_desc(kLanes, it.cols, kAByFeature, kBByFeature);
-      const uint32_t buf = tile & 1, acc = tmem + buf * kMaxCols;
-      ok = mbar_wait(&sm.acc_empty[buf], (tile / 2 & 1) ^ 1, kWaitTimeoutNs);
-      if (!ok) break;
-      tc_fence_after();
-      for (int kb = 0; kb < it.blocks; ++kb, ++n) {
-        const int s = n % kStages;
-        ok = mbar_wait(&sm.full[s], n / kStages & 1, kWaitTimeoutNs);
+  } else if (warp == kMmaWarp && rank == 0) {
+    if (lane == 0) {
+      uint32_t tile = 0;
+      bool ok = true;
+      for (int64_t idx = pair; ok && idx < items; idx += pairs) {
+        const Item it = item_at<MODE, FP8, GATED>(p, table, idx);
+        if (it.blocks == 0) continue;
+        const uint32_t idesc = instr_desc(2 * kLanes, it.cols, kAByFeature, kBByFeature);
+        const uint32_t buf = tile & 1, acc = tmem + buf * kMaxCols;
+        ok = mbar_wait(&sm.acc_empty[buf], (tile / 2 & 1) ^ 1, kWaitTimeoutNs);
         if (!ok) break;
         tc_fence_after();
-        uint8_t* a = ring + s * (kABytes + kBBytes);
-        int steps = kDepth / 16;
-        if (MODE == kByWeights) {
-          // rows past the segment's end are another's, or nobody's: products
-          // in steps of 16 rows, zeros up to a step's end
-          const int left = it.rows - kb * kDepth;
-          if (left < kDepth) {
-            steps = (left + 15) / 16;
-            const int panels = (FP8 ? 0 : (it.cols + 63) / 64) + 2;
-            const int pieces = (steps * 16 - left) * 8;
-            for (int i = lane; i < panels * pieces; i += 32) {
-              const int panel = i / pieces, at = i % pieces;
-              *reinterpret_cast<uint4*>(a + panel * kPanel + left * 128 + at * 16) =
-                  make_uint4(0, 0, 0, 0);
-            }
-            fence_async_shared();
-            __syncwarp();
-          }
-        }
-        if (lane == 0) {
-          const uint32_t at = smem_addr(a), bt = at + kABytes;
-          const uint64_t da = smem_desc(at, kAByFeature ? kPanel : 16, 1024);
-          const uint64_t db = smem_desc(bt, kBByFeature ? kPanel : 16, 1024);
+        for (int kb = 0; kb < it.blocks; ++kb, at.next(stages)) {
+          ok = mbar_wait(&sm.full[at.s], at.phase, kWaitTimeoutNs);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t a = smem_addr(ring + at.s * stage_bytes), b = a + kABytes;
+          const uint64_t da = smem_desc(a, kAByFeature ? kPanel : 16, 1024);
+          const uint64_t db = smem_desc(b, kBByFeature ? kPanel : 16, 1024);
           // 16 of the reduction further: 32 bytes of a row, or 16 rows
-          const uint32_t as = (kAByFeature ? 2048 : 32) >> 4, bs = (kBByFeature ? 2048 : 32) >> 4;
-          for (int i = 0; i < steps; ++i)
-            mma_bf16(acc, da + i * as, db + i * bs, idesc, kb > 0 || i > 0);
-          mma_commit(smem_addr(&sm.empty[s]));
-          if (kb == it.blocks - 1) mma_commit(smem_addr(&sm.acc_full[buf]));
+          constexpr uint32_t as = (kAByFeature ? 2048 : 32) >> 4, bs = (kBByFeature ? 2048 : 32) >> 4;
+          const int steps =
+              MODE == kByWeights ? min(kDepth / 16, (it.rows - kb * kDepth + 15) / 16) : kDepth / 16;
+#pragma unroll
+          for (int i = 0; i < kDepth / 16; ++i)
+            if (i < steps) mma_bf16(acc, da + i * as, db + i * bs, idesc, kb > 0 || i > 0);
+          mma_commit(smem_addr(&sm.empty[at.s]));
         }
-        __syncwarp();
+        if (ok) mma_commit(smem_addr(&sm.acc_full[buf]));
+        ++tile;
       }
-      ++tile;
-    }
-    if (!ok) {
-      // products in flight end before the tensor memory is given back
-      if (lane == 0) {
+      if (!ok) {
+        // products in flight end before the tensor memory is given back
+        record_error(p.err, ERRBIT_TIMEOUT);
         mma_commit(smem_addr(&sm.drained));
         mbar_wait(&sm.drained, 0, kWaitTimeoutNs);
-        record_error(p.err, ERRBIT_TIMEOUT);
       }
-      __syncwarp();
     }
+    __syncwarp();
+  } else if (MODE == kByWeights && warp == kClearWarp) {
+    // Rows past the segment's end are another expert's, or nobody's: products
+    // take steps of 16 rows, and this CTA's operands are zero up to a step's end.
+    bool ok = true;
+    uint32_t phases = 0;
+    for (int64_t idx = pair; ok && idx < items; idx += pairs) {
+      const Item it = item_at<MODE, FP8, GATED>(p, table, idx);
+      for (int kb = 0; kb < it.blocks; ++kb, at.next(stages)) {
+        const int left = it.rows - kb * kDepth;
+        if (left >= kDepth) continue;
+        ok = mbar_wait(&sm.last[at.s], phases >> at.s & 1, kWaitTimeoutNs);
+        if (!ok) break;
+        phases ^= 1u << at.s;
+        uint8_t* a = ring + at.s * stage_bytes;
+        const int panels = kLanes / 64 + (FP8 ? 0 : it.cols / 128);
+        const int pieces = (round16(left) - left) * 8;
+        for (int i = lane; i < panels * pieces; i += 32)
+          *reinterpret_cast<uint4*>(a + i / pieces * kPanel + left * 128 + i % pieces * 16) =
+              make_uint4(0, 0, 0, 0);
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(at_rank(smem_addr(&sm.full[at.s]), 0));
+      }
+    }
+    if (!ok && lane == 0) record_error(p.err, ERRBIT_TIMEOUT);
+    __syncwarp();
   } else if (FP8 && warp >= kFirstConvertWarp) {
     const int t = threadIdx.x - kFirstConvertWarp * 32;
     const int scales = p.x_width / 128;
-    uint32_t n = 0;
     bool ok = true;
-    for (int64_t idx = blockIdx.x; ok && idx < items; idx += gridDim.x) {
-      const Item it = item_at<MODE, GATED>(p, table, idx);
-      for (int kb = 0; kb < it.blocks; ++kb, ++n) {
-        // pieces of 16 values: forward, 4 of each of the rows of this block's
-        // 64 inputs; by weights, 16 of each of its 64 rows
-        uint4 q[8];
-        float sc[8];
+    for (int64_t idx = pair; ok && idx < items; idx += pairs) {
+      const Item it = item_at<MODE, FP8, GATED>(p, table, idx);
+      const int half = it.cols / 2;
+      // pieces of 16 values: forward, 4 of each of the rows for this step's 64
+      // inputs; by weights, 8 of each of its 64 rows
+      uint4 q[kAhead][kPieces];
+      float sc[kAhead][kPieces];
+      const auto load = [&](int kb, uint4 (&to)[kPieces], float (&scale)[kPieces]) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int row = kBByFeature ? t / 16 + 8 * i : t / 4 + 32 * i;
-          const int x = kBByFeature ? it.c0 + t % 16 * 16 : kb * kDepth + t % 4 * 16;
-          const int r = kBByFeature ? kb * kDepth + row : row;
-          q[i] = make_uint4(0, 0, 0, 0);
-          sc[i] = 0.0f;
-          if (r < it.rows && x < p.x_width) {
-            const int64_t at = int64_t(it.row0) + r;
-            q[i] = __ldg(reinterpret_cast<const uint4*>(p.xq + at * p.x_width + x));
-            sc[i] = __ldg(p.xs + at * scales + x / 128);
+        for (int i = 0; i < kPieces; ++i) {
+          const int row = kBByFeature ? kb * kDepth + t / 8 + 16 * i : t / 4 + 32 * i;
+          const int c = kBByFeature ? t % 8 * 16 : t % 4 * 16;
+          const int x = kBByFeature ? it.c0 + int(rank) * half + c : kb * kDepth + c;
+          to[i] = make_uint4(0, 0, 0, 0);
+          scale[i] = 0.0f;
+          if (row < it.rows && x < p.x_width && kb < it.blocks && c < (kBByFeature ? half : 64)) {
+            const int64_t r = int64_t(it.row0) + row;
+            to[i] = __ldg(reinterpret_cast<const uint4*>(p.xq + r * p.x_width + x));
+            scale[i] = __ldg(p.xs + r * scales + x / 128);
           }
         }
-        const int s = n % kStages;
-        ok = mbar_wait(&sm.empty[s], (n / kStages & 1) ^ 1, kWaitTimeoutNs);
-        if (!ok) break;
-        uint8_t* b = ring + s * (kABytes + kBBytes) + kABytes;
+      };
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int row = kBByFeature ? t / 16 + 8 * i : t / 4 + 32 * i;
-          if (!kBByFeature && row >= it.cols) break;
-          if (kBByFeature && t % 16 * 16 >= it.cols) break;
-          uint4 lo, hi;
-          widen16(q[i], sc[i], lo, hi);
-          uint8_t* to = b + (kBByFeature ? t % 16 / 4 * kPanel : 0) + row * 128;
-          const int c = 2 * (t % 4);
-          *reinterpret_cast<uint4*>(to + ((c ^ (row & 7)) * 16)) = lo;
-          *reinterpret_cast<uint4*>(to + (((c + 1) ^ (row & 7)) * 16)) = hi;
+      for (int d = 0; d < kAhead; ++d) load(d, q[d], sc[d]);
+      for (int kb0 = 0; ok && kb0 < it.blocks; kb0 += kAhead) {
+#pragma unroll
+        for (int d = 0; d < kAhead; ++d) {
+          if (!ok || kb0 + d >= it.blocks) break;
+          ok = mbar_wait(&sm.empty[at.s], at.phase ^ 1, kWaitTimeoutNs);
+          if (!ok) break;
+          uint8_t* b = ring + at.s * stage_bytes + kABytes;
+#pragma unroll
+          for (int i = 0; i < kPieces; ++i) {
+            const int row = kBByFeature ? t / 8 + 16 * i : t / 4 + 32 * i;
+            if (kBByFeature ? t % 8 * 16 >= half : row >= half) break;
+            uint4 lo, hi;
+            if (kBByFeature || rank == 0)
+              widen16<false>(q[d][i], sc[d][i], lo, hi);
+            else
+              widen16<true>(q[d][i], sc[d][i], lo, hi);
+            uint8_t* to = b + (kBByFeature ? t % 8 / 4 * kPanel : 0) + row * 128;
+            const int c = 2 * (t % 4);
+            *reinterpret_cast<uint4*>(to + ((c ^ (row & 7)) * 16)) = lo;
+            *reinterpret_cast<uint4*>(to + (((c + 1) ^ (row & 7)) * 16)) = hi;
+          }
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(at_rank(smem_addr(&sm.full[at.s]), 0));
+          at.next(stages);
+          load(kb0 + d + kAhead, q[d], sc[d]);
         }
-        fence_async_shared();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&sm.full[s]));
       }
     }
     if (!ok && lane == 0) record_error(p.err, ERRBIT_TIMEOUT);
     __syncwarp();
   } else if (warp < kEpilogueWarps) {
-    uint8_t* mine = staging + warp * kStaging;
-    const uint32_t mine_at = smem_addr(mine);
+    uint8_t* mine = staging + warp * (staging_of(MODE) / kEpilogueWarps);
     uint32_t tile = 0;
+    int turn = 0;
     bool ok = true;
-    for (int64_t idx = blockIdx.x; ok && idx < items; idx += gridDim.x) {
-      const Item it = item_at<MODE, GATED>(p, table, idx);
+    for (int64_t idx = pair; ok && idx < items; idx += pairs) {
+      const Item it = item_at<MODE, FP8, GATED>(p, table, idx);
       const uint32_t buf = tile & 1;
       const uint32_t acc = tmem + buf * kMaxCols + (uint32_t(warp * 32) << 16);
       if (it.blocks > 0) {
         // a tile's whole reduction may pass before: under 4 us a step
         ok = mbar_wait(&sm.acc_full[buf], tile / 2 & 1,
-                       kWaitTimeoutNs + uint64_t(it.blocks) * 4000);
+                               kWaitTimeoutNs + uint64_t(it.blocks) * 4000);
         if (!ok) break;
         tc_fence_after();
       }
       if (MODE == kByWeights) {
         constexpr int kWide = OUT32 ? 32 : 64;      // columns of 128 bytes
+        const int m = it.m0 + int(rank) * kLanes + warp * 32;
         for (int c = 0; c < it.cols; c += kWide) {
-          if (it.c0 + c >= p.cols || it.m0 + warp * 32 >= p.M) break;
+          if (it.c0 + c >= p.cols || m >= p.M) break;
           uint32_t r[kWide / 32][32];
 #pragma unroll
           for (int h = 0; h < kWide / 32; ++h) {
@@ -419,7 +504,10 @@ __global__ void __launch_bounds__(32 * (kFirstConvertWarp + (FP8 ? kConvertWarps
             }
           }
           tmem_wait_load();
-          if (lane == 0) tma_store_wait_read<0>();
+          // two pieces in turn: the one before the last has left this one
+          uint8_t* piece = mine + turn * 4096;
+          turn ^= 1;
+          if (lane == 0) tma_store_wait_read<1>();
           __syncwarp();
 #pragma unroll
           for (int v = 0; v < 8; ++v) {
@@ -433,30 +521,44 @@ __global__ void __launch_bounds__(32 * (kFirstConvertWarp + (FP8 ? kConvertWarps
                              pack_bf16x2(__uint_as_float(u[4]), __uint_as_float(u[5])),
                              pack_bf16x2(__uint_as_float(u[6]), __uint_as_float(u[7])));
             }
-            *reinterpret_cast<uint4*>(mine + lane * 128 + ((v ^ (lane & 7)) * 16)) = w;
+            *reinterpret_cast<uint4*>(piece + lane * 128 + ((v ^ (lane & 7)) * 16)) = w;
           }
           fence_async_shared();
           __syncwarp();
           if (lane == 0) {
             if (OUT32 && p.add)
-              tma_add_3d(&maps.out, mine_at, it.c0 + c, it.m0 + warp * 32, it.e);
+              tma_add_3d(&maps.out, smem_addr(piece), it.c0 + c, m, it.e);
             else
-              tma_store_3d(&maps.out, mine_at, it.c0 + c, it.m0 + warp * 32, it.e);
+              tma_store_3d(&maps.out, smem_addr(piece), it.c0 + c, m, it.e);
             tma_store_commit();
           }
         }
       } else {
         constexpr int kWidth = GATED ? 16 : 32;             // features of this warp
         constexpr int kPitch = GATED ? 48 : 80;             // bytes of a staged row
-        const int m = it.m0 + warp * kWidth;
-        for (int c = 0; c < it.cols; c += 32) {
+        const int m = it.m0 + int(rank) * (kEpilogueWarps * kWidth) + warp * kWidth;
+        const int rows = FP8 ? it.cols / 2 : it.cols;
+        for (int c = 0; c < rows; c += 32) {
           if (m >= p.M) break;
           uint32_t r0[16], r1[16];
           tmem_load_16x32(acc + c, r0);
           tmem_load_16x32(acc + c + (16u << 16), r1);
-          tmem_wait_load();
+          if (FP8) {
+            // the sums of the rests
+            uint32_t s0[16], s1[16];
+            tmem_load_16x32(acc + rows + c, s0);
+            tmem_load_16x32(acc + rows + c + (16u << 16), s1);
+            tmem_wait_load();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              r0[i] = __float_as_uint(__uint_as_float(r0[i]) + __uint_as_float(s0[i]));
+              r1[i] = __float_as_uint(__uint_as_float(r1[i]) + __uint_as_float(s1[i]));
+            }
+          } else {
+            tmem_wait_load();
+          }
           // matrices of 8 features by 8 rows, transposed on the way
-          const uint32_t at = mine_at + (lane % 8 + lane / 16 * 8) * kPitch + (lane / 8 % 2) * 16;
+          const uint32_t to = smem_addr(mine) + (lane % 8 + lane / 16 * 8) * kPitch + (lane / 8 % 2) * 16;
           if (GATED) {
             float y[16];
 #pragma unroll
@@ -464,7 +566,7 @@ __global__ void __launch_bounds__(32 * (kFirstConvertWarp + (FP8 ? kConvertWarps
               y[i] = silu(__uint_as_float(r0[i])) * __uint_as_float(r1[i]);
 #pragma unroll
             for (int j = 0; j < 4; j += 2)
-              stmatrix_t4(at + j * 8 * kPitch, pack_bf16x2(y[4 * j], y[4 * j + 1]),
+              stmatrix_t4(to + j * 8 * kPitch, pack_bf16x2(y[4 * j], y[4 * j + 1]),
                           pack_bf16x2(y[4 * j + 2], y[4 * j + 3]),
                           pack_bf16x2(y[4 * j + 4], y[4 * j + 5]),
                           pack_bf16x2(y[4 * j + 6], y[4 * j + 7]));
@@ -479,7 +581,7 @@ __global__ void __launch_bounds__(32 * (kFirstConvertWarp + (FP8 ? kConvertWarps
                   w[i] = pack_bf16x2(__uint_as_float(h ? r1[4 * j + 2 * i] : r0[4 * j + 2 * i]),
                                      __uint_as_float(h ? r1[4 * j + 2 * i + 1]
                                                        : r0[4 * j + 2 * i + 1]));
-                stmatrix_t4(at + j * 8 * kPitch + h * 32, w[0], w[1], w[2], w[3]);
+                stmatrix_t4(to + j * 8 * kPitch + h * 32, w[0], w[1], w[2], w[3]);
               }
           }
           __syncwarp();
@@ -498,7 +600,7 @@ __global__ void __launch_bounds__(32 * (kFirstConvertWarp + (FP8 ? kConvertWarps
       if (it.blocks > 0) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&sm.acc_empty[buf]));
+        if (lane == 0) mbar_arrive_cluster(at_rank(smem_addr(&sm.acc_empty[buf]), 0));
         ++tile;
       }
     }
@@ -507,7 +609,7 @@ __global__ void __launch_bounds__(32 * (kFirstConvertWarp + (FP8 ? kConvertWarps
     __syncwarp();
   }
   tc_fence_before();
-  __syncthreads();
+  cluster_sync();
   tc_fence_after();
   if (warp == kMmaWarp) tmem_free(tmem, 2 * kMaxCols);
 }
@@ -583,34 +685,38 @@ cudaError_t encode_weights(CUtensorMap* m, bool f32, const void* base, int E, in
                    {uint64_t(H), uint64_t(N) * H}, {f32 ? 32u : 64u, uint32_t(high), 1});
 }
 
-size_t smem_bytes(int table) {
-  return 1024 + kStages * (kABytes + kBBytes) + kEpilogueWarps * kStaging + sizeof(Smem) +
-         sizeof(int) * table;
+// Dynamic shared memory: the ring takes what the staging pieces, the barriers
+// and the table of the most experts leave of 227 KiB.
+constexpr int kSmemLimit = 227 * 1024;
+
+constexpr int rest_bytes(Mode m, int table) {
+  return 1024 + staging_of(m) + int(sizeof(Smem)) + 4 * table;
 }
 
 template <Mode MODE, bool FP8, bool GATED, bool OUT32>
-cudaError_t launch(const MmMaps& maps, const MmParams& p, int64_t most_items, cudaStream_t s) {
+cudaError_t launch(const MmMaps& maps, MmParams p, int64_t most_items, cudaStream_t s) {
   auto* kernel = expert_mm_kernel<MODE, FP8, GATED, OUT32>;
-  // once per kernel and device: the limit for any number of experts
+  // once per kernel and device
   static std::atomic<uint64_t> raised{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !(raised.load(std::memory_order_acquire) >> dev & 1)) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             int(smem_bytes(2049)));
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
     if (e != cudaSuccess) return e;
     if (dev < 64) raised.fetch_or(uint64_t(1) << dev, std::memory_order_release);
   }
-  const int sms = device_info().sm_count;
-  const int grid = int(most_items < sms ? most_items : sms);
-  return launch_pdl(kernel, dim3(grid), dim3(32 * (kFirstConvertWarp + (FP8 ? kConvertWarps : 0))),
-                    smem_bytes(MODE == kByWeights ? 0 : p.E + 1), s, maps, p);
+  const int rest = rest_bytes(MODE, MODE == kByWeights ? 0 : p.E + 1);
+  p.ring_bytes = (kSmemLimit - rest) / 1024 * 1024;
+  const int64_t pairs = device_info().sm_count / 2;
+  const int grid = 2 * int(most_items < pairs ? most_items : pairs);
+  return launch_pdl(kernel, dim3(grid), dim3(threads_of(FP8)), size_t(p.ring_bytes + rest), s,
+                    maps, p);
 }
 
 // Tiles that `rows` rows of E experts can make, at most, by feature tiles.
-int64_t most_row_tiles(int rows, int E) {
-  return int64_t(rows) / kMaxCols + (rows < E ? rows : E);
+int64_t most_row_tiles(int rows, int E, bool fp8) {
+  return int64_t(rows) / rows_of(fp8) + (rows < E ? rows : E);
 }
 
 MmParams params(const ep_expert_config* cfg, int cap, const int32_t* start, const int32_t* end,
@@ -629,7 +735,7 @@ cudaError_t forward(const ep_expert_config* c, int cap, int num_rows, const void
                     void* out, int32_t* err, cudaStream_t s) {
   MmParams p = params(c, cap, start, end, err);
   const int H = c->in_features, N = c->out_features, I = N / 2;
-  const int features = c->gated ? kLanes / 2 : kLanes;
+  const int features = c->gated ? kLanes : 2 * kLanes;
   p.M = c->gated ? I : N;
   p.depth = H;
   p.m_tiles = (p.M + features - 1) / features;
@@ -651,11 +757,11 @@ cudaError_t forward(const ep_expert_config* c, int cap, int num_rows, const void
     p.xs = x_scale;
     p.x_width = H;
   } else {
-    for (int i = 0; i < 4 && e == cudaSuccess; ++i)
-      e = encode_rows(&maps.b[i], x, cap, H, 16 << i);
+    for (int i = 0; i < 5 && e == cudaSuccess; ++i)
+      e = encode_rows(&maps.b[i], x, cap, H, 8 << i);
   }
   if (e != cudaSuccess) return e;
-  const int64_t items = most_row_tiles(num_rows, p.E) * p.m_tiles;
+  const int64_t items = most_row_tiles(num_rows, p.E, c->x_fp8) * p.m_tiles;
   if (c->gated)
     return c->x_fp8 ? launch<kForward, true, true, false>(maps, p, items, s)
                     : launch<kForward, false, true, false>(maps, p, items, s);
@@ -669,16 +775,16 @@ cudaError_t by_rows(const ep_expert_config* c, int cap, int num_rows, const void
   MmParams p = params(c, cap, start, end, err);
   p.M = c->in_features;
   p.depth = c->out_features;
-  p.m_tiles = (p.M + kLanes - 1) / kLanes;
+  p.m_tiles = (p.M + 2 * kLanes - 1) / (2 * kLanes);
   p.out = static_cast<__nv_bfloat16*>(dx);
   MmMaps maps;
   cudaError_t e = encode_weights(&maps.a, false, w, c->num_experts, c->out_features,
                                  c->in_features, kDepth);
-  for (int i = 0; i < 4 && e == cudaSuccess; ++i)
-    e = encode_rows(&maps.b[i], dy, cap, c->out_features, 16 << i);
+  for (int i = 0; i < 5 && e == cudaSuccess; ++i)
+    e = encode_rows(&maps.b[i], dy, cap, c->out_features, 8 << i);
   if (e != cudaSuccess) return e;
-  return launch<kByRows, false, false, false>(maps, p, most_row_tiles(num_rows, p.E) * p.m_tiles,
-                                              s);
+  const int64_t items = most_row_tiles(num_rows, p.E, false) * p.m_tiles;
+  return launch<kByRows, false, false, false>(maps, p, items, s);
 }
 
 cudaError_t by_weights(const ep_expert_config* c, int cap, const void* dy, const void* x,
@@ -688,7 +794,7 @@ cudaError_t by_weights(const ep_expert_config* c, int cap, const void* dy, const
   const bool f32 = type != EP_GRAD_BF16;
   p.M = c->out_features;
   p.cols = c->in_features;
-  p.m_tiles = (p.M + kLanes - 1) / kLanes;
+  p.m_tiles = (p.M + 2 * kLanes - 1) / (2 * kLanes);
   p.n_tiles = (p.cols + kMaxCols - 1) / kMaxCols;
   p.add = type == EP_GRAD_FP32_ADD;
   const int64_t size = int64_t(p.E) * p.M * p.cols * (f32 ? 4 : 2);

@@ -55,9 +55,12 @@ def silu(g):
         return g / (1 + np.exp(-g))
 
 
-def forward(x, w, gated):
-    """(y, bound) of one expert's rows, the last rounding to bf16 included."""
+def forward(x, w, gated, fp8=False):
+    """(y, bound) of one expert's rows, the last rounding to bf16 included.  E4M3 rows enter in
+    two bf16 parts, whose sum is off by half a step of the second: 2^-16 of the value."""
     y, d = product(x, w)
+    if fp8:
+        d = 2 * d + EPS * abs(y) + BF16 * BF16 * (abs(x) @ abs(w).T)
     if gated:
         half = w.shape[0] // 2
         (g, u), (dg, du) = (y[:, :half], y[:, half:]), (d[:, :half], d[:, half:])

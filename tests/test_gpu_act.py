@@ -131,11 +131,11 @@ def test_a_checkpoint_is_a_row_in_8_bits(ep):
     _, q, s = case.save(ep)
     w = ref.bf16(np.random.default_rng(5).standard_normal((3, 40, 256)) / 16)
     out = ep.expert_mm(ep.ExpertConfig(3, 256, 40, x_fp8=True), q, w.cuda(), *case.seg, x_scale=s)
-    x = ref.f64(torch.from_numpy(case.kept(q.cpu(), s.cpu()).astype(np.float32)).bfloat16())
+    x = ref.f64(ref.values(q, s))
     for e, n in enumerate(case.counts):
         rows = slice(int(case.start[e]), int(case.end[e]))
         if n:
-            y, err = ref.forward(x[rows], ref.f64(w[e]), False)
+            y, err = ref.forward(x[rows], ref.f64(w[e]), False, True)
             assert (abs(ref.f64(out[rows]) - y) <= err).all()
 
 

@@ -43,12 +43,14 @@ class Case:
         if fp8:
             q, self.scale = ref.quantise(torch.from_numpy(x) * 3)
             q[~torch.from_numpy(self.own)] = 0x7F      # NaN
-            self.x = ref.f64(ref.values(q, self.scale).bfloat16())
+            v = ref.values(q, self.scale)
+            self.xf, self.x = ref.f64(v), ref.f64(v.bfloat16())
             self.dx, self.dscale = q.cuda(), self.scale.cuda()
         else:
             x[~self.own] = np.nan
             t = ref.bf16(x)
             self.x, self.dx, self.dscale = ref.f64(t), t.cuda(), None
+            self.xf = self.x
         dy = rng.standard_normal((self.cap, N)).astype(np.float32)
         dy[~self.own] = np.nan
         self.dy = ref.bf16(dy)
@@ -79,7 +81,8 @@ class Case:
                 assert (abs(got[rows] - y) <= err).all(), (e, abs(got[rows] - y).max())
 
     def check_forward(self, got):
-        self.check_rows(got, lambda e, r: ref.forward(self.x[r], ref.f64(self.w[e]), self.gated))
+        self.check_rows(got, lambda e, r: ref.forward(self.xf[r], ref.f64(self.w[e]), self.gated,
+                                                       self.dscale is not None))
 
     def check_backward(self, grad_x, grad_w, before=None):
         self.check_rows(grad_x, lambda e, r: ref.by_rows(ref.f64(self.dy[r]), ref.f64(self.w[e])))
