@@ -29,7 +29,7 @@
 //
 // E4M3 rows: the scale changes along the reduction (every 128 inputs), so it
 // cannot be applied to a sum.  Forward, value * scale enters as two bf16
-// parts, the nearest and the rest (16 bits of it together): the first CTA's
+// parts, its upper 16 bits and the rest: the first CTA's
 // columns are the first parts, the second's the rests, and the epilogue adds
 // the two sums.  That halves the rows a tile holds; the weights are what costs
 // at the sizes that prompts and decode have.  dW takes bf16(value * scale)
@@ -61,8 +61,9 @@ constexpr int kPanel = 64 * kDepth * 2;         // 64 features by 64 rows
 constexpr int kRowGroup = 8;                    // row tiles that share weight tiles in L2
 
 constexpr int kEpilogueWarps = 4, kCopyWarp = 4, kMmaWarp = 5, kClearWarp = 6;
-constexpr int kFirstConvertWarp = 7, kConvertWarps = 4;
-constexpr int kPieces = 4;         // of 16 values a converting thread has in a step
+constexpr int kFirstConvertWarp = 7, kConvertWarps = 8;
+constexpr int kPieces = 2;         // of 16 values a converting thread has in a step
+static_assert(32 * kConvertWarps * kPieces * 16 == kMaxCols / 2 * kDepth);
 constexpr int kAhead = 4;          // steps that it loads ahead
 
 __host__ __device__ constexpr int threads_of(bool fp8) { return 32 * (kFirstConvertWarp + (fp8 ? kConvertWarps : 0)); }
@@ -180,8 +181,12 @@ __device__ __forceinline__ Item item_at(const MmParams& p, const int* table, int
 
 __device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
 
-// 16 E4M3 values times their scale as bf16, or what that rounding left.
-template <bool REST>
+// How E4M3 values times their scale become bf16: by the nearest, or in two
+// parts, the upper 16 bits and the rest.
+enum Part { kNearest, kUpper, kRest };
+
+// 16 of them.
+template <Part PART>
 __device__ __forceinline__ void widen16(uint4 q, float scale, uint4& lo, uint4& hi) {
   const uint32_t w[4] = {q.x, q.y, q.z, q.w};
   uint32_t r[8];
@@ -196,12 +201,13 @@ __device__ __forceinline__ void widen16(uint4 q, float scale, uint4& lo, uint4& 
         : "r"(h));
     a *= scale;
     b *= scale;
-    r[i] = pack_bf16x2(a, b);
-    if (REST) {
-      // 0 beside an infinity, which would leave inf - inf
-      const float x = bf16_lo(r[i]), y = bf16_hi(r[i]);
-      r[i] = pack_bf16x2(fabsf(x) < INFINITY ? a - x : 0.0f, fabsf(y) < INFINITY ? b - y : 0.0f);
-    }
+    if (PART == kUpper)
+      r[i] = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+    else if (PART == kRest)
+      r[i] = pack_bf16x2(a - __uint_as_float(__float_as_uint(a) & 0xffff0000u),
+                         b - __uint_as_float(__float_as_uint(b) & 0xffff0000u));
+    else
+      r[i] = pack_bf16x2(a, b);
   }
   lo = make_uint4(r[0], r[1], r[2], r[3]);
   hi = make_uint4(r[4], r[5], r[6], r[7]);
@@ -215,7 +221,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
   uint8_t* staging = ring + p.ring_bytes;
   Smem& sm = *reinterpret_cast<Smem*>(staging + staging_of(MODE));
   int* table = reinterpret_cast<int*>(&sm + 1);
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const uint32_t rank = cluster_rank();
   constexpr bool kAByFeature = MODE != kForward;      // inner dimension of A: features
   constexpr bool kBByFeature = MODE == kByWeights;
@@ -285,31 +291,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
   Ring at;
 
   if (warp == kCopyWarp) {
-    if (lane == 0) {
-      bool ok = true;
-      uint64_t n = 0;      // stages filled so far
-      for (int64_t idx = pair; ok && idx < items; idx += pairs) {
-        const Item it = item_at<MODE, FP8, GATED>(p, table, idx);
-        const int half = it.cols / 2;
-        // bytes of this CTA's copies into a stage
-        const int bytes = kABytes + (FP8 ? 0 : half * kDepth * 2);
-        const int m0 = it.m0 + int(rank) * (GATED ? kLanes / 2 : kLanes);
-        const int col0 = int(rank) * half;
-        for (int kb = 0; kb < it.blocks; ++kb, ++n, at.next(stages)) {
-          ok = mbar_wait(&sm.empty[at.s], at.phase ^ 1, kWaitTimeoutNs);
-          if (!ok) break;
-          const uint32_t a = smem_addr(ring + at.s * stage_bytes), b = a + kABytes;
-          const int k0 = kb * kDepth;
-          uint32_t bar = at_rank(smem_addr(&sm.full[at.s]), 0);
-          if (MODE == kByWeights && it.rows - k0 < kDepth) {
-            // cleared past the segment's end before it counts as full
-            bar = smem_addr(&sm.last[at.s]);
+    bool ok = true;
+    uint64_t n = 0;      // stages filled so far
+    for (int64_t idx = pair; ok && idx < items; idx += pairs) {
+      const Item it = item_at<MODE, FP8, GATED>(p, table, idx);
+      const int half = it.cols / 2;
+      // bytes of this CTA's copies into a stage
+      const int bytes = kABytes + (FP8 ? 0 : half * kDepth * 2);
+      const int m0 = it.m0 + int(rank) * (GATED ? kLanes / 2 : kLanes);
+      const int col0 = int(rank) * half;
+      for (int kb = 0; kb < it.blocks; ++kb, ++n, at.next(stages)) {
+        ok = mbar_wait(&sm.empty[at.s], at.phase ^ 1, kWaitTimeoutNs);
+        if (!ok) break;
+        const uint32_t a = smem_addr(ring + at.s * stage_bytes), b = a + kABytes;
+        const int k0 = kb * kDepth;
+        // cleared past the segment's end before it counts as full
+        const bool last = MODE == kByWeights && it.rows - k0 < kDepth;
+        const uint32_t full = at_rank(smem_addr(&sm.full[at.s]), 0);
+        const uint32_t bar = last ? smem_addr(&sm.last[at.s]) : full;
+        if (elect_one()) {
+          if (last)
             mbar_arrive_expect_tx(&sm.last[at.s], bytes);
-          } else if (rank == 0) {
+          else if (rank == 0)
             mbar_arrive_expect_tx(&sm.full[at.s], 2 * bytes);
-          } else {
-            mbar_arrive_cluster(bar);
-          }
+          else
+            mbar_arrive_cluster(full);
           if (MODE == kForward) {
             if (GATED)
               tma_load_5d(a, &maps.a, bar, k0, 0, 0, m0 / 16, it.e);
@@ -322,11 +328,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
             tma_load_2d(a, &maps.a, bar, m0, it.row0 + k0);
             tma_load_2d(a + kPanel, &maps.a, bar, m0 + 64, it.row0 + k0);
           }
-          if (FP8) continue;
-          if (kBByFeature) {
+          if (!FP8 && kBByFeature) {
             for (int c = 0; c < half; c += 64)
               tma_load_2d(b + c / 64 * kPanel, &maps.b[0], bar, it.c0 + col0 + c, it.row0 + k0);
-          } else {
+          } else if (!FP8) {
             // boxes of the binary digits of the CTA's rows
             int r = 0;
 #pragma unroll
@@ -337,54 +342,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
               }
           }
         }
+        __syncwarp();
       }
-      if (!ok) {
-        record_error(p.err, ERRBIT_TIMEOUT);
-        // the first CTA's barriers count the copies of both, which land before
-        // the pair may end (the second CTA waits for the first one's end)
-        for (uint64_t i = n < uint64_t(stages) ? 0 : n - stages; rank == 0 && i < n; ++i)
-          if (!mbar_wait(&sm.full[i % stages], i / stages & 1, kWaitTimeoutNs))
-            record_error(p.err, ERRBIT_TIMEOUT_PENDING);
-      }
+    }
+    if (!ok && lane == 0) {
+      record_error(p.err, ERRBIT_TIMEOUT);
+      // the first CTA's barriers count the copies of both, which land before
+      // the pair may end (the second CTA waits for the first one's end)
+      for (uint64_t i = n < uint64_t(stages) ? 0 : n - stages; rank == 0 && i < n; ++i)
+        if (!mbar_wait(&sm.full[i % stages], i / stages & 1, kWaitTimeoutNs))
+          record_error(p.err, ERRBIT_TIMEOUT_PENDING);
     }
     __syncwarp();
   } else if (warp == kMmaWarp && rank == 0) {
-    if (lane == 0) {
-      uint32_t tile = 0;
-      bool ok = true;
-      for (int64_t idx = pair; ok && idx < items; idx += pairs) {
-        const Item it = item_at<MODE, FP8, GATED>(p, table, idx);
-        if (it.blocks == 0) continue;
-        const uint32_t idesc = instr_desc(2 * kLanes, it.cols, kAByFeature, kBByFeature);
-        const uint32_t buf = tile & 1, acc = tmem + buf * kMaxCols;
-        ok = mbar_wait(&sm.acc_empty[buf], (tile / 2 & 1) ^ 1, kWaitTimeoutNs);
+    uint32_t tile = 0;
+    bool ok = true;
+    for (int64_t idx = pair; ok && idx < items; idx += pairs) {
+      const Item it = item_at<MODE, FP8, GATED>(p, table, idx);
+      if (it.blocks == 0) continue;
+      const uint32_t idesc = instr_desc(2 * kLanes, it.cols, kAByFeature, kBByFeature);
+      const uint32_t buf = tile & 1, acc = tmem + buf * kMaxCols;
+      ok = mbar_wait(&sm.acc_empty[buf], (tile / 2 & 1) ^ 1, kWaitTimeoutNs);
+      if (!ok) break;
+      tc_fence_after();
+      for (int kb = 0; kb < it.blocks; ++kb, at.next(stages)) {
+        ok = mbar_wait(&sm.full[at.s], at.phase, kWaitTimeoutNs);
         if (!ok) break;
         tc_fence_after();
-        for (int kb = 0; kb < it.blocks; ++kb, at.next(stages)) {
-          ok = mbar_wait(&sm.full[at.s], at.phase, kWaitTimeoutNs);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t a = smem_addr(ring + at.s * stage_bytes), b = a + kABytes;
-          const uint64_t da = smem_desc(a, kAByFeature ? kPanel : 16, 1024);
-          const uint64_t db = smem_desc(b, kBByFeature ? kPanel : 16, 1024);
-          // 16 of the reduction further: 32 bytes of a row, or 16 rows
-          constexpr uint32_t as = (kAByFeature ? 2048 : 32) >> 4, bs = (kBByFeature ? 2048 : 32) >> 4;
-          const int steps =
-              MODE == kByWeights ? min(kDepth / 16, (it.rows - kb * kDepth + 15) / 16) : kDepth / 16;
+        const uint32_t a = smem_addr(ring + at.s * stage_bytes), b = a + kABytes;
+        const uint64_t da = smem_desc(a, kAByFeature ? kPanel : 16, 1024);
+        const uint64_t db = smem_desc(b, kBByFeature ? kPanel : 16, 1024);
+        // 16 of the reduction further: 32 bytes of a row, or 16 rows
+        constexpr uint32_t as = (kAByFeature ? 2048 : 32) >> 4, bs = (kBByFeature ? 2048 : 32) >> 4;
+        const int steps =
+            MODE == kByWeights ? min(kDepth / 16, (it.rows - kb * kDepth + 15) / 16) : kDepth / 16;
+        if (elect_one()) {
 #pragma unroll
           for (int i = 0; i < kDepth / 16; ++i)
             if (i < steps) mma_bf16(acc, da + i * as, db + i * bs, idesc, kb > 0 || i > 0);
           mma_commit(smem_addr(&sm.empty[at.s]));
+          if (kb == it.blocks - 1) mma_commit(smem_addr(&sm.acc_full[buf]));
         }
-        if (ok) mma_commit(smem_addr(&sm.acc_full[buf]));
-        ++tile;
+        __syncwarp();
       }
-      if (!ok) {
-        // products in flight end before the tensor memory is given back
+      ++tile;
+    }
+    if (!ok) {
+      // products in flight end before the tensor memory is given back
+      if (elect_one()) {
         record_error(p.err, ERRBIT_TIMEOUT);
         mma_commit(smem_addr(&sm.drained));
-        mbar_wait(&sm.drained, 0, kWaitTimeoutNs);
       }
+      __syncwarp();
+      mbar_wait(&sm.drained, 0, kWaitTimeoutNs);
     }
     __syncwarp();
   } else if (MODE == kByWeights && warp == kClearWarp) {
@@ -427,7 +437,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
       const auto load = [&](int kb, uint4 (&to)[kPieces], float (&scale)[kPieces]) {
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
-          const int row = kBByFeature ? kb * kDepth + t / 8 + 16 * i : t / 4 + 32 * i;
+          const int row = kBByFeature ? kb * kDepth + t / 8 + kConvertWarps * 4 * i
+                                      : t / 4 + kConvertWarps * 8 * i;
           const int c = kBByFeature ? t % 8 * 16 : t % 4 * 16;
           const int x = kBByFeature ? it.c0 + int(rank) * half + c : kb * kDepth + c;
           to[i] = make_uint4(0, 0, 0, 0);
@@ -450,13 +461,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
           uint8_t* b = ring + at.s * stage_bytes + kABytes;
 #pragma unroll
           for (int i = 0; i < kPieces; ++i) {
-            const int row = kBByFeature ? t / 8 + 16 * i : t / 4 + 32 * i;
+            const int row = t / (kBByFeature ? 8 : 4) + kConvertWarps * (kBByFeature ? 4 : 8) * i;
             if (kBByFeature ? t % 8 * 16 >= half : row >= half) break;
             uint4 lo, hi;
-            if (kBByFeature || rank == 0)
-              widen16<false>(q[d][i], sc[d][i], lo, hi);
+            if (kBByFeature)
+              widen16<kNearest>(q[d][i], sc[d][i], lo, hi);
+            else if (rank == 0)
+              widen16<kUpper>(q[d][i], sc[d][i], lo, hi);
             else
-              widen16<true>(q[d][i], sc[d][i], lo, hi);
+              widen16<kRest>(q[d][i], sc[d][i], lo, hi);
             uint8_t* to = b + (kBByFeature ? t % 8 / 4 * kPanel : 0) + row * 128;
             const int c = 2 * (t % 4);
             *reinterpret_cast<uint4*>(to + ((c ^ (row & 7)) * 16)) = lo;
