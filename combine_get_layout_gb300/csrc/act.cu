@@ -63,8 +63,8 @@ __device__ void count_rows(const ActParams& p, int* table) {
 
 // A warp's walk over the parts of all experts' rows, a step at a time.
 struct Walk {
-  int64_t r;             // row among the experts' rows
-  int64_t row;           // in the buffers
+  int64_t r = 0;         // row among the experts' rows
+  int64_t row = 0;       // in the buffers
   int part, col, end;    // part of it, first column of the step, end of the part
   int e = -1;
   int first;             // buffer row of the expert's first
@@ -138,10 +138,11 @@ __device__ __forceinline__ void unpack8(uint2 v, float scale, float* f) {
 // 1 / (1 + exp(-x)) by the hardware's exponential and reciprocal: within
 // (2 + |x|) 2^-22 of itself, far inside the rounding to bf16 behind it, at a
 // quarter of the instructions that expf and a division take (which bound the
-// kernels: save of 32768 rows 146 us with them).
+// kernels).  Below 2^-126 it is 0.
 __device__ __forceinline__ float sigmoid(float x) {
-  float r;
-  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.0f + __expf(-x)));
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.44269504088896340736f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
   return r;
 }
 
@@ -152,32 +153,46 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// The codes of eight values f (packed: v) of a block that 16 aligned lanes
-// hold, and the block's scale: amax / 448 and the codes of the quotients as
-// in quantize_group16.  All 32 lanes call.
-__device__ __forceinline__ uint2 quantize8(uint4 v, const float* f, float* scale) {
+// The larger of the magnitudes of eight values, in both halves.
+__device__ __forceinline__ uint32_t most8(uint4 v) {
   constexpr uint32_t kMagnitude = 0x7fff7fff;
-  uint32_t m = max2(max2(v.x & kMagnitude, v.y & kMagnitude),
-                    max2(v.z & kMagnitude, v.w & kMagnitude));
+  const uint32_t m = max2(max2(v.x & kMagnitude, v.y & kMagnitude),
+                          max2(v.z & kMagnitude, v.w & kMagnitude));
+  return max2(m, __byte_perm(m, m, 0x1032));
+}
+
+// The codes of eight values f (packed: v) of a block with this maximum, and
+// the block's scale: amax / 448 and the codes of the quotients as in
+// quantize_group16.
+__device__ __forceinline__ uint2 quantize8(uint4 v, const float* f, float amax, float* scale) {
+  // |a| / 448 by its reciprocal and one exact remainder is the IEEE quotient
+  // for every bf16 value from 2^-90 on (all were compared)
+  constexpr float kPart = 1.0f / 448.0f;
+  if (amax >= 0x1p-90f && amax <= 0x1.fffffep127f) {
+    const float q0 = amax * kPart;
+    const float s = fmaf(fmaf(-q0, 448.0f, amax), kPart, q0);
+    *scale = s;
+    // scaled_quotient's, the signs from the values (a quotient of -0 is -0)
+    const float y = __frcp_rn(s);
+    uint32_t c[4];
 #pragma unroll
-  for (int o = 8; o >= 1; o >>= 1) m = max2(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const float amax = fmaxf(fmaxf(bf16_lo(m), bf16_hi(m)), 0.0f);
+    for (int j = 0; j < 4; ++j) {
+      const float a = f[2 * j], b = f[2 * j + 1];
+      const float qa = a * y, qb = b * y;
+      c[j] = pack_e4m3x2(fmaf(fmaf(-qa, s, a), y, qa), fmaf(fmaf(-qb, s, b), y, qb));
+    }
+    constexpr uint32_t kSigns = 0x80808080;
+    return make_uint2(__byte_perm(c[0], c[1], 0x5410) | (__byte_perm(v.x, v.y, 0x7531) & kSigns),
+                      __byte_perm(c[2], c[3], 0x5410) | (__byte_perm(v.z, v.w, 0x7531) & kSigns));
+  }
   *scale = 0.0f;
   if (amax == 0.0f) return make_uint2(0, 0);
   const float s = __fdiv_rn(amax, 448.0f);
   *scale = s;
-  const BlockQuotient div(s);
   uint32_t c[4];
-  if (div.fast) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      c[j] = pack_e4m3x2(scaled_quotient(f[2 * j], s, div.y),
-                         scaled_quotient(f[2 * j + 1], s, div.y));
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      c[j] = pack_e4m3x2(__fdiv_rn(f[2 * j], s), __fdiv_rn(f[2 * j + 1], s));
-  }
+  for (int j = 0; j < 4; ++j)
+    c[j] = pack_e4m3x2(__fdiv_rn(f[2 * j], s), __fdiv_rn(f[2 * j + 1], s));
   return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
 }
 
@@ -189,39 +204,52 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) act_save_kernel(const Ac
   const int blocks = (p.I + kBlock - 1) / kBlock;
   Walk w;
   uint4 g, u;
+  const uint8_t* h = nullptr;      // of the row
   const auto load = [&] {
     const int c = w.col + lane * 8;
-    const uint8_t* h = p.h + (w.row * 2 * p.I + c) * 2;
     g = u = make_uint4(0, 0, 0, 0);
     if (c < w.end) {
-      g = ld_stream_u4(h);
-      u = ld_stream_u4(h + int64_t(p.I) * 2);
+      g = ld_stream_u4(h + c * 2);
+      u = ld_stream_u4(h + (c + p.I) * 2);
     }
   };
   bool there = w.begin(p, table);
-  if (there) load();
+  int64_t row = w.row;
+  if (there) {
+    h = p.h + row * 4 * p.I;
+    load();
+  }
   while (there) {
     const uint4 gv = g, uv = u;
-    const int64_t row = w.row;
+    uint8_t* const a = p.a + row * 2 * p.I;
+    uint8_t* const q = p.q + row * 2 * p.I;
+    float* const s = p.scale + row * 2 * blocks;
     const int c = w.col + lane * 8;
     const bool in = c < w.end;
     there = w.next(p, table);
-    if (there) load();
+    if (there) {
+      if (w.row != row) h = p.h + w.row * 4 * p.I;
+      load();
+    }
+    row = w.row;
+    // both maxima in one word
+    uint32_t m = __byte_perm(most8(gv), most8(uv), 0x5410);
+#pragma unroll
+    for (int o = 8; o >= 1; o >>= 1) m = max2(m, __shfl_xor_sync(0xffffffffu, m, o));
     float x[8], y[8], x_scale, y_scale;
     unpack(gv, x);
     unpack(uv, y);
-    const uint2 xq = quantize8(gv, x, &x_scale), yq = quantize8(uv, y, &y_scale);
+    const uint2 xq = quantize8(gv, x, bf16_lo(m), &x_scale);
+    const uint2 yq = quantize8(uv, y, bf16_hi(m), &y_scale);
 #pragma unroll
     for (int j = 0; j < 8; ++j) y[j] *= x[j] * sigmoid(x[j]);
     if (in) {
-      *reinterpret_cast<uint4*>(p.a + (row * p.I + c) * 2) = pack(y);
-      uint8_t* q = p.q + row * 2 * p.I + c;
-      *reinterpret_cast<uint2*>(q) = xq;
-      *reinterpret_cast<uint2*>(q + p.I) = yq;
+      *reinterpret_cast<uint4*>(a + c * 2) = pack(y);
+      *reinterpret_cast<uint2*>(q + c) = xq;
+      *reinterpret_cast<uint2*>(q + c + p.I) = yq;
       if (lane % 16 == 0) {
-        float* s = p.scale + row * 2 * blocks + c / kBlock;
-        s[0] = x_scale;
-        s[blocks] = y_scale;
+        s[c / kBlock] = x_scale;
+        s[c / kBlock + blocks] = y_scale;
       }
     }
   }

@@ -62,9 +62,10 @@ constexpr int kRowGroup = 8;                    // row tiles that share weight t
 
 constexpr int kEpilogueWarps = 4, kCopyWarp = 4, kMmaWarp = 5, kClearWarp = 6;
 constexpr int kFirstConvertWarp = 7, kConvertWarps = 8;
-constexpr int kPieces = 2;         // of 16 values a converting thread has in a step
-static_assert(32 * kConvertWarps * kPieces * 16 == kMaxCols / 2 * kDepth);
-constexpr int kAhead = 4;          // steps that it loads ahead
+constexpr int kConvertGroups = 2;  // of warps, that take steps in turn
+constexpr int kPieces = 4;         // of 16 values a converting thread has in a step
+constexpr int kAhead = 2;          // steps of its own that it loads ahead
+static_assert(32 * kConvertWarps / kConvertGroups * kPieces * 16 == kMaxCols / 2 * kDepth);
 
 __host__ __device__ constexpr int threads_of(bool fp8) { return 32 * (kFirstConvertWarp + (fp8 ? kConvertWarps : 0)); }
 // Bytes that the epilogue's warps stage a tile's pieces in.
@@ -231,7 +232,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
     prefetch_map(&maps.a);
     if (!FP8) prefetch_map(&maps.b[0]);
     for (int s = 0; s < kMaxStages; ++s) {
-      mbar_init(&sm.full[s], FP8 ? 2 + 2 * kConvertWarps : 2);
+      mbar_init(&sm.full[s], FP8 ? 2 + 2 * kConvertWarps / kConvertGroups : 2);
       mbar_init(&sm.empty[s], 1);
       mbar_init(&sm.last[s], 1);
     }
@@ -424,63 +425,89 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
     if (!ok && lane == 0) record_error(p.err, ERRBIT_TIMEOUT);
     __syncwarp();
   } else if (FP8 && warp >= kFirstConvertWarp) {
-    const int t = threadIdx.x - kFirstConvertWarp * 32;
+    // Two groups of four warps take steps in turn, and load theirs two turns
+    // ahead, past the ends of tiles.
+    constexpr int kThreads = 32 * kConvertWarps / kConvertGroups;
+    const int group = (warp - kFirstConvertWarp) / (kConvertWarps / kConvertGroups);
+    const int t = (threadIdx.x - kFirstConvertWarp * 32) % kThreads;
+    // pieces of 16 values: forward, 4 of each of the rows for a step's 64
+    // inputs; by weights, 8 of each of its 64 rows
+    constexpr int kOfRow = kBByFeature ? 8 : 4;
+    const int row_t = t / kOfRow, c_t = t % kOfRow * 16;
     const int scales = p.x_width / 128;
-    bool ok = true;
-    for (int64_t idx = pair; ok && idx < items; idx += pairs) {
-      const Item it = item_at<MODE, FP8, GATED>(p, table, idx);
-      const int half = it.cols / 2;
-      // pieces of 16 values: forward, 4 of each of the rows for this step's 64
-      // inputs; by weights, 8 of each of its 64 rows
-      uint4 q[kAhead][kPieces];
-      float sc[kAhead][kPieces];
-      const auto load = [&](int kb, uint4 (&to)[kPieces], float (&scale)[kPieces]) {
+    uint4 q[kAhead][kPieces];
+    float sc[kAhead][kPieces];
+    int halves[kAhead];         // columns of the step's tile a CTA, 0 past the last one
+    int64_t idx = pair;
+    int kb = 0;
+    Item it = {};
+    bool more = idx < items;
+    if (more) it = item_at<MODE, FP8, GATED>(p, table, idx);
+    const auto step = [&] {
+      if (!more || ++kb < it.blocks) return;
+      kb = 0;
+      do {
+        idx += pairs;
+        more = idx < items;
+        if (more) it = item_at<MODE, FP8, GATED>(p, table, idx);
+      } while (more && it.blocks == 0);
+    };
+    const auto load = [&](uint4 (&to)[kPieces], float (&scale)[kPieces], int& half) {
+      half = more ? it.cols / 2 : 0;
+      const int x = kBByFeature ? it.c0 + int(rank) * half + c_t : kb * kDepth + c_t;
+      const int row0 = kBByFeature ? kb * kDepth + row_t : row_t;
+      const bool in = more && x < p.x_width && (!kBByFeature || c_t < half);
+      const int64_t r0 = int64_t(it.row0) + row0;
+      const uint8_t* from = p.xq + r0 * p.x_width + x;
+      const float* s = p.xs + r0 * scales + x / 128;
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        const int r = kThreads / kOfRow * i;
+        to[i] = make_uint4(0, 0, 0, 0);
+        scale[i] = 0.0f;
+        if (in && row0 + r < it.rows) {
+          to[i] = __ldg(reinterpret_cast<const uint4*>(from + int64_t(r) * p.x_width));
+          scale[i] = __ldg(s + int64_t(r) * scales);
+        }
+      }
+      for (int g = 0; g < kConvertGroups; ++g) step();
+    };
+    // to the first step, and this group's first
+    --kb;
+    for (int g = 0; g <= group; ++g) step();
+    for (int g = 0; g < group; ++g) at.next(stages);
+#pragma unroll
+    for (int d = 0; d < kAhead; ++d) load(q[d], sc[d], halves[d]);
+    bool ok = true, some = true;
+    while (ok && some) {
+#pragma unroll
+      for (int d = 0; d < kAhead; ++d) {
+        const int half = halves[d];
+        some = half > 0;
+        if (!some) break;
+        ok = mbar_wait(&sm.empty[at.s], at.phase ^ 1, kWaitTimeoutNs);
+        if (!ok) break;
+        uint8_t* b = ring + at.s * stage_bytes + kABytes + (kBByFeature ? c_t / 64 * kPanel : 0);
+        const int c = c_t % 64 / 8;
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
-          const int row = kBByFeature ? kb * kDepth + t / 8 + kConvertWarps * 4 * i
-                                      : t / 4 + kConvertWarps * 8 * i;
-          const int c = kBByFeature ? t % 8 * 16 : t % 4 * 16;
-          const int x = kBByFeature ? it.c0 + int(rank) * half + c : kb * kDepth + c;
-          to[i] = make_uint4(0, 0, 0, 0);
-          scale[i] = 0.0f;
-          if (row < it.rows && x < p.x_width && kb < it.blocks && c < (kBByFeature ? half : 64)) {
-            const int64_t r = int64_t(it.row0) + row;
-            to[i] = __ldg(reinterpret_cast<const uint4*>(p.xq + r * p.x_width + x));
-            scale[i] = __ldg(p.xs + r * scales + x / 128);
-          }
+          const int row = row_t + kThreads / kOfRow * i;
+          if (kBByFeature ? c_t >= half : row >= half) break;
+          uint4 lo, hi;
+          if (kBByFeature)
+            widen16<kNearest>(q[d][i], sc[d][i], lo, hi);
+          else if (rank == 0)
+            widen16<kUpper>(q[d][i], sc[d][i], lo, hi);
+          else
+            widen16<kRest>(q[d][i], sc[d][i], lo, hi);
+          *reinterpret_cast<uint4*>(b + row * 128 + ((c ^ (row & 7)) * 16)) = lo;
+          *reinterpret_cast<uint4*>(b + row * 128 + (((c + 1) ^ (row & 7)) * 16)) = hi;
         }
-      };
-#pragma unroll
-      for (int d = 0; d < kAhead; ++d) load(d, q[d], sc[d]);
-      for (int kb0 = 0; ok && kb0 < it.blocks; kb0 += kAhead) {
-#pragma unroll
-        for (int d = 0; d < kAhead; ++d) {
-          if (!ok || kb0 + d >= it.blocks) break;
-          ok = mbar_wait(&sm.empty[at.s], at.phase ^ 1, kWaitTimeoutNs);
-          if (!ok) break;
-          uint8_t* b = ring + at.s * stage_bytes + kABytes;
-#pragma unroll
-          for (int i = 0; i < kPieces; ++i) {
-            const int row = t / (kBByFeature ? 8 : 4) + kConvertWarps * (kBByFeature ? 4 : 8) * i;
-            if (kBByFeature ? t % 8 * 16 >= half : row >= half) break;
-            uint4 lo, hi;
-            if (kBByFeature)
-              widen16<kNearest>(q[d][i], sc[d][i], lo, hi);
-            else if (rank == 0)
-              widen16<kUpper>(q[d][i], sc[d][i], lo, hi);
-            else
-              widen16<kRest>(q[d][i], sc[d][i], lo, hi);
-            uint8_t* to = b + (kBByFeature ? t % 8 / 4 * kPanel : 0) + row * 128;
-            const int c = 2 * (t % 4);
-            *reinterpret_cast<uint4*>(to + ((c ^ (row & 7)) * 16)) = lo;
-            *reinterpret_cast<uint4*>(to + (((c + 1) ^ (row & 7)) * 16)) = hi;
-          }
-          fence_async_shared();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(at_rank(smem_addr(&sm.full[at.s]), 0));
-          at.next(stages);
-          load(kb0 + d + kAhead, q[d], sc[d]);
-        }
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(at_rank(smem_addr(&sm.full[at.s]), 0));
+        for (int g = 0; g < kConvertGroups; ++g) at.next(stages);
+        load(q[d], sc[d], halves[d]);
       }
     }
     if (!ok && lane == 0) record_error(p.err, ERRBIT_TIMEOUT);

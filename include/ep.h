@@ -753,8 +753,8 @@ EP_API int32_t ep_expert_mm_backward(const ep_expert_config *cfg, int32_t cap, i
  * bytes [cap, 2 I]; d_scale: device fp32 [cap, 2 ceil(I / 128)].  I (width):
  * a multiple of 8, <= 2^19.  num_experts in [1, 2048], cap, num_rows and the
  * segments as in ep_expert_mm; rows of no expert are not written.  d_a is
- * computed from h itself, in fp32, rounded once.  Returns EP_OK or an
- * error. */
+ * computed from h itself, in fp32, rounded once (1 / (1 + exp(-g)) under
+ * 2^-126 counts as 0).  Returns EP_OK or an error. */
 EP_API int32_t ep_act_save(int32_t num_experts, int32_t width, int32_t cap, int32_t num_rows,
                            const void *d_h, const int32_t *d_expert_start,
                            const int32_t *d_expert_end, void *d_a, uint8_t *d_q, float *d_scale,
@@ -766,7 +766,8 @@ EP_API int32_t ep_act_save(int32_t num_experts, int32_t width, int32_t cap, int3
  *                                        grad_a g c]
  *   d_a (device bf16 [cap, I] or NULL) = g c u, the activation again, which
  *     the weight gradient of the product behind it needs
- * in fp32, rounded once.  Sizes as in ep_act_save.  Returns EP_OK or an
+ * in fp32, rounded once (c under 2^-126 counts as 0).  Sizes as in
+ * ep_act_save.  Returns EP_OK or an
  * error. */
 EP_API int32_t ep_act_backward(int32_t num_experts, int32_t width, int32_t cap, int32_t num_rows,
                                const void *d_grad_a, const uint8_t *d_q, const float *d_scale,

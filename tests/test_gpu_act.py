@@ -117,7 +117,9 @@ def test_values_at_the_ends(ep):
         want = (f[:, :128] / (1 + torch.exp(-f[:, :128])) * f[:, 128:])
     fin = torch.isfinite(want) & (abs(want) < 3.3e38)
     d = abs(a.cpu().double() - want)
-    assert (d[fin] <= 2.0 ** -7 * abs(want[fin]) + 1e-38).all()
+    # a sigmoid under 2^-126 counts as 0: the whole value may be missing there
+    lost = torch.where(torch.sigmoid(f[:, :128]) < 2.0 ** -125, abs(want), 0)
+    assert (d[fin] <= (2.0 ** -7 * abs(want) + lost + 1e-38)[fin]).all()
     assert torch.isnan(a[3, 5]) and torch.isfinite(a[3, :5]).all()
     cfg = ep.Config(6, 256, 1, 1, 1, 1, True)
     layout = ep.get_layout(cfg, torch.zeros((6, 1), dtype=torch.int64, device="cuda"))
@@ -191,3 +193,26 @@ def test_segments_are_clipped(ep, start, end):
     for got, want in ((a, b), (q, r), (s, t)):
         assert torch.equal(got.cpu()[own], want.cpu()[own])
         assert (got.cpu()[~own] == 77).all()
+
+
+def test_codes_are_a_dispatchs(ep):
+    """Every bf16 maximum of a block, with values of all magnitudes below it: the codes and scales
+    that an FP8 dispatch gives the same rows."""
+    top = torch.arange(0, 0x7F81, dtype=torch.int32, device="cuda").to(torch.int16)
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    h = torch.randint(0, 1 << 15, (len(top), 128), device="cuda", generator=gen, dtype=torch.int32)
+    h = torch.minimum(h % (top.int()[:, None] + 1), top.int()[:, None]).to(torch.int16)
+    h[:, ::2] |= -(1 << 15)
+    h[:, 5] = top
+    h = h.view(torch.bfloat16)
+    h = torch.cat([h, h.flip(0)], 1).contiguous()
+    n = len(h)
+    seg = (torch.tensor([0], dtype=torch.int32, device="cuda"),
+           torch.tensor([n], dtype=torch.int32, device="cuda"), n)
+    _, q, s = ep.act_save(h, *seg)
+    cfg = ep.Config(n, 256, 1, 1, 1, 1, True)
+    layout = ep.get_layout(cfg, torch.zeros((n, 1), dtype=torch.int64, device="cuda"))
+    want_q, want_s, _ = ep.dispatch(cfg, layout, h)
+    assert torch.equal(s, want_s[:n])
+    nan = (want_q[:n] & 0x7F) == 0x7F
+    assert torch.equal((q & 0x7F) == 0x7F, nan) and torch.equal(q[~nan], want_q[:n][~nan])
