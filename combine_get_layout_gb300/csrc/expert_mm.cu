@@ -64,7 +64,7 @@ constexpr int kEpilogueWarps = 4, kCopyWarp = 4, kMmaWarp = 5, kClearWarp = 6;
 constexpr int kFirstConvertWarp = 7, kConvertWarps = 8;
 constexpr int kConvertGroups = 2;  // of warps, that take steps in turn
 constexpr int kPieces = 4;         // of 16 values a converting thread has in a step
-constexpr int kAhead = 2;          // steps of its own that it loads ahead
+constexpr int kAhead = 4;          // steps of its own whose scales it loads ahead
 static_assert(32 * kConvertWarps / kConvertGroups * kPieces * 16 == kMaxCols / 2 * kDepth);
 
 __host__ __device__ constexpr int threads_of(bool fp8) { return 32 * (kFirstConvertWarp + (fp8 ? kConvertWarps : 0)); }
@@ -82,7 +82,6 @@ struct MmParams {
   int n_tiles;        // by weights
   const int32_t *start, *end;
   __nv_bfloat16* out;
-  const uint8_t* xq;
   const float* xs;
   int x_width;        // features of an E4M3 row
   int ring_bytes;     // of the stages
@@ -100,6 +99,7 @@ struct Smem {
   uint64_t full[kMaxStages];       // of the first CTA: both CTAs' operands are there
   uint64_t empty[kMaxStages];      // the products have read this CTA's
   uint64_t last[kMaxStages];       // a last step along the rows has landed here
+  uint64_t raw[kMaxStages];        // E4M3 rows have landed here
   uint64_t acc_full[2];
   uint64_t acc_empty[2];           // of the first CTA: both have read it out
   uint64_t drained;
@@ -196,19 +196,20 @@ __device__ __forceinline__ void widen16(uint4 q, float scale, uint4& lo, uint4& 
     const uint16_t two = uint16_t(w[i / 2] >> (16 * (i % 2)));
     uint32_t h;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(two));
-    float a, b;
-    asm("{\n\t.reg .f16 l, u;\n\tmov.b32 {l, u}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, u;\n\t}"
-        : "=f"(a), "=f"(b)
-        : "r"(h));
-    a *= scale;
-    b *= scale;
+    uint32_t a, b;
+    asm("{\n\t.reg .f16 l, u;\n\t.reg .f32 x, y;\n\t.reg .b64 v, s;\n\t"
+        "mov.b32 {l, u}, %2;\n\tcvt.f32.f16 x, l;\n\tcvt.f32.f16 y, u;\n\t"
+        "mov.b64 v, {x, y};\n\tmov.b64 s, {%3, %3};\n\tmul.rn.f32x2 v, v, s;\n\t"
+        "mov.b64 {%0, %1}, v;\n\t}"
+        : "=r"(a), "=r"(b)
+        : "r"(h), "f"(scale));
     if (PART == kUpper)
-      r[i] = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+      r[i] = __byte_perm(a, b, 0x7632);
     else if (PART == kRest)
-      r[i] = pack_bf16x2(a - __uint_as_float(__float_as_uint(a) & 0xffff0000u),
-                         b - __uint_as_float(__float_as_uint(b) & 0xffff0000u));
+      r[i] = pack_bf16x2(__uint_as_float(a) - __uint_as_float(a & 0xffff0000u),
+                         __uint_as_float(b) - __uint_as_float(b & 0xffff0000u));
     else
-      r[i] = pack_bf16x2(a, b);
+      r[i] = pack_bf16x2(__uint_as_float(a), __uint_as_float(b));
   }
   lo = make_uint4(r[0], r[1], r[2], r[3]);
   hi = make_uint4(r[4], r[5], r[6], r[7]);
@@ -227,14 +228,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
   constexpr bool kAByFeature = MODE != kForward;      // inner dimension of A: features
   constexpr bool kBByFeature = MODE == kByWeights;
   constexpr int kRows = rows_of(FP8);
+  constexpr int kRawWidth = kBByFeature ? 128 : kDepth;   // E4M3 values of a row in a step
 
   if (warp == kCopyWarp && lane == 0) {
     prefetch_map(&maps.a);
-    if (!FP8) prefetch_map(&maps.b[0]);
+    prefetch_map(&maps.b[MODE == kByWeights ? 0 : 4]);
     for (int s = 0; s < kMaxStages; ++s) {
       mbar_init(&sm.full[s], FP8 ? 2 + 2 * kConvertWarps / kConvertGroups : 2);
       mbar_init(&sm.empty[s], 1);
       mbar_init(&sm.last[s], 1);
+      mbar_init(&sm.raw[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sm.acc_full[b], 1);
@@ -283,7 +286,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
     const int rows = round16(sm.most) / (FP8 ? 1 : 2);
     stage_bytes = kABytes + rows * (kDepth * 2);
   }
-  const int stages = min(kMaxStages, p.ring_bytes / stage_bytes);
+  // E4M3: a stage is always the same group's.  A group that skipped uses of a
+  // stage could take the one before last for the last (their parities are
+  // alike) where copies land out of order.
+  int stages = min(kMaxStages, p.ring_bytes / stage_bytes);
+  if (FP8) stages -= stages % kConvertGroups;
   tc_fence_before();
   cluster_sync();
   tc_fence_after();
@@ -329,16 +336,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
             tma_load_2d(a, &maps.a, bar, m0, it.row0 + k0);
             tma_load_2d(a + kPanel, &maps.a, bar, m0 + 64, it.row0 + k0);
           }
-          if (!FP8 && kBByFeature) {
-            for (int c = 0; c < half; c += 64)
-              tma_load_2d(b + c / 64 * kPanel, &maps.b[0], bar, it.c0 + col0 + c, it.row0 + k0);
-          } else if (!FP8) {
-            // boxes of the binary digits of the CTA's rows
+          const uint32_t b_bar = FP8 ? smem_addr(&sm.raw[at.s]) : bar;
+          if (FP8) mbar_arrive_expect_tx(&sm.raw[at.s], kRawWidth * (kBByFeature ? kDepth : half));
+          if (kBByFeature) {
+            for (int c = 0; c < half; c += FP8 ? 128 : 64)
+              tma_load_2d(b + c / 64 * kPanel, &maps.b[0], b_bar, it.c0 + col0 + c,
+                          it.row0 + k0);
+          } else {
+            // boxes of the binary digits of the CTA's rows; E4M3: all rows
+            constexpr int kPitch = FP8 ? kRawWidth : kDepth * 2;
             int r = 0;
 #pragma unroll
-            for (int i = 4; i >= 0; --i)
+            for (int i = 4; i >= (FP8 ? 1 : 0); --i)
               if (half & (8 << i)) {
-                tma_load_2d(b + r * 128, &maps.b[i], bar, k0, it.row0 + col0 + r);
+                tma_load_2d(b + r * kPitch, &maps.b[i], b_bar, k0,
+                            it.row0 + (FP8 ? 0 : col0) + r);
                 r += 8 << i;
               }
           }
@@ -350,8 +362,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
       record_error(p.err, ERRBIT_TIMEOUT);
       // the first CTA's barriers count the copies of both, which land before
       // the pair may end (the second CTA waits for the first one's end)
-      for (uint64_t i = n < uint64_t(stages) ? 0 : n - stages; rank == 0 && i < n; ++i)
-        if (!mbar_wait(&sm.full[i % stages], i / stages & 1, kWaitTimeoutNs))
+      for (uint64_t i = n < uint64_t(stages) ? 0 : n - stages; i < n; ++i)
+        if ((FP8 && !mbar_wait(&sm.raw[i % stages], i / stages & 1, kWaitTimeoutNs)) ||
+            (rank == 0 && !mbar_wait(&sm.full[i % stages], i / stages & 1, kWaitTimeoutNs)))
           record_error(p.err, ERRBIT_TIMEOUT_PENDING);
     }
     __syncwarp();
@@ -425,21 +438,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
     if (!ok && lane == 0) record_error(p.err, ERRBIT_TIMEOUT);
     __syncwarp();
   } else if (FP8 && warp >= kFirstConvertWarp) {
-    // Two groups of four warps take steps in turn, and load theirs two turns
-    // ahead, past the ends of tiles.
+    // Two groups of four warps take steps in turn; the rows' bytes come by
+    // tensor copies, their scales are loaded kAhead turns ahead, past the ends
+    // of tiles.
     constexpr int kThreads = 32 * kConvertWarps / kConvertGroups;
     const int group = (warp - kFirstConvertWarp) / (kConvertWarps / kConvertGroups);
     const int t = (threadIdx.x - kFirstConvertWarp * 32) % kThreads;
     // pieces of 16 values: forward, 4 of each of the rows for a step's 64
     // inputs; by weights, 8 of each of its 64 rows
-    constexpr int kOfRow = kBByFeature ? 8 : 4;
+    constexpr int kOfRow = kRawWidth / 16;
     const int row_t = t / kOfRow, c_t = t % kOfRow * 16;
     const int scales = p.x_width / 128;
-    uint4 q[kAhead][kPieces];
     float sc[kAhead][kPieces];
     int halves[kAhead];         // columns of the step's tile a CTA, 0 past the last one
+    int lefts[kAhead];          // rows of the segment from the step's first on
     int64_t idx = pair;
-    int kb = 0;
+    int kb = -1;
     Item it = {};
     bool more = idx < items;
     if (more) it = item_at<MODE, FP8, GATED>(p, table, idx);
@@ -452,62 +466,65 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
         if (more) it = item_at<MODE, FP8, GATED>(p, table, idx);
       } while (more && it.blocks == 0);
     };
-    const auto load = [&](uint4 (&to)[kPieces], float (&scale)[kPieces], int& half) {
+    const auto load = [&](float (&scale)[kPieces], int& half, int& left) {
       half = more ? it.cols / 2 : 0;
-      const int x = kBByFeature ? it.c0 + int(rank) * half + c_t : kb * kDepth + c_t;
-      const int row0 = kBByFeature ? kb * kDepth + row_t : row_t;
-      const bool in = more && x < p.x_width && (!kBByFeature || c_t < half);
-      const int64_t r0 = int64_t(it.row0) + row0;
-      const uint8_t* from = p.xq + r0 * p.x_width + x;
+      left = it.rows - (kBByFeature ? kb * kDepth : 0);
+      const int x = kBByFeature ? it.c0 + int(rank) * half : kb * kDepth;
+      const int64_t r0 = int64_t(it.row0) + it.rows - left + row_t;
       const float* s = p.xs + r0 * scales + x / 128;
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
         const int r = kThreads / kOfRow * i;
-        to[i] = make_uint4(0, 0, 0, 0);
-        scale[i] = 0.0f;
-        if (in && row0 + r < it.rows) {
-          to[i] = __ldg(reinterpret_cast<const uint4*>(from + int64_t(r) * p.x_width));
-          scale[i] = __ldg(s + int64_t(r) * scales);
-        }
+        scale[i] = more && row_t + r < left && x < p.x_width ? __ldg(s + int64_t(r) * scales) : 0.0f;
       }
       for (int g = 0; g < kConvertGroups; ++g) step();
     };
-    // to the first step, and this group's first
-    --kb;
-    for (int g = 0; g <= group; ++g) step();
+    for (int g = 0; g <= group; ++g) step();      // to this group's first
     for (int g = 0; g < group; ++g) at.next(stages);
 #pragma unroll
-    for (int d = 0; d < kAhead; ++d) load(q[d], sc[d], halves[d]);
+    for (int d = 0; d < kAhead; ++d) load(sc[d], halves[d], lefts[d]);
     bool ok = true, some = true;
     while (ok && some) {
 #pragma unroll
       for (int d = 0; d < kAhead; ++d) {
-        const int half = halves[d];
+        const int half = halves[d], left = lefts[d];
         some = half > 0;
         if (!some) break;
-        ok = mbar_wait(&sm.empty[at.s], at.phase ^ 1, kWaitTimeoutNs);
+        ok = mbar_wait(&sm.raw[at.s], at.phase, kWaitTimeoutNs);
         if (!ok) break;
-        uint8_t* b = ring + at.s * stage_bytes + kABytes + (kBByFeature ? c_t / 64 * kPanel : 0);
+        // the bytes lie where the operand comes to lie: the group takes them
+        // all out before it writes
+        uint8_t* to = ring + at.s * stage_bytes + kABytes;
+        uint4 q[kPieces];
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)
+          if (kBByFeature || row_t + kThreads / kOfRow * i < half)
+            q[i] = *reinterpret_cast<const uint4*>(to + (t + i * kThreads) * 16);
+        asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(kThreads) : "memory");
+        if (kBByFeature) to += c_t / 64 * kPanel;
         const int c = c_t % 64 / 8;
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
           const int row = row_t + kThreads / kOfRow * i;
           if (kBByFeature ? c_t >= half : row >= half) break;
           uint4 lo, hi;
-          if (kBByFeature)
-            widen16<kNearest>(q[d][i], sc[d][i], lo, hi);
-          else if (rank == 0)
-            widen16<kUpper>(q[d][i], sc[d][i], lo, hi);
-          else
-            widen16<kRest>(q[d][i], sc[d][i], lo, hi);
-          *reinterpret_cast<uint4*>(b + row * 128 + ((c ^ (row & 7)) * 16)) = lo;
-          *reinterpret_cast<uint4*>(b + row * 128 + (((c + 1) ^ (row & 7)) * 16)) = hi;
+          if (kBByFeature) {
+            // a row of another segment, or of none, may hold anything
+            if (row >= left) q[i] = make_uint4(0, 0, 0, 0);
+            widen16<kNearest>(q[i], sc[d][i], lo, hi);
+          } else if (rank == 0) {
+            widen16<kUpper>(q[i], sc[d][i], lo, hi);
+          } else {
+            widen16<kRest>(q[i], sc[d][i], lo, hi);
+          }
+          *reinterpret_cast<uint4*>(to + row * 128 + ((c ^ (row & 7)) * 16)) = lo;
+          *reinterpret_cast<uint4*>(to + row * 128 + (((c + 1) ^ (row & 7)) * 16)) = hi;
         }
         fence_async_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(at_rank(smem_addr(&sm.full[at.s]), 0));
         for (int g = 0; g < kConvertGroups; ++g) at.next(stages);
-        load(q[d], sc[d], halves[d]);
+        load(sc[d], halves[d], lefts[d]);
       }
     }
     if (!ok && lane == 0) record_error(p.err, ERRBIT_TIMEOUT);
@@ -712,6 +729,22 @@ cudaError_t encode(CUtensorMap* m, bool f32, const void* base, const uint64_t (&
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// E4M3 [rows, width] in boxes of `wide` columns by `high` rows.
+cudaError_t encode_bytes(CUtensorMap* m, const void* base, int rows, int width, int wide,
+                         int high) {
+  EncodeFn fn;
+  cudaError_t e = encoder(&fn);
+  if (e != cudaSuccess) return e;
+  const cuuint64_t n[2] = {cuuint64_t(width), cuuint64_t(rows)}, s[1] = {cuuint64_t(width)};
+  const cuuint32_t b[2] = {cuuint32_t(wide), cuuint32_t(high)}, step[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), n, s, b, step,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? cudaSuccess
+             : cudaErrorInvalidValue;
+}
+
 // [rows, width] in boxes of 64 columns by `high` rows.
 cudaError_t encode_rows(CUtensorMap* m, const void* base, int rows, int width, int high) {
   return encode<2>(m, false, base, {uint64_t(width), uint64_t(rows)}, {uint64_t(width)},
@@ -793,9 +826,10 @@ cudaError_t forward(const ep_expert_config* c, int cap, int num_rows, const void
     e = encode_weights(&maps.a, false, w, c->num_experts, N, H, kLanes);
   }
   if (c->x_fp8) {
-    p.xq = static_cast<const uint8_t*>(x);
     p.xs = x_scale;
     p.x_width = H;
+    for (int i = 1; i < 5 && e == cudaSuccess; ++i)
+      e = encode_bytes(&maps.b[i], x, cap, H, kDepth, 8 << i);
   } else {
     for (int i = 0; i < 5 && e == cudaSuccess; ++i)
       e = encode_rows(&maps.b[i], x, cap, H, 8 << i);
@@ -843,9 +877,9 @@ cudaError_t by_weights(const ep_expert_config* c, int cap, const void* dy, const
   cudaError_t e = encode_rows(&maps.a, dy, cap, p.M, kDepth);
   if (e == cudaSuccess) e = encode_weights(&maps.out, f32, dw, p.E, p.M, p.cols, 32);
   if (c->x_fp8) {
-    p.xq = static_cast<const uint8_t*>(x);
     p.xs = x_scale;
     p.x_width = p.cols;
+    if (e == cudaSuccess) e = encode_bytes(&maps.b[0], x, cap, p.cols, 128, kDepth);
   } else if (e == cudaSuccess) {
     e = encode_rows(&maps.b[0], x, cap, p.cols, kDepth);
   }
