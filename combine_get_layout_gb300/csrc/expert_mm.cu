@@ -40,7 +40,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
-#include <cmath>
+#include <type_traits>
 
 #include "../../include/ep.h"
 #include "ep_internal.h"
@@ -61,15 +61,19 @@ constexpr int kPanel = 64 * kDepth * 2;         // 64 features by 64 rows
 constexpr int kRowGroup = 8;                    // row tiles that share weight tiles in L2
 
 constexpr int kEpilogueWarps = 4, kCopyWarp = 4, kMmaWarp = 5, kClearWarp = 6;
-constexpr int kFirstConvertWarp = 7, kConvertWarps = 8;
-constexpr int kConvertGroups = 2;  // of warps, that take steps in turn
+constexpr int kFirstConvertWarp = 7, kConvertWarps = 12;
+constexpr int kConvertGroups = 3;  // of warps, that take steps in turn
 constexpr int kPieces = 4;         // of 16 values a converting thread has in a step
-constexpr int kAhead = 4;          // steps of its own whose scales it loads ahead
+constexpr int kAhead = 2;          // steps of its own whose scales it loads ahead
 static_assert(32 * kConvertWarps / kConvertGroups * kPieces * 16 == kMaxCols / 2 * kDepth);
 
 __host__ __device__ constexpr int threads_of(bool fp8) { return 32 * (kFirstConvertWarp + (fp8 ? kConvertWarps : 0)); }
 // Bytes that the epilogue's warps stage a tile's pieces in.
 __host__ __device__ constexpr int staging_of(Mode m) { return kEpilogueWarps * (m == kByWeights ? 8192 : 2560); }
+// E4M3: scales that the converting warps share.
+__host__ __device__ constexpr int scales_of(Mode m) {
+  return kConvertGroups * 2 * (m == kByWeights ? kDepth : kMaxCols / 2);
+}
 // Rows of a tile: two columns each for E4M3 rows of a forward product.
 __host__ __device__ constexpr int rows_of(bool fp8) { return fp8 ? kMaxCols / 2 : kMaxCols; }
 
@@ -188,9 +192,8 @@ enum Part { kNearest, kUpper, kRest };
 
 // 16 of them.
 template <Part PART>
-__device__ __forceinline__ void widen16(uint4 q, float scale, uint4& lo, uint4& hi) {
+__device__ __forceinline__ void widen16(uint4 q, float scale, uint32_t (&r)[8]) {
   const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-  uint32_t r[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const uint16_t two = uint16_t(w[i / 2] >> (16 * (i % 2)));
@@ -211,8 +214,47 @@ __device__ __forceinline__ void widen16(uint4 q, float scale, uint4& lo, uint4& 
     else
       r[i] = pack_bf16x2(__uint_as_float(a), __uint_as_float(b));
   }
-  lo = make_uint4(r[0], r[1], r[2], r[3]);
-  hi = make_uint4(r[4], r[5], r[6], r[7]);
+}
+
+// Out of line: rare, and the loop around it is to stay small (the kernel is
+// slowed by instruction fetch before anything else where it does not).
+template <Part PART>
+__device__ __noinline__ void widen16_apart(uint4 q, float scale, uint32_t (&r)[8]) {
+  widen16<PART>(q, scale, r);
+}
+
+// The two parts of 16 products without conversions.  Shifted four bits up, a
+// magnitude of E4M3 is that of a bf16 2^-120 as large.  Of the scale, times
+// 2^120, the first part takes its nearest number of four bits, by which any
+// E4M3 value is exact in bf16, the second what is left, rounded twice to 8
+// bits: together within 2^-12 of the product.  Scales of 128 and more (2^120
+// of which bf16 does not hold) and NaN go the way above.
+template <Part PART>
+__device__ __forceinline__ void part16(uint4 q, float scale, uint32_t (&r)[8]) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+  uint32_t nan = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) nan |= (w[i] & 0x7f7f7f7fu) + 0x01010101u;
+  if ((nan & 0x80808080u) != 0 || !(fabsf(scale) < 128.0f)) {
+    uint32_t apart[8];
+    widen16_apart<PART>(q, scale, apart);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = apart[i];
+    return;
+  }
+  const float first = __uint_as_float((__float_as_uint(scale) + 0x00080000u) & 0xfff00000u);
+  const float part = (PART == kUpper ? first : scale - first) * 0x1p120f;
+  const uint32_t both = pack_bf16x2(part, part);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t up = (w[i] & 0x80808080u) | (w[i] >> 4 & 0x07070707u);
+    const uint32_t low = w[i] << 4 & 0xf0f0f0f0u;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      asm("mul.rn.bf16x2 %0, %1, %2;"
+          : "=r"(r[2 * i + j])
+          : "r"(__byte_perm(low, up, j ? 0x7362 : 0x5140)), "r"(both));
+  }
 }
 
 template <Mode MODE, bool FP8, bool GATED, bool OUT32>
@@ -222,7 +264,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   uint8_t* staging = ring + p.ring_bytes;
   Smem& sm = *reinterpret_cast<Smem*>(staging + staging_of(MODE));
-  int* table = reinterpret_cast<int*>(&sm + 1);
+  float* scale_at = reinterpret_cast<float*>(&sm + 1);
+  int* table = reinterpret_cast<int*>(scale_at + (FP8 ? scales_of(MODE) : 0));
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const uint32_t rank = cluster_rank();
   constexpr bool kAByFeature = MODE != kForward;      // inner dimension of A: features
@@ -449,7 +492,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
     constexpr int kOfRow = kRawWidth / 16;
     const int row_t = t / kOfRow, c_t = t % kOfRow * 16;
     const int scales = p.x_width / 128;
-    float sc[kAhead][kPieces];
+    // one scale a thread, of its row, shared through two buffers a group
+    constexpr int kScaled = kBByFeature ? kDepth : kThreads;
+    float* const shared = scale_at + group * 2 * kScaled;
+    int turn = 0;
+    float sc[kAhead];
     int halves[kAhead];         // columns of the step's tile a CTA, 0 past the last one
     int lefts[kAhead];          // rows of the segment from the step's first on
     int64_t idx = pair;
@@ -466,17 +513,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
         if (more) it = item_at<MODE, FP8, GATED>(p, table, idx);
       } while (more && it.blocks == 0);
     };
-    const auto load = [&](float (&scale)[kPieces], int& half, int& left) {
+    const auto load = [&](float& scale, int& half, int& left) {
       half = more ? it.cols / 2 : 0;
       left = it.rows - (kBByFeature ? kb * kDepth : 0);
       const int x = kBByFeature ? it.c0 + int(rank) * half : kb * kDepth;
-      const int64_t r0 = int64_t(it.row0) + it.rows - left + row_t;
-      const float* s = p.xs + r0 * scales + x / 128;
-#pragma unroll
-      for (int i = 0; i < kPieces; ++i) {
-        const int r = kThreads / kOfRow * i;
-        scale[i] = more && row_t + r < left && x < p.x_width ? __ldg(s + int64_t(r) * scales) : 0.0f;
-      }
+      scale = 0.0f;
+      if (more && t < kScaled && t < left && x < p.x_width)
+        scale = __ldg(p.xs + (int64_t(it.row0) + it.rows - left + t) * scales + x / 128);
       for (int g = 0; g < kConvertGroups; ++g) step();
     };
     for (int g = 0; g <= group; ++g) step();      // to this group's first
@@ -484,49 +527,62 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
 #pragma unroll
     for (int d = 0; d < kAhead; ++d) load(sc[d], halves[d], lefts[d]);
     bool ok = true, some = true;
-    while (ok && some) {
+    const auto convert = [&](auto which) {
+      constexpr Part PART = decltype(which)::value;
+      while (ok && some) {
 #pragma unroll
-      for (int d = 0; d < kAhead; ++d) {
-        const int half = halves[d], left = lefts[d];
-        some = half > 0;
-        if (!some) break;
-        ok = mbar_wait(&sm.raw[at.s], at.phase, kWaitTimeoutNs);
-        if (!ok) break;
-        // the bytes lie where the operand comes to lie: the group takes them
-        // all out before it writes
-        uint8_t* to = ring + at.s * stage_bytes + kABytes;
-        uint4 q[kPieces];
+        for (int d = 0; d < kAhead; ++d) {
+          const int half = halves[d], left = lefts[d];
+          some = half > 0;
+          if (!some) break;
+          ok = mbar_wait(&sm.raw[at.s], at.phase, kWaitTimeoutNs);
+          if (!ok) break;
+          // the bytes lie where the operand comes to lie: the group takes them
+          // all out before it writes
+          uint8_t* to = ring + at.s * stage_bytes + kABytes;
+          uint4 q[kPieces];
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i)
-          if (kBByFeature || row_t + kThreads / kOfRow * i < half)
-            q[i] = *reinterpret_cast<const uint4*>(to + (t + i * kThreads) * 16);
-        asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(kThreads) : "memory");
-        if (kBByFeature) to += c_t / 64 * kPanel;
-        const int c = c_t % 64 / 8;
+          for (int i = 0; i < kPieces; ++i)
+            if (kBByFeature || row_t + kThreads / kOfRow * i < half)
+              q[i] = *reinterpret_cast<const uint4*>(to + (t + i * kThreads) * 16);
+          float* const mine = shared + turn * kScaled;
+          turn ^= 1;
+          if (t < kScaled) mine[t] = sc[d];
+          asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(kThreads) : "memory");
+          if (kBByFeature) to += c_t / 64 * kPanel;
+          const int c = c_t % 64 / 8;
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-          const int row = row_t + kThreads / kOfRow * i;
-          if (kBByFeature ? c_t >= half : row >= half) break;
-          uint4 lo, hi;
-          if (kBByFeature) {
-            // a row of another segment, or of none, may hold anything
-            if (row >= left) q[i] = make_uint4(0, 0, 0, 0);
-            widen16<kNearest>(q[i], sc[d][i], lo, hi);
-          } else if (rank == 0) {
-            widen16<kUpper>(q[i], sc[d][i], lo, hi);
-          } else {
-            widen16<kRest>(q[i], sc[d][i], lo, hi);
+          for (int i = 0; i < kPieces; ++i) {
+            const int row = row_t + kThreads / kOfRow * i;
+            if (kBByFeature ? c_t >= half : row >= half) break;
+            const float scale = mine[row];
+            uint32_t r[8];
+            if constexpr (PART == kNearest) {
+              // a row of another segment, or of none, may hold anything
+              if (row >= left) q[i] = make_uint4(0, 0, 0, 0);
+              widen16<PART>(q[i], scale, r);
+            } else {
+              part16<PART>(q[i], scale, r);
+            }
+            *reinterpret_cast<uint4*>(to + row * 128 + ((c ^ (row & 7)) * 16)) =
+                make_uint4(r[0], r[1], r[2], r[3]);
+            *reinterpret_cast<uint4*>(to + row * 128 + (((c + 1) ^ (row & 7)) * 16)) =
+                make_uint4(r[4], r[5], r[6], r[7]);
           }
-          *reinterpret_cast<uint4*>(to + row * 128 + ((c ^ (row & 7)) * 16)) = lo;
-          *reinterpret_cast<uint4*>(to + row * 128 + (((c + 1) ^ (row & 7)) * 16)) = hi;
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(at_rank(smem_addr(&sm.full[at.s]), 0));
+          for (int g = 0; g < kConvertGroups; ++g) at.next(stages);
+          load(sc[d], halves[d], lefts[d]);
         }
-        fence_async_shared();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(at_rank(smem_addr(&sm.full[at.s]), 0));
-        for (int g = 0; g < kConvertGroups; ++g) at.next(stages);
-        load(sc[d], halves[d], lefts[d]);
       }
-    }
+    };
+    if constexpr (kBByFeature)
+      convert(std::integral_constant<Part, kNearest>());
+    else if (rank == 0)
+      convert(std::integral_constant<Part, kUpper>());
+    else
+      convert(std::integral_constant<Part, kRest>());
     if (!ok && lane == 0) record_error(p.err, ERRBIT_TIMEOUT);
     __syncwarp();
   } else if (warp < kEpilogueWarps) {
@@ -762,9 +818,10 @@ cudaError_t encode_weights(CUtensorMap* m, bool f32, const void* base, int E, in
 // and the table of the most experts leave of 227 KiB.
 constexpr int kSmemLimit = 227 * 1024;
 
-constexpr int rest_bytes(Mode m, int table) {
-  return 1024 + staging_of(m) + int(sizeof(Smem)) + 4 * table;
+constexpr int rest_bytes(Mode m, bool fp8, int table) {
+  return 1024 + staging_of(m) + int(sizeof(Smem)) + 4 * ((fp8 ? scales_of(m) : 0) + table);
 }
+static_assert(kSmemLimit - rest_bytes(kByWeights, true, 0) >= 6 * (kABytes + kBBytes));
 
 template <Mode MODE, bool FP8, bool GATED, bool OUT32>
 cudaError_t launch(const MmMaps& maps, MmParams p, int64_t most_items, cudaStream_t s) {
@@ -779,7 +836,7 @@ cudaError_t launch(const MmMaps& maps, MmParams p, int64_t most_items, cudaStrea
     if (e != cudaSuccess) return e;
     if (dev < 64) raised.fetch_or(uint64_t(1) << dev, std::memory_order_release);
   }
-  const int rest = rest_bytes(MODE, MODE == kByWeights ? 0 : p.E + 1);
+  const int rest = rest_bytes(MODE, FP8, MODE == kByWeights ? 0 : p.E + 1);
   p.ring_bytes = (kSmemLimit - rest) / 1024 * 1024;
   const int64_t pairs = device_info().sm_count / 2;
   const int grid = 2 * int(most_items < pairs ? most_items : pairs);

@@ -685,7 +685,7 @@ EP_API int32_t ep_expert_w4(const ep_w4_config *cfg, int32_t cap, int32_t num_ro
  * ep_combine, with W_e [N, H] in bf16, and the gradients by the rows and by
  * the weights: for prompts, training, and decode with unquantised weights.
  * Any number of rows an expert, none among them.  Sums are fp32, rounded once
- * at the end.  E4M3 rows enter the product as value * scale to 16 bits, the
+ * at the end.  E4M3 rows enter the product as value * scale to 12 bits, the
  * weights' gradient as bf16(value * scale).  The same call gives the same
  * bits. */
 typedef struct {

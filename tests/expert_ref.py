@@ -57,10 +57,11 @@ def silu(g):
 
 def forward(x, w, gated, fp8=False):
     """(y, bound) of one expert's rows, the last rounding to bf16 included.  E4M3 rows enter in
-    two bf16 parts, whose sum is off by half a step of the second: 2^-16 of the value."""
+    two bf16 parts whose sum is off by up to 2^-12 of the value: the second, at most 2^-4 of
+    it, is rounded twice to 8 bits (of the scale's rest, and of the product)."""
     y, d = product(x, w)
     if fp8:
-        d = 2 * d + EPS * abs(y) + BF16 * BF16 * (abs(x) @ abs(w).T)
+        d = 2 * d + EPS * abs(y) + 2.0 ** -12 * (abs(x) @ abs(w).T)
     if gated:
         half = w.shape[0] // 2
         (g, u), (dg, du) = (y[:, :half], y[:, half:]), (d[:, :half], d[:, half:])
