@@ -257,6 +257,19 @@ __device__ __forceinline__ void part16(uint4 q, float scale, uint32_t (&r)[8]) {
   }
 }
 
+// A barrier of `threads` threads (whole warps): whether all of them are `ok`.
+// Each comes to it whether its own wait ran out or not, and all go on alike.
+__device__ __forceinline__ bool group_agrees(int id, int threads, bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.aligned.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(all)
+      : "r"(uint32_t(ok)), "r"(id), "r"(threads)
+      : "memory");
+  return all != 0;
+}
+
 template <Mode MODE, bool FP8, bool GATED, bool OUT32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
     expert_mm_kernel(const __grid_constant__ MmMaps maps, const MmParams p) {
@@ -536,9 +549,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
           some = half > 0;
           if (!some) break;
           ok = mbar_wait(&sm.raw[at.s], at.phase, kWaitTimeoutNs);
-          if (!ok) break;
-          // the bytes lie where the operand comes to lie: the group takes them
-          // all out before it writes
           uint8_t* to = ring + at.s * stage_bytes + kABytes;
           uint4 q[kPieces];
 #pragma unroll
@@ -548,7 +558,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
           float* const mine = shared + turn * kScaled;
           turn ^= 1;
           if (t < kScaled) mine[t] = sc[d];
-          asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(kThreads) : "memory");
+          ok = group_agrees(group + 1, kThreads, ok);
+          if (!ok) break;
           if (kBByFeature) to += c_t / 64 * kPanel;
           const int c = c_t % 64 / 8;
 #pragma unroll
