@@ -16,6 +16,7 @@
 #include "../../include/ep.h"
 #include "ep_internal.h"
 #include "fp8_quant.cuh"
+#include "segments.cuh"
 
 namespace ep {
 namespace {
@@ -37,28 +38,13 @@ struct ActParams {
 };
 
 // Rows of the experts before each one: table[E + 1] in shared memory.
-__device__ void count_rows(const ActParams& p, int* table) {
-  const int lane = threadIdx.x % 32;
-  for (int e = threadIdx.x; e < p.E; e += kThreads) {
-    const int s = min(max(__ldg(p.start + e), 0), p.cap);
-    table[e + 1] = max(min(__ldg(p.end + e), p.cap) - s, 0);
-  }
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    int64_t sum = 0;
-    for (int e0 = 0; e0 < p.E; e0 += 32) {
-      int64_t v = e0 + lane < p.E ? table[e0 + lane + 1] : 0;
-#pragma unroll
-      for (int o = 1; o < 32; o *= 2) {
-        const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += u;
-      }
-      if (e0 + lane < p.E) table[e0 + lane + 1] = int(min(sum + v, int64_t(INT32_MAX)));
-      sum += __shfl_sync(0xffffffffu, v, 31);
-    }
-    if (lane == 0) table[0] = 0;
-  }
-  __syncthreads();
+__device__ __forceinline__ void count_rows(const ActParams& p, int* table) {
+  __shared__ int64_t partial[kThreads / 32];
+  count_experts(p.E, table, partial, [&](int e) {
+    int first, rows;
+    clip_segment(p.start, p.end, p.cap, e, first, rows);
+    return rows;
+  });
 }
 
 // A warp's walk over the parts of all experts' rows, a step at a time.
@@ -72,16 +58,9 @@ struct Walk {
   __device__ __forceinline__ bool enter(const ActParams& p, const int* table) {
     if (r >= table[p.E]) return false;
     if (e < 0 || r < table[e] || r >= table[e + 1]) {
-      int lo = 0, hi = p.E;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (table[mid] <= r)
-          lo = mid;
-        else
-          hi = mid;
-      }
-      e = lo;
-      first = min(max(__ldg(p.start + e), 0), p.cap);
+      e = expert_of(table, p.E, r);
+      int rows;
+      clip_segment(p.start, p.end, p.cap, e, first, rows);
     }
     row = int64_t(first) + (r - table[e]);
     col = part * p.part;

@@ -44,6 +44,7 @@
 
 #include "../../include/ep.h"
 #include "ep_internal.h"
+#include "segments.cuh"
 #include "tcgen05.cuh"
 
 namespace ep {
@@ -119,11 +120,15 @@ struct Item {
   int blocks;         // steps of 64 along the reduction
 };
 
-// The segment of expert e, clipped to the rows that there are.
+// The segment of expert e.
 __device__ __forceinline__ void segment(const MmParams& p, int e, int& row0, int& rows) {
-  const int s = min(max(__ldg(p.start + e), 0), p.cap);
-  rows = max(min(__ldg(p.end + e), p.cap) - s, 0);
-  row0 = s;
+  clip_segment(p.start, p.end, p.cap, e, row0, rows);
+}
+
+// a / b for a >= 0, b > 0: 32-bit division where that does, a fifth of the
+// 64-bit one's instructions.
+__device__ __forceinline__ int64_t quotient(int64_t a, int b) {
+  return a >> 32 == 0 ? int64_t(uint32_t(a) / uint32_t(b)) : a / b;
 }
 
 __device__ __forceinline__ int round16(int n) { return (n + 15) & ~15; }
@@ -146,7 +151,7 @@ __device__ __forceinline__ Item item_at(const MmParams& p, const int* table, int
   constexpr int kFeatures = GATED ? kLanes : 2 * kLanes;      // of a pair
   if (MODE == kByWeights) {
     const int tiles = p.m_tiles * p.n_tiles;
-    it.e = int(idx / tiles);
+    it.e = int(quotient(idx, tiles));
     const int local = int(idx - int64_t(it.e) * tiles);
     it.m0 = local / p.n_tiles * kFeatures;
     it.c0 = local % p.n_tiles * kMaxCols;
@@ -156,19 +161,11 @@ __device__ __forceinline__ Item item_at(const MmParams& p, const int* table, int
     return it;
   }
   // the expert by its first row tile, then features outside, row tiles inside
-  const int q = int(idx / p.m_tiles);
-  int lo = 0, hi = p.E;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (table[mid] <= q)
-      lo = mid;
-    else
-      hi = mid;
-  }
+  const int lo = expert_of(table, p.E, quotient(idx, p.m_tiles));
   it.e = lo;
   const int tiles = table[lo + 1] - table[lo];
   int64_t local = idx - int64_t(table[lo]) * p.m_tiles;
-  const int group = int(local / (int64_t(kRowGroup) * p.m_tiles));
+  const int group = int(quotient(local, kRowGroup * p.m_tiles));
   local -= int64_t(group) * kRowGroup * p.m_tiles;
   const int in_group = min(kRowGroup, tiles - group * kRowGroup);
   it.m0 = int(local) / in_group * kFeatures;
@@ -313,29 +310,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
     // row tiles of the experts before each one, and the largest tile
     __syncthreads();
     int most = 0;
-    for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
+    count_experts(p.E, table, reinterpret_cast<int64_t*>(staging), [&](int e) {
       int row0, rows;
       segment(p, e, row0, rows);
-      table[e + 1] = int((int64_t(rows) + kRows - 1) / kRows);
       most = max(most, min(rows, kRows));
-    }
+      return int((int64_t(rows) + kRows - 1) / kRows);
+    });
     most = __reduce_max_sync(0xffffffffu, most);
     if (lane == 0) atomicMax(&sm.most, most);
-    __syncthreads();
-    if (warp == 0) {
-      int64_t sum = 0;
-      for (int e0 = 0; e0 < p.E; e0 += 32) {
-        int64_t v = e0 + lane < p.E ? table[e0 + lane + 1] : 0;
-#pragma unroll
-        for (int o = 1; o < 32; o *= 2) {
-          const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
-          if (lane >= o) v += u;
-        }
-        if (e0 + lane < p.E) table[e0 + lane + 1] = int(min(sum + v, int64_t(INT32_MAX)));
-        sum += __shfl_sync(0xffffffffu, v, 31);
-      }
-      if (lane == 0) table[0] = 0;
-    }
     __syncthreads();
     items = int64_t(table[p.E]) * p.m_tiles;
     // E4M3: all rows in each CTA, else half of them; in groups of eight
