@@ -59,6 +59,7 @@ constexpr int kMaxStages = 12;
 constexpr int kABytes = kLanes * kDepth * 2;
 constexpr int kBBytes = kMaxCols / 2 * kDepth * 2;      // a CTA's half, at most
 constexpr int kPanel = 64 * kDepth * 2;         // 64 features by 64 rows
+constexpr uint64_t kStepNs = 4000;              // far above what a stage takes
 constexpr int kRowGroup = 8;                    // row tiles that share weight tiles in L2
 
 constexpr int kEpilogueWarps = 4, kCopyWarp = 4, kMmaWarp = 5, kClearWarp = 6;
@@ -179,6 +180,13 @@ __device__ __forceinline__ Item item_at(const MmParams& p, const int* table, int
   it.c0 = 0;
   it.blocks = (p.depth + kDepth - 1) / kDepth;
   return it;
+}
+
+// mbar_wait for something that so many steps of a stage come before.
+__device__ __forceinline__ bool wait_for_steps(uint64_t* bar, uint32_t parity, uint64_t steps) {
+  for (uint64_t i = 0; i <= steps * kStepNs / kWaitTimeoutNs; ++i)
+    if (mbar_wait(bar, parity, kWaitTimeoutNs)) return true;
+  return false;
 }
 
 __device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
@@ -454,13 +462,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
     // take steps of 16 rows, and this CTA's operands are zero up to a step's end.
     bool ok = true;
     uint32_t phases = 0;
+    uint64_t passed = 0;      // steps since the last wait
     for (int64_t idx = pair; ok && idx < items; idx += pairs) {
       const Item it = item_at<MODE, FP8, GATED>(p, table, idx);
-      for (int kb = 0; kb < it.blocks; ++kb, at.next(stages)) {
+      for (int kb = 0; kb < it.blocks; ++kb, ++passed, at.next(stages)) {
         const int left = it.rows - kb * kDepth;
         if (left >= kDepth) continue;
-        ok = mbar_wait(&sm.last[at.s], phases >> at.s & 1, kWaitTimeoutNs);
+        // all steps before pass meanwhile
+        ok = wait_for_steps(&sm.last[at.s], phases >> at.s & 1, passed);
         if (!ok) break;
+        passed = 0;
         phases ^= 1u << at.s;
         uint8_t* a = ring + at.s * stage_bytes;
         const int panels = kLanes / 64 + (FP8 ? 0 : it.cols / 128);
@@ -588,9 +599,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
       const uint32_t buf = tile & 1;
       const uint32_t acc = tmem + buf * kMaxCols + (uint32_t(warp * 32) << 16);
       if (it.blocks > 0) {
-        // a tile's whole reduction may pass before: under 4 us a step
-        ok = mbar_wait(&sm.acc_full[buf], tile / 2 & 1,
-                               kWaitTimeoutNs + uint64_t(it.blocks) * 4000);
+        // the tile's whole reduction may pass before
+        ok = wait_for_steps(&sm.acc_full[buf], tile / 2 & 1, it.blocks);
         if (!ok) break;
         tc_fence_after();
       }

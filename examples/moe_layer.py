@@ -3,11 +3,13 @@
 ``decode_step``: router gate -> layout and FP8 dispatch -> experts with 4-bit weights (gate and
 up with the gated activation, then down) -> combine.  ``router_training_step``: router gate with
 the balance loss -> dispatch and combine -> gradients of both back to the router's logits.
+``training_step``: the whole layer with bf16 experts, forward and backward; the rows of the FP8
+dispatch and the activation's input are kept in 8 bits for the weights' gradients.
 
     python examples/moe_layer.py [--tokens 128] [--hidden 7168] [--inner 2048] [--experts 256]
-                                 [--topk 8] [--steps 50]
+                                 [--topk 8] [--steps 50] [--train]
 
-runs both on random weights, compares them with plain torch and prints the time of a step.
+runs the first two, or with --train the third, on random weights, compares them with plain torch and prints the time of a step.
 """
 
 from __future__ import annotations
@@ -124,6 +126,65 @@ def training_reference(K, x, logits, factors, dy, grad_loss):
     return y.detach(), loss.detach(), xs.grad, l.grad
 
 
+class TrainedExperts:
+    """Gate-up and down matrices of E experts in bf16."""
+
+    def __init__(self, num_experts, hidden, inner, seed=0):
+        gen = torch.Generator(device="cuda").manual_seed(seed)
+        self.up_cfg = ep.ExpertConfig(num_experts, hidden, 2 * inner, x_fp8=True)
+        self.down_cfg = ep.ExpertConfig(num_experts, inner, hidden)
+        self.up, self.down = (
+            torch.empty((num_experts, n, h), dtype=torch.bfloat16, device="cuda").normal_(
+                0, h ** -0.5, generator=gen) for n, h in ((2 * inner, hidden), (hidden, inner)))
+
+
+def training_step(cfg, router, experts, x, logits, dy, grad_loss, layout=None):
+    """The layer's forward and backward pass for the gradient dy of y and the coefficients grad_loss
+    of the balance and z losses (cfg: FP8 dispatch).  Returns (y, loss, grad_x, grad_logits, grad_up,
+    grad_down)."""
+    e = experts
+    idx, w, count, _, tokens, loss = ep.route_balance(router, logits)
+    layout = ep.get_layout(cfg, idx, layout)
+    seg = layout.expert_start, layout.expert_end, idx.numel()
+    rows, scale, _ = ep.dispatch(cfg, layout, x)
+    h = ep.expert_mm(e.up_cfg, rows, e.up, *seg, x_scale=scale, err=layout.err)
+    a, h_q, h_scale = ep.act_save(h, *seg)
+    out = ep.expert_mm(e.down_cfg, a, e.down, *seg, err=layout.err)
+    y = ep.combine(cfg, layout, out, w)
+    del h, a       # rows, scale, h_q and h_scale are what the backward pass keeps, and out
+    grad_out, grad_w = ep.combine_backward(cfg, layout, dy, w, out)
+    grad_a, _ = ep.expert_mm_backward(e.down_cfg, grad_out, *seg, w=e.down, err=layout.err)
+    grad_h, a = ep.act_backward(grad_a, h_q, h_scale, *seg)
+    _, grad_down = ep.expert_mm_backward(e.down_cfg, grad_out, *seg, x=a, err=layout.err)
+    grad_rows, grad_up = ep.expert_mm_backward(e.up_cfg, grad_h, *seg, w=e.up, x=rows,
+                                               x_scale=scale, err=layout.err)
+    grad_x, _ = ep.dispatch_backward(cfg, layout, grad_rows)
+    grad_logits = ep.route_backward(router, logits, idx, grad_w, None, None, count, tokens,
+                                    grad_loss)
+    return y, loss, grad_x, grad_logits, grad_up, grad_down
+
+
+def layer_reference(K, experts, x, logits, dy, grad_loss):
+    """The same by autograd in fp64 from unquantised rows and activations."""
+    l = logits.double().requires_grad_(True)
+    xs = x.double().requires_grad_(True)
+    up, down = (m.double().requires_grad_(True) for m in (experts.up, experts.down))
+    T, E = l.shape
+    p = torch.softmax(l, 1)
+    s, idx = p.topk(K, 1)
+    w = s / s.sum(1, keepdim=True)
+    y = torch.zeros_like(xs)
+    for e in idx.unique().tolist():
+        t, k = (idx == e).nonzero(as_tuple=True)
+        gate, value = (xs[t] @ up[e].T).chunk(2, -1)
+        out = torch.nn.functional.silu(gate) * value @ down[e].T
+        y = y.index_add(0, t, out * w[t, k, None])
+    share = torch.bincount(idx.flatten(), minlength=E).double() * E / (K * T)
+    loss = torch.stack([(share * p.mean(0)).sum(), torch.logsumexp(l, 1).square().mean()])
+    ((y * dy.double()).sum() + (loss * grad_loss.double()).sum()).backward()
+    return y.detach(), loss.detach(), xs.grad, l.grad, up.grad, down.grad
+
+
 def _clock(step, steps):
     for _ in range(5):
         step()
@@ -164,10 +225,37 @@ def run(tokens=128, hidden=7168, inner=2048, experts=256, topk=8, steps=50):
     return out
 
 
+def run_training(tokens=4096, hidden=7168, inner=2048, experts=256, topk=8, steps=10, check=True):
+    """The whole layer's training step; returns its time and, with `check`, its errors (norm of the
+    difference over the norm; the fp64 reference is for small layers)."""
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    x, dy = (torch.randn((tokens, hidden), device="cuda", generator=gen).bfloat16()
+             for _ in range(2))
+    logits = torch.randn((tokens, experts), device="cuda", generator=gen)
+    grad_loss = torch.tensor([0.01, 0.001], device="cuda")
+    cfg = ep.Config(tokens, hidden, topk, experts, 1, use_fp8_dispatch=True)
+    e = TrainedExperts(experts, hidden, inner)
+    a = cfg, ep.RouterConfig(experts, topk), e, x, logits, dy, grad_loss
+    layout = ep.Layout(cfg)
+    got, out = training_step(*a, layout=layout), {}
+    assert ep.check_error(layout) == ep.EP_OK
+    if check:
+        want = layer_reference(topk, e, x, logits, dy, grad_loss)
+        names = "y", "loss", "grad_x", "grad_logits", "grad_up", "grad_down"
+        for name, g, r in zip(names, got, want):
+            out[name + "_error"] = float((g.double() - r).norm() / r.norm())
+    del got
+    out["us"] = _clock(lambda: training_step(*a, layout=layout), steps)
+    return out
+
+
 if __name__ == "__main__":
     ap = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     for name, default in (("tokens", 128), ("hidden", 7168), ("inner", 2048), ("experts", 256),
                           ("topk", 8), ("steps", 50)):
         ap.add_argument("--" + name, type=int, default=default)
-    for k, v in run(**vars(ap.parse_args())).items():
+    ap.add_argument("--train", action="store_true", help="the bf16 layer's training step, timed")
+    args = vars(ap.parse_args())
+    train = args.pop("train")
+    for k, v in (run_training(check=False, **args) if train else run(**args)).items():
         print("%-28s %.6g" % (k, v))
