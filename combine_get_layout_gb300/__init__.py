@@ -72,6 +72,7 @@ ABI_SYMBOLS = (
     "ep_expert_w4",
     "ep_expert_mm",
     "ep_expert_mm_backward",
+    "ep_selftest_expert_timeout",
     "ep_act_save",
     "ep_act_backward",
     "ep_check_error",
@@ -217,6 +218,8 @@ def _load():
     L.ep_expert_w4.argtypes = [P(EpW4Config), i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp]
     L.ep_expert_mm.restype = i32
     L.ep_expert_mm.argtypes = [P(EpExpertConfig), i32, i32, vp, vp, vp, vp, vp, vp, vp, vp]
+    L.ep_selftest_expert_timeout.restype = i32
+    L.ep_selftest_expert_timeout.argtypes = L.ep_expert_mm.argtypes
     L.ep_expert_mm_backward.restype = i32
     L.ep_expert_mm_backward.argtypes = [P(EpExpertConfig), i32, i32, vp, vp, vp, vp, vp, vp, vp,
                                         vp, i32, vp, vp]
@@ -411,6 +414,12 @@ def ep_expert_mm(cfg, cap, num_rows, d_x, d_x_scale, d_w, d_expert_start, d_expe
                  d_err, stream) -> int:
     return _lib.ep_expert_mm(cfg, cap, num_rows, d_x, d_x_scale, d_w, d_expert_start,
                              d_expert_end, d_out, d_err, stream)
+
+
+def ep_selftest_expert_timeout(cfg, cap, num_rows, d_x, d_x_scale, d_w, d_expert_start,
+                               d_expert_end, d_out, d_err, stream) -> int:
+    return _lib.ep_selftest_expert_timeout(cfg, cap, num_rows, d_x, d_x_scale, d_w,
+                                           d_expert_start, d_expert_end, d_out, d_err, stream)
 
 
 def ep_expert_mm_backward(cfg, cap, num_rows, d_grad_out, d_w, d_x, d_x_scale, d_expert_start,

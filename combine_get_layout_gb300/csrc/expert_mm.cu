@@ -20,8 +20,8 @@
 // operand byte is read from there half as often, and its half of the
 // features' accumulator.  One persistent pair on two SMs, warps in roles: four
 // read accumulators out, one issues tensor copies (TMA), one (of the first
-// CTA) the products, four turn E4M3 rows into bf16 operands where the rows are
-// in 8 bits, and one clears what a last step along the rows must not see.
+// CTA) the products, twelve turn E4M3 rows into bf16 operands where the rows
+// are in 8 bits, and one clears what a last step along the rows must not see.
 // Operand tiles, 64 of the reduction each, pass through a ring of stages in
 // shared memory, as many as fit for the columns that the experts' rows need;
 // two accumulators alternate in tensor memory, so that one tile's epilogue
@@ -29,12 +29,13 @@
 //
 // E4M3 rows: the scale changes along the reduction (every 128 inputs), so it
 // cannot be applied to a sum.  Forward, value * scale enters as two bf16
-// parts, its upper 16 bits and the rest: the first CTA's
-// columns are the first parts, the second's the rests, and the epilogue adds
-// the two sums.  That halves the rows a tile holds; the weights are what costs
-// at the sizes that prompts and decode have.  dW takes bf16(value * scale)
-// alone, one rounding of 2^-9 of the value at most, as rows have that were
-// never quantised: there the products cost, and two parts would double them.
+// parts, 12 bits of it together: the first CTA's columns are the first parts,
+// the second's the others, and the epilogue adds the two sums.  That halves
+// the rows a tile holds; the weights are what costs at the sizes that prompts
+// and decode have.  dW takes bf16(value * scale) alone, one rounding of 2^-9
+// of the value at most, as rows have that were never quantised: there the
+// products cost, and two parts would double them.
+//
 // Sums are fp32 in tensor memory, rounded once on the way out.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -93,6 +94,7 @@ struct MmParams {
   int ring_bytes;     // of the stages
   int32_t* err;
   bool add;           // by weights: to what is there
+  bool stall;         // self-test: the first pair's copies never come
 };
 
 struct MmMaps {
@@ -175,7 +177,8 @@ __device__ __forceinline__ Item item_at(const MmParams& p, const int* table, int
   segment(p, lo, row0, rows);
   const int per = round16(int((int64_t(rows) + tiles - 1) / tiles));
   it.row0 = row0 + tile * per;
-  it.rows = min(per, rows - tile * per);
+  // (a table that came to its limit has fewer tiles than the rows need)
+  it.rows = min(min(per, rows_of(FP8)), rows - tile * per);
   it.cols = round16(max(it.rows, 1)) * (FP8 ? 2 : 1);
   it.c0 = 0;
   it.blocks = (p.depth + kDepth - 1) / kDepth;
@@ -308,8 +311,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
     sm.most = 0;
     fence_mbar_init();
   }
-  if (warp == kMmaWarp) tmem_alloc(&sm.tmem, 2 * kMaxCols);
   pdl_wait();
+  // not before: the kernel ahead may still want tensor memory of its own
+  if (warp == kMmaWarp) tmem_alloc(&sm.tmem, 2 * kMaxCols);
   int64_t items;
   int stage_bytes = kABytes + kBBytes;
   if (MODE == kByWeights) {
@@ -345,7 +349,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
   Ring at;
 
   if (warp == kCopyWarp) {
-    bool ok = true;
+    bool ok = !p.stall || pair != 0;
     uint64_t n = 0;      // stages filled so far
     for (int64_t idx = pair; ok && idx < items; idx += pairs) {
       const Item it = item_at<MODE, FP8, GATED>(p, table, idx);
@@ -865,8 +869,9 @@ MmParams params(const ep_expert_config* cfg, int cap, const int32_t* start, cons
 
 cudaError_t forward(const ep_expert_config* c, int cap, int num_rows, const void* x,
                     const float* x_scale, const void* w, const int32_t* start, const int32_t* end,
-                    void* out, int32_t* err, cudaStream_t s) {
+                    void* out, int32_t* err, cudaStream_t s, bool stall = false) {
   MmParams p = params(c, cap, start, end, err);
+  p.stall = stall;
   const int H = c->in_features, N = c->out_features, I = N / 2;
   const int features = c->gated ? kLanes : 2 * kLanes;
   p.M = c->gated ? I : N;
@@ -972,6 +977,19 @@ int32_t ep_expert_mm(const ep_expert_config* cfg, int32_t cap, int32_t num_rows,
   if (cap == 0 || num_rows == 0) return EP_OK;
   return status(forward(cfg, cap, num_rows, d_x, d_x_scale, d_w, d_expert_start, d_expert_end,
                         d_out, d_err, static_cast<cudaStream_t>(stream)));
+}
+
+int32_t ep_selftest_expert_timeout(const ep_expert_config* cfg, int32_t cap, int32_t num_rows,
+                                   const void* d_x, const float* d_x_scale, const void* d_w,
+                                   const int32_t* d_expert_start, const int32_t* d_expert_end,
+                                   void* d_out, int32_t* d_err, void* stream) {
+  if (!config_ok(cfg) || cap < 1 || num_rows < 1) return EP_ERR_INVALID_ARG;
+  if (!aligned(d_w) || !aligned(d_expert_start) || !aligned(d_expert_end) || !aligned(d_x) ||
+      !aligned(d_out) || !aligned(d_err))
+    return EP_ERR_INVALID_ARG;
+  if (cfg->x_fp8 ? !aligned(d_x_scale) : d_x_scale != nullptr) return EP_ERR_INVALID_ARG;
+  return status(forward(cfg, cap, num_rows, d_x, d_x_scale, d_w, d_expert_start, d_expert_end,
+                        d_out, d_err, static_cast<cudaStream_t>(stream), true));
 }
 
 int32_t ep_expert_mm_backward(const ep_expert_config* cfg, int32_t cap, int32_t num_rows,

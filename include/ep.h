@@ -706,8 +706,8 @@ typedef struct {
  *   rows [N/2, N) the up matrix's.
  * d_expert_start, d_expert_end: device int32 [E] at least, a layout's: expert
  *   e owns rows [start[e], end[e]), clipped to [0, cap); none when empty.
- * d_out: device bf16 [cap, N] ([cap, N/2] when gated); rows of no expert
- *   are not written.
+ * d_out: device bf16 [cap, N] ([cap, N/2] when gated), apart from the
+ *   inputs; rows of no expert are not written.
  * d_err: a layout's error word (device int32), or NULL: a wait inside the
  *   kernel that gave up is recorded there (EP_ERR_TIMEOUT by
  *   ep_check_error; the outputs are then undefined).
@@ -717,6 +717,18 @@ EP_API int32_t ep_expert_mm(const ep_expert_config *cfg, int32_t cap, int32_t nu
                             const void *d_x, const float *d_x_scale, const void *d_w,
                             const int32_t *d_expert_start, const int32_t *d_expert_end,
                             void *d_out, int32_t *d_err, void *stream);
+
+/* Self-test: ep_expert_mm of which one pair of CTAs never gets its first
+ * operands.  Every wait behind them gives up after a second, the kernel ends,
+ * and d_err (device int32, not NULL) holds the timeout; d_out is undefined.
+ * Other arguments as in ep_expert_mm, with at least one row.  Returns EP_OK
+ * when launched, or an error. */
+EP_API int32_t ep_selftest_expert_timeout(const ep_expert_config *cfg, int32_t cap,
+                                          int32_t num_rows, const void *d_x,
+                                          const float *d_x_scale, const void *d_w,
+                                          const int32_t *d_expert_start,
+                                          const int32_t *d_expert_end, void *d_out,
+                                          int32_t *d_err, void *stream);
 
 /* Types of the weights' gradient. */
 #define EP_GRAD_BF16 0

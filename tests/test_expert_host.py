@@ -74,6 +74,9 @@ def test_product_arguments_rejected(ep):
          [(0, None), (1, -1), (2, -1), (3, None), (3, M), (4, A), (5, None), (5, M), (6, None),
           (6, M), (7, None), (7, M), (8, None), (8, M), (9, M)])
     vary(ep.ep_expert_mm, ep, [q, 4, 4, A, A, A, A, A, A, None, None], [(4, None), (4, M)])
+    vary(ep.ep_selftest_expert_timeout, ep, [c, 4, 4, A, None, A, A, A, A, A, None],
+         [(0, None), (1, 0), (2, 0)] + [(i, v) for i in (3, 5, 6, 7, 8, 9) for v in (None, M)]
+         + [(4, A)])
     assert ep.ep_expert_mm(c, 0, 5, None, None, A, A, A, None, None, None) == ep.EP_OK
     assert ep.ep_expert_mm(c, 5, 0, A, None, A, A, A, A, None, None) == ep.EP_OK
 

@@ -309,3 +309,23 @@ def test_rows_past_32_bit_offsets(ep):
         assert (abs(ref.f64(gx[rows]) - y) <= err).all()
         y, err = ref.by_weights(ref.f64(dy[rows]), ref.f64(x[rows]), False)
         assert (abs(ref.f64(gw[e]) - y) <= err).all()
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(gated=True), dict(fp8=True)], ids=str)
+def test_waits_that_run_out_are_reported(ep, kw):
+    """Copies that never come: the kernel ends by itself, the error word says so, and the next call
+    is right."""
+    case = Case(ep, [40, 3], 1152, 320, **kw)
+    err, out = torch.zeros(4, dtype=torch.int32, device="cuda"), case.out(case.cfg.out_width)
+    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    stream = torch.cuda.current_stream().cuda_stream
+    torch.cuda.synchronize()
+    st = ep.ep_selftest_expert_timeout(case.cfg.c(), case.cap, case.rows, ptr(case.dx),
+                                       ptr(case.dscale), ptr(case.dw), ptr(case.dstart),
+                                       ptr(case.dend), ptr(out), ptr(err), stream)
+    assert st == ep.EP_OK
+    torch.cuda.synchronize()
+    assert err[0].item() & 4 and (err[1:] == 0).all()
+    err.zero_()
+    case.check_forward(case.forward(ep, err=err))
+    assert (err == 0).all()
