@@ -32,9 +32,10 @@
 // parts, 12 bits of it together: the first CTA's columns are the first parts,
 // the second's the others, and the epilogue adds the two sums.  That halves
 // the rows a tile holds; the weights are what costs at the sizes that prompts
-// and decode have.  dW takes bf16(value * scale) alone, one rounding of 2^-9
-// of the value at most, as rows have that were never quantised: there the
-// products cost, and two parts would double them.
+// and decode have.  A dW in fp32 takes two parts too, 17 bits together.  A dW
+// in bf16 takes bf16(value * scale) alone, one rounding of 2^-9 of the value
+// at most, as rows have that were never quantised and as its own sums get at
+// the end: there the products cost, and two parts would double them.
 //
 // Sums are fp32 in tensor memory, rounded once on the way out.
 #include <cuda_bf16.h>
@@ -77,8 +78,12 @@ __host__ __device__ constexpr int staging_of(Mode m) { return kEpilogueWarps * (
 __host__ __device__ constexpr int scales_of(Mode m) {
   return kConvertGroups * 2 * (m == kByWeights ? kDepth : kMaxCols / 2);
 }
-// Rows of a tile: two columns each for E4M3 rows of a forward product.
-__host__ __device__ constexpr int rows_of(bool fp8) { return fp8 ? kMaxCols / 2 : kMaxCols; }
+// Whether E4M3 values enter as two bf16 parts, with a column each.
+__host__ __device__ constexpr bool in_two_parts(Mode m, bool fp8, bool out32) {
+  return fp8 && (m == kForward || out32);
+}
+// Rows of a tile (by weights: features of its N side).
+__host__ __device__ constexpr int rows_of(bool two) { return two ? kMaxCols / 2 : kMaxCols; }
 
 struct MmParams {
   int E, cap;
@@ -148,7 +153,7 @@ struct Ring {
   }
 };
 
-template <Mode MODE, bool FP8, bool GATED>
+template <Mode MODE, bool TWO, bool GATED>
 __device__ __forceinline__ Item item_at(const MmParams& p, const int* table, int64_t idx) {
   Item it;
   constexpr int kFeatures = GATED ? kLanes : 2 * kLanes;      // of a pair
@@ -157,8 +162,8 @@ __device__ __forceinline__ Item item_at(const MmParams& p, const int* table, int
     it.e = int(quotient(idx, tiles));
     const int local = int(idx - int64_t(it.e) * tiles);
     it.m0 = local / p.n_tiles * kFeatures;
-    it.c0 = local % p.n_tiles * kMaxCols;
-    it.cols = p.cols - it.c0 > kMaxCols / 2 ? kMaxCols : kMaxCols / 2;
+    it.c0 = local % p.n_tiles * rows_of(TWO);
+    it.cols = p.cols - it.c0 > rows_of(TWO) / 2 ? kMaxCols : kMaxCols / 2;
     segment(p, it.e, it.row0, it.rows);
     it.blocks = int((int64_t(it.rows) + kDepth - 1) / kDepth);
     return it;
@@ -178,8 +183,8 @@ __device__ __forceinline__ Item item_at(const MmParams& p, const int* table, int
   const int per = round16(int((int64_t(rows) + tiles - 1) / tiles));
   it.row0 = row0 + tile * per;
   // (a table that came to its limit has fewer tiles than the rows need)
-  it.rows = min(min(per, rows_of(FP8)), rows - tile * per);
-  it.cols = round16(max(it.rows, 1)) * (FP8 ? 2 : 1);
+  it.rows = min(min(per, rows_of(TWO)), rows - tile * per);
+  it.cols = round16(max(it.rows, 1)) * (TWO ? 2 : 1);
   it.c0 = 0;
   it.blocks = (p.depth + kDepth - 1) / kDepth;
   return it;
@@ -194,9 +199,9 @@ __device__ __forceinline__ bool wait_for_steps(uint64_t* bar, uint32_t parity, u
 
 __device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
 
-// How E4M3 values times their scale become bf16: by the nearest, or in two
-// parts, the upper 16 bits and the rest.
-enum Part { kNearest, kUpper, kRest };
+// How E4M3 values times their scale become bf16: the nearest, or what that
+// leaves.
+enum Part { kNearest, kRest };
 
 // 16 of them.
 template <Part PART>
@@ -214,13 +219,9 @@ __device__ __forceinline__ void widen16(uint4 q, float scale, uint32_t (&r)[8]) 
         "mov.b64 {%0, %1}, v;\n\t}"
         : "=r"(a), "=r"(b)
         : "r"(h), "f"(scale));
-    if (PART == kUpper)
-      r[i] = __byte_perm(a, b, 0x7632);
-    else if (PART == kRest)
-      r[i] = pack_bf16x2(__uint_as_float(a) - __uint_as_float(a & 0xffff0000u),
-                         __uint_as_float(b) - __uint_as_float(b & 0xffff0000u));
-    else
-      r[i] = pack_bf16x2(__uint_as_float(a), __uint_as_float(b));
+    const float x = __uint_as_float(a), y = __uint_as_float(b);
+    r[i] = pack_bf16x2(x, y);
+    if (PART == kRest) r[i] = pack_bf16x2(x - bf16_lo(r[i]), y - bf16_hi(r[i]));
   }
 }
 
@@ -251,7 +252,7 @@ __device__ __forceinline__ void part16(uint4 q, float scale, uint32_t (&r)[8]) {
     return;
   }
   const float first = __uint_as_float((__float_as_uint(scale) + 0x00080000u) & 0xfff00000u);
-  const float part = (PART == kUpper ? first : scale - first) * 0x1p120f;
+  const float part = (PART == kNearest ? first : scale - first) * 0x1p120f;
   const uint32_t both = pack_bf16x2(part, part);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -291,7 +292,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
   const uint32_t rank = cluster_rank();
   constexpr bool kAByFeature = MODE != kForward;      // inner dimension of A: features
   constexpr bool kBByFeature = MODE == kByWeights;
-  constexpr int kRows = rows_of(FP8);
+  constexpr bool kTwo = in_two_parts(MODE, FP8, OUT32);
+  constexpr int kRows = rows_of(kTwo);
   constexpr int kRawWidth = kBByFeature ? 128 : kDepth;   // E4M3 values of a row in a step
 
   if (warp == kCopyWarp && lane == 0) {
@@ -352,12 +354,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
     bool ok = !p.stall || pair != 0;
     uint64_t n = 0;      // stages filled so far
     for (int64_t idx = pair; ok && idx < items; idx += pairs) {
-      const Item it = item_at<MODE, FP8, GATED>(p, table, idx);
+      const Item it = item_at<MODE, kTwo, GATED>(p, table, idx);
       const int half = it.cols / 2;
       // bytes of this CTA's copies into a stage
       const int bytes = kABytes + (FP8 ? 0 : half * kDepth * 2);
       const int m0 = it.m0 + int(rank) * (GATED ? kLanes / 2 : kLanes);
-      const int col0 = int(rank) * half;
+      const int col0 = kTwo ? 0 : int(rank) * half;
       for (int kb = 0; kb < it.blocks; ++kb, ++n, at.next(stages)) {
         ok = mbar_wait(&sm.empty[at.s], at.phase ^ 1, kWaitTimeoutNs);
         if (!ok) break;
@@ -422,7 +424,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
     uint32_t tile = 0;
     bool ok = true;
     for (int64_t idx = pair; ok && idx < items; idx += pairs) {
-      const Item it = item_at<MODE, FP8, GATED>(p, table, idx);
+      const Item it = item_at<MODE, kTwo, GATED>(p, table, idx);
       if (it.blocks == 0) continue;
       const uint32_t idesc = instr_desc(2 * kLanes, it.cols, kAByFeature, kBByFeature);
       const uint32_t buf = tile & 1, acc = tmem + buf * kMaxCols;
@@ -468,7 +470,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
     uint32_t phases = 0;
     uint64_t passed = 0;      // steps since the last wait
     for (int64_t idx = pair; ok && idx < items; idx += pairs) {
-      const Item it = item_at<MODE, FP8, GATED>(p, table, idx);
+      const Item it = item_at<MODE, kTwo, GATED>(p, table, idx);
       for (int kb = 0; kb < it.blocks; ++kb, ++passed, at.next(stages)) {
         const int left = it.rows - kb * kDepth;
         if (left >= kDepth) continue;
@@ -513,25 +515,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
     int kb = -1;
     Item it = {};
     bool more = idx < items;
-    if (more) it = item_at<MODE, FP8, GATED>(p, table, idx);
+    if (more) it = item_at<MODE, kTwo, GATED>(p, table, idx);
     const auto step = [&] {
       if (!more || ++kb < it.blocks) return;
       kb = 0;
       do {
         idx += pairs;
         more = idx < items;
-        if (more) it = item_at<MODE, FP8, GATED>(p, table, idx);
+        if (more) it = item_at<MODE, kTwo, GATED>(p, table, idx);
       } while (more && it.blocks == 0);
     };
     const auto load = [&](float& scale, int& half, int& left) {
       half = more ? it.cols / 2 : 0;
       left = it.rows - (kBByFeature ? kb * kDepth : 0);
-      const int x = kBByFeature ? it.c0 + int(rank) * half : kb * kDepth;
+      const int x = kBByFeature ? it.c0 + (kTwo ? 0 : int(rank) * half) : kb * kDepth;
       scale = 0.0f;
       if (more && t < kScaled && t < left && x < p.x_width)
         scale = __ldg(p.xs + (int64_t(it.row0) + it.rows - left + t) * scales + x / 128);
+      // (unrolled, the loop outgrows the instruction cache: 65536 rows forward
+      // 3694 us, and 3130 like this)
+#pragma unroll 1
       for (int g = 0; g < kConvertGroups; ++g) step();
     };
+#pragma unroll 1
     for (int g = 0; g <= group; ++g) step();      // to this group's first
     for (int g = 0; g < group; ++g) at.next(stages);
 #pragma unroll
@@ -542,7 +548,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
       while (ok && some) {
 #pragma unroll
         for (int d = 0; d < kAhead; ++d) {
-          const int half = halves[d], left = lefts[d];
+          const int half = halves[d];
+          [[maybe_unused]] const int left = lefts[d];
           some = half > 0;
           if (!some) break;
           ok = mbar_wait(&sm.raw[at.s], at.phase, kWaitTimeoutNs);
@@ -565,7 +572,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
             if (kBByFeature ? c_t >= half : row >= half) break;
             const float scale = mine[row];
             uint32_t r[8];
-            if constexpr (PART == kNearest) {
+            if constexpr (kBByFeature) {
               // a row of another segment, or of none, may hold anything
               if (row >= left) q[i] = make_uint4(0, 0, 0, 0);
               widen16<PART>(q[i], scale, r);
@@ -585,10 +592,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
         }
       }
     };
-    if constexpr (kBByFeature)
+    if (!kTwo || rank == 0)
       convert(std::integral_constant<Part, kNearest>());
-    else if (rank == 0)
-      convert(std::integral_constant<Part, kUpper>());
     else
       convert(std::integral_constant<Part, kRest>());
     if (!ok && lane == 0) record_error(p.err, ERRBIT_TIMEOUT);
@@ -599,7 +604,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
     int turn = 0;
     bool ok = true;
     for (int64_t idx = pair; ok && idx < items; idx += pairs) {
-      const Item it = item_at<MODE, FP8, GATED>(p, table, idx);
+      const Item it = item_at<MODE, kTwo, GATED>(p, table, idx);
       const uint32_t buf = tile & 1;
       const uint32_t acc = tmem + buf * kMaxCols + (uint32_t(warp * 32) << 16);
       if (it.blocks > 0) {
@@ -611,7 +616,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
       if (MODE == kByWeights) {
         constexpr int kWide = OUT32 ? 32 : 64;      // columns of 128 bytes
         const int m = it.m0 + int(rank) * kLanes + warp * 32;
-        for (int c = 0; c < it.cols; c += kWide) {
+        const int cols = kTwo ? it.cols / 2 : it.cols;
+        for (int c = 0; c < cols; c += kWide) {
           if (it.c0 + c >= p.cols || m >= p.M) break;
           uint32_t r[kWide / 32][32];
 #pragma unroll
@@ -624,6 +630,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
             }
           }
           tmem_wait_load();
+          if (kTwo && it.blocks > 0) {
+            // the sums of the rests
+            uint32_t rest[32];
+            tmem_load_32x32(acc + cols + c, rest);
+            tmem_wait_load();
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              r[0][i] = __float_as_uint(__uint_as_float(r[0][i]) + __uint_as_float(rest[i]));
+          }
           // two pieces in turn: the one before the last has left this one
           uint8_t* piece = mine + turn * 4096;
           turn ^= 1;
@@ -934,7 +949,8 @@ cudaError_t by_weights(const ep_expert_config* c, int cap, const void* dy, const
   p.M = c->out_features;
   p.cols = c->in_features;
   p.m_tiles = (p.M + 2 * kLanes - 1) / (2 * kLanes);
-  p.n_tiles = (p.cols + kMaxCols - 1) / kMaxCols;
+  const int wide = rows_of(in_two_parts(kByWeights, c->x_fp8 != 0, f32));
+  p.n_tiles = (p.cols + wide - 1) / wide;
   p.add = type == EP_GRAD_FP32_ADD;
   const int64_t size = int64_t(p.E) * p.M * p.cols * (f32 ? 4 : 2);
   if (cap == 0) return p.add ? cudaSuccess : cudaMemsetAsync(dw, 0, size, s);

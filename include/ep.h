@@ -686,8 +686,8 @@ EP_API int32_t ep_expert_w4(const ep_w4_config *cfg, int32_t cap, int32_t num_ro
  * the weights: for prompts, training, and decode with unquantised weights.
  * Any number of rows an expert, none among them.  Sums are fp32, rounded once
  * at the end.  E4M3 rows enter the product as value * scale to 12 bits, the
- * weights' gradient as bf16(value * scale).  The same call gives the same
- * bits. */
+ * weights' gradient as value * scale to 17 bits where it is fp32, and as
+ * bf16(value * scale) where it is bf16.  The same call gives the same bits. */
 typedef struct {
   int32_t num_experts;   /* E in [1, 2048]                                   */
   int32_t in_features;   /* H: a multiple of 8 (of 128 when x_fp8), <= 2^20  */

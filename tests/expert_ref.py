@@ -77,8 +77,12 @@ def by_rows(dy, w):
     return y, d * (1 + BF16) + BF16 * abs(y) + 1e-38
 
 
-def by_weights(dy, x, f32):
+def by_weights(dy, x, f32, fp8=False):
+    """fp8 with f32: x enters in two bf16 parts, the nearest and the rest: off
+    by half a step of the second, 2^-17."""
     y, d = product(np.ascontiguousarray(dy.T), np.ascontiguousarray(x.T))
+    if fp8 and f32:
+        d = 2 * d + EPS * abs(y) + BF16 * BF16 / 2 * (abs(dy).T @ abs(x))
     last = EPS if f32 else BF16
     return y, d * (1 + last) + last * abs(y) + 1e-38
 

@@ -90,7 +90,8 @@ class Case:
         got = ref.f64(grad_w)
         for e, n in enumerate(self.counts):
             rows = slice(int(self.start[e]), int(self.end[e]))
-            y, err = ref.by_weights(ref.f64(self.dy[rows]), self.x[rows], f32)
+            y, err = ref.by_weights(ref.f64(self.dy[rows]), (self.xf if f32 else self.x)[rows], f32,
+                                    self.dscale is not None)
             if before is not None:
                 was = ref.f64(before[e])
                 y, err = y + was, err + ref.EPS * (abs(y) + abs(was))
@@ -154,10 +155,12 @@ def test_gated_rows_of_odd_width(ep):
     case.check_forward(case.forward(ep))
 
 
+@pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("counts", [[5, 0, 300], [0, 0]])
-def test_gradient_added_to_what_is_there(ep, counts):
-    case = Case(ep, counts, 136, 72)
-    before = torch.randn(len(counts), 72, 136, device="cuda")
+def test_gradient_added_to_what_is_there(ep, counts, fp8):
+    H = 384 if fp8 else 136
+    case = Case(ep, counts, H, 72, fp8=fp8)
+    before = torch.randn(len(counts), 72, H, device="cuda")
     grad_w = before.clone()
     grad_x, got = case.backward(ep, grad_w=grad_w, accumulate=True)
     assert got is grad_w
