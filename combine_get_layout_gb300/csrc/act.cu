@@ -106,7 +106,8 @@ __device__ __forceinline__ void unpack8(uint2 v, float scale, float* f) {
     uint32_t h;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(two));
     float a, b;
-    asm("{\n\t.reg .f16 l, u;\n\tmov.b32 {l, u}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, u;\n\t}"
+    asm("{\n\t.reg .f16 l, u;\n\tmov.b32 {l, u}, %2;\n\t"
+        "cvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, u;\n\t}"
         : "=f"(a), "=f"(b)
         : "r"(h));
     f[2 * i] = a * scale;

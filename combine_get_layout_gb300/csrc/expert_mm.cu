@@ -71,9 +71,13 @@ constexpr int kPieces = 4;         // of 16 values a converting thread has in a 
 constexpr int kAhead = 2;          // steps of its own whose scales it loads ahead
 static_assert(32 * kConvertWarps / kConvertGroups * kPieces * 16 == kMaxCols / 2 * kDepth);
 
-__host__ __device__ constexpr int threads_of(bool fp8) { return 32 * (kFirstConvertWarp + (fp8 ? kConvertWarps : 0)); }
+__host__ __device__ constexpr int threads_of(bool fp8) {
+  return 32 * (kFirstConvertWarp + (fp8 ? kConvertWarps : 0));
+}
 // Bytes that the epilogue's warps stage a tile's pieces in.
-__host__ __device__ constexpr int staging_of(Mode m) { return kEpilogueWarps * (m == kByWeights ? 8192 : 2560); }
+__host__ __device__ constexpr int staging_of(Mode m) {
+  return kEpilogueWarps * (m == kByWeights ? 8192 : 2560);
+}
 // E4M3: scales that the converting warps share.
 __host__ __device__ constexpr int scales_of(Mode m) {
   return kConvertGroups * 2 * (m == kByWeights ? kDepth : kMaxCols / 2);
@@ -282,8 +286,10 @@ __device__ __forceinline__ bool group_agrees(int id, int threads, bool ok) {
 template <Mode MODE, bool FP8, bool GATED, bool OUT32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
     expert_mm_kernel(const __grid_constant__ MmMaps maps, const MmParams p) {
-  extern __shared__ uint8_t raw[];
-  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ uint8_t shared_bytes[];
+  // 1024-byte swizzle groups: what an operand's address is rounded up by is
+  // the same in both CTAs
+  uint8_t* ring = shared_bytes + (1023 & -smem_addr(shared_bytes));
   uint8_t* staging = ring + p.ring_bytes;
   Smem& sm = *reinterpret_cast<Smem*>(staging + staging_of(MODE));
   float* scale_at = reinterpret_cast<float*>(&sm + 1);
@@ -493,7 +499,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
     if (!ok && lane == 0) record_error(p.err, ERRBIT_TIMEOUT);
     __syncwarp();
   } else if (FP8 && warp >= kFirstConvertWarp) {
-    // Two groups of four warps take steps in turn; the rows' bytes come by
+    // Three groups of four warps take steps in turn; the rows' bytes come by
     // tensor copies, their scales are loaded kAhead turns ahead, past the ends
     // of tiles.
     constexpr int kThreads = 32 * kConvertWarps / kConvertGroups;
@@ -614,6 +620,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
         tc_fence_after();
       }
       if (MODE == kByWeights) {
+        // (adding nothing would still turn -0 and subnormal values into 0)
+        if (p.add && it.blocks == 0) continue;
         constexpr int kWide = OUT32 ? 32 : 64;      // columns of 128 bytes
         const int m = it.m0 + int(rank) * kLanes + warp * 32;
         const int cols = kTwo ? it.cols / 2 : it.cols;
@@ -693,7 +701,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
             tmem_wait_load();
           }
           // matrices of 8 features by 8 rows, transposed on the way
-          const uint32_t to = smem_addr(mine) + (lane % 8 + lane / 16 * 8) * kPitch + (lane / 8 % 2) * 16;
+          const uint32_t to =
+              smem_addr(mine) + (lane % 8 + lane / 16 * 8) * kPitch + (lane / 8 % 2) * 16;
           if (GATED) {
             float y[16];
 #pragma unroll

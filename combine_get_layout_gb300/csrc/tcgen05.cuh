@@ -130,8 +130,9 @@ __device__ __forceinline__ void fence_async_shared() {
 
 // ---- tensor cores, used by pairs ------------------------------------------------
 
-// All 32 lanes of a warp in each CTA of the pair; the address of `cols` (a power of two, 32 to 512) columns of
-// tensor memory goes to *at (shared).  Waits until they are free.
+// All 32 lanes of a warp in each CTA of the pair; the address of `cols` (a
+// power of two, 32 to 512) columns of tensor memory goes to *at (shared).
+// Waits until they are free.
 __device__ __forceinline__ void tmem_alloc(uint32_t* at, uint32_t cols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                    smem_addr(at)),

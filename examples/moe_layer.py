@@ -9,7 +9,8 @@ dispatch and the activation's input are kept in 8 bits for the weights' gradient
     python examples/moe_layer.py [--tokens 128] [--hidden 7168] [--inner 2048] [--experts 256]
                                  [--topk 8] [--steps 50] [--train]
 
-runs the first two, or with --train the third, on random weights, compares them with plain torch and prints the time of a step.
+runs the first two on random weights, compares them with plain torch and prints the time of a step;
+with --train it times the third.
 """
 
 from __future__ import annotations
@@ -140,8 +141,8 @@ class TrainedExperts:
 
 def training_step(cfg, router, experts, x, logits, dy, grad_loss, layout=None):
     """The layer's forward and backward pass for the gradient dy of y and the coefficients grad_loss
-    of the balance and z losses (cfg: FP8 dispatch).  Returns (y, loss, grad_x, grad_logits, grad_up,
-    grad_down)."""
+    of the balance and z losses (cfg: FP8 dispatch).  Returns (y, loss, grad_x, grad_logits,
+    grad_up, grad_down)."""
     e = experts
     idx, w, count, _, tokens, loss = ep.route_balance(router, logits)
     layout = ep.get_layout(cfg, idx, layout)

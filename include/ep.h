@@ -733,7 +733,8 @@ EP_API int32_t ep_selftest_expert_timeout(const ep_expert_config *cfg, int32_t c
 /* Types of the weights' gradient. */
 #define EP_GRAD_BF16 0
 #define EP_GRAD_FP32 1
-#define EP_GRAD_FP32_ADD 2   /* added to what d_grad_w holds */
+#define EP_GRAD_FP32_ADD 2   /* added to what d_grad_w holds (subnormal
+                                values count as 0) */
 
 /* Gradients of ep_expert_mm (gated = 0; ep_act_backward is the gated
  * activation's) for d_grad_out, device bf16 [cap, N].  Either or both:

@@ -60,15 +60,20 @@ class Case:
                                  1))
 
 
+def name_of(c):
+    return str(c) if len(str(c)) < 99 else str(dict(c, counts=len(c["counts"])))
+
+
 CASES = [
     dict(counts=[1], I=8), dict(counts=[1], I=128), dict(counts=[3, 0, 2], I=136, A=8),
     dict(counts=[0, 0, 9], I=1000), dict(counts=[5, 1], I=512), dict(counts=[2, 7], I=520, A=128),
     dict(counts=[1] * 70, I=16), dict(counts=[40, 33], I=2048, A=16), dict(counts=[0, 0], I=64),
-    dict(counts=[300, 0, 1], I=1408, extra=5), dict(counts=[1] * 33, I=24), dict(counts=[4], I=7168),
+    dict(counts=[300, 0, 1], I=1408, extra=5), dict(counts=[1] * 33, I=24),
+    dict(counts=[4], I=7168), dict(counts=[1, 1], I=1 << 19), dict(counts=[0, 1, 2, 0] * 512, I=16),
 ]
 
 
-@pytest.mark.parametrize("c", CASES, ids=str)
+@pytest.mark.parametrize("c", CASES, ids=name_of)
 def test_save(ep, c):
     case = Case(**c)
     a, q, s = case.save(ep)
@@ -81,7 +86,7 @@ def test_save(ep, c):
     assert (s.cpu()[~own] == MARK).all()
 
 
-@pytest.mark.parametrize("c", CASES, ids=str)
+@pytest.mark.parametrize("c", CASES, ids=name_of)
 def test_backward(ep, c):
     case = Case(**c)
     q, s = case.codes()
