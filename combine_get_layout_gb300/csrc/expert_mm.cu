@@ -62,6 +62,7 @@ constexpr int kABytes = kLanes * kDepth * 2;
 constexpr int kBBytes = kMaxCols / 2 * kDepth * 2;      // a CTA's half, at most
 constexpr int kPanel = 64 * kDepth * 2;         // 64 features by 64 rows
 constexpr uint64_t kStepNs = 4000;              // far above what a stage takes
+constexpr int kMostParts = 4;                   // pairs that share a reduction: 8 CTAs
 constexpr int kRowGroup = 8;                    // row tiles that share weight tiles in L2
 
 constexpr int kEpilogueWarps = 4, kCopyWarp = 4, kMmaWarp = 5, kClearWarp = 6;
@@ -96,6 +97,7 @@ struct MmParams {
   int cols;           // by weights: features of the N side
   int m_tiles;
   int n_tiles;        // by weights
+  int parts;          // of a tile's reduction
   const int32_t *start, *end;
   __nv_bfloat16* out;
   const float* xs;
@@ -120,6 +122,9 @@ struct Smem {
   uint64_t acc_full[2];
   uint64_t acc_empty[2];           // of the first CTA: both have read it out
   uint64_t drained;
+  // a reduction in parts: the other parts' sums are there (of the first pair);
+  // this CTA's have been read (of the others)
+  uint64_t sums_full, sums_read;
   uint32_t tmem;
   int most;                        // rows of a tile, at most
 };
@@ -130,6 +135,7 @@ struct Item {
   int c0;             // by weights: first feature of the N side
   int cols;           // columns of the product
   int blocks;         // steps of 64 along the reduction
+  int first, steps;   // of them, this pair's
 };
 
 // The segment of expert e.
@@ -157,8 +163,19 @@ struct Ring {
   }
 };
 
+// A part of a reduction, `of` parts in all.
+struct Part {
+  int number, of;
+};
+
+__device__ __forceinline__ void share(Item& it, Part part) {
+  it.first = int(int64_t(it.blocks) * part.number / part.of);
+  it.steps = int(int64_t(it.blocks) * (part.number + 1) / part.of) - it.first;
+}
+
 template <Mode MODE, bool TWO, bool GATED>
-__device__ __forceinline__ Item item_at(const MmParams& p, const int* table, int64_t idx) {
+__device__ __forceinline__ Item item_at(const MmParams& p, const int* table, int64_t idx,
+                                        Part part) {
   Item it;
   constexpr int kFeatures = GATED ? kLanes : 2 * kLanes;      // of a pair
   if (MODE == kByWeights) {
@@ -170,6 +187,7 @@ __device__ __forceinline__ Item item_at(const MmParams& p, const int* table, int
     it.cols = p.cols - it.c0 > rows_of(TWO) / 2 ? kMaxCols : kMaxCols / 2;
     segment(p, it.e, it.row0, it.rows);
     it.blocks = int((int64_t(it.rows) + kDepth - 1) / kDepth);
+    share(it, part);
     return it;
   }
   // the expert by its first row tile, then features outside, row tiles inside
@@ -191,6 +209,7 @@ __device__ __forceinline__ Item item_at(const MmParams& p, const int* table, int
   it.cols = round16(max(it.rows, 1)) * (TWO ? 2 : 1);
   it.c0 = 0;
   it.blocks = (p.depth + kDepth - 1) / kDepth;
+  share(it, part);
   return it;
 }
 
@@ -201,14 +220,21 @@ __device__ __forceinline__ bool wait_for_steps(uint64_t* bar, uint32_t parity, u
   return false;
 }
 
+// The same, for what other CTAs of the cluster wrote to their shared memory.
+__device__ __forceinline__ bool wait_for_sums(uint64_t* bar, uint32_t parity, uint64_t steps) {
+  for (uint64_t i = 0; i <= steps * kStepNs / kWaitTimeoutNs; ++i)
+    if (mbar_wait_acquire(bar, parity, kWaitTimeoutNs)) return true;
+  return false;
+}
+
 __device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
 
 // How E4M3 values times their scale become bf16: the nearest, or what that
 // leaves.
-enum Part { kNearest, kRest };
+enum Bits { kNearest, kRest };
 
 // 16 of them.
-template <Part PART>
+template <Bits PART>
 __device__ __forceinline__ void widen16(uint4 q, float scale, uint32_t (&r)[8]) {
   const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
@@ -231,7 +257,7 @@ __device__ __forceinline__ void widen16(uint4 q, float scale, uint32_t (&r)[8]) 
 
 // Out of line: rare, and the loop around it is to stay small (the kernel is
 // slowed by instruction fetch before anything else where it does not).
-template <Part PART>
+template <Bits PART>
 __device__ __noinline__ void widen16_apart(uint4 q, float scale, uint32_t (&r)[8]) {
   widen16<PART>(q, scale, r);
 }
@@ -242,7 +268,7 @@ __device__ __noinline__ void widen16_apart(uint4 q, float scale, uint32_t (&r)[8
 // E4M3 value is exact in bf16, the second what is left, rounded twice to 8
 // bits: together within 2^-12 of the product.  Scales of 128 and more (2^120
 // of which bf16 does not hold) and NaN go the way above.
-template <Part PART>
+template <Bits PART>
 __device__ __forceinline__ void part16(uint4 q, float scale, uint32_t (&r)[8]) {
   const uint32_t w[4] = {q.x, q.y, q.z, q.w};
   uint32_t nan = 0;
@@ -283,8 +309,8 @@ __device__ __forceinline__ bool group_agrees(int id, int threads, bool ok) {
   return all != 0;
 }
 
-template <Mode MODE, bool FP8, bool GATED, bool OUT32>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
+template <Mode MODE, bool FP8, bool GATED, bool OUT32, bool SPLIT>
+__global__ void __launch_bounds__(threads_of(FP8), 1)
     expert_mm_kernel(const __grid_constant__ MmMaps maps, const MmParams p) {
   extern __shared__ uint8_t shared_bytes[];
   // 1024-byte swizzle groups: what an operand's address is rounded up by is
@@ -295,7 +321,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
   float* scale_at = reinterpret_cast<float*>(&sm + 1);
   int* table = reinterpret_cast<int*>(scale_at + (FP8 ? scales_of(MODE) : 0));
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
-  const uint32_t rank = cluster_rank();
+  const uint32_t lead = SPLIT ? cluster_rank() & ~1u : 0u, rank = cluster_rank() & 1;
+  const int parts = SPLIT ? p.parts : 1;
+  const Part part{int(lead / 2), parts};
   constexpr bool kAByFeature = MODE != kForward;      // inner dimension of A: features
   constexpr bool kBByFeature = MODE == kByWeights;
   constexpr bool kTwo = in_two_parts(MODE, FP8, OUT32);
@@ -316,6 +344,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
       mbar_init(&sm.acc_empty[b], 2 * kEpilogueWarps);
     }
     mbar_init(&sm.drained, 1);
+    mbar_init(&sm.sums_full, kEpilogueWarps * (parts - 1 > 0 ? parts - 1 : 1));
+    mbar_init(&sm.sums_read, kEpilogueWarps);
     sm.most = 0;
     fence_mbar_init();
   }
@@ -353,27 +383,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
-  const int64_t pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+  // clusters, a pair each, or as many as share a tile's reduction
+  const int64_t pair = blockIdx.x / (2 * parts), pairs = gridDim.x / (2 * parts);
   Ring at;
 
   if (warp == kCopyWarp) {
     bool ok = !p.stall || pair != 0;
     uint64_t n = 0;      // stages filled so far
+    [[maybe_unused]] uint32_t tile = 0;
     for (int64_t idx = pair; ok && idx < items; idx += pairs) {
-      const Item it = item_at<MODE, kTwo, GATED>(p, table, idx);
+      const Item it = item_at<MODE, kTwo, GATED>(p, table, idx, part);
       const int half = it.cols / 2;
       // bytes of this CTA's copies into a stage
       const int bytes = kABytes + (FP8 ? 0 : half * kDepth * 2);
       const int m0 = it.m0 + int(rank) * (GATED ? kLanes / 2 : kLanes);
       const int col0 = kTwo ? 0 : int(rank) * half;
-      for (int kb = 0; kb < it.blocks; ++kb, ++n, at.next(stages)) {
+      for (int kb = 0; kb < it.steps; ++kb, ++n, at.next(stages)) {
         ok = mbar_wait(&sm.empty[at.s], at.phase ^ 1, kWaitTimeoutNs);
         if (!ok) break;
         const uint32_t a = smem_addr(ring + at.s * stage_bytes), b = a + kABytes;
-        const int k0 = kb * kDepth;
+        const int k0 = (it.first + kb) * kDepth;
         // cleared past the segment's end before it counts as full
         const bool last = MODE == kByWeights && it.rows - k0 < kDepth;
-        const uint32_t full = at_rank(smem_addr(&sm.full[at.s]), 0);
+        const uint32_t full = at_rank(smem_addr(&sm.full[at.s]), lead);
         const uint32_t bar = last ? smem_addr(&sm.last[at.s]) : full;
         if (elect_one()) {
           if (last)
@@ -415,6 +447,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
         }
         __syncwarp();
       }
+      // the sums of this part lie where the operands of its next tile come
+      if (SPLIT && ok && part.number > 0 && idx + pairs < items) {
+        ok = wait_for_steps(&sm.sums_read, tile & 1, it.blocks);
+        ++tile;
+      }
     }
     if (!ok && lane == 0) {
       record_error(p.err, ERRBIT_TIMEOUT);
@@ -430,14 +467,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
     uint32_t tile = 0;
     bool ok = true;
     for (int64_t idx = pair; ok && idx < items; idx += pairs) {
-      const Item it = item_at<MODE, kTwo, GATED>(p, table, idx);
-      if (it.blocks == 0) continue;
+      const Item it = item_at<MODE, kTwo, GATED>(p, table, idx, part);
+      if (it.steps == 0) continue;
       const uint32_t idesc = instr_desc(2 * kLanes, it.cols, kAByFeature, kBByFeature);
       const uint32_t buf = tile & 1, acc = tmem + buf * kMaxCols;
       ok = mbar_wait(&sm.acc_empty[buf], (tile / 2 & 1) ^ 1, kWaitTimeoutNs);
       if (!ok) break;
       tc_fence_after();
-      for (int kb = 0; kb < it.blocks; ++kb, at.next(stages)) {
+      for (int kb = 0; kb < it.steps; ++kb, at.next(stages)) {
         ok = mbar_wait(&sm.full[at.s], at.phase, kWaitTimeoutNs);
         if (!ok) break;
         tc_fence_after();
@@ -447,13 +484,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
         // 16 of the reduction further: 32 bytes of a row, or 16 rows
         constexpr uint32_t as = (kAByFeature ? 2048 : 32) >> 4, bs = (kBByFeature ? 2048 : 32) >> 4;
         const int steps =
-            MODE == kByWeights ? min(kDepth / 16, (it.rows - kb * kDepth + 15) / 16) : kDepth / 16;
+            MODE == kByWeights
+                ? min(kDepth / 16, (it.rows - (it.first + kb) * kDepth + 15) / 16)
+                : kDepth / 16;
         if (elect_one()) {
 #pragma unroll
           for (int i = 0; i < kDepth / 16; ++i)
             if (i < steps) mma_bf16(acc, da + i * as, db + i * bs, idesc, kb > 0 || i > 0);
-          mma_commit(smem_addr(&sm.empty[at.s]));
-          if (kb == it.blocks - 1) mma_commit(smem_addr(&sm.acc_full[buf]));
+          mma_commit(smem_addr(&sm.empty[at.s]), lead);
+          if (kb == it.steps - 1) mma_commit(smem_addr(&sm.acc_full[buf]), lead);
         }
         __syncwarp();
       }
@@ -463,7 +502,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
       // products in flight end before the tensor memory is given back
       if (elect_one()) {
         record_error(p.err, ERRBIT_TIMEOUT);
-        mma_commit(smem_addr(&sm.drained));
+        mma_commit(smem_addr(&sm.drained), lead);
       }
       __syncwarp();
       mbar_wait(&sm.drained, 0, kWaitTimeoutNs);
@@ -476,9 +515,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
     uint32_t phases = 0;
     uint64_t passed = 0;      // steps since the last wait
     for (int64_t idx = pair; ok && idx < items; idx += pairs) {
-      const Item it = item_at<MODE, kTwo, GATED>(p, table, idx);
-      for (int kb = 0; kb < it.blocks; ++kb, ++passed, at.next(stages)) {
-        const int left = it.rows - kb * kDepth;
+      const Item it = item_at<MODE, kTwo, GATED>(p, table, idx, part);
+      for (int kb = 0; kb < it.steps; ++kb, ++passed, at.next(stages)) {
+        const int left = it.rows - (it.first + kb) * kDepth;
         if (left >= kDepth) continue;
         // all steps before pass meanwhile
         ok = wait_for_steps(&sm.last[at.s], phases >> at.s & 1, passed);
@@ -493,7 +532,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
               make_uint4(0, 0, 0, 0);
         fence_async_shared();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(at_rank(smem_addr(&sm.full[at.s]), 0));
+        if (lane == 0) mbar_arrive_cluster(at_rank(smem_addr(&sm.full[at.s]), lead));
       }
     }
     if (!ok && lane == 0) record_error(p.err, ERRBIT_TIMEOUT);
@@ -521,20 +560,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
     int kb = -1;
     Item it = {};
     bool more = idx < items;
-    if (more) it = item_at<MODE, kTwo, GATED>(p, table, idx);
+    if (more) it = item_at<MODE, kTwo, GATED>(p, table, idx, part);
     const auto step = [&] {
-      if (!more || ++kb < it.blocks) return;
+      if (!more || ++kb < it.steps) return;
       kb = 0;
       do {
         idx += pairs;
         more = idx < items;
-        if (more) it = item_at<MODE, kTwo, GATED>(p, table, idx);
-      } while (more && it.blocks == 0);
+        if (more) it = item_at<MODE, kTwo, GATED>(p, table, idx, part);
+      } while (more && it.steps == 0);
     };
     const auto load = [&](float& scale, int& half, int& left) {
       half = more ? it.cols / 2 : 0;
-      left = it.rows - (kBByFeature ? kb * kDepth : 0);
-      const int x = kBByFeature ? it.c0 + (kTwo ? 0 : int(rank) * half) : kb * kDepth;
+      const int at_k = (it.first + kb) * kDepth;
+      left = it.rows - (kBByFeature ? at_k : 0);
+      const int x = kBByFeature ? it.c0 + (kTwo ? 0 : int(rank) * half) : at_k;
       scale = 0.0f;
       if (more && t < kScaled && t < left && x < p.x_width)
         scale = __ldg(p.xs + (int64_t(it.row0) + it.rows - left + t) * scales + x / 128);
@@ -550,7 +590,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
     for (int d = 0; d < kAhead; ++d) load(sc[d], halves[d], lefts[d]);
     bool ok = true, some = true;
     const auto convert = [&](auto which) {
-      constexpr Part PART = decltype(which)::value;
+      constexpr Bits PART = decltype(which)::value;
       while (ok && some) {
 #pragma unroll
         for (int d = 0; d < kAhead; ++d) {
@@ -592,45 +632,77 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
           }
           fence_async_shared();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(at_rank(smem_addr(&sm.full[at.s]), 0));
+          if (lane == 0) mbar_arrive_cluster(at_rank(smem_addr(&sm.full[at.s]), lead));
           for (int g = 0; g < kConvertGroups; ++g) at.next(stages);
           load(sc[d], halves[d], lefts[d]);
         }
       }
     };
     if (!kTwo || rank == 0)
-      convert(std::integral_constant<Part, kNearest>());
+      convert(std::integral_constant<Bits, kNearest>());
     else
-      convert(std::integral_constant<Part, kRest>());
+      convert(std::integral_constant<Bits, kRest>());
     if (!ok && lane == 0) record_error(p.err, ERRBIT_TIMEOUT);
     __syncwarp();
   } else if (warp < kEpilogueWarps) {
     uint8_t* mine = staging + warp * (staging_of(MODE) / kEpilogueWarps);
     uint32_t tile = 0;
+    [[maybe_unused]] uint32_t joined = 0;
     int turn = 0;
     bool ok = true;
     for (int64_t idx = pair; ok && idx < items; idx += pairs) {
-      const Item it = item_at<MODE, kTwo, GATED>(p, table, idx);
+      const Item it = item_at<MODE, kTwo, GATED>(p, table, idx, part);
       const uint32_t buf = tile & 1;
       const uint32_t acc = tmem + buf * kMaxCols + (uint32_t(warp * 32) << 16);
-      if (it.blocks > 0) {
+      if (it.steps > 0) {
         // the tile's whole reduction may pass before
-        ok = wait_for_steps(&sm.acc_full[buf], tile / 2 & 1, it.blocks);
+        ok = wait_for_steps(&sm.acc_full[buf], tile / 2 & 1, it.steps);
         if (!ok) break;
         tc_fence_after();
       }
+      if (SPLIT && part.number == 0) {
+        ok = wait_for_sums(&sm.sums_full, joined & 1, it.blocks);
+        if (!ok) break;
+      }
+      // Sums of 32 columns: a part that is not the first leaves them where its
+      // operands were (the products have read all of them, and the copying
+      // warp waits), the first adds the others' to its own, in their order.
+      const auto join = [&](int chunk, uint32_t (&v)[32]) {
+        const uint32_t at = (chunk * kEpilogueWarps + warp) * 4096 + lane * 16;
+        if (part.number > 0) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<uint4*>(ring + at + i * 512) =
+                make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          return;
+        }
+#pragma unroll 1
+        for (int other = 1; other < parts; ++other) {
+          const uint32_t from = at_rank(smem_addr(ring) + at, rank + 2 * other);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint4 w = load_cluster(from + i * 512);
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              v[4 * i + j] =
+                  __float_as_uint(__uint_as_float(v[4 * i + j]) + __uint_as_float(u[j]));
+          }
+        }
+      };
       if (MODE == kByWeights) {
         // (adding nothing would still turn -0 and subnormal values into 0)
-        if (p.add && it.blocks == 0) continue;
+        if (!SPLIT && p.add && it.blocks == 0) continue;
         constexpr int kWide = OUT32 ? 32 : 64;      // columns of 128 bytes
         const int m = it.m0 + int(rank) * kLanes + warp * 32;
         const int cols = kTwo ? it.cols / 2 : it.cols;
+#pragma unroll 1
         for (int c = 0; c < cols; c += kWide) {
           if (it.c0 + c >= p.cols || m >= p.M) break;
           uint32_t r[kWide / 32][32];
 #pragma unroll
           for (int h = 0; h < kWide / 32; ++h) {
-            if (it.blocks > 0) {
+            if (it.steps > 0) {
               tmem_load_32x32(acc + c + h * 32, r[h]);
             } else {
 #pragma unroll
@@ -638,7 +710,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
             }
           }
           tmem_wait_load();
-          if (kTwo && it.blocks > 0) {
+          if (kTwo && it.steps > 0) {
             // the sums of the rests
             uint32_t rest[32];
             tmem_load_32x32(acc + cols + c, rest);
@@ -646,6 +718,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               r[0][i] = __float_as_uint(__uint_as_float(r[0][i]) + __uint_as_float(rest[i]));
+          }
+          if (SPLIT) {
+#pragma unroll
+            for (int h = 0; h < kWide / 32; ++h) join(c / 32 + h, r[h]);
+            if (part.number > 0) continue;
           }
           // two pieces in turn: the one before the last has left this one
           uint8_t* piece = mine + turn * 4096;
@@ -681,24 +758,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
         constexpr int kPitch = GATED ? 48 : 80;             // bytes of a staged row
         const int m = it.m0 + int(rank) * (kEpilogueWarps * kWidth) + warp * kWidth;
         const int rows = FP8 ? it.cols / 2 : it.cols;
+#pragma unroll 1
         for (int c = 0; c < rows; c += 32) {
           if (m >= p.M) break;
-          uint32_t r0[16], r1[16];
-          tmem_load_16x32(acc + c, r0);
-          tmem_load_16x32(acc + c + (16u << 16), r1);
-          if (FP8) {
-            // the sums of the rests
-            uint32_t s0[16], s1[16];
-            tmem_load_16x32(acc + rows + c, s0);
-            tmem_load_16x32(acc + rows + c + (16u << 16), s1);
-            tmem_wait_load();
+          uint32_t r[32];      // of 16 lanes, and of the 16 behind them
+          uint32_t(&r0)[16] = *reinterpret_cast<uint32_t(*)[16]>(r);
+          uint32_t(&r1)[16] = *reinterpret_cast<uint32_t(*)[16]>(r + 16);
+          if (it.steps > 0) {
+            tmem_load_16x32(acc + c, r0);
+            tmem_load_16x32(acc + c + (16u << 16), r1);
+            if (FP8) {
+              // the sums of the rests
+              uint32_t s0[16], s1[16];
+              tmem_load_16x32(acc + rows + c, s0);
+              tmem_load_16x32(acc + rows + c + (16u << 16), s1);
+              tmem_wait_load();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              r0[i] = __float_as_uint(__uint_as_float(r0[i]) + __uint_as_float(s0[i]));
-              r1[i] = __float_as_uint(__uint_as_float(r1[i]) + __uint_as_float(s1[i]));
+              for (int i = 0; i < 16; ++i) {
+                r0[i] = __float_as_uint(__uint_as_float(r0[i]) + __uint_as_float(s0[i]));
+                r1[i] = __float_as_uint(__uint_as_float(r1[i]) + __uint_as_float(s1[i]));
+              }
+            } else {
+              tmem_wait_load();
             }
           } else {
-            tmem_wait_load();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) r[i] = 0;
+          }
+          if (SPLIT) {
+            join(c / 32, r);
+            if (part.number > 0) continue;
           }
           // matrices of 8 features by 8 rows, transposed on the way
           const uint32_t to =
@@ -741,11 +830,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(FP8), 1)
           __syncwarp();
         }
       }
-      if (it.blocks > 0) {
+      if (it.steps > 0) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(at_rank(smem_addr(&sm.acc_empty[buf]), 0));
+        if (lane == 0) mbar_arrive_cluster(at_rank(smem_addr(&sm.acc_empty[buf]), lead));
         ++tile;
+      }
+      if (SPLIT) {
+        ++joined;
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0 && part.number > 0)
+          mbar_arrive_release(at_rank(smem_addr(&sm.sums_full), rank));
+        for (int other = 1; lane == 0 && part.number == 0 && other < parts; ++other)
+          mbar_arrive_release(at_rank(smem_addr(&sm.sums_read), rank + 2 * other));
       }
     }
     if (MODE == kByWeights && lane == 0) tma_store_wait<0>();
@@ -854,9 +952,9 @@ constexpr int rest_bytes(Mode m, bool fp8, int table) {
 }
 static_assert(kSmemLimit - rest_bytes(kByWeights, true, 0) >= 6 * (kABytes + kBBytes));
 
-template <Mode MODE, bool FP8, bool GATED, bool OUT32>
-cudaError_t launch(const MmMaps& maps, MmParams p, int64_t most_items, cudaStream_t s) {
-  auto* kernel = expert_mm_kernel<MODE, FP8, GATED, OUT32>;
+template <Mode MODE, bool FP8, bool GATED, bool OUT32, bool SPLIT>
+cudaError_t launch_parts(const MmMaps& maps, MmParams p, int clusters, cudaStream_t s) {
+  auto* kernel = expert_mm_kernel<MODE, FP8, GATED, OUT32, SPLIT>;
   // once per kernel and device
   static std::atomic<uint64_t> raised{0};
   int dev = 0;
@@ -869,10 +967,35 @@ cudaError_t launch(const MmMaps& maps, MmParams p, int64_t most_items, cudaStrea
   }
   const int rest = rest_bytes(MODE, FP8, MODE == kByWeights ? 0 : p.E + 1);
   p.ring_bytes = (kSmemLimit - rest) / 1024 * 1024;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * p.parts * clusters);
+  cfg.blockDim = dim3(threads_of(FP8));
+  cfg.dynamicSmemBytes = size_t(p.ring_bytes + rest);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2 * p.parts;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, maps, p);
+}
+
+// most_items: tiles at most; steps: of a tile's reduction (about).
+template <Mode MODE, bool FP8, bool GATED, bool OUT32>
+cudaError_t launch(const MmMaps& maps, MmParams p, int64_t most_items, int64_t steps,
+                   cudaStream_t s) {
   const int64_t pairs = device_info().sm_count / 2;
-  const int grid = 2 * int(most_items < pairs ? most_items : pairs);
-  return launch_pdl(kernel, dim3(grid), dim3(threads_of(FP8)), size_t(p.ring_bytes + rest), s,
-                    maps, p);
+  // Where tiles leave half the pairs or more without work, two or four of them
+  // share a tile's reduction, down to four steps each.
+  p.parts = 1;
+  while (p.parts < kMostParts && most_items * p.parts * 2 <= pairs && steps >= 8 * p.parts)
+    p.parts *= 2;
+  const int clusters = int(most_items < pairs / p.parts ? most_items : pairs / p.parts);
+  return p.parts > 1 ? launch_parts<MODE, FP8, GATED, OUT32, true>(maps, p, clusters, s)
+                     : launch_parts<MODE, FP8, GATED, OUT32, false>(maps, p, clusters, s);
 }
 
 // Tiles that `rows` rows of E experts can make, at most, by feature tiles.
@@ -925,11 +1048,12 @@ cudaError_t forward(const ep_expert_config* c, int cap, int num_rows, const void
   }
   if (e != cudaSuccess) return e;
   const int64_t items = most_row_tiles(num_rows, p.E, c->x_fp8) * p.m_tiles;
+  const int64_t steps = (p.depth + kDepth - 1) / kDepth;
   if (c->gated)
-    return c->x_fp8 ? launch<kForward, true, true, false>(maps, p, items, s)
-                    : launch<kForward, false, true, false>(maps, p, items, s);
-  return c->x_fp8 ? launch<kForward, true, false, false>(maps, p, items, s)
-                  : launch<kForward, false, false, false>(maps, p, items, s);
+    return c->x_fp8 ? launch<kForward, true, true, false>(maps, p, items, steps, s)
+                    : launch<kForward, false, true, false>(maps, p, items, steps, s);
+  return c->x_fp8 ? launch<kForward, true, false, false>(maps, p, items, steps, s)
+                  : launch<kForward, false, false, false>(maps, p, items, steps, s);
 }
 
 cudaError_t by_rows(const ep_expert_config* c, int cap, int num_rows, const void* dy,
@@ -947,10 +1071,11 @@ cudaError_t by_rows(const ep_expert_config* c, int cap, int num_rows, const void
     e = encode_rows(&maps.b[i], dy, cap, c->out_features, 8 << i);
   if (e != cudaSuccess) return e;
   const int64_t items = most_row_tiles(num_rows, p.E, false) * p.m_tiles;
-  return launch<kByRows, false, false, false>(maps, p, items, s);
+  const int64_t steps = (p.depth + kDepth - 1) / kDepth;
+  return launch<kByRows, false, false, false>(maps, p, items, steps, s);
 }
 
-cudaError_t by_weights(const ep_expert_config* c, int cap, const void* dy, const void* x,
+cudaError_t by_weights(const ep_expert_config* c, int cap, int num_rows, const void* dy, const void* x,
                        const float* x_scale, const int32_t* start, const int32_t* end, void* dw,
                        int type, int32_t* err, cudaStream_t s) {
   MmParams p = params(c, cap, start, end, err);
@@ -975,11 +1100,12 @@ cudaError_t by_weights(const ep_expert_config* c, int cap, const void* dy, const
   }
   if (e != cudaSuccess) return e;
   const int64_t items = int64_t(p.E) * p.m_tiles * p.n_tiles;
+  const int64_t steps = int64_t(num_rows) / p.E / kDepth;
   if (f32)
-    return c->x_fp8 ? launch<kByWeights, true, false, true>(maps, p, items, s)
-                    : launch<kByWeights, false, false, true>(maps, p, items, s);
-  return c->x_fp8 ? launch<kByWeights, true, false, false>(maps, p, items, s)
-                  : launch<kByWeights, false, false, false>(maps, p, items, s);
+    return c->x_fp8 ? launch<kByWeights, true, false, true>(maps, p, items, steps, s)
+                    : launch<kByWeights, false, false, true>(maps, p, items, steps, s);
+  return c->x_fp8 ? launch<kByWeights, true, false, false>(maps, p, items, steps, s)
+                  : launch<kByWeights, false, false, false>(maps, p, items, steps, s);
 }
 
 }  // namespace
@@ -1040,7 +1166,7 @@ int32_t ep_expert_mm_backward(const ep_expert_config* cfg, int32_t cap, int32_t 
     e = by_rows(cfg, cap, num_rows, d_grad_out, d_w, d_expert_start, d_expert_end, d_grad_x, d_err,
                 s);
   if (e == cudaSuccess && d_grad_w != nullptr)
-    e = by_weights(cfg, cap, d_grad_out, d_x, d_x_scale, d_expert_start, d_expert_end, d_grad_w,
+    e = by_weights(cfg, cap, num_rows, d_grad_out, d_x, d_x_scale, d_expert_start, d_expert_end, d_grad_w,
                    grad_w_type, d_err, s);
   return status(e);
 }

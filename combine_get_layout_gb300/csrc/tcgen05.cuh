@@ -18,7 +18,7 @@ __device__ __forceinline__ bool elect_one() {
   return one != 0;
 }
 
-// ---- pairs of CTAs (clusters of two) ------------------------------------------
+// ---- pairs of CTAs (in clusters of one or more pairs) ------------------------------------------
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -49,6 +49,30 @@ __device__ __forceinline__ void cluster_sync() {
 // operations, about 1 us: every case ran at half its speed.)
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// The same, handing over what the warp wrote before to a CTA of the cluster
+// that waits by mbar_wait_acquire.
+__device__ __forceinline__ void mbar_arrive_release(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+               : "memory");
+}
+
+__device__ __forceinline__ bool mbar_wait_acquire(uint64_t* bar, uint32_t parity,
+                                                  uint64_t timeout_ns) {
+  const bool ok = mbar_wait(bar, parity, timeout_ns);
+  asm volatile("fence.acq_rel.cluster;" ::: "memory");
+  return ok;
+}
+
+// 16 bytes of a CTA's shared memory (address from at_rank).
+__device__ __forceinline__ uint4 load_cluster(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(at)
+               : "memory");
+  return v;
 }
 
 // ---- tensor copies ----------------------------------------------------------
@@ -180,13 +204,13 @@ __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uin
       : "memory");
 }
 
-// Arrives on the barriers at this place in both CTAs when this thread's
-// products so far are done.
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
+// Arrives on the barriers at this place in both CTAs, the first of which has
+// this rank in the cluster, when this thread's products so far are done.
+__device__ __forceinline__ void mma_commit(uint32_t bar, uint32_t lead) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
       "[%0], %1;" ::"r"(bar),
-      "h"(uint16_t(3))
+      "h"(uint16_t(3u << lead))
       : "memory");
 }
 

@@ -188,10 +188,39 @@ def test_one_gradient_alone(ep):
     assert only_w[0] is None and torch.equal(only_w[1], gw)
 
 
-def test_more_rows_than_said(ep):
-    """num_rows sizes the launch, not the work."""
-    case = Case(ep, [700, 3, 290], 128, 392, A=8)
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("H", [128, 1152])
+def test_more_rows_than_said(ep, H, fp8):
+    """num_rows sizes the launch, not the work; with the longer reduction, pairs that share it take
+    one tile after another."""
+    case = Case(ep, [700, 3, 290], H, 392, A=8, fp8=fp8)
     case.check_forward(case.forward(ep, num_rows=1))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("c", [
+    dict(counts=[1], H=7168, N=128), dict(counts=[3, 0, 1], H=1024, N=520),
+    dict(counts=[40, 200], H=640, N=264), dict(counts=[0, 1000, 30], H=128, N=136),
+    dict(counts=[520], H=384, N=8), dict(counts=[1, 2100], H=256, N=72, A=16)], ids=str)
+def test_reductions_in_parts(ep, c, fp8):
+    """Few tiles and a long reduction, along the inputs, the outputs or the rows."""
+    case = Case(ep, fp8=fp8, **c)
+    case.check_forward(case.forward(ep))
+    for dtype in (torch.bfloat16, torch.float32):
+        case.check_backward(*case.backward(ep, grad_w_dtype=dtype))
+    first, again = case.forward(ep), case.forward(ep)
+    assert torch.equal(first, again)
+    if c["N"] % 32 == 0 or c["N"] == 128:
+        gated = Case(ep, fp8=fp8, gated=True, **c)
+        gated.check_forward(gated.forward(ep))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_sum_in_parts_added_to_what_is_there(ep, fp8):
+    case = Case(ep, [1500, 0], 128, 72, fp8=fp8)
+    before = torch.randn(2, 72, 128, device="cuda")
+    grad_w = before.clone()
+    case.check_backward(*case.backward(ep, grad_w=grad_w, accumulate=True), before)
 
 
 def test_no_rows(ep):
