@@ -1,5 +1,5 @@
 """Python binding of libep_gb300.so (MoE dispatch / combine layout on GB300,
-with the router gate before it and experts' 4-bit products inside).
+with the router gate before it and experts' products inside).
 
 Two layers, both argument marshalling only -- every step of layout, dispatch
 and combine runs in the library's CUDA kernels:
@@ -7,11 +7,11 @@ and combine runs in the library's CUDA kernels:
 * ``ep_*`` functions with the C ABI's names and arguments (include/ep.h),
   taking ``EpConfig`` / ``EpLayout`` ctypes structures and raw pointers.
 * A torch layer (``Config``, ``Layout``, ``get_layout``, ``dispatch``,
-  ``combine``, ``route``, ``expert_w4``, ...) that allocates device buffers with torch, passes
-  ``tensor.data_ptr()`` and the current CUDA stream, and raises ``EpError``
+  ``combine``, ``route``, ``expert_w4``, ``expert_mm``, ...) that allocates device
+  buffers with torch, passes ``tensor.data_ptr()`` and the current CUDA stream, and raises ``EpError``
   on a non-zero status.  torch provides memory and streams, nothing else.
-  The calls of the router gate and of the experts' products go through a
-  small compiled extension (ep_torch_calls) instead of ctypes.
+  The calls of the router gate, of the experts' products and of the
+  activation between them go through a small compiled extension (ep_torch_calls) instead of ctypes.
 
 There is no fallback: if the shared library is missing, importing this
 package raises.  Build it with ``python combine_get_layout_gb300/build_lib.py``.
