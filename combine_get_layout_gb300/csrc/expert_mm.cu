@@ -693,13 +693,13 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
         }
       };
       if (MODE == kByWeights) {
-        // (adding nothing would still turn -0 and subnormal values into 0)
-        if (!SPLIT && p.add && it.blocks == 0) continue;
         constexpr int kWide = OUT32 ? 32 : 64;      // columns of 128 bytes
         const int m = it.m0 + int(rank) * kLanes + warp * 32;
         const int cols = kTwo ? it.cols / 2 : it.cols;
+        // (adding nothing would still turn -0 and subnormal values into 0)
+        const bool nothing = OUT32 && p.add && it.blocks == 0;
 #pragma unroll 1
-        for (int c = 0; c < cols; c += kWide) {
+        for (int c = 0; c < cols && !nothing; c += kWide) {
           if (it.c0 + c >= p.cols || m >= p.M) break;
           uint32_t r[kWide / 32][32];
 #pragma unroll

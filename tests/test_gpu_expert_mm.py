@@ -219,8 +219,10 @@ def test_reductions_in_parts(ep, c, fp8):
 def test_sum_in_parts_added_to_what_is_there(ep, fp8):
     case = Case(ep, [1500, 0], 128, 72, fp8=fp8)
     before = torch.randn(2, 72, 128, device="cuda")
+    before[:, 0, :2] = torch.tensor([-0.0, 1e-40], device="cuda")
     grad_w = before.clone()
     case.check_backward(*case.backward(ep, grad_w=grad_w, accumulate=True), before)
+    assert torch.equal(grad_w[1].view(torch.int32), before[1].view(torch.int32))
 
 
 def test_no_rows(ep):
@@ -269,6 +271,37 @@ def test_what_is_not_finite_stays_in_its_row(ep, bad):
     assert not torch.isfinite(bw[0][:, 5]).any() and not torch.isfinite(bw[1][9]).any()
     at = torch.isfinite(bw)
     assert torch.equal(bw[at], gw[at]) and int((~at).sum()) == 136 + 128
+
+
+@pytest.mark.parametrize("bad", ["code", "scale", "infinite scale"])
+def test_what_is_not_finite_in_8_bits_stays_in_its_row(ep, bad):
+    case = Case(ep, [20, 40], 256, 136, fp8=True)
+    good, (_, gw) = case.forward(ep), case.backward(ep)
+    if bad == "code":
+        case.dx[7, 5] = 0xFF
+    else:
+        case.dscale[7, 0] = np.nan if bad == "scale" else np.inf
+    out, (_, bw) = case.forward(ep), case.backward(ep)
+    assert not torch.isfinite(out[7]).any()
+    keep = torch.arange(case.cap, device="cuda") != 7
+    assert torch.equal(out[keep], good[keep]) and torch.equal(bw[1], gw[1])
+    columns = [5] if bad == "code" else list(range(128))
+    rest = [c for c in range(256) if c not in columns]
+    assert not torch.isfinite(bw[0][:, columns]).any()
+    assert torch.equal(bw[0][:, rest], gw[0][:, rest])
+
+
+@pytest.mark.parametrize("scale", [300.0, 127.9, 1e-30, 1e20, -3.0, 2.0 ** -140])
+def test_scales_of_any_size(ep, scale):
+    case = Case(ep, [30, 0, 7], 256, 72, fp8=True)
+    case.dscale *= scale
+    case.xf = ref.f64(ref.values(case.dx, case.dscale))
+    case.x = ref.f64(ref.values(case.dx, case.dscale).bfloat16())
+    case.xf[~case.own], case.x[~case.own] = 0, 0
+    case.check_forward(case.forward(ep))
+    if abs(scale) > 1e-35:
+        for dtype in (torch.bfloat16, torch.float32):
+            case.check_backward(*case.backward(ep, grad_w_dtype=dtype))
 
 
 @pytest.mark.parametrize("fp8", [False, True])
