@@ -62,6 +62,10 @@ constexpr int kABytes = kLanes * kDepth * 2;
 constexpr int kBBytes = kMaxCols / 2 * kDepth * 2;      // a CTA's half, at most
 constexpr int kPanel = 64 * kDepth * 2;         // 64 features by 64 rows
 constexpr uint64_t kStepNs = 4000;              // far above what a stage takes
+// Rows whose sum an fp32 gradient takes from one accumulator: the tensor cores
+// drop what lies below the accumulator's last bit, about 2^-26 of the sum for
+// each 16 rows (19,400 rows in one sum: off by 2.2e-5 in the norm).
+constexpr int kMostRows = 2048;
 constexpr int kMostParts = 4;                   // pairs that share a reduction: 8 CTAs
 constexpr int kRowGroup = 8;                    // row tiles that share weight tiles in L2
 
@@ -137,6 +141,8 @@ struct Item {
   int cols;           // columns of the product
   int blocks;         // steps of 64 along the reduction
   int first, steps;   // of them, this pair's
+  int piece;          // of the segment's rows, by kMostRows
+  bool more;          // pieces behind it
 };
 
 // The segment of expert e.
@@ -174,10 +180,12 @@ __device__ __forceinline__ void share(Item& it, Part part) {
   it.steps = int(int64_t(it.blocks) * (part.number + 1) / part.of) - it.first;
 }
 
-template <Mode MODE, bool TWO, bool GATED>
+template <Mode MODE, bool TWO, bool GATED, bool OUT32>
 __device__ __forceinline__ Item item_at(const MmParams& p, const int* table, int64_t idx,
-                                        Part part) {
+                                        int piece, Part part) {
   Item it;
+  it.piece = piece;
+  it.more = false;
   constexpr int kFeatures = GATED ? kLanes : 2 * kLanes;      // of a pair
   if (MODE == kByWeights) {
     const int tiles = p.m_tiles * p.n_tiles;
@@ -187,6 +195,12 @@ __device__ __forceinline__ Item item_at(const MmParams& p, const int* table, int
     it.c0 = local % p.n_tiles * rows_of(TWO);
     it.cols = p.cols - it.c0 > rows_of(TWO) / 2 ? kMaxCols : kMaxCols / 2;
     segment(p, it.e, it.row0, it.rows);
+    if (OUT32) {
+      const int64_t most = int64_t(kMostRows) * part.of, left = it.rows - piece * most;
+      it.row0 += int(piece * most);
+      it.more = left > most;
+      it.rows = int(min(left, most));
+    }
     it.blocks = int((int64_t(it.rows) + kDepth - 1) / kDepth);
     share(it, part);
     return it;
@@ -213,6 +227,29 @@ __device__ __forceinline__ Item item_at(const MmParams& p, const int* table, int
   share(it, part);
   return it;
 }
+
+// A pair's way over the items, the pieces of one after another.
+template <Mode MODE, bool TWO, bool GATED, bool OUT32>
+struct Walk {
+  const MmParams& p;
+  const int* table;
+  int64_t idx, items, pairs;
+  Part part;
+  Item it = {};
+
+  __device__ __forceinline__ Walk(const MmParams& params, const int* t, int64_t first,
+                                  int64_t pairs_, int64_t items_, Part part_)
+      : p(params), table(t), idx(first), items(items_), pairs(pairs_), part(part_) {
+    if (there()) it = item_at<MODE, TWO, GATED, OUT32>(p, table, idx, 0, part);
+  }
+  __device__ __forceinline__ bool there() const { return idx < items; }
+  __device__ __forceinline__ bool last() const { return !it.more && idx + pairs >= items; }
+  __device__ __forceinline__ void next() {
+    const int piece = it.more ? it.piece + 1 : 0;
+    if (!it.more) idx += pairs;
+    if (there()) it = item_at<MODE, TWO, GATED, OUT32>(p, table, idx, piece, part);
+  }
+};
 
 // mbar_wait for something that so many steps of a stage come before.
 __device__ __forceinline__ bool wait_for_steps(uint64_t* bar, uint32_t parity, uint64_t steps) {
@@ -386,14 +423,15 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
   const uint32_t tmem = sm.tmem;
   // clusters, a pair each, or as many as share a tile's reduction
   const int64_t pair = blockIdx.x / (2 * parts), pairs = gridDim.x / (2 * parts);
+  using Tiles = Walk<MODE, kTwo, GATED, OUT32>;
   Ring at;
 
   if (warp == kCopyWarp) {
     bool ok = !p.stall || pair != 0;
     uint64_t n = 0;      // stages filled so far
     [[maybe_unused]] uint32_t tile = 0;
-    for (int64_t idx = pair; ok && idx < items; idx += pairs) {
-      const Item it = item_at<MODE, kTwo, GATED>(p, table, idx, part);
+    for (Tiles tiles(p, table, pair, pairs, items, part); ok && tiles.there(); tiles.next()) {
+      const Item& it = tiles.it;
       const int half = it.cols / 2;
       // bytes of this CTA's copies into a stage
       const int bytes = kABytes + (FP8 ? 0 : half * kDepth * 2);
@@ -449,7 +487,7 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
         __syncwarp();
       }
       // the sums of this part lie where the operands of its next tile come
-      if (SPLIT && ok && part.number > 0 && idx + pairs < items) {
+      if (SPLIT && ok && part.number > 0 && !tiles.last()) {
         ok = wait_for_steps(&sm.sums_read, tile & 1, it.blocks);
         ++tile;
       }
@@ -467,8 +505,8 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
   } else if (warp == kMmaWarp && rank == 0) {
     uint32_t tile = 0;
     bool ok = true;
-    for (int64_t idx = pair; ok && idx < items; idx += pairs) {
-      const Item it = item_at<MODE, kTwo, GATED>(p, table, idx, part);
+    for (Tiles tiles(p, table, pair, pairs, items, part); ok && tiles.there(); tiles.next()) {
+      const Item& it = tiles.it;
       if (it.steps == 0) continue;
       const uint32_t idesc = instr_desc(2 * kLanes, it.cols, kAByFeature, kBByFeature);
       const uint32_t buf = tile & 1, acc = tmem + buf * kMaxCols;
@@ -515,8 +553,8 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
     bool ok = true;
     uint32_t phases = 0;
     uint64_t passed = 0;      // steps since the last wait
-    for (int64_t idx = pair; ok && idx < items; idx += pairs) {
-      const Item it = item_at<MODE, kTwo, GATED>(p, table, idx, part);
+    for (Tiles tiles(p, table, pair, pairs, items, part); ok && tiles.there(); tiles.next()) {
+      const Item& it = tiles.it;
       for (int kb = 0; kb < it.steps; ++kb, ++passed, at.next(stages)) {
         const int left = it.rows - (it.first + kb) * kDepth;
         if (left >= kDepth) continue;
@@ -557,18 +595,16 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
     float sc[kAhead];
     int halves[kAhead];         // columns of the step's tile a CTA, 0 past the last one
     int lefts[kAhead];          // rows of the segment from the step's first on
-    int64_t idx = pair;
+    Tiles tiles(p, table, pair, pairs, items, part);
+    const Item& it = tiles.it;
     int kb = -1;
-    Item it = {};
-    bool more = idx < items;
-    if (more) it = item_at<MODE, kTwo, GATED>(p, table, idx, part);
+    bool more = tiles.there();
     const auto step = [&] {
       if (!more || ++kb < it.steps) return;
       kb = 0;
       do {
-        idx += pairs;
-        more = idx < items;
-        if (more) it = item_at<MODE, kTwo, GATED>(p, table, idx, part);
+        tiles.next();
+        more = tiles.there();
       } while (more && it.steps == 0);
     };
     const auto load = [&](float& scale, int& half, int& left) {
@@ -650,10 +686,9 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
     uint32_t tile = 0;
     [[maybe_unused]] uint32_t joined = 0;
     int turn = 0;
-    const uint64_t policy = MODE == kByWeights ? l2_policy(p.leaves_l2) : 0;
     bool ok = true;
-    for (int64_t idx = pair; ok && idx < items; idx += pairs) {
-      const Item it = item_at<MODE, kTwo, GATED>(p, table, idx, part);
+    for (Tiles tiles(p, table, pair, pairs, items, part); ok && tiles.there(); tiles.next()) {
+      const Item& it = tiles.it;
       const uint32_t buf = tile & 1;
       const uint32_t acc = tmem + buf * kMaxCols + (uint32_t(warp * 32) << 16);
       if (it.steps > 0) {
@@ -664,6 +699,10 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
       }
       if (SPLIT && part.number == 0) {
         ok = wait_for_sums(&sm.sums_full, joined & 1, it.blocks);
+        if (!ok) break;
+      } else if (SPLIT && joined > 0) {
+        // (a part without steps has waited for nothing yet)
+        ok = wait_for_steps(&sm.sums_read, (joined - 1) & 1, it.blocks);
         if (!ok) break;
       }
       // Sums of 32 columns: a part that is not the first leaves them where its
@@ -698,6 +737,13 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
         const int cols = kTwo ? it.cols / 2 : it.cols;
         // (adding nothing would still turn -0 and subnormal values into 0)
         const bool nothing = OUT32 && p.add && it.blocks == 0;
+        // what more is added to stays
+        const uint64_t policy = l2_policy(p.leaves_l2 && !it.more);
+        // the pieces before have to be there
+        if (OUT32 && it.piece > 0) {
+          if (lane == 0) tma_store_wait<0>();
+          __syncwarp();
+        }
 #pragma unroll 1
         for (int c = 0; c < cols && !nothing; c += kWide) {
           if (it.c0 + c >= p.cols || m >= p.M) break;
@@ -748,7 +794,7 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
           fence_async_shared();
           __syncwarp();
           if (lane == 0) {
-            if (OUT32 && p.add)
+            if (OUT32 && (p.add || it.piece > 0))
               tma_add_3d(&maps.out, smem_addr(piece), it.c0 + c, m, it.e);
             else
               tma_store_3d(&maps.out, smem_addr(piece), it.c0 + c, m, it.e, policy);

@@ -742,7 +742,8 @@ EP_API int32_t ep_selftest_expert_timeout(const ep_expert_config *cfg, int32_t c
  *   expert (rows of no expert are not written); needs d_w.
  * d_grad_w: device [E, N, H] of grad_w_type or NULL: the sum over expert e's
  *   rows of grad_out_r x_r^T, 0 for an expert without rows (with
- *   EP_GRAD_FP32_ADD: what it holds stays); needs the rows d_x (and
+ *   EP_GRAD_FP32_ADD: what it holds stays); an fp32 gradient of more than
+ *   2048 rows adds sums of that many; needs the rows d_x (and
  *   d_x_scale) of the forward call.  Rows of no expert are not read into it.
  * num_rows sizes the launch for d_grad_x as in ep_expert_mm; d_grad_w is
  * written whatever it is.  d_grad_x and d_grad_w overlap no input.  Returns

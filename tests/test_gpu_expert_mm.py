@@ -362,8 +362,36 @@ def test_two_calls_at_once(ep):
 def test_a_long_reduction(ep):
     """Sums over 200,000 rows stay within fp32's error of sums of 16."""
     case = Case(ep, [200000], 8, 16)
-    gx, gw = case.backward(ep, grad_w_dtype=torch.float32)
-    case.check_backward(gx, gw)
+    for dtype in (torch.float32, torch.bfloat16):
+        gx, gw = case.backward(ep, grad_w_dtype=dtype)
+        case.check_backward(gx, gw)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("c", [
+    dict(counts=[2049, 0, 20000], H=128, N=72), dict(counts=[4100] * 3, H=640, N=1104),
+    dict(counts=[2048, 4096, 1], H=384, N=8), dict(counts=[30001], H=256, N=64),
+    dict(counts=[16400], H=128, N=2800), dict(counts=[8230, 8200], H=128, N=96)], ids=str)
+def test_long_sums_in_32_bits(ep, c, fp8):
+    """An fp32 gradient is off by what one sum of 2048 rows is: 128 times a dropped last bit of the
+    sum so far, which is no longer than the whole in the norm (twice, for the two parts of E4M3
+    rows, and half a step of their second, 2^-17), and a rounding for each of the sums added."""
+    case = Case(ep, fp8=fp8, **c)
+    before = torch.randn(len(c["counts"]), c["N"], c["H"], device="cuda")
+    grad_w = before.clone()
+    _, got = case.backward(ep, grad_w_dtype=torch.float32)
+    case.backward(ep, grad_w=grad_w, accumulate=True)
+    for _ in range(5):
+        assert torch.equal(case.backward(ep, grad_w_dtype=torch.float32)[1], got)
+    for e, n in enumerate(c["counts"]):
+        rows = slice(int(case.start[e]), int(case.end[e]))
+        y = ref.f64(case.dy[rows]).T @ case.xf[rows]
+        norm = np.linalg.norm(y) or 1.0
+        off = (129 + n / 2048) * ref.EPS * (2 if fp8 else 1) + (2.0 ** -17 if fp8 else 0)
+        assert np.linalg.norm(ref.f64(got[e]) - y) <= off * norm, e
+        was = ref.f64(before[e])
+        off = off * norm + (2 + n / 2048) * ref.EPS * np.linalg.norm(abs(y) + abs(was))
+        assert np.linalg.norm(ref.f64(grad_w[e]) - y - was) <= off, e
 
 
 def test_rows_past_32_bit_offsets(ep):
