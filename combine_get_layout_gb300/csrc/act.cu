@@ -10,6 +10,9 @@
 // adjacent columns a lane, so that every access of a warp is one contiguous
 // piece; 16 lanes hold one block of 128, whose maximum is four shuffles.  The
 // loads of a warp's next step are issued before the present one is computed.
+//
+// 32768 rows of 2 x 2048: save 94.5 us (541 MB, 5.7 TB/s; two issue slots of
+// three are taken), backward 107 us (675 MB, 6.3 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

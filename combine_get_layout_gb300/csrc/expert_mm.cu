@@ -38,6 +38,13 @@
 // the end: there the products cost, and two parts would double them.
 //
 // Sums are fp32 in tensor memory, rounded once on the way out.
+//
+// What bounds it: the weights' bytes where experts have few rows (one token by
+// 8 of 256 experts of 4096 x 7168: 75 us, 470 MB at 6.3 TB/s; 128 tokens 2070
+// us, 7.1 TB/s), the tensor cores from about 300 rows an expert on (16384 rows
+// by 4096 x 7168: 502 us, 1915 TFLOP/s, 575 under the power cap), the written
+// bytes for dW of few rows (15 GB in 2.4 to 3.0 ms).  A single CTA's tile (128
+// x 256, cta_group::1) took 733 us for the 16384 rows.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -67,7 +74,9 @@ constexpr uint64_t kStepNs = 4000;              // far above what a stage takes
 // each 16 rows (19,400 rows in one sum: off by 2.2e-5 in the norm).
 constexpr int kMostRows = 2048;
 constexpr int kMostParts = 4;                   // pairs that share a reduction: 8 CTAs
-constexpr int kRowGroup = 8;                    // row tiles that share weight tiles in L2
+// Row tiles that share weight tiles in L2.  65536 rows by 4096 x 4096 in groups
+// of 1, 8 and 64: 1095, 1120 and 1315 us; matrices beyond L2 need the sharing.
+constexpr int kRowGroup = 8;
 
 constexpr int kEpilogueWarps = 4, kCopyWarp = 4, kMmaWarp = 5, kClearWarp = 6;
 constexpr int kFirstConvertWarp = 7, kConvertWarps = 12;
@@ -1037,10 +1046,16 @@ template <Mode MODE, bool FP8, bool GATED, bool OUT32>
 cudaError_t launch(const MmMaps& maps, MmParams p, int64_t most_items, int64_t steps,
                    cudaStream_t s) {
   const int64_t pairs = device_info().sm_count / 2;
-  // Where tiles leave half the pairs or more without work, two or four of them
-  // share a tile's reduction, down to four steps each.
+  // Where tiles leave most pairs without work, two or four of them share a
+  // tile's reduction, down to 16 steps each: 8 rows by 1024 x 7168, in 1, 2 and
+  // 4 parts, 19.7, 13.8 and 11.5 us; dW of 8192 rows, 512 x 512, 38.8, 27.6 and
+  // 23.5; but 8 steps a part 7.5 us alone, 8.4 shared.  Clusters fill three
+  // quarters of the SMs at most: what does not fit into the groups of SMs that
+  // clusters are placed in would come in a second round (16 clusters of 8:
+  // 39.8 us, 32 of 4 23.5).
   p.parts = 1;
-  while (p.parts < kMostParts && most_items * p.parts * 2 <= pairs && steps >= 8 * p.parts)
+  while (p.parts < kMostParts && most_items * p.parts * 2 <= pairs * 3 / 4 &&
+         steps >= 32 * p.parts)
     p.parts *= 2;
   const int clusters = int(most_items < pairs / p.parts ? most_items : pairs / p.parts);
   return p.parts > 1 ? launch_parts<MODE, FP8, GATED, OUT32, true>(maps, p, clusters, s)
