@@ -7,12 +7,20 @@
 
 namespace ep {
 
+// Rows [first, first + rows) of what [start, end) holds of [0, cap).  (Ends are
+// compared, not subtracted, before they are clipped: an end far below its
+// start would leave 32 bits, and come back as a large number of rows.)
+__host__ __device__ __forceinline__ void clip_rows(int32_t start, int32_t end, int cap, int& first,
+                                                   int& rows) {
+  first = start < 0 ? 0 : start < cap ? start : cap;
+  const int past = end < cap ? end : cap;
+  rows = past > first ? past - first : 0;
+}
+
 // Rows [first, first + rows) of expert e among `cap`.
 __device__ __forceinline__ void clip_segment(const int32_t* start, const int32_t* end, int cap,
                                              int e, int& first, int& rows) {
-  const int s = min(max(__ldg(start + e), 0), cap);
-  rows = max(min(__ldg(end + e), cap) - s, 0);
-  first = s;
+  clip_rows(__ldg(start + e), __ldg(end + e), cap, first, rows);
 }
 
 // table[e] = the sum of count(0..e-1), for e = 0..E, at most INT32_MAX (where
