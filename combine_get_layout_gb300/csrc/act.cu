@@ -129,6 +129,26 @@ __device__ __forceinline__ float sigmoid(float x) {
   return r;
 }
 
+// What lanes past a row's end hold: NaN, which no maximum takes from a block
+// that has a value, and which leaves a block of NaN alone one.
+constexpr uint32_t kNoValue = 0x7fff7fff;
+
+// A block of zeros and NaN has a maximum of 0, and 0 in all its codes as in a
+// dispatch; its scale is -0 (no other block's is), by which the backward pass
+// knows it: it reads as NaN.
+constexpr uint32_t kNanAmongZeros = 0x80000000;
+
+__device__ __forceinline__ float kept_scale(float s) {
+  return __float_as_uint(s) == kNanAmongZeros ? __uint_as_float(0x7fffffff) : s;
+}
+
+__device__ __forceinline__ bool any_nan(const float* f) {
+  bool nan = false;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) nan |= f[j] != f[j];
+  return nan;
+}
+
 // The larger of two pairs of magnitudes; NaN is not larger.
 __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
   uint32_t r;
@@ -146,7 +166,8 @@ __device__ __forceinline__ uint32_t most8(uint4 v) {
 
 // The codes of eight values f (packed: v) of a block with this maximum, and
 // the block's scale: amax / 448 and the codes of the quotients as in
-// quantize_group16.
+// quantize_group16, but for a block of NaN alone: its maximum, and so its
+// scale and codes, are NaN.
 __device__ __forceinline__ uint2 quantize8(uint4 v, const float* f, float amax, float* scale) {
   // |a| / 448 by its reciprocal and one exact remainder is the IEEE quotient
   // for every bf16 value from 2^-90 on (all were compared)
@@ -190,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) act_save_kernel(const Ac
   const uint8_t* h = nullptr;      // of the row
   const auto load = [&] {
     const int c = w.col + lane * 8;
-    g = u = make_uint4(0, 0, 0, 0);
+    g = u = make_uint4(kNoValue, kNoValue, kNoValue, kNoValue);
     if (c < w.end) {
       g = ld_stream_u4(h + c * 2);
       u = ld_stream_u4(h + (c + p.I) * 2);
@@ -224,6 +245,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) act_save_kernel(const Ac
     unpack(uv, y);
     const uint2 xq = quantize8(gv, x, bf16_lo(m), &x_scale);
     const uint2 yq = quantize8(uv, y, bf16_hi(m), &y_scale);
+    // (one vote a step where no block is 0)
+    if (__any_sync(0xffffffffu, (m & 0xffffu) == 0 || m >> 16 == 0)) {
+      const uint32_t block = 0xffffu << (lane & 16);
+      const uint32_t x_nan = __ballot_sync(0xffffffffu, in && any_nan(x)) & block;
+      const uint32_t y_nan = __ballot_sync(0xffffffffu, in && any_nan(y)) & block;
+      if ((m & 0xffffu) == 0 && x_nan != 0) x_scale = __uint_as_float(kNanAmongZeros);
+      if (m >> 16 == 0 && y_nan != 0) y_scale = __uint_as_float(kNanAmongZeros);
+    }
 #pragma unroll
     for (int j = 0; j < 8; ++j) y[j] *= x[j] * sigmoid(x[j]);
     if (in) {
@@ -273,8 +302,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) act_backward_kernel(cons
     if (there) load();
     if (!in) continue;
     unpack(dv, da);
-    unpack8(gv, g_scale, x);
-    unpack8(uv, u_scale, y);
+    unpack8(gv, kept_scale(g_scale), x);
+    unpack8(uv, kept_scale(u_scale), y);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float t = sigmoid(x[j]);
