@@ -260,18 +260,28 @@ struct Walk {
   }
 };
 
-// mbar_wait for something that so many steps of a stage come before.
+// Waits of a whole warp.  A lane polls, and may give up, on its own: all go on
+// together and alike, as the warp-wide instructions behind a wait ask (elect,
+// tcgen05.ld, barriers).
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+  const bool ok = mbar_wait(bar, parity, kWaitTimeoutNs);
+  return __all_sync(0xffffffffu, ok);
+}
+
+// For something that so many steps of a stage come before.
 __device__ __forceinline__ bool wait_for_steps(uint64_t* bar, uint32_t parity, uint64_t steps) {
-  for (uint64_t i = 0; i <= steps * kStepNs / kWaitTimeoutNs; ++i)
-    if (mbar_wait(bar, parity, kWaitTimeoutNs)) return true;
-  return false;
+  bool ok = false;
+  for (uint64_t i = 0; !ok && i <= steps * kStepNs / kWaitTimeoutNs; ++i)
+    ok = mbar_wait(bar, parity, kWaitTimeoutNs);
+  return __all_sync(0xffffffffu, ok);
 }
 
 // The same, for what other CTAs of the cluster wrote to their shared memory.
 __device__ __forceinline__ bool wait_for_sums(uint64_t* bar, uint32_t parity, uint64_t steps) {
-  for (uint64_t i = 0; i <= steps * kStepNs / kWaitTimeoutNs; ++i)
-    if (mbar_wait_acquire(bar, parity, kWaitTimeoutNs)) return true;
-  return false;
+  bool ok = false;
+  for (uint64_t i = 0; !ok && i <= steps * kStepNs / kWaitTimeoutNs; ++i)
+    ok = mbar_wait_acquire(bar, parity, kWaitTimeoutNs);
+  return __all_sync(0xffffffffu, ok);
 }
 
 __device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
@@ -347,6 +357,7 @@ __device__ __forceinline__ void part16(uint4 q, float scale, uint32_t (&r)[8]) {
 // Each comes to it whether its own wait ran out or not, and all go on alike.
 __device__ __forceinline__ bool group_agrees(int id, int threads, bool ok) {
   uint32_t all;
+  __syncwarp();
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
       "barrier.cta.red.and.aligned.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
@@ -447,7 +458,7 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
       const int m0 = it.m0 + int(rank) * (GATED ? kLanes / 2 : kLanes);
       const int col0 = kTwo ? 0 : int(rank) * half;
       for (int kb = 0; kb < it.steps; ++kb, ++n, at.next(stages)) {
-        ok = mbar_wait(&sm.empty[at.s], at.phase ^ 1, kWaitTimeoutNs);
+        ok = warp_wait(&sm.empty[at.s], at.phase ^ 1);
         if (!ok) break;
         const uint32_t a = smem_addr(ring + at.s * stage_bytes), b = a + kABytes;
         const int k0 = (it.first + kb) * kDepth;
@@ -519,11 +530,11 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
       if (it.steps == 0) continue;
       const uint32_t idesc = instr_desc(2 * kLanes, it.cols, kAByFeature, kBByFeature);
       const uint32_t buf = tile & 1, acc = tmem + buf * kMaxCols;
-      ok = mbar_wait(&sm.acc_empty[buf], (tile / 2 & 1) ^ 1, kWaitTimeoutNs);
+      ok = warp_wait(&sm.acc_empty[buf], (tile / 2 & 1) ^ 1);
       if (!ok) break;
       tc_fence_after();
       for (int kb = 0; kb < it.steps; ++kb, at.next(stages)) {
-        ok = mbar_wait(&sm.full[at.s], at.phase, kWaitTimeoutNs);
+        ok = warp_wait(&sm.full[at.s], at.phase);
         if (!ok) break;
         tc_fence_after();
         const uint32_t a = smem_addr(ring + at.s * stage_bytes), b = a + kABytes;
@@ -644,7 +655,7 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
           [[maybe_unused]] const int left = lefts[d];
           some = half > 0;
           if (!some) break;
-          ok = mbar_wait(&sm.raw[at.s], at.phase, kWaitTimeoutNs);
+          ok = warp_wait(&sm.raw[at.s], at.phase);
           uint8_t* to = ring + at.s * stage_bytes + kABytes;
           uint4 q[kPieces];
 #pragma unroll
