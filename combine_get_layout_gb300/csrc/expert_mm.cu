@@ -29,20 +29,27 @@
 //
 // E4M3 rows: the scale changes along the reduction (every 128 inputs), so it
 // cannot be applied to a sum.  Forward, value * scale enters as two bf16
-// parts, 12 bits of it together: the first CTA's columns are the first parts,
-// the second's the others, and the epilogue adds the two sums.  That halves
-// the rows a tile holds; the weights are what costs at the sizes that prompts
-// and decode have.  A dW in fp32 takes two parts too, 17 bits together.  A dW
-// in bf16 takes bf16(value * scale) alone, one rounding of 2^-9 of the value
-// at most, as rows have that were never quantised and as its own sums get at
-// the end: there the products cost, and two parts would double them.
+// parts, together within 1.4 * 2^-12 of it: the first CTA's columns are the
+// first parts, the second's the others, and the epilogue adds the two sums.
+// That halves the rows a tile holds, which costs nothing where the weights'
+// bytes bound the product: up to some 50 rows an expert (64 experts of 4096 x
+// 4096: 32 rows 335 us, in bf16 343; 100 rows 390 and 351; 256 rows 740 and
+// 392).  A dW in fp32 takes two parts too, 17 bits together.  A dW in bf16
+// takes bf16(value * scale) alone, a rounding of 2^-8 of the value at most, as
+// rows have that were never quantised and as its own sums get at the end (off
+// in the norm by 0.0023, and by 0.0017 without it): there the products cost,
+// and two parts would double them.  Who wants them asks for fp32.
 //
-// Sums are fp32 in tensor memory, rounded once on the way out.
+// Sums are fp32 in tensor memory, rounded once on the way out.  The tensor
+// cores drop what lies below the accumulator's last bit, with each 16 of the
+// reduction: about 2^-26 of a sum of one sign, which comes to 7e-6 for 7168
+// inputs and to 1e-3, half the last rounding's size, for 2^20.
 //
 // What bounds it: the weights' bytes where experts have few rows (one token by
 // 8 of 256 experts of 4096 x 7168: 75 us, 470 MB at 6.3 TB/s; 128 tokens 2070
 // us, 7.1 TB/s), the tensor cores from about 300 rows an expert on (16384 rows
-// by 4096 x 7168: 502 us, 1915 TFLOP/s, 575 under the power cap), the written
+// by 4096 x 7168: 502 to 509 us alone, 1900 TFLOP/s, 565 to 585 under the power
+// cap, where cuBLAS takes 481 to 517 and 553 to 560), the written
 // bytes for dW of few rows (15 GB in 2.4 to 3.0 ms).  A single CTA's tile (128
 // x 256, cta_group::1) took 733 us for the 16384 rows.
 #include <cuda_bf16.h>
@@ -323,8 +330,9 @@ __device__ __noinline__ void widen16_apart(uint4 q, float scale, uint32_t (&r)[8
 // magnitude of E4M3 is that of a bf16 2^-120 as large.  Of the scale, times
 // 2^120, the first part takes its nearest number of four bits, by which any
 // E4M3 value is exact in bf16, the second what is left, rounded twice to 8
-// bits: together within 2^-12 of the product.  Scales of 128 and more (2^120
-// of which bf16 does not hold) and NaN go the way above.
+// bits: together within 1.4 * 2^-12 of the product (1.31 over all mantissas).
+// Scales of 128 and more (2^120 of which bf16 does not hold) and NaN go the way
+// above; of scales below 2^-126 the first part is none.
 template <Bits PART>
 __device__ __forceinline__ void part16(uint4 q, float scale, uint32_t (&r)[8]) {
   const uint32_t w[4] = {q.x, q.y, q.z, q.w};

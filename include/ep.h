@@ -684,10 +684,14 @@ EP_API int32_t ep_expert_w4(const ep_w4_config *cfg, int32_t cap, int32_t num_ro
  * y_r = W_e x_r for the rows r of every expert e, between ep_dispatch and
  * ep_combine, with W_e [N, H] in bf16, and the gradients by the rows and by
  * the weights: for prompts, training, and decode with unquantised weights.
- * Any number of rows an expert, none among them.  Sums are fp32, rounded once
- * at the end.  E4M3 rows enter the product as value * scale to 12 bits, the
- * weights' gradient as value * scale to 17 bits where it is fp32, and as
- * bf16(value * scale) where it is bf16.  The same call gives the same bits. */
+ * Any number of rows an expert, none among them.  Sums are fp32 (the tensor
+ * cores' own: for each 16 of a reduction about 2^-26 of a sum of one sign is
+ * dropped), rounded once at the end.  E4M3 rows enter the product as value *
+ * scale to within 1.4 * 2^-12 of it, the weights' gradient as value * scale to
+ * 17 bits (2^-17) where it is fp32, and as bf16(value * scale), 2^-8 of it at
+ * most, where it is bf16; in each form, parts of an operand below 2^-133 are
+ * lost (and for scales below 2^-126 the product takes 8 bits).  The same call
+ * gives the same bits. */
 typedef struct {
   int32_t num_experts;   /* E in [1, 2048]                                   */
   int32_t in_features;   /* H: a multiple of 8 (of 128 when x_fp8), <= 2^20  */
