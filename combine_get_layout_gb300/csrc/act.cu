@@ -189,8 +189,11 @@ __device__ __forceinline__ uint2 quantize8(uint4 v, const float* f, float amax, 
     return make_uint2(__byte_perm(c[0], c[1], 0x5410) | (__byte_perm(v.x, v.y, 0x7531) & kSigns),
                       __byte_perm(c[2], c[3], 0x5410) | (__byte_perm(v.z, v.w, 0x7531) & kSigns));
   }
-  *scale = 0.0f;
+  // (amax itself: 0, or NaN; lanes past a row's end come here too, and divide
+  // nothing)
+  *scale = amax;
   if (amax == 0.0f) return make_uint2(0, 0);
+  if (amax != amax) return make_uint2(0x7f7f7f7f, 0x7f7f7f7f);
   const float s = __fdiv_rn(amax, 448.0f);
   *scale = s;
   uint32_t c[4];
