@@ -767,11 +767,11 @@ EP_API int32_t ep_expert_mm_backward(const ep_expert_config *cfg, int32_t cap, i
  * last one maybe short.  Where 128 divides I these are rows as an FP8
  * dispatch writes them, and ep_expert_mm takes them.
  * What is not finite stays so for ep_act_backward.  A maximum leaves NaN out:
- * beside other values a NaN is kept by its own code.  A block of NaN alone has
- * a NaN scale; one of NaN and zeros has the dispatch's codes (0) and a scale of
- * -0, which ep_act_backward reads as NaN, all of it (a product reads zeros, as
- * a dispatch leaves them); one with an infinity has an infinite scale, and
- * reads as NaN too. */
+ * beside other values a NaN is kept by its own code.  A dispatch leaves 0 of a
+ * block without any other value than NaN and zeros; here a block of NaN alone
+ * has a NaN scale, and one of NaN and zeros a dispatch's codes (0) and a scale
+ * of -0, which ep_act_backward reads as NaN, all of it (a product reads zeros).
+ * A block with an infinity has an infinite scale, and reads as NaN too. */
 
 /* d_h: device bf16 [cap, 2 I]; d_a: device bf16 [cap, I]; d_q: device E4M3
  * bytes [cap, 2 I]; d_scale: device fp32 [cap, 2 ceil(I / 128)].  I (width):
